@@ -358,6 +358,190 @@ SWAB_API swab_status band_attention_bwd_noalloc(const swab_desc *desc, float sca
                                                 const void *dO, const float *lse, void *dQ,
                                                 void *dK, void *dV, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Answering with the banded attention: rotary positions, a paged key / value
+ * cache and the attention of a few new tokens a request over it.  One step of
+ * a running batch is
+ *     cache_slots      lengths -> block table, slot of every new token
+ *     rotary_append    Q, K rotated; K, V written to their slots
+ *     band_decode      attention of the new tokens over the cache
+ * and needs no value on the host, so the three can be captured in a CUDA graph
+ * and replayed.  No counterpart on the pages; the key set of a query is theirs
+ * (band on the left with dilation, leading global tokens), continued one
+ * token at a time.
+ *
+ * Tokens of a step are flat: row t of the [tokens, heads, head_dim] tensors
+ * belongs to request r when q_start[r] <= t < q_start[r + 1]; rows from
+ * q_start[batch] on are padding.
+ *
+ * The cache holds K and V as two tensors [n_blocks, hk, page, head_dim].  A
+ * request's positions j = 0, 1, ... lie in blocks of `page` positions; block
+ * number j / page is found in column c of the request's row of the block table
+ * [batch, cols] (int32 block ids), at row j mod page of the block:
+ *     c = j / page                                        below cols,
+ *     c = pinned + (j / page - pinned) mod (cols - pinned)  from there on when
+ *         `ring` is set: the blocks behind the first `pinned` ones are recycled
+ *         once a window has left them.
+ * A slot is block * page + row.
+ *
+ * What lies in device memory is not seen by the host checks: a block id or
+ * slot outside the cache is never addressed (its key counts as absent, its
+ * token is not written) and raises SWAB_ERR_INVALID_ARG in the device status
+ * word (swab_device_status).  Id -1 is an empty column: absent, no error.
+ * ------------------------------------------------------------------------- */
+
+/* Rotary positions over tokens [b, n] with h query heads and hk key heads. */
+typedef struct swab_rotary_desc {
+    int32_t b, n;          /* tokens, b * n >= 1 */
+    int32_t h, hk;         /* heads of Q (>= 1) and of K (>= 0; 0: no K) */
+    int32_t head_dim;      /* a multiple of 16 bytes, at most 512 */
+    int32_t rot_dim;       /* leading channels that turn: even, 0..head_dim */
+    int32_t interleaved;   /* 0: pairs (c, c + rot_dim / 2); 1: pairs (2c, 2c + 1) */
+    int32_t dtype;         /* swab_dtype */
+    float scale;           /* factor on cos and sin */
+    int32_t pos0;          /* added to every position */
+    /* Element strides over (b, n, head) of Q, K, their outputs, and V
+     * (rotary_append), the channels adjacent; three zeros = contiguous
+     * [b, n, heads, head_dim].  Multiples of 16 bytes; the rows of an output
+     * must not overlap. */
+    int64_t q_stride[3], k_stride[3], qo_stride[3], ko_stride[3], v_stride[3];
+} swab_rotary_desc;
+
+/* Ways of scaling the frequencies f_k = base^(-2k / rot_dim) to contexts longer
+ * than the `original` one by `factor`: */
+typedef enum swab_rotary_scaling {
+    SWAB_ROTARY_NONE = 0,
+    SWAB_ROTARY_LINEAR = 1, /* f_k / factor: positions interpolated */
+    SWAB_ROTARY_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) */
+    SWAB_ROTARY_YARN = 3,   /* Peng et al., "YaRN: Efficient Context Window Extension":
+                               f_k / factor where pair k turns less than `low` times within
+                               the original context, f_k where more than `high` times, a
+                               linear ramp over the pair index between; cos and sin scaled by
+                               0.1 ln(factor) + 1 */
+    SWAB_ROTARY_BANDS = 4   /* the same limits with the blend linear in the turns */
+} swab_rotary_scaling;
+
+/* Fills the HOST array turns[rot_dim / 2] with the frequencies in turns a
+ * position, as the fraction of one turn times 2^64 (rounded), and *scale with
+ * the factor on cos and sin.  A position times such a number, modulo 2^64, is
+ * the angle's fraction of a turn without loss, however far the position.
+ * rot_dim even, >= 2; base > 1; factor >= 1; original > 0 and 0 < low < high for
+ * YARN and BANDS (else SWAB_ERR_INVALID_ARG).  Needs no GPU. */
+SWAB_API swab_status rotary_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                                        double original, double low, double high, uint64_t *turns,
+                                        float *scale);
+
+/* Rotary positions: with t = 2 pi * frac(p * turns[k] / 2^64) for the position
+ * p = pos[bb, i] + pos0 (pos NULL: p = i + pos0) and pair k = (a, b) of a head,
+ *     y_a = scale * (x_a cos t - x_b sin t),  y_b = scale * (x_b cos t + x_a sin t),
+ * channels from rot_dim on copied; fp32, rounded once.  Q -> Qo and, with
+ * hk > 0, K -> Ko.  turns: DEVICE array of rot_dim / 2 (NULL when rot_dim is
+ * 0); pos: DEVICE int32 [b, n].  An output may be its own input (same pointer
+ * and strides), no other overlap. */
+SWAB_API swab_status rotary(const swab_rotary_desc *desc, const uint64_t *turns, const int32_t *pos,
+                            const void *Q, const void *K, void *Qo, void *Ko, void *stream);
+/* Gradient of rotary: the same with t -> -t, dQo -> dQ and dKo -> dK (q_stride,
+ * k_stride are those of the inputs dQo, dKo; qo_stride, ko_stride of dQ, dK). */
+SWAB_API swab_status rotary_bwd(const swab_rotary_desc *desc, const uint64_t *turns, const int32_t *pos,
+                                const void *dQo, const void *dKo, void *dQ, void *dK, void *stream);
+
+typedef struct swab_cache_desc {
+    int32_t batch;     /* requests, 1..65535 */
+    int32_t page;      /* positions a block: 16, 32, 64 or 128 */
+    int32_t n_blocks;  /* blocks of the cache, >= 1; n_blocks * page < 2^31 */
+    int32_t cols;      /* columns of the block table, >= 1 */
+    int32_t ring;      /* 1: columns from `pinned` on are recycled */
+    int32_t pinned;    /* 0..cols - 1; 0 without ring */
+} swab_cache_desc;
+
+/* Block tables and slot maps from request lengths, for a step that adds
+ * n_new[r] tokens to request r's lens[r] (negative values count as 0).
+ *   q_start [batch + 1]: exclusive running sum of n_new (saturating).
+ *   table [batch, cols]: the columns that become used, columns ceil(lens / page)
+ *     to ceil((lens + n_new) / page) (at most cols), take the next blocks
+ *     free_list[used[0]], free_list[used[0] + 1], ... in the order of the
+ *     requests; the other columns stay.
+ *   slots, pos [tokens]: slot and position + pos0 of every new token; rows past
+ *     q_start[batch] get -1 and 0, tokens past `tokens` are not written.  Where
+ *     a step adds more than a recycled table holds, tokens whose block the
+ *     same step recycles get slot -1.
+ *   lens_out [batch] = lens + n_new; used_out[0] = used[0] + blocks taken.
+ * A request whose blocks are not all there -- the list (n_free long) runs out in
+ * or before it, or, without ring, its length passes cols * page -- gets none:
+ * its slots are -1 and lens_out[r] = lens[r]; used_out[1] counts the blocks
+ * missing (0: every request was served).  Such a request's rows of a
+ * following band_decode are meaningless.
+ * All arrays DEVICE int32, 4-byte aligned; lens_out may be lens and used_out
+ * (2 elements) may be used, no other overlap. */
+SWAB_API swab_status cache_slots(const swab_cache_desc *cache, int32_t tokens, int32_t pos0,
+                                 const int32_t *lens, const int32_t *n_new, int32_t *table,
+                                 const int32_t *free_list, int32_t n_free, const int32_t *used,
+                                 int32_t *lens_out, int32_t *used_out, int32_t *q_start,
+                                 int32_t *slots, int32_t *pos, void *stream);
+
+/* rotary on Q and K fused with the cache write: Q -> Qo rotated; K rotated and V
+ * as it is into row slots[t] of Kc, Vc [n_blocks, hk, page, head_dim].  b * n
+ * tokens, slots and pos as written by cache_slots; a token with slot -1 is not
+ * written (its Q still turns).  rot_dim 0: a plain append (turns, pos may be
+ * NULL; Q and Qo both NULL leave Q out).  hk >= 1.  Slots other than -1 must
+ * differ from each other.  cache->batch, cols, ring, pinned are not used. */
+SWAB_API swab_status rotary_append(const swab_rotary_desc *desc, const swab_cache_desc *cache,
+                                   const uint64_t *turns, const int32_t *pos, const int32_t *slots,
+                                   const void *Q, const void *K, const void *V, void *Qo, void *Kc,
+                                   void *Vc, void *stream);
+
+typedef struct swab_decode_desc {
+    swab_cache_desc cache;
+    int32_t tokens;       /* rows of Q, O, lse, >= 1 */
+    int32_t h, hk;        /* query heads, key heads (h a multiple of hk): query head q reads key
+                             head q / (h / hk); h / hk at most 128 */
+    int32_t head_dim;     /* a multiple of 16 bytes, at most 256 */
+    int32_t w;            /* keys on the left, 0..2^30 (at least the longest context: all of them) */
+    int32_t dilation;     /* 0..SWAB_MAX_DILATION; key stride dilation + 1 */
+    int32_t n_sink;       /* leading positions every later query attends to, >= 0 */
+    int32_t max_q;        /* most new tokens of a request, >= 1 */
+    int32_t max_len;      /* longest context, >= 1 (divides the work; longer ones stay right) */
+    int32_t prefix_len;   /* positions of the shared prefix, 0: none */
+    int32_t dtype;        /* swab_dtype of Q, K, V, O */
+    int64_t q_row_stride; /* elements between rows of Q, 0 = h * head_dim; multiple of 16 bytes */
+    int64_t out_row_stride; /* the same of O */
+} swab_decode_desc;
+
+/* Bytes of workspace band_decode needs (0 if it needs none, or desc is bad). */
+SWAB_API size_t band_decode_workspace(const swab_decode_desc *desc);
+
+/* Banded attention of the new tokens over the cache.  Request r holds lens[r]
+ * positions, its m = q_start[r + 1] - q_start[r] new tokens among them (the
+ * last ones), so row q_start[r] + a is the query at position
+ * i = lens[r] - m + a and attends to
+ *     the positions j = i - k * (dilation + 1), 0 <= k <= w, j >= n_sink,
+ *     the positions j < n_sink, j <= i,
+ *     with prefix_len > 0 also every position of the shared prefix,
+ * each once:  O = softmax(scale * q . K) . V,  lse = log of its sum of
+ * exponentials ([tokens, h] fp32, may be NULL).  A query without a key (an
+ * inconsistent length, absent blocks) gets O = 0 and lse = -inf.  Rows past
+ * q_start[batch] are left as they were.
+ * The shared prefix lies in the same cache: positions p of it in block
+ * prefix_table[p / page] ([ceil(prefix_len / page)], DEVICE int32); it comes
+ * before position 0 of every request and is read once for all of them.  It
+ * stays visible whatever the window, like the global tokens of the banded
+ * calls.
+ * With ring, the recycled columns must hold a step's window:
+ * w * (dilation + 1) + max_q <= (cols - pinned - 1) * page + 1, and the pinned
+ * ones the sinks: n_sink <= pinned * page (else SWAB_ERR_INVALID_ARG).
+ * Every key and value that some query of the same request attends to has to
+ * be finite; the others are never used, whatever they hold.
+ * workspace: band_decode_workspace(desc) bytes of device memory, 16-byte
+ * aligned (NULL if 0); its contents on entry do not matter, and calls that may
+ * overlap on the GPU need one each.  The call launches up to three kernels,
+ * ordered on the stream like one.  Results do not depend on timing (no
+ * atomics). */
+SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, const void *Q,
+                                 const void *Kc, const void *Vc, const int32_t *table,
+                                 const int32_t *lens, const int32_t *q_start,
+                                 const int32_t *prefix_table, void *O, float *lse, void *workspace,
+                                 void *stream);
+
 /* Human-readable name of a status code (static string). */
 SWAB_API const char *swab_status_string(swab_status status);
 

@@ -30,6 +30,8 @@ API_FUNCTIONS = ("add_bias_transpose", "global_attention", "global_attention_bwd
                  "band_softmax_bwd", "band_attention", "band_attention_bwd",
                  "band_attention_bwd_workspace", "band_attention_bwd_noalloc",
                  "band_attention_dropout_mask_bytes",
+                 "rotary_frequencies", "rotary", "rotary_bwd", "cache_slots", "rotary_append",
+                 "band_decode", "band_decode_workspace",
                  "swab_status_string", "swab_device_status",
                  "swab_selftest_wait_timeout", "swab_bounds_checked", "swab_bounds_report",
                  "swab_selftest_bounds", "swab_version")
@@ -159,6 +161,9 @@ def load():
                 "swab_bounds_report": [ctypes.POINTER(ctypes.c_uint64), i32],
                 "swab_selftest_bounds": [P],
             }
+            from . import serve
+
+            sigs.update(serve.signatures())
             for name, args in sigs.items():
                 fn = getattr(lib, name)
                 fn.argtypes = args
@@ -169,6 +174,8 @@ def load():
             lib.band_attention_bwd_workspace.restype = ctypes.c_size_t
             lib.band_attention_dropout_mask_bytes.argtypes = [D]
             lib.band_attention_dropout_mask_bytes.restype = ctypes.c_size_t
+            lib.band_decode_workspace.argtypes = [ctypes.POINTER(serve._DecodeDesc)]
+            lib.band_decode_workspace.restype = ctypes.c_size_t
             lib.swab_status_string.restype = ctypes.c_char_p
             lib.swab_status_string.argtypes = [ctypes.c_int]
             lib.swab_version.restype = ctypes.c_char_p

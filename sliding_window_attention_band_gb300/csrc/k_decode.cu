@@ -1,0 +1,220 @@
+// k_decode.cu -- banded attention of a few new tokens a request over the paged
+// cache: the general kernel (every type and head size) and the joining of the
+// parts of a split key axis.
+//
+// A query's keys are a list: the shared prefix, the leading global tokens, the
+// band (ascending).  The list is cut into pieces; a block takes one (request,
+// query head, piece) and runs through it once with the running maximum m and
+// sum l of the softmax, in log2 units and fp32:
+//     m' = max(m, x),  l' = l 2^(m - m') + 2^(x - m'),  o' = o 2^(m - m') + 2^(x - m') v.
+// The pieces are joined as O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
+#include "swab_internal.h"
+#include "swab_decode.cuh"
+
+static constexpr unsigned kSwabFile = 13;   // site id of the bounds checks
+
+namespace swab {
+namespace {
+
+constexpr int kThreads = 128;
+
+template <typename T>
+__device__ __forceinline__ void widen16(const uint4 &v, float *f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 4) {
+            f[k] = __uint_as_float(w[k]);
+        } else {
+            f[2 * k] = lo16<T>(w[k]);
+            f[2 * k + 1] = hi16<T>(w[k]);
+        }
+    }
+}
+
+// A key belongs to a group of kLanes lanes, 16 bytes of its row a lane (kVec
+// times when the row has more than 32 pieces); kThreads / kLanes keys at a time.
+template <typename T, int kLanes, int kVec>
+__global__ void __launch_bounds__(kThreads) k_decode_general(const __grid_constant__ DecodeArgs p) {
+    constexpr int kV = 16 / sizeof(T), kE = kV * kVec, kGroups = kThreads / kLanes;
+    __shared__ float so[kGroups][kLanes * kE];
+    __shared__ float2 sml[kGroups];
+    const int split = blockIdx.x, head = blockIdx.y, r = blockIdx.z;
+    const int kvh = head / p.group, sub = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const int pieces = p.hd / kV;
+    pdl_trigger();                   // k_decode_join, which waits for this grid
+    const Request q = request_of(p, r);
+    for (int a = 0; a < q.m; ++a) {
+        const KeyList keys = keys_of(p, q, a, a);
+        const long long n = keys.count + p.prefix_len, lo = (long long)split * p.chunk;
+        const long long hi = split == p.nsplit - 1 ? n : min(n, lo + p.chunk);
+        const long long row = q.row0 + a;
+        const T *qrow = reinterpret_cast<const T *>(p.Q) + row * p.q_stride + (long long)head * p.hd;
+        float qf[kE], o[kE], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            const int piece = lane + v * kLanes;
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (piece < pieces) raw = *reinterpret_cast<const uint4 *>(GPN(p.bnd, qrow + piece * kV, 16));
+            widen16<T>(raw, qf + v * kV);
+        }
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = 0.f;
+        // every lane group makes the same number of steps: the shuffles below
+        // need the whole warp
+        const int steps = lo < hi ? (int)((hi - lo + kGroups - 1) / kGroups) : 0;
+        for (int s = 0; s < steps; ++s) {
+            const long long u = lo + (long long)s * kGroups + sub;
+            long long line = -1;
+            if (u < hi) line = u < p.prefix_len ? prefix_line(p, (int)u, kvh) : key_line(p, q, keys.at((int)(u - p.prefix_len)), kvh);
+            uint4 kr[kVec], vr[kVec];
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                const int piece = lane + v * kLanes;
+                kr[v] = vr[v] = make_uint4(0, 0, 0, 0);
+                if (line >= 0 && piece < pieces) {
+                    const long long at = line * p.hd + piece * kV;
+                    kr[v] = ldg16(GPN(p.bnd, reinterpret_cast<const T *>(p.Kc) + at, 16));
+                    vr[v] = ldg16(GPN(p.bnd, reinterpret_cast<const T *>(p.Vc) + at, 16));
+                }
+            }
+            float x = 0.f;
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                float kf[kV];
+                widen16<T>(kr[v], kf);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) x = fmaf(qf[v * kV + e], kf[e], x);
+            }
+#pragma unroll
+            for (int d = kLanes / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+            if (line < 0) continue;
+            x *= p.scale_log2;
+            const float mn = fmaxf(m, x), corr = m == -INFINITY ? 0.f : exp2f(m - mn), pr = exp2f(x - mn);
+            l = fmaf(l, corr, pr);
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                float vf[kV];
+                widen16<T>(vr[v], vf);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) o[v * kV + e] = fmaf(pr, vf[e], o[v * kV + e] * corr);
+            }
+            m = mn;
+        }
+        __syncthreads();                 // the previous query's reads of the buffers
+#pragma unroll
+        for (int e = 0; e < kE; ++e) so[sub][lane * kE + e] = o[e];
+        if (lane == 0) sml[sub] = make_float2(m, l);
+        __syncthreads();
+        float M = -INFINITY, L = 0.f;
+        for (int g = 0; g < kGroups; ++g) M = fmaxf(M, sml[g].x);
+        for (int g = 0; g < kGroups; ++g)
+            if (sml[g].x != -INFINITY) L += sml[g].y * exp2f(sml[g].x - M);
+        const long long th = row * p.h + head;
+        for (int c = threadIdx.x; c < p.hd; c += kThreads) {
+            const int piece = c / kV, at = piece % kLanes * kE + piece / kLanes * kV + c % kV;
+            float y = 0.f;
+            for (int g = 0; g < kGroups; ++g)
+                if (sml[g].x != -INFINITY) y += so[g][at] * exp2f(sml[g].x - M);
+            if (p.nparts > 1)
+                *GP(p.bnd, p.po + (th * p.nparts + split) * p.hd + c) = y;
+            else
+                *GP(p.bnd, reinterpret_cast<T *>(p.O) + row * p.o_stride + (long long)head * p.hd + c) =
+                    Elt<T>::from_f(L > 0.f ? y / L : 0.f);
+        }
+        if (threadIdx.x == 0) {
+            if (p.nparts > 1) *GP(p.bnd, p.pml + th * p.nparts + split) = make_float2(M, L);
+            else if (p.lse) *GP(p.bnd, p.lse + th) = lse_of(M, L);
+        }
+    }
+}
+
+// Joins the parts of one (token, head): kW warps share them (a warp where there
+// are few; four, over shared memory, where a long context was cut into many).
+// A lane holds the channels lane, lane + 32, ...
+template <typename T, int kW>
+__global__ void __launch_bounds__(kThreads) k_decode_join(const __grid_constant__ DecodeArgs p) {
+    constexpr int kMaxPer = 8, kPairs = kThreads / 32 / kW;      // head_dim <= 256
+    __shared__ float so[kW > 1 ? kW : 1][kMaxPer * 32];
+    __shared__ float sl[kW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part0 = warp % kW;
+    const long long th = (long long)blockIdx.x * kPairs + warp / kW;
+    const long long row = th / p.h;
+    const int head = (int)(th - row * p.h);
+    pdl_wait();                                                  // the parts are there
+    if (row >= p.tokens || row >= *GP(p.bnd, p.q_start + p.batch)) return;   // with kW = 4: the whole block
+    const float2 *ml = p.pml + th * p.nparts;
+    const float *po = p.po + th * p.nparts * p.hd;
+    float M = -INFINITY, L = 0.f;
+    for (int s = lane; s < p.nparts; s += 32) M = fmaxf(M, GP(p.bnd, ml + s)->x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float o[kMaxPer];
+#pragma unroll
+    for (int e = 0; e < kMaxPer; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int s = part0; s < p.nparts; s += kW) {
+        const float2 v = *GP(p.bnd, ml + s);
+        const float f = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
+        L = fmaf(v.y, f, L);
+#pragma unroll
+        for (int e = 0; e < kMaxPer; ++e) {
+            const int c = lane + 32 * e;
+            if (c < p.hd) o[e] = fmaf(*GP(p.bnd, po + (long long)s * p.hd + c), f, o[e]);
+        }
+    }
+    if constexpr (kW > 1) {
+#pragma unroll
+        for (int e = 0; e < kMaxPer; ++e) so[warp][lane + 32 * e] = o[e];
+        if (lane == 0) sl[warp] = L;
+        __syncthreads();
+        if (warp > 0) return;
+        L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) L += sl[w];
+#pragma unroll
+        for (int e = 0; e < kMaxPer; ++e) {
+            o[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) o[e] += so[w][lane + 32 * e];
+        }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int e = 0; e < kMaxPer; ++e) {
+        const int c = lane + 32 * e;
+        if (c < p.hd) *GP(p.bnd, reinterpret_cast<T *>(p.O) + row * p.o_stride + (long long)head * p.hd + c) = Elt<T>::from_f(o[e] * inv);
+    }
+    if (lane == 0 && p.lse) *GP(p.bnd, p.lse + th) = lse_of(M, L);
+}
+
+template <typename T>
+cudaError_t launch_general_t(const DecodeArgs &a, cudaStream_t st) {
+    const dim3 grid((unsigned)a.nsplit, (unsigned)a.h, (unsigned)a.batch);
+    const int pieces = a.hd * (int)sizeof(T) / 16;
+    if (pieces <= 4) k_decode_general<T, 4, 1><<<grid, kThreads, 0, st>>>(a);
+    else if (pieces <= 8) k_decode_general<T, 8, 1><<<grid, kThreads, 0, st>>>(a);
+    else if (pieces <= 16) k_decode_general<T, 16, 1><<<grid, kThreads, 0, st>>>(a);
+    else if (pieces <= 32) k_decode_general<T, 32, 1><<<grid, kThreads, 0, st>>>(a);
+    else k_decode_general<T, 32, 2><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_join_t(const DecodeArgs &a, cudaStream_t st) {
+    const long long pairs = (long long)a.tokens * a.h;
+    if (a.nparts > 8) return launch_dependent(&k_decode_join<T, 4>, dim3((unsigned)pairs), kThreads, 0, st, a);
+    return launch_dependent(&k_decode_join<T, 1>, dim3((unsigned)((pairs + 3) / 4)), kThreads, 0, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_general(DType dt, const DecodeArgs &a, cudaStream_t st) {
+    return dt == kF32 ? launch_general_t<float>(a, st) : dt == kF16 ? launch_general_t<__half>(a, st) : launch_general_t<__nv_bfloat16>(a, st);
+}
+
+cudaError_t launch_decode_join(DType dt, const DecodeArgs &a, cudaStream_t st) {
+    return dt == kF32 ? launch_join_t<float>(a, st) : dt == kF16 ? launch_join_t<__half>(a, st) : launch_join_t<__nv_bfloat16>(a, st);
+}
+
+}  // namespace swab

@@ -284,11 +284,6 @@ unsigned *status_word() {
 // into the kernels' arguments and, for the tensor maps' footprints, into a
 // thread-local copy.  In the regular build SWAB_BOUNDS is SWAB_OK.
 // ---------------------------------------------------------------------------
-struct Extent {
-    const void *p;
-    size_t bytes;
-};
-
 size_t round16(size_t bytes) { return (bytes + 15) / 16 * 16; }
 
 // Byte sizes of a call's buffers as the descriptor lays them out.
@@ -440,6 +435,26 @@ swab_status band_t_common(const swab_desc *desc, float alpha, const void *Bd, co
 }
 
 }  // namespace
+
+// What the entry points of swab_serve.cu share with this file.
+unsigned *device_status_word() { return status_word(); }
+swab_status status_of(cudaError_t e) { return from_cuda(e); }
+#if SWAB_BOUNDS_CHECK
+swab_status call_extents(Bounds *b, std::initializer_list<Extent> ext) { return set_bounds(b, ext); }
+#endif
+bool encode_tiled(CUtensorMap *map, DType dt, int rank, const void *base, const cuuint64_t *dims,
+                  const cuuint64_t *strides, const cuuint32_t *box) {
+    auto enc = get_encode();
+    if (!enc) return false;
+#if SWAB_BOUNDS_CHECK
+    if (!map_fits(base, rank, dims, strides, elt_size(dt))) return false;
+#endif
+    const CUtensorMapDataType ty = dt == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(map, ty, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Raises a kernel's dynamic shared-memory limit on the current device to at
 // least `bytes`; cudaFuncSetAttribute runs only when the limit recorded for

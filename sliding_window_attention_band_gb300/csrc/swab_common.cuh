@@ -18,6 +18,7 @@ constexpr int kMaxStride = SWAB_MAX_DILATION + 1;
 constexpr int kMaxGlobal = SWAB_MAX_GLOBAL;
 
 // Bits of the device status word (bit k <-> swab_status k).
+constexpr unsigned kErrInvalid = 1u << SWAB_ERR_INVALID_ARG;   // a block id or slot outside the cache
 constexpr unsigned kErrTimeout = 1u << SWAB_ERR_TIMEOUT;
 constexpr unsigned kErrBounds = 1u << SWAB_ERR_BOUNDS;
 

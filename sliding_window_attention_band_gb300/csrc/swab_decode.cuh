@@ -1,0 +1,121 @@
+// swab_decode.cuh -- what the decode kernels share: a request's rows, the list
+// of positions its queries attend to, and where a position lies in the cache.
+#pragma once
+
+#include "swab_internal.h"
+
+namespace swab {
+
+// Programmatic dependents: the kernels of a call may start while the one before
+// runs; pdl_wait returns when that one is complete and its writes are visible.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" :::); }
+
+// Launches a kernel as a programmatic dependent of the stream's last one.
+template <typename... A>
+cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The new tokens of request r: m rows from row0, the first at position i0 of a
+// context of `len` positions.
+struct Request {
+    int r, m, row0, len, i0;
+    const int *trow;     // its row of the block table
+    int ring_lo;         // recycled positions below this one are gone
+};
+
+constexpr unsigned kDecodeFile = 14;   // site id of the bounds checks in this header
+
+__device__ __forceinline__ Request request_of(const DecodeArgs &p, int r) {
+    [[maybe_unused]] constexpr unsigned kSwabFile = kDecodeFile;
+    Request q;
+    const int a = max(*GP(p.bnd, p.q_start + r), 0), b = min(*GP(p.bnd, p.q_start + r + 1), p.tokens);
+    q.r = r;
+    q.row0 = a;
+    q.m = max(b - a, 0);
+    const int m_all = *GP(p.bnd, p.q_start + r + 1) - *GP(p.bnd, p.q_start + r);
+    q.len = max(*GP(p.bnd, p.lens + r), 0);
+    q.i0 = q.len - m_all;
+    q.trow = p.table + (long long)r * p.cols;
+    q.ring_lo = 0;
+    if (p.ring && q.len > 0) q.ring_lo = max(((q.len - 1) >> p.page_log2) - (p.cols - p.pinned) + 1, 0) << p.page_log2;
+    return q;
+}
+
+// Positions that at least one of the queries a_lo..a_hi attends to, ascending:
+// the sinks 0..nsink-1, then band_lo, band_lo + step, ...  With a key stride
+// the queries have keys of their own, so the list is made for one (a_lo = a_hi).
+struct KeyList {
+    int count, nsink, band_lo, step;
+    __device__ __forceinline__ int at(int u) const { return u < nsink ? u : band_lo + (u - nsink) * step; }
+};
+
+__device__ __forceinline__ KeyList keys_of(const DecodeArgs &p, const Request &q, int a_lo, int a_hi) {
+    KeyList k;
+    const int lo = q.i0 + a_lo, hi = q.i0 + a_hi;
+    k.step = p.stride;
+    k.nsink = max(min(p.n_sink, hi + 1), 0);
+    int cnt = 0;
+    k.band_lo = 0;
+    if (p.stride == 1) {
+        k.band_lo = (int)max((long long)lo - p.w, (long long)p.n_sink);
+        cnt = max(hi - k.band_lo + 1, 0);
+    } else if (lo >= p.n_sink) {
+        const int t = min((lo - p.n_sink) / p.stride, p.w);
+        k.band_lo = lo - t * p.stride;
+        cnt = t + 1;
+    }
+    k.count = k.nsink + cnt;
+    return k;
+}
+
+// Does the query at position i attend to position j of such a list?
+__device__ __forceinline__ bool attends(const DecodeArgs &p, int i, int j) {
+    return j <= i && (j < p.n_sink || (long long)i - j <= (long long)p.w * p.stride);
+}
+
+// Line (row of head_dim values) of head kvh at row `off` of block `id`, or -1:
+// an absent column, or an id outside the cache (recorded).
+__device__ __forceinline__ long long block_line(const DecodeArgs &p, int id, int off, int kvh) {
+    if ((unsigned)id >= (unsigned)p.n_blocks) {
+        if (id != -1) atomicOr(p.err, kErrInvalid);
+        return -1;
+    }
+    return (((long long)id * p.hk + kvh) << p.page_log2) + off;
+}
+__device__ __forceinline__ long long key_line(const DecodeArgs &p, const Request &q, int j, int kvh) {
+    [[maybe_unused]] constexpr unsigned kSwabFile = kDecodeFile;
+    const int lb = j >> p.page_log2;
+    int col = lb;
+    if (lb >= p.cols) {
+        if (!p.ring) {                 // a context longer than its table
+            atomicOr(p.err, kErrInvalid);
+            return -1;
+        }
+        col = p.pinned + (lb - p.pinned) % (p.cols - p.pinned);
+    }
+    if (lb >= p.pinned && j < q.ring_lo) return -1;
+    return block_line(p, *GP(p.bnd, q.trow + col), j & ((1 << p.page_log2) - 1), kvh);
+}
+__device__ __forceinline__ long long prefix_line(const DecodeArgs &p, int j, int kvh) {
+    [[maybe_unused]] constexpr unsigned kSwabFile = kDecodeFile;
+    return block_line(p, *GP(p.bnd, p.ptable + (j >> p.page_log2)), j & ((1 << p.page_log2) - 1), kvh);
+}
+
+// log-sum-exp from the maximum (log2 units) and the sum
+__device__ __forceinline__ float lse_of(float M, float L) {
+    return L > 0.f ? M * 0.6931471805599453f + logf(L) : -INFINITY;
+}
+
+}  // namespace swab

@@ -6,7 +6,10 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
+
+#include <initializer_list>
 
 #include "swab_common.cuh"
 
@@ -278,6 +281,83 @@ cudaError_t launch_band_attention_bwd_glob(DType dt, const TmapSet &mq, const Tm
 
 cudaError_t launch_band_softmax(DType dt, const SoftmaxArgs &a, cudaStream_t st);
 cudaError_t launch_band_softmax_bwd(DType dt, const SoftmaxArgs &a, cudaStream_t st);
+
+// A buffer of a call and its size, for the bounds-checked build.
+struct Extent {
+    const void *p;
+    size_t bytes;
+};
+// What the two files of entry points share (swab_api.cu).
+unsigned *device_status_word();
+swab_status status_of(cudaError_t e);
+#if SWAB_BOUNDS_CHECK
+swab_status call_extents(Bounds *b, std::initializer_list<Extent> ext);
+#endif
+// a tiled map with 128-byte swizzle and zero fill over 16-bit elements
+bool encode_tiled(CUtensorMap *map, DType dt, int rank, const void *base, const cuuint64_t *dims,
+                  const cuuint64_t *strides, const cuuint32_t *box);
+
+// ---------------------------------------------------------------------------
+// answering: rotary positions, block tables, the paged cache, decode
+// ---------------------------------------------------------------------------
+struct RotaryArgs {
+    const void *Q, *K, *V;     // V with the cache write only
+    void *Qo, *Ko;             // Ko without the cache write
+    void *Kc, *Vc;             // the cache [n_blocks, hk, page, hd]
+    const unsigned long long *turns;
+    const int *pos, *slots;
+    long long sq[3], sk[3], sv[3], sqo[3], sko[3];   // strides over (b, n, head)
+    long long tokens;          // b * n
+    int n, hq, hk, hd, rot;    // hq: query heads handled (0 leaves Q out)
+    int interleaved, backward;
+    int pos0;
+    float scale;
+    int page_log2, n_slots;
+    unsigned *err;
+    int tile;                  // tokens a block takes at a time (set by the launcher)
+#if SWAB_BOUNDS_CHECK
+    Bounds bnd;
+#endif
+};
+cudaError_t launch_rotary(DType dt, bool append, RotaryArgs a, cudaStream_t st);
+
+struct CacheSlotsArgs {
+    const int *lens, *n_new, *free_list, *used;
+    int *table, *lens_out, *used_out, *q_start, *slots, *pos;
+    int batch, page_log2, n_blocks, cols, ring, pinned, n_free, tokens, pos0;
+    int table_pass, state;     // what a launch writes (set by the launcher)
+    unsigned *err;
+#if SWAB_BOUNDS_CHECK
+    Bounds bnd;
+#endif
+};
+cudaError_t launch_cache_slots(CacheSlotsArgs a, cudaStream_t st);
+
+struct DecodeArgs {
+    const void *Q, *Kc, *Vc;
+    void *O;
+    float *lse;                // or null
+    const int *table, *lens, *q_start, *ptable;
+    float *po;                 // parts: [tokens, h, nparts, hd] and their (max, sum)
+    float2 *pml;               // [tokens, h, nparts]
+    long long q_stride, o_stride;
+    int batch, tokens, h, hk, group, hd;
+    int w, stride, n_sink, prefix_len;
+    int page_log2, n_blocks, cols, ring, pinned;
+    int nsplit, chunk;         // pieces of the key list of a query and their length
+    int nparts;                // parts joined for a query (1: written directly)
+    int npre, pre_chunks, pre_tokens;   // the prefix kernel: pieces, 128-key chunks of one, tokens of a tile
+    float scale_log2;
+    unsigned *err;
+#if SWAB_BOUNDS_CHECK
+    Bounds bnd;
+#endif
+};
+cudaError_t launch_decode_general(DType dt, const DecodeArgs &a, cudaStream_t st);
+cudaError_t launch_decode_rows(DType dt, const DecodeArgs &a, int max_q, cudaStream_t st);
+cudaError_t launch_decode_prefix(DType dt, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                                 const DecodeArgs &a, cudaStream_t st);
+cudaError_t launch_decode_join(DType dt, const DecodeArgs &a, cudaStream_t st);
 
 // rows of one dense [BH, n, 64] tile box: band_qk loads 128-row boxes,
 // the gather kernels 64-row boxes.

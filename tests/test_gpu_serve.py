@@ -1,0 +1,701 @@
+"""Rotary positions, block tables, the cache write and decode against the fp64
+oracle (oracle/serve.py), on the GPU.
+
+Tolerances, set before the first run.  A stored value is off by at most half a
+step of its type (u = eps / 2 relative).  Rotary: cos and sin come from an
+argument within 2^-25 pi rad, sincospi within 2 ulp, the factor, the products
+and the sum round once each: together below 2^-21 (|x_a| + |x_b|).  Decode: a
+score of hd products in fp32 is within X (hd + 8) 2^-24 (X = the largest sum of
+|q| |k| times the scale), times log2 e, and 2^x within 2^-21, so a weight is
+within `delta` relatively; a sum of N weights adds N 2^-24; the tensor-core
+kernels round a weight to 16 bits once more (u, and for fp16 at most 2^-25 of
+the reference weight below its normal range).  O is a quotient of two such sums,
+its numerator bounded by A = sum p |v|.
+"""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import sliding_window_attention_band_gb300 as swab
+from oracle import serve as orc
+
+pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("device_status_guard")]
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+INVALID_BIT = 1 << 1
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def smallest_half_step(dtype):
+    """Half the spacing below the normal range (fp16: its values reach it)."""
+    return torch.finfo(dtype).tiny * torch.finfo(dtype).eps / 2
+
+
+def randn(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def bits(t):
+    return t.contiguous().view({1: torch.uint8, 2: torch.int16, 4: torch.int32, 8: torch.int64}[t.element_size()])
+
+
+def same_bits(a, b):
+    assert torch.equal(bits(a), bits(b))
+
+
+# ---------------------------------------------------------------------------
+# rotary
+# ---------------------------------------------------------------------------
+def rotary_bound(x, ref, rot, interleaved, scale, dtype):
+    """Per element: half a step of the result plus 2^-21 (|x_a| + |x_b|) scale."""
+    a = np.abs(x)
+    pair = np.zeros_like(a)
+    if rot:
+        k = np.arange(rot // 2)
+        one, two = (2 * k, 2 * k + 1) if interleaved else (k, k + rot // 2)
+        s = a[..., one] + a[..., two]
+        pair[..., one] = pair[..., two] = s * abs(scale) * 2.0 ** -21
+    return pair + (np.abs(ref) + pair) * half_step(dtype) + smallest_half_step(dtype)
+
+
+def check_rotary(got, x, pos, freq, scale, interleaved, dtype, backward=False):
+    ref = orc.rotary(f64(x), pos, freq, scale, interleaved, backward)
+    err = np.abs(f64(got) - ref)
+    bound = rotary_bound(f64(x), ref, 2 * len(freq), interleaved, scale, dtype)
+    assert (err <= bound).all(), float((err - bound).max())
+    same_bits(got[..., 2 * len(freq):], x[..., 2 * len(freq):])      # the rest is copied
+
+
+ROTARY = [  # b, n, h, hk, hd, rot, interleaved, scaling
+    (1, 1, 1, 0, 64, 64, False, "none"),
+    (1, 1, 4, 2, 64, 64, True, "linear"),
+    (2, 33, 5, 1, 80, 20, False, "yarn"),
+    (2, 33, 5, 1, 80, 20, True, "bands"),
+    (3, 70, 12, 4, 128, 128, False, "yarn"),
+    (3, 70, 12, 4, 128, 64, True, "ntk"),
+    (1, 257, 3, 3, 96, 96, False, "none"),
+    (1, 9, 2, 2, 512, 510, False, "none"),
+    (1, 5000, 2, 1, 64, 32, False, "none"),
+    (2, 7, 3, 1, 64, 0, False, "none"),
+    (1, 12, 3, 1, 64, 2, True, "none"),
+]
+
+
+def frequencies(rot, scaling):
+    factor, original = {"none": (1, 0), "linear": (4, 0), "ntk": (8, 0), "yarn": (16, 8192), "bands": (8, 8192)}[scaling]
+    if rot == 0:
+        return None, np.zeros(0), 1.0
+    turns, scale = swab.rotary_frequencies(rot, 10000.0, scaling, factor, original)
+    freq, _ = orc.frequencies(rot, 10000.0, scaling, factor, original, 1.0, 32.0 if scaling == "yarn" else 4.0)
+    return turns.cuda(), freq, scale
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("case", ROTARY)
+def test_rotary_matches_the_oracle(case, dtype):
+    b, n, h, hk, hd, rot, inter, scaling = case
+    turns, freq, scale = frequencies(rot, scaling)
+    q, k = randn((b, n, h, hd), dtype, 1), randn((b, n, max(hk, 1), hd), dtype, 2)
+    rng = np.random.default_rng(3)
+    pos = rng.integers(0, 1_000_000, (b, n))
+    d = swab.RotaryDesc(b, n, h, hk, hd, rot, inter, scale, dtype=dtype)
+    for fn, back in ((swab.rotary, False), (swab.rotary_bwd, True)):
+        qo, ko = torch.empty_like(q), torch.full_like(k, 3.0)
+        fn(d, turns, q, qo, k if hk else None, ko if hk else None, pos=i32(pos))
+        check_rotary(qo, q, pos, freq, scale, inter, dtype, back)
+        if hk:
+            check_rotary(ko, k, pos, freq, scale, inter, dtype, back)
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_rotary_positions_at_the_ends_of_their_range(dtype):
+    """Negative positions, 0 and the last int32; pos None counts from pos0 in every sequence."""
+    turns, freq, scale = frequencies(64, "none")
+    pos = np.array([[-1, 0, 1, 2 ** 31 - 1, -2 ** 31, 2 ** 24 + 1]])
+    x = randn((1, 6, 2, 64), dtype, 4)
+    y = torch.empty_like(x)
+    swab.rotary(swab.RotaryDesc(1, 6, 2, 0, 64, 64, dtype=dtype), turns, x, y, pos=i32(pos))
+    check_rotary(y, x, pos, freq, 1.0, False, dtype)
+    x = randn((3, 5, 2, 64), dtype, 5)
+    y = torch.empty_like(x)
+    swab.rotary(swab.RotaryDesc(3, 5, 2, 0, 64, 64, pos0=1000, dtype=dtype), turns, x, y)
+    check_rotary(y, x, np.tile(1000 + np.arange(5), (3, 1)), freq, 1.0, False, dtype)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotary_on_strided_views_and_in_place(inter):
+    """Q, K inside a merged projection, outputs head-major; then in place, which gives the same bits."""
+    b, n, h, hk, hd, rot = 2, 37, 4, 2, 64, 32
+    turns, freq, scale = frequencies(rot, "none")
+    qkv = randn((b, n, h + 2 * hk, hd), BF16, 6)
+    q, k = qkv[:, :, :h], qkv[:, :, h:h + hk]
+    pos = np.tile(np.arange(n) + 7, (b, 1))
+    d = swab.RotaryDesc(b, n, h, hk, hd, rot, inter, dtype=BF16)
+    qo = torch.empty(b, h, n, hd, dtype=BF16, device="cuda").transpose(1, 2)
+    ko = torch.empty(b, hk, n, hd, dtype=BF16, device="cuda").transpose(1, 2)
+    swab.rotary(d, turns, q, qo, k, ko, pos=i32(pos))
+    check_rotary(qo, q, pos, freq, scale, inter, BF16)
+    check_rotary(ko, k, pos, freq, scale, inter, BF16)
+    v = qkv[:, :, h + hk:].clone()
+    swab.rotary(d, turns, q, q, k, k, pos=i32(pos))
+    same_bits(q, qo)
+    same_bits(k, ko)
+    same_bits(qkv[:, :, h + hk:], v)
+    # one row of positions and heads read for every batch entry
+    one = randn((1, n, h, hd), BF16, 8).expand(b, n, h, hd)
+    out = torch.empty(b, n, h, hd, dtype=BF16, device="cuda")
+    swab.rotary(swab.RotaryDesc(b, n, h, 0, hd, rot, inter, dtype=BF16), turns, one, out, pos=i32(pos))
+    check_rotary(out, one, pos, freq, scale, inter, BF16)
+
+
+def test_rotary_gradient_against_differences():
+    """The map is linear, so a difference over any step is its derivative: (f(x + e) - f(x - e)) / 2 along unit
+    steps, f = sum(g * y).  Both sides carry fp32 roundings only: y and g below 8 in magnitude, two values each."""
+    b, n, h, hd, rot = 1, 3, 1, 16, 12
+    turns, _, scale = frequencies(rot, "yarn")
+    d = swab.RotaryDesc(b, n, h, 0, hd, rot, False, scale, dtype=F32)
+    x, g = randn((b, n, h, hd), F32, 9), randn((b, n, h, hd), F32, 10)
+    pos = i32([[5, 1000, 70000]])
+    dx = torch.empty_like(x)
+    swab.rotary_bwd(d, turns, g, dx, pos=pos)
+
+    def f(v):
+        y = torch.empty_like(v)
+        swab.rotary(d, turns, v, y, pos=pos)
+        return (y.double() * g.double()).sum().item()
+
+    for at in range(0, x.numel(), 5):
+        e = torch.zeros(x.numel(), device="cuda").view_as(x)
+        e.view(-1)[at] = 1.0
+        assert abs((f(x + e) - f(x - e)) / 2 - dx.view(-1)[at].item()) <= 8 * 8 * 2.0 ** -21
+
+
+# ---------------------------------------------------------------------------
+# block tables and slots
+# ---------------------------------------------------------------------------
+def run_slots(cache, lens, new, table, free, used, tokens, pos0=0, in_place=False):
+    t, L = i32(table), i32(lens)
+    U = torch.tensor([used, -7], dtype=torch.int32).cuda()
+    lo, uo = (L, U) if in_place else (torch.full_like(L, -9), torch.full_like(U, -9))
+    e = lambda k: torch.full((k,), -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    start, slots, pos = e(len(lens) + 1), e(tokens), e(tokens)
+    swab.cache_slots(cache, L, i32(new), t, i32(free) if len(free) else e(0), U if in_place else U[:1].contiguous(), lo, uo,
+                     start, slots, pos, pos0=pos0)
+    return [x.cpu().numpy() for x in (t, lo, uo, start, slots, pos)]
+
+
+def slots_case(batch, page, cols, ring, pinned, len_hi, new_hi, seed, short=0):
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, len_hi + 1, batch)
+    new = rng.integers(0, new_hi + 1, batch)
+    have = np.minimum(-(-lens // page), cols)
+    want = np.minimum(-(-(lens + new) // page), cols)
+    n_blocks = int(want.sum()) + 7
+    perm = rng.permutation(n_blocks)
+    table, at = np.full((batch, cols), -1), 0
+    for r in range(batch):
+        table[r, :have[r]] = perm[at:at + have[r]]
+        at += have[r]
+    free = np.concatenate([[n_blocks - 1] * 2, perm[at:]])[:max(2, 2 + int((want - have).sum()) - short)]
+    return swab.CacheDesc(batch, page, n_blocks, cols, ring, pinned), lens, new, table, free
+
+
+SLOTS = [  # batch, page, cols, ring, pinned, len_hi, new_hi, missing blocks
+    (1, 16, 4, False, 0, 0, 1, 0),
+    (1, 16, 40, False, 0, 300, 300, 0),
+    (7, 64, 6, True, 0, 2000, 1, 0),
+    (7, 64, 6, True, 2, 2000, 700, 0),
+    (64, 32, 300, False, 0, 5000, 3, 0),
+    (1500, 128, 90, False, 0, 9000, 5, 0),
+    (300, 16, 5, True, 1, 100, 60, 0),
+    (40, 16, 600, False, 0, 4000, 900, 0),
+    (40, 16, 600, False, 0, 4000, 900, 25),
+    (40, 16, 120, False, 0, 1500, 900, 0),       # some requests pass the table
+    (2, 16, 2, True, 1, 4, 200, 0),              # a step longer than the recycled table
+    (3, 16, 8, False, 0, 100, 0, 0),             # nothing new
+]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("case", SLOTS)
+def test_cache_slots_matches_the_oracle(case, in_place):
+    batch, page, cols, ring, pinned, len_hi, new_hi, short = case
+    cache, lens, new, table, free = slots_case(batch, page, cols, ring, pinned, len_hi, new_hi, 11, short)
+    tokens = int(new.sum()) + 5
+    got = run_slots(cache, lens, new, table, free, 2, tokens, pos0=13, in_place=in_place)
+    want = orc.cache_slots(lens, new, table, free, 2, page, cols, ring, pinned, tokens, 13)
+    for name, g, w in zip(("table", "lens", "used", "start", "slots", "pos"), got, want):
+        np.testing.assert_array_equal(g, w, err_msg=name)
+    live = got[4][got[4] >= 0]
+    assert len(np.unique(live)) == len(live)       # no two tokens share a slot
+
+
+def test_cache_slots_writes_no_token_past_its_rows_and_takes_negative_counts_as_none():
+    cache, _, _, table, free = slots_case(4, 16, 10, False, 0, 0, 0, 12)
+    free = np.arange(cache.n_blocks)
+    lens, new = [-5, 3, 0, 16], [4, -2, 100, 1]
+    got = run_slots(cache, lens, new, table, free[:7], 0, 50)
+    want = orc.cache_slots(lens, new, table, free[:7], 0, 16, 10, tokens=50)
+    for g, w in zip(got, want):
+        np.testing.assert_array_equal(g, w)
+    assert swab.device_status(reset=True) == 0
+
+
+def test_cache_slots_flags_blocks_outside_the_cache():
+    cache = swab.CacheDesc(2, 16, 4, 3)
+    table = [[4, -1, -1], [1, -1, -1]]              # block 4 of a cache of 4
+    got = run_slots(cache, [3, 3], [2, 2], table, [2, 3], 0, 4)
+    np.testing.assert_array_equal(got[4], [-1, -1, 19, 20])
+    assert swab.device_status(reset=True) == INVALID_BIT
+
+
+# ---------------------------------------------------------------------------
+# the cache write
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("case", [(1, 4, 2, 64, 64, False, 16), (23, 5, 1, 80, 20, True, 16), (200, 12, 4, 128, 64, False, 64),
+                                  (9, 2, 2, 64, 0, False, 128), (6000, 2, 1, 64, 64, True, 32)])
+def test_rotary_append_matches_the_oracle(case, dtype):
+    T, h, hk, hd, rot, inter, page = case
+    turns, freq, scale = frequencies(rot, "bands")
+    rng = np.random.default_rng(20)
+    n_blocks = T // page + 3
+    slots = rng.permutation(n_blocks * page)[:T]
+    slots[rng.random(T) < 0.2] = -1
+    pos = rng.integers(0, 100000, T)
+    qkv = randn((T, h + 2 * hk, hd), dtype, 21)
+    q, k, v = qkv.split([h, hk, hk], dim=1)
+    kc, vc = randn((n_blocks, hk, page, hd), dtype, 22), randn((n_blocks, hk, page, hd), dtype, 23)
+    k0, v0 = kc.clone(), vc.clone()
+    qo = torch.empty(T, h, hd, dtype=dtype, device="cuda")
+    d = swab.RotaryDesc(1, T, h, hk, hd, rot, inter, scale, dtype=dtype)
+    cache = swab.CacheDesc(1, page, n_blocks, 1)
+    swab.rotary_append(d, cache, turns, q, k, v, i32(pos), i32(slots), qo, kc, vc)
+    check_rotary(qo, q, pos, freq, scale, inter, dtype)
+    keep = slots >= 0
+    b, o = torch.tensor(slots[keep] // page).cuda(), torch.tensor(slots[keep] % page).cuda()
+    rows = torch.tensor(np.nonzero(keep)[0]).cuda()
+    check_rotary(kc[b, :, o], k[rows], pos[keep], freq, scale, inter, dtype)
+    same_bits(vc[b, :, o], v[rows])
+    untouched = torch.ones(n_blocks, page, dtype=torch.bool, device="cuda")
+    untouched[b, o] = False
+    same_bits(kc.transpose(1, 2)[untouched], k0.transpose(1, 2)[untouched])
+    same_bits(vc.transpose(1, 2)[untouched], v0.transpose(1, 2)[untouched])
+    # without Q: the same cache
+    k1, v1 = k0.clone(), v0.clone()
+    swab.rotary_append(d, cache, turns, None, k, v, i32(pos), i32(slots), None, k1, v1)
+    same_bits(k1, kc)
+    same_bits(v1, vc)
+
+
+def test_rotary_append_skips_and_flags_slots_outside_the_cache():
+    cache = swab.CacheDesc(1, 16, 2, 1)
+    d = swab.RotaryDesc(1, 4, 1, 1, 64, 0, dtype=F16)
+    q, k, v = (randn((4, 1, 64), F16, s) for s in (1, 2, 3))
+    kc, vc = torch.zeros(2, 1, 16, 64, dtype=F16, device="cuda"), torch.zeros(2, 1, 16, 64, dtype=F16, device="cuda")
+    swab.rotary_append(d, cache, None, q, k, v, None, i32([32, -2, 31, -1]), torch.empty_like(q), kc, vc)
+    assert swab.device_status(reset=True) == INVALID_BIT
+    same_bits(kc[1, 0, 15], k[2, 0])
+    same_bits(vc[1, 0, 15], v[2, 0])
+    assert int((kc != 0).any(-1).sum()) == 1
+
+
+# ---------------------------------------------------------------------------
+# decode
+# ---------------------------------------------------------------------------
+class Decode:
+    """A batch over a cache that holds NaN wherever no query of a request looks."""
+
+    def __init__(self, dtype, lens, new, h, hk, hd, page=16, w=None, dilation=0, n_sink=0, ring=False, prefix=0, pad=0, seed=0,
+                 max_len=None, qscale=1.0):
+        rng = np.random.default_rng(seed)
+        self.dtype, self.lens, self.new = dtype, list(lens), list(new)
+        self.w = 1 << 30 if w is None else w
+        self.dilation, self.n_sink, self.ring, self.prefix = dilation, n_sink, ring, prefix
+        B, s = len(lens), dilation + 1
+        max_q = max(1, max(new))
+        self.pinned = -(-n_sink // page) if ring else 0
+        cols = self.pinned + -(-(self.w * s + max_q - 1) // page) + 1 if ring else max(1, -(-max(lens) // page))
+        used = [min(-(-x // page), cols) for x in lens]
+        pre = -(-prefix // page)
+        n_blocks = sum(used) + pre + 2
+        perm = rng.permutation(n_blocks)
+        table, at = np.full((B, cols), -1), 0
+        for r in range(B):
+            table[r, :used[r]] = perm[at:at + used[r]]
+            at += used[r]
+        self.table, self.ptable = table, perm[at:at + pre]
+        self.q_start = np.concatenate([[0], np.cumsum(new)])
+        self.tokens = int(self.q_start[-1]) + pad
+        self.q = randn((max(1, self.tokens), h, hd), dtype, seed + 1, qscale)
+        self.kc = torch.full((n_blocks, hk, page, hd), float("nan"), dtype=dtype, device="cuda")
+        self.vc = torch.full_like(self.kc, float("nan"))
+        rows = [(self.ptable[p // page], p % page) for p in range(prefix)]
+        for r in range(B):
+            seen = set()
+            for i in range(lens[r] - new[r], lens[r]):
+                seen |= set(orc.keys_of(i, self.w, dilation, n_sink))
+            rows += [(table[r, orc.column(j // page, cols, ring, self.pinned)], j % page) for j in sorted(seen)]
+        if rows:
+            b, o = (torch.tensor([int(x[k]) for x in rows]).cuda() for k in (0, 1))
+            self.kc[b, :, o] = randn((len(rows), hk, hd), dtype, seed + 2)
+            self.vc[b, :, o] = randn((len(rows), hk, hd), dtype, seed + 3)
+        self.cache = swab.CacheDesc(B, page, n_blocks, cols, ring, self.pinned)
+        self.desc = swab.DecodeDesc(self.cache, max(1, self.tokens), h, hk, hd, self.w, dilation, n_sink, max_q,
+                                    max_len or max(1, max(lens)), prefix, dtype)
+        self.scale = hd ** -0.5
+
+    def run(self, stream=None, lse=True):
+        o = torch.full_like(self.q, 7.0)
+        l = torch.full(self.q.shape[:2], 7.0, dtype=F32, device="cuda") if lse else None
+        ws = torch.empty(swab.band_decode_workspace(self.desc), dtype=torch.uint8, device="cuda")
+        swab.band_decode(self.desc, self.scale, self.q, self.kc, self.vc, i32(self.table), i32(self.lens), i32(self.q_start),
+                         o, l, ws, i32(self.ptable) if self.prefix else None, stream=stream)
+        return o, l
+
+    def oracle(self):
+        return orc.decode(f64(self.q), f64(self.kc), f64(self.vc), self.table, self.lens, self.q_start, self.scale, self.w,
+                          self.dilation, self.n_sink, self.ring, self.pinned, self.ptable, self.prefix)
+
+    def check(self, o=None, lse=None):
+        if o is None:
+            o, lse = self.run()
+        O, L, A, X = self.oracle()
+        u, hd, n = half_step(self.dtype), self.q.shape[2], self.prefix + max(self.lens) + 4
+        delta = (X * (hd + 8) * 2.0 ** -24 * 1.5 + 2.0 ** -21)[..., None]
+        weight = 0.0 if self.dtype == F32 else u
+        tiny = n * 2.0 ** -25 * 6.0 if self.dtype == F16 else 0.0        # |v| below 6
+        bound = A * (2 * delta + 2 * n * 2.0 ** -24 + weight) + tiny
+        bound = bound + (np.abs(O) + bound) * u + smallest_half_step(self.dtype)
+        live = int(self.q_start[-1])
+        live = min(live, self.tokens)
+        err = np.abs(f64(o)[:live] - O[:live])
+        assert (err <= bound[:live]).all(), float(np.nanmax(err / np.maximum(bound[:live], 1e-30)))
+        if lse is not None:
+            got = f64(lse)[:live]
+            empty = np.isneginf(L[:live])
+            assert (np.isneginf(got) == empty).all()
+            lb = (delta[..., 0] + n * 2.0 ** -24 + (np.abs(L) + 1) * 2.0 ** -22)[:live]
+            diff = np.abs(np.where(empty, 0.0, got) - np.where(empty, 0.0, L[:live]))
+            assert (diff <= np.where(empty, 0.0, lb)).all(), float(diff.max())
+            assert (f64(lse)[live:] == 7.0).all()
+        assert (f64(o)[live:] == 7.0).all()              # rows of no request stay as they were
+
+
+LENGTHS = [([1], [1]), ([5], [1]), ([16, 17, 1, 33], [1, 1, 1, 1]), ([300, 1, 47], [1, 1, 1]),
+           ([40, 0, 9, 64], [3, 0, 1, 4]), ([2, 70], [2, 0])]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("heads", [(4, 4, 64), (8, 2, 128), (6, 1, 64), (5, 5, 80), (2, 2, 256), (3, 1, 128)])
+def test_decode_matches_the_oracle(heads, dtype):
+    for k, (lens, new) in enumerate(LENGTHS):
+        Decode(dtype, lens, new, *heads, seed=30 + k, pad=k % 3).check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("case", [
+    dict(w=0), dict(w=7), dict(w=16, n_sink=3), dict(w=31, n_sink=16, page=32), dict(w=5, dilation=1),
+    dict(w=9, dilation=3, n_sink=5), dict(w=20, ring=True), dict(w=20, ring=True, n_sink=20, page=16),
+    dict(w=6, dilation=2, ring=True, n_sink=1), dict(w=100, n_sink=90), dict(w=3, n_sink=400), dict(w=40, dilation=15)])
+def test_decode_windows_and_sinks(case, dtype):
+    for heads in ((4, 2, 64), (2, 1, 128)):
+        for k, (lens, new) in enumerate(LENGTHS[1:]):
+            Decode(dtype, lens, new, *heads, seed=50 + k, **case).check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("prefix", [1, 15, 16, 100, 129, 700])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (7, 1, 128), (3, 3, 64), (2, 2, 80)])
+def test_decode_behind_a_shared_prefix(heads, prefix, dtype):
+    for k, (lens, new) in enumerate(LENGTHS[1:]):
+        Decode(dtype, lens, new, *heads, prefix=prefix, seed=70 + k, pad=k % 2).check()
+    Decode(dtype, [80, 3], [2, 1], *heads, prefix=prefix, w=11, n_sink=2, page=32, seed=80).check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("case", [
+    dict(lens=[5000], new=[1], h=4, hk=1, hd=128, page=64), dict(lens=[3000, 17, 4100], new=[1, 1, 1], h=4, hk=2, hd=64, page=128),
+    dict(lens=[2500, 900], new=[4, 7], h=16, hk=2, hd=128, page=32),          # more rows than a tile
+    dict(lens=[1500], new=[1], h=128, hk=1, hd=64, page=16),                  # one key head for 128
+    dict(lens=[2600, 2601], new=[1, 2], h=4, hk=4, hd=64, w=2048, page=64, ring=True),
+    dict(lens=[100] * 70, new=[1] * 70, h=8, hk=2, hd=64, prefix=1000),       # more prefix rows than a tile
+    dict(lens=[30] * 9, new=[3] * 9, h=20, hk=4, hd=128, prefix=600, page=64),
+    dict(lens=[700], new=[40], h=2, hk=1, hd=64)])
+def test_decode_long_and_wide(case, dtype):
+    Decode(dtype, seed=90, **case).check()
+
+
+def test_decode_of_contexts_longer_than_announced():
+    """max_len divides the work only."""
+    for dtype in (F16, F32):
+        Decode(dtype, [900, 40], [1, 1], 4, 2, 64, max_len=1, seed=95).check()
+        Decode(dtype, [900, 40], [2, 1], 4, 2, 64, max_len=300, prefix=40, seed=96).check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_decode_with_large_scores(dtype):
+    """Scores of a few hundred: the running maximum keeps the weights finite."""
+    Decode(dtype, [200, 31], [1, 2], 4, 2, 64, qscale=40.0, prefix=50, seed=97).check()
+
+
+def test_decode_without_keys():
+    """Contexts shorter than their new tokens, empty columns: rows without a key give 0 and -inf."""
+    for dtype in (F16, F32):
+        c = Decode(dtype, [4, 20], [2, 1], 4, 2, 64, seed=98)
+        c.lens[0] = 1                                  # two new tokens, one position held
+        c.check()
+        c.lens[0] = 0
+        c.check()
+        c = Decode(dtype, [4, 20], [2, 1], 4, 2, 64, seed=99)
+        c.table[0, :] = -1                             # nothing allocated: absent, not an error
+        c.check()
+    assert swab.device_status(reset=True) == 0
+
+
+def test_decode_skips_and_flags_blocks_outside_the_cache():
+    for dtype in (F16, F32):
+        for prefix in (0, 40):
+            c = Decode(dtype, [40, 20], [1, 1], 4, 2, 64, prefix=prefix, seed=100)
+            c.table[0, 1] = c.cache.n_blocks
+            c.table[1, 0] = -5
+            if prefix:
+                c.ptable = c.ptable.copy()
+                c.ptable[1] = 1 << 30
+            c.check()
+            assert swab.device_status(reset=True) == INVALID_BIT
+        c = Decode(dtype, [40, 20], [1, 1], 4, 2, 64, seed=101)
+        c.kc.nan_to_num_(0.5)
+        c.vc.nan_to_num_(0.5)
+        c.lens[0] = 200                                # longer than its table
+        c.check()
+        assert swab.device_status(reset=True) == INVALID_BIT
+
+
+def test_decode_row_strides_and_optional_lse():
+    c = Decode(BF16, [70, 9], [2, 1], 4, 2, 64, seed=102)
+    want, lse = c.run()
+    c.check(want, lse)
+    qkv = torch.zeros(c.tokens, 8, 64, dtype=BF16, device="cuda")
+    qkv[:, :4] = c.q
+    out = torch.full((c.tokens, 6, 64), 5.0, dtype=BF16, device="cuda")
+    d = swab.DecodeDesc(c.cache, c.tokens, 4, 2, 64, c.w, max_q=2, max_len=70, dtype=BF16, q_row_stride=512, out_row_stride=384)
+    ws = torch.empty(swab.band_decode_workspace(d), dtype=torch.uint8, device="cuda")
+    swab.band_decode(d, c.scale, qkv[:, :4], c.kc, c.vc, i32(c.table), i32(c.lens), i32(c.q_start), out[:, :4], None, ws)
+    same_bits(out[:, :4], want)
+    assert (out[:, 4:] == 5.0).all()
+    same_bits(c.run(lse=False)[0], want)
+
+
+def test_decode_fewer_rows_than_tokens():
+    """Rows past `tokens` are neither read nor written."""
+    c = Decode(F16, [30, 20], [3, 2], 4, 2, 64, seed=103)
+    want, _ = c.run()
+    c.tokens, full = 4, c.q
+    c.q = full[:4].contiguous()
+    c.desc = swab.DecodeDesc(c.cache, 4, 4, 2, 64, c.w, max_q=3, max_len=30, dtype=F16)
+    same_bits(c.run()[0], want[:4])
+
+
+def test_decode_repeats_bitwise_on_other_streams_and_two_at_once():
+    a = Decode(BF16, [3000, 40], [1, 1], 8, 2, 128, prefix=500, seed=104)
+    b = Decode(F16, [900] * 5, [2] * 5, 4, 4, 64, w=300, seed=105)
+    wa, wb = a.run(), b.run()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(4):
+        with torch.cuda.stream(s1):
+            got.append((a.run(), wa))
+        with torch.cuda.stream(s2):
+            got.append((b.run(stream=s2), wb))
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in got:
+        same_bits(o, wo)
+        same_bits(l, wl)
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+class Server:
+    """A small serving loop: a window of 24, 4 leading global tokens, recycled blocks, everything on the GPU."""
+
+    H, HK, HD, W, PAGE, SINK = 4, 4, 64, 24, 16, 4
+
+    def __init__(self, batch, max_q, dtype, prefix=0, w=None, ring=True):
+        self.w, self.dtype, self.batch, self.max_q = self.W if w is None else w, dtype, batch, max_q
+        pinned = 1 if ring else 0
+        cols = pinned + -(-(self.w + max_q - 1) // self.PAGE) + 1 if ring else 20
+        pre = -(-prefix // self.PAGE)
+        n_blocks = batch * cols + pre + 1
+        self.cache = swab.CacheDesc(batch, self.PAGE, n_blocks, cols, ring, pinned)
+        self.free = torch.randperm(n_blocks - pre, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+        self.prefix, self.ptable = prefix, torch.arange(n_blocks - pre, n_blocks, dtype=torch.int32, device="cuda")
+        z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.lens, self.used, self.start = z(batch), z(2), z(batch + 1)
+        self.table = z(batch, cols) - 1
+        self.kc = torch.full((n_blocks, self.HK, self.PAGE, self.HD), float("nan"), dtype=dtype, device="cuda")
+        self.vc = torch.full_like(self.kc, float("nan"))
+        self.turns = swab.rotary_frequencies(self.HD)[0].cuda()
+
+    def buffers(self, tokens):
+        z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+        self.rot = swab.RotaryDesc(1, tokens, self.H, self.HK, self.HD, self.HD, dtype=self.dtype)
+        self.dec = swab.DecodeDesc(self.cache, tokens, self.H, self.HK, self.HD, self.w, n_sink=self.SINK, max_q=self.max_q,
+                                   max_len=2000, prefix_len=self.prefix, dtype=self.dtype)
+        self.n_new, self.slots, self.pos = z(self.batch), z(tokens), z(tokens)
+        self.qkv = z(tokens, self.H + 2 * self.HK, self.HD, t=self.dtype)
+        self.q, self.k, self.v = self.qkv.split([self.H, self.HK, self.HK], dim=1)
+        self.qo, self.o = z(tokens, self.H, self.HD, t=self.dtype), z(tokens, self.H, self.HD, t=self.dtype)
+        self.lse = z(tokens, self.H, t=F32)
+        self.ws = torch.empty(max(1, swab.band_decode_workspace(self.dec)), dtype=torch.uint8, device="cuda")
+
+    def step(self):
+        swab.cache_slots(self.cache, self.lens, self.n_new, self.table, self.free, self.used, self.lens, self.used,
+                         self.start, self.slots, self.pos, pos0=self.prefix)
+        swab.rotary_append(self.rot, self.cache, self.turns, self.q, self.k, self.v, self.pos, self.slots, self.qo, self.kc,
+                           self.vc)
+        swab.band_decode(self.dec, self.HD ** -0.5, self.qo, self.kc, self.vc, self.table, self.lens, self.start, self.o,
+                         self.lse, self.ws, self.ptable if self.prefix else None)
+
+
+def full_attention(x, w, n_sink, dtype, prefix=None):
+    """fp64 attention of a whole sequence x [n, heads of Q, K, V, hd], q and k rotated and rounded to the type,
+    and how far a step-by-step result may be off.  The rounded q and k of the kernel and of this function may
+    differ by one step (2 u) where the two sums round apart, which moves a score by at most 4 u X, X = the largest
+    sum of |q| |k| times the scale, and a weighted mean by 2 (e^(4 u X) - 1) A; the weights and the result round
+    to u each, the fp32 sums are far below u."""
+    n, H, HK = x.shape[0], Server.H, Server.HK
+    freq, _ = orc.frequencies(Server.HD)
+    p0 = 0 if prefix is None else len(prefix)
+    pos = p0 + np.arange(n)
+    rnd = lambda y: f64(torch.tensor(y).to(dtype))  # noqa: E731
+    q, k, v = rnd(orc.rotary(x[:, :H], pos, freq)), rnd(orc.rotary(x[:, H:H + HK], pos, freq)), x[:, H + HK:]
+    if prefix is not None:
+        pk, pv = rnd(orc.rotary(prefix[:, H:H + HK], np.arange(p0), freq)), prefix[:, H + HK:]
+    out, bound, u = np.zeros((n, H, Server.HD)), np.zeros((n, H, Server.HD)), half_step(dtype)
+    for i in range(n):
+        keys = orc.keys_of(i, w, 0, n_sink)
+        for h in range(H):
+            kk, vv = k[keys, h], v[keys, h]
+            if prefix is not None:
+                kk, vv = np.concatenate([pk[:, h], kk]), np.concatenate([pv[:, h], vv])
+            s = kk @ q[i, h] * Server.HD ** -0.5
+            e = np.exp(s - s.max())
+            A, X = e @ np.abs(vv) / e.sum(), (np.abs(kk) @ np.abs(q[i, h])).max() * Server.HD ** -0.5
+            out[i, h] = e @ vv / e.sum()
+            bound[i, h] = A * (2 * np.expm1(4 * u * X) + 2 * u) + np.abs(out[i, h]) * u + 2.0 ** -18
+    return out, bound
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("graph", [False, True])
+def test_steps_give_the_attention_of_the_whole_sequence(dtype, graph):
+    """Requests that grow by 1 to 4 tokens a step, eager or as replays of one captured graph, against fp64
+    attention over each finished sequence."""
+    torch.manual_seed(5)
+    B, steps = 3, 30
+    s = Server(B, 4, dtype)
+    s.buffers(B * 4)
+    rng = np.random.default_rng(6)
+    data = [randn((steps * 4, s.H + 2 * s.HK, s.HD), dtype, 200 + r) for r in range(B)]
+    news = rng.integers(0, 5, (steps, B))
+    s.n_new.zero_()
+    s.step()                                           # warm up: no tokens
+    torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.step()
+    got, at = [[] for _ in range(B)], [0] * B
+    for t in range(steps):
+        s.n_new.copy_(i32(news[t]))
+        rows = torch.cat([data[r][at[r]:at[r] + news[t][r]] for r in range(B)])
+        s.qkv[:len(rows)] = rows
+        g.replay() if graph else s.step()
+        first = 0
+        for r in range(B):
+            got[r].append(s.o[first:first + news[t][r]].clone())
+            first += news[t][r]
+            at[r] += int(news[t][r])
+    assert int(s.used[1]) == 0
+    for r in range(B):
+        want, bound = full_attention(f64(data[r])[:at[r]], s.w, s.SINK, dtype)
+        assert (np.abs(f64(torch.cat(got[r])) - want) <= bound).all()
+
+
+def test_prompt_then_steps_behind_a_shared_prefix():
+    """The prefix is appended once through its own table, then three requests decode behind it."""
+    dtype, P, B, n = F16, 50, 3, 9
+    s = Server(B, 1, dtype, prefix=P, w=100, ring=False)
+    pre = randn((P, s.H + 2 * s.HK, s.HD), dtype, 300)
+    slots = i32([int(s.ptable[p // s.PAGE]) * s.PAGE + p % s.PAGE for p in range(P)])
+    q, k, v = pre.split([s.H, s.HK, s.HK], dim=1)
+    swab.rotary_append(swab.RotaryDesc(1, P, s.H, s.HK, s.HD, s.HD, dtype=dtype), s.cache, s.turns, None, k, v,
+                       i32(np.arange(P)), slots, None, s.kc, s.vc)
+    s.buffers(B)
+    data = [randn((n, s.H + 2 * s.HK, s.HD), dtype, 310 + r) for r in range(B)]
+    got = []
+    for t in range(n):
+        s.n_new.fill_(1)
+        s.qkv.copy_(torch.stack([data[r][t] for r in range(B)]))
+        s.step()
+        got.append(s.o.clone())
+    for r in range(B):
+        want, bound = full_attention(f64(data[r]), 100, s.SINK, dtype, f64(pre))
+        assert (np.abs(f64(torch.stack([x[r] for x in got])) - want) <= bound).all()
+
+
+def test_last_rows_agree_with_the_banded_forward():
+    """rotary, then band_attention over the sequence; the cache write and band_decode give its last rows."""
+    n, h, hd, w = 200, 4, 64, 40
+    x = randn((n, 3 * h, hd), F16, 400)
+    q, k, v = x.split([h, h, h], dim=1)
+    turns = swab.rotary_frequencies(hd)[0].cuda()
+    d = swab.RotaryDesc(1, n, h, h, hd, hd, dtype=F16)
+    qo, ko = torch.empty(1, h, n, hd, dtype=F16, device="cuda"), torch.empty(1, h, n, hd, dtype=F16, device="cuda")
+    swab.rotary(d, turns, q, qo.transpose(1, 2), k, ko.transpose(1, 2))
+    O = torch.empty(h, n, hd, dtype=F16, device="cuda")
+    swab.band_attention(swab.Desc(1, h, n, hd, w, 0, dtype=F16), hd ** -0.5, qo[0], ko[0],
+                        v.transpose(0, 1).contiguous(), O, torch.empty(h, n, dtype=F32, device="cuda"))
+    cache = swab.CacheDesc(1, 16, 13, 13)
+    kc, vc = (torch.full((13, h, 16, hd), float("nan"), dtype=F16, device="cuda") for _ in range(2))
+    table = i32([np.random.default_rng(1).permutation(13)])
+    slots = i32([int(table[0, j // 16]) * 16 + j % 16 for j in range(n)])
+    flat = torch.empty(n, h, hd, dtype=F16, device="cuda")
+    swab.rotary_append(d, cache, turns, q, k, v, i32(np.arange(n)), slots, flat, kc, vc)
+    same_bits(flat, qo[0].transpose(0, 1))
+    m = 5
+    dd = swab.DecodeDesc(cache, m, h, h, hd, w, max_q=m, dtype=F16)
+    o = torch.empty(m, h, hd, dtype=F16, device="cuda")
+    ws = torch.empty(max(1, swab.band_decode_workspace(dd)), dtype=torch.uint8, device="cuda")
+    swab.band_decode(dd, hd ** -0.5, flat[-m:], kc, vc, table, i32([n]), i32([0, m]), o, None, ws)
+    # each side is within A (2^-11 weights + sums) + half a step of the exact value, A <= 4.5
+    bound = 2 * (4.5 * (2.0 ** -11 + 2.0 ** -13) + 4.5 * 2.0 ** -11)
+    assert (o.float() - O[:, -m:].transpose(0, 1).float()).abs().max().item() <= bound
+
+
+@pytest.mark.skipif(os.environ.get("SWAB_BOUNDS_CHECK") == "1", reason="is that run")
+def test_bounds_checked_build_records_nothing():
+    """This file on the bounds-checked build: an access outside the call's buffers fails a status check."""
+    res = subprocess.run([sys.executable, "-m", "pytest", os.path.abspath(__file__), "-m", "gpu", "-x", "-q"], cwd=ROOT,
+                         env=dict(os.environ, SWAB_BOUNDS_CHECK="1"), capture_output=True, text=True, timeout=1500)
+    assert res.returncode == 0, res.stdout[-3000:] + res.stderr[-2000:]
