@@ -1,0 +1,382 @@
+// k_decode_rows.cu -- banded attention of a few new tokens a request over the
+// paged cache, fp16 / bf16 with head_dim 64 or 128: the query heads that share
+// a key head, of all the new tokens of a request, are the rows of one tile, so
+// every key and value is read from memory once for all of them.
+//
+// HBM-bound (4 flops a row for every 2 bytes): what counts is bytes in flight.
+// A warp owns groups of 16 keys (group g of the block's piece goes to warp
+// g mod 4) and runs on its own: it looks the 16 lines up in the block table one
+// stage ahead, brings them in with 16-byte cp.async into a ring of its own, and
+// waits for nobody until the end.  A group is 16 rows x 16 keys of mma.sync
+// m16n8k16 (the rows are few: a 128-row tcgen05 tile would be 7/8 padding and
+// would need the gathered lines staged for it): S = Q K^T with Q in registers,
+// the softmax on the accumulator, O += P V with P repacked in registers (the
+// accumulator's layout is the A operand's).  The running maximum is raised only
+// when a score exceeds it by 2^8, so the usual group needs no exchange between
+// lanes; a weight is rounded to 16 bits for the product (at most 2^8, inside
+// fp16), the sums stay fp32.  Lines of 16-byte pieces are stored with the piece
+// number xor (line mod 8), so the eight lines of an ldmatrix miss each other's
+// banks.  Absent keys are zero-filled, so whatever the cache holds there cannot
+// reach a product.
+//
+// The warps' (m, l, O) are joined in shared memory; the pieces of a split key
+// list (few requests, long contexts) go to the workspace and are joined by
+// k_decode_join.
+#include <type_traits>
+
+#include "swab_internal.h"
+#include "swab_decode.cuh"
+
+static constexpr unsigned kSwabFile = 15;   // site id of the bounds checks
+
+namespace swab {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kKeys = 16;          // keys of a group
+constexpr float kSlack = 8.f;      // log2 headroom of the running maximum
+
+template <int HD> struct Shape {
+    static constexpr int kStages = HD == 128 ? 3 : 6;
+    static constexpr int kTile = kKeys * HD * 2;             // bytes of 16 lines
+    static constexpr int kStage = 2 * kTile;                 // K and V
+    static constexpr int kRing = kStages * kStage;           // of a warp: 24 KB
+    static constexpr int kSmem = kWarps * kRing;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// NT: 16-row tiles of a block.  Grid: (piece, key head and row tile, request).
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant__ DecodeArgs p) {
+    using S = Shape<HD>;
+    constexpr int kRows = 16 * NT, kSteps = HD / 16, kPieces = HD / 8;   // 16-byte pieces of a line
+    constexpr int kPer = 32 / kPieces;                                   // lines of a copy instruction
+    constexpr int kPad = HD + 8;                                         // floats of a row in the final exchange
+    static_assert(kRows * kPad * 4 <= S::kRing, "a warp's O fits its ring");
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 sml[kWarps][kRows];
+    __shared__ float swt[kWarps][kRows];
+    __shared__ float2 stot[kRows];
+    __shared__ uint32_t sok[kWarps][S::kStages];   // which keys of the group in a stage are there
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int split = blockIdx.x, r = blockIdx.z;
+    const int kvh = (int)(blockIdx.y % (unsigned)p.hk), tile0 = (int)(blockIdx.y / (unsigned)p.hk);
+    const int tiles_y = gridDim.y / p.hk;
+    pdl_trigger();                               // k_decode_join, which waits for this grid
+    const Request q = request_of(p, r);
+    uint8_t *ring = smem + warp * S::kRing;
+    const uint32_t ring_s = smem_u32(ring);
+    // tiles of rows: with a key stride each token has its own
+    const int per_tok = (p.group + kRows - 1) / kRows;
+    const int ntiles = p.stride == 1 ? (q.m * p.group + kRows - 1) / kRows : q.m * per_tok;
+
+    for (int tile = tile0; tile < ntiles; tile += tiles_y) {
+        // row 0 of the tile and how many there are, counted over (token, head of the group)
+        int row0, nrows;
+        if (p.stride == 1) {
+            row0 = tile * kRows;
+            nrows = min(kRows, q.m * p.group - row0);
+        } else {
+            const int part = tile % per_tok;
+            row0 = tile / per_tok * p.group + part * kRows;
+            nrows = min(kRows, p.group - part * kRows);
+        }
+        const int a_lo = row0 / p.group, a_hi = (row0 + nrows - 1) / p.group;
+        const KeyList keys = keys_of(p, q, a_lo, a_hi);
+        const int lo = min((long long)split * p.chunk, (long long)keys.count);
+        const int hi = split == p.nsplit - 1 ? keys.count : (int)min((long long)lo + p.chunk, (long long)keys.count);
+        const int groups = (hi - lo + kKeys - 1) / kKeys;
+        const int mine = groups > warp ? (groups - warp + kWarps - 1) / kWarps : 0;   // of this warp
+
+        // line of key (lane mod 16) of the warp's group n, -1 when there is none
+        auto look_up = [&](int n) -> long long {
+            const int u = lo + kKeys * (warp + kWarps * n) + (lane & 15);
+            return n < mine && u < hi ? key_line(p, q, keys.at(u), kvh) : -1;
+        };
+        auto load = [&](int stage, long long line) {
+            const uint32_t dst = ring_s + stage * S::kStage;
+            const uint32_t there = __ballot_sync(0xffffffffu, line >= 0) & 0xffffu;
+            if (lane == 0) sok[warp][stage] = there;
+#pragma unroll
+            for (int i = 0; i < kKeys / kPer; ++i) {
+                const int row = i * kPer + lane / kPieces, piece = lane % kPieces;
+                const long long ln = __shfl_sync(0xffffffffu, line, row);
+                const uint32_t bytes = ln >= 0 ? 16u : 0u;
+                const long long at = (ln >= 0 ? ln : 0) * HD + piece * 8;
+                const uint32_t to = dst + row * (HD * 2) + ((piece ^ (row & 7)) << 4);
+                cp_async16(to, GPN(p.bnd, reinterpret_cast<const T *>(p.Kc) + at, 16), bytes);
+                cp_async16(to + S::kTile, GPN(p.bnd, reinterpret_cast<const T *>(p.Vc) + at, 16), bytes);
+            }
+        };
+
+        // fill the ring; the lines of the stage after it are looked up meanwhile
+        long long first[S::kStages];
+#pragma unroll
+        for (int s = 0; s < S::kStages; ++s) first[s] = look_up(s);
+#pragma unroll
+        for (int s = 0; s < S::kStages - 1; ++s) {
+            if (s < mine) load(s, first[s]);
+            cp_commit();
+        }
+        long long next = first[S::kStages - 1];
+
+        // Q of the tile as A operands
+        uint32_t qa[NT][kSteps][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int rr = 16 * t + g + 8 * half;
+                const bool live = rr < nrows;
+                const int row = row0 + (live ? rr : 0), a = row / p.group, hh = kvh * p.group + row - a * p.group;
+                const T *src = reinterpret_cast<const T *>(p.Q) + (long long)(q.row0 + a) * p.q_stride + (long long)hh * HD + 2 * t4;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const uint32_t x0 = *GP(p.bnd, reinterpret_cast<const uint32_t *>(src + 16 * k));
+                    const uint32_t x1 = *GP(p.bnd, reinterpret_cast<const uint32_t *>(src + 16 * k + 8));
+                    qa[t][k][half] = live ? x0 : 0u;
+                    qa[t][k][half + 2] = live ? x1 : 0u;
+                }
+            }
+        // positions of this lane's rows (row g + 8 e of tile t)
+        int pos[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) pos[t][e] = q.i0 + (row0 + min(16 * t + g + 8 * e, nrows - 1)) / p.group;
+        const int pos_lo = q.i0 + a_lo, pos_hi = q.i0 + a_hi;
+
+        float o[NT][HD / 8][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][d][e] = 0.f;
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.f;
+        }
+
+        int stage = 0;
+        for (int n = 0; n < mine; ++n) {
+            // the ring's free stage takes group n + kStages - 1
+            const long long ahead = look_up(n + S::kStages);
+            if (n + S::kStages - 1 < mine) load(stage == 0 ? S::kStages - 1 : stage - 1, next);
+            cp_commit();
+            next = ahead;
+            cp_wait<S::kStages - 1>();
+            __syncwarp();
+            const uint32_t kt = ring_s + stage * S::kStage, vt = kt + S::kTile;
+
+            float c[NT][2][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[t][0][e] = c[t][1][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                uint32_t b[4];
+                const int row = (lane & 7) + ((lane >> 4) << 3), piece = 2 * k + ((lane >> 3) & 1);
+                ldsm4(kt + row * (HD * 2) + ((piece ^ (row & 7)) << 4), b);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma16816<T>(c[t][0], qa[t][k], b[0], b[1]);
+                    mma16816<T>(c[t][1], qa[t][k], b[2], b[3]);
+                }
+            }
+            // which of the group's keys each row attends to
+            const int u0 = lo + kKeys * (warp + kWarps * n);
+            const uint32_t ok = sok[warp][stage];
+            const int j_lo = keys.at(u0), j_hi = keys.at(u0 + kKeys - 1);
+            const bool all = ok == 0xffffu && j_hi <= pos_lo && (j_hi < p.n_sink || (long long)pos_hi - j_lo <= (long long)p.w * p.stride);
+            uint32_t pa[NT][4];
+            bool up = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = c[t][x][e] * p.scale_log2;
+                        if (!all) {
+                            const int col = 8 * x + 2 * t4 + (e & 1);
+                            const bool see = ((ok >> col) & 1u) && attends(p, pos[t][e >> 1], keys.at(u0 + col));
+                            v = see ? v : -INFINITY;
+                        }
+                        c[t][x][e] = v;
+                    }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mx = fmaxf(fmaxf(c[t][0][2 * e], c[t][0][2 * e + 1]), fmaxf(c[t][1][2 * e], c[t][1][2 * e + 1]));
+                    up |= mx > m[t][e] + kSlack;
+                }
+            }
+            if (__any_sync(0xffffffffu, up)) {   // raise the maxima, scale what was summed so far
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(fmaxf(c[t][0][2 * e], c[t][0][2 * e + 1]), fmaxf(c[t][1][2 * e], c[t][1][2 * e + 1]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        const float mn = fmaxf(m[t][e], mx);
+                        const float f = m[t][e] == -INFINITY ? 0.f : ex2(m[t][e] - mn);
+                        m[t][e] = mn;
+                        l[t][e] *= f;
+#pragma unroll
+                        for (int d = 0; d < HD / 8; ++d) {
+                            o[t][d][2 * e] *= f;
+                            o[t][d][2 * e + 1] *= f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mb = m[t][e] == -INFINITY ? 0.f : m[t][e];
+                    const float p0 = ex2(c[t][0][2 * e] - mb), p1 = ex2(c[t][0][2 * e + 1] - mb);
+                    const float p2 = ex2(c[t][1][2 * e] - mb), p3 = ex2(c[t][1][2 * e + 1] - mb);
+                    l[t][e] += (p0 + p1) + (p2 + p3);
+                    pa[t][e] = pack2<T>(p0, p1);
+                    pa[t][e + 2] = pack2<T>(p2, p3);
+                }
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d) {
+                uint32_t b[4];
+                const int row = (lane & 7) + (((lane >> 3) & 1) << 3), piece = 2 * d + (lane >> 4);
+                ldsm4t(vt + row * (HD * 2) + ((piece ^ (row & 7)) << 4), b);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma16816<T>(o[t][2 * d], pa[t], b[0], b[1]);
+                    mma16816<T>(o[t][2 * d + 1], pa[t], b[2], b[3]);
+                }
+            }
+            __syncwarp();                        // every lane has read the stage
+            stage = stage + 1 == S::kStages ? 0 : stage + 1;
+        }
+        cp_wait<0>();
+        __syncwarp();
+
+        // join the warps: O of each into its own ring, then all threads sum
+        float *mine_o = reinterpret_cast<float *>(ring);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float s = l[t][e];
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                const int row = 16 * t + g + 8 * e;
+                if (t4 == 0) sml[warp][row] = make_float2(m[t][e], s);
+#pragma unroll
+                for (int d = 0; d < HD / 8; ++d)
+                    *reinterpret_cast<float2 *>(mine_o + row * kPad + 8 * d + 2 * t4) = make_float2(o[t][d][2 * e], o[t][d][2 * e + 1]);
+            }
+        __syncthreads();
+        if (threadIdx.x < kRows) {
+            const int row = threadIdx.x;
+            float M = -INFINITY, L = 0.f;
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w][row].x);
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = sml[w][row].x == -INFINITY ? 0.f : ex2(sml[w][row].x - M);
+                swt[w][row] = f;
+                L = fmaf(sml[w][row].y, f, L);
+            }
+            stot[row] = make_float2(M, L);
+            if (row < nrows) {
+                const int a = (row0 + row) / p.group, hh = kvh * p.group + row0 + row - a * p.group;
+                const long long th = (long long)(q.row0 + a) * p.h + hh;
+                if (p.nparts > 1) *GP(p.bnd, p.pml + th * p.nparts + split) = make_float2(M, L);
+                else if (p.lse) *GP(p.bnd, p.lse + th) = lse_of(M, L);
+            }
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < nrows * (HD / 4); e += kThreads) {
+            const int row = e / (HD / 4), c4 = e % (HD / 4) * 4;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = swt[w][row];
+                const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<float *>(smem + w * S::kRing) + row * kPad + c4);
+                y.x = fmaf(v.x, f, y.x);
+                y.y = fmaf(v.y, f, y.y);
+                y.z = fmaf(v.z, f, y.z);
+                y.w = fmaf(v.w, f, y.w);
+            }
+            const int a = (row0 + row) / p.group, hh = kvh * p.group + row0 + row - a * p.group;
+            const long long tok = q.row0 + a, th = tok * p.h + hh;
+            if (p.nparts > 1) {
+                *reinterpret_cast<float4 *>(GPN(p.bnd, p.po + (th * p.nparts + split) * HD + c4, 16)) = y;
+            } else {
+                const float inv = stot[row].y > 0.f ? 1.f / stot[row].y : 0.f;
+                *reinterpret_cast<uint2 *>(GPN(p.bnd, reinterpret_cast<T *>(p.O) + tok * p.o_stride + (long long)hh * HD + c4, 8)) =
+                    make_uint2(pack2<T>(y.x * inv, y.y * inv), pack2<T>(y.z * inv, y.w * inv));
+            }
+        }
+        __syncthreads();                         // the rings are free for the next tile
+    }
+    // the join waits for this grid alone: with a shared prefix, end after its kernel
+    if (p.npre > 0) pdl_wait();
+}
+
+template <typename T, int HD, int NT>
+cudaError_t launch_nt(const DecodeArgs &a, int tiles, cudaStream_t st) {
+    const void *fn = reinterpret_cast<const void *>(&k_decode_rows<T, HD, NT>);
+    const cudaError_t e = ensure_smem(fn, Shape<HD>::kSmem);
+    if (e != cudaSuccess) return e;
+    const int most = 65535 / a.hk;
+    const dim3 grid((unsigned)a.nsplit, (unsigned)(a.hk * (tiles < most ? tiles : most)), (unsigned)a.batch);
+    // behind the prefix kernel it may start at once: it reads nothing of it
+    if (a.npre > 0) return launch_dependent(&k_decode_rows<T, HD, NT>, grid, kThreads, Shape<HD>::kSmem, st, a);
+    k_decode_rows<T, HD, NT><<<grid, kThreads, Shape<HD>::kSmem, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int HD>
+cudaError_t launch_hd(const DecodeArgs &a, int max_q, cudaStream_t st) {
+    // one 16-row tile where the rows fit it, else tiles of 32
+    const long long rows = a.stride == 1 ? (long long)max_q * a.group : a.group;
+    const long long each = a.stride == 1 ? 1 : max_q;
+    if (rows <= 16) return launch_nt<T, HD, 1>(a, (int)each, st);
+    return launch_nt<T, HD, 2>(a, (int)((rows + 31) / 32 * each < 65535 ? (rows + 31) / 32 * each : 65535), st);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_rows(DType dt, const DecodeArgs &a, int max_q, cudaStream_t st) {
+    if (dt == kF16) return a.hd == 64 ? launch_hd<__half, 64>(a, max_q, st) : launch_hd<__half, 128>(a, max_q, st);
+    return a.hd == 64 ? launch_hd<__nv_bfloat16, 64>(a, max_q, st) : launch_hd<__nv_bfloat16, 128>(a, max_q, st);
+}
+
+}  // namespace swab

@@ -195,7 +195,7 @@ long long most_keys(const swab_decode_desc *d) {
 DecodePlan plan_decode(const swab_decode_desc *d) {
     DecodePlan p{};
     const long long group = d->h / d->hk, batch = d->cache.batch;
-    p.rows = false;                  // one kernel for every type and head size so far
+    p.rows = d->dtype != SWAB_F32 && (d->head_dim == 64 || d->head_dim == 128);
     // the key list of a query (general kernel) or of a request's rows is cut
     // where there are fewer blocks than the GPU holds
     long long keys = most_keys(d), blocks = batch, hold, least;
@@ -228,6 +228,20 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
         p.bytes = p.parts_bytes + lines * 8;
     }
     return p;
+}
+
+// Tensor maps of the prefix kernel: Q as {hd, h, tokens}, a tile the heads of a
+// group for pre_tokens tokens; the cache as {hd, page, n_blocks * hk}, a block
+// of one key head at a time; 64 channels (128 bytes) wide.
+bool prefix_maps(const swab_decode_desc *d, const DecodeArgs &a, DType dt, CUtensorMap *mq, CUtensorMap *mk, CUtensorMap *mv) {
+    const cuuint64_t hd = (cuuint64_t)d->head_dim;
+    const cuuint64_t qd[3] = {hd, (cuuint64_t)d->h, (cuuint64_t)d->tokens}, qs[2] = {hd * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)a.group, (cuuint32_t)a.pre_tokens};
+    const cuuint64_t page = (cuuint64_t)d->cache.page;
+    const cuuint64_t kd[3] = {hd, page, (cuuint64_t)d->cache.n_blocks * d->hk}, ks[2] = {hd * 2, page * hd * 2};
+    const cuuint32_t kb[3] = {64, (cuuint32_t)page, 1};
+    return encode_tiled(mq, dt, 3, a.Q, qd, qs, qb) && encode_tiled(mk, dt, 3, a.Kc, kd, ks, kb) &&
+           encode_tiled(mv, dt, 3, a.Vc, kd, ks, kb);
 }
 
 }  // namespace
@@ -431,7 +445,14 @@ SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, cons
                           {lse, (size_t)desc->tokens * desc->h * 4}, {plan.bytes ? workspace : nullptr, plan.bytes})) != SWAB_OK)
         return s;
     if (!(a.err = device_status_word())) return SWAB_ERR_CUDA;
-    cudaError_t e = launch_decode_general(dt, a, as_stream(stream));
+    cudaError_t e = cudaSuccess;
+    if (plan.npre > 0) {
+        CUtensorMap mq, mk, mv;
+        if (!prefix_maps(desc, a, dt, &mq, &mk, &mv)) return status_of(cudaErrorInvalidValue);
+        e = launch_decode_prefix(dt, mq, mk, mv, a, as_stream(stream));
+    }
+    if (e == cudaSuccess)
+        e = plan.rows ? launch_decode_rows(dt, a, desc->max_q, as_stream(stream)) : launch_decode_general(dt, a, as_stream(stream));
     if (e == cudaSuccess && a.nparts > 1) e = launch_decode_join(dt, a, as_stream(stream));
     return status_of(e);
 }
