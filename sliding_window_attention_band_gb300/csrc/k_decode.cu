@@ -65,15 +65,15 @@ __global__ void __launch_bounds__(kThreads) k_decode_general(const __grid_consta
         const int steps = lo < hi ? (int)((hi - lo + kGroups - 1) / kGroups) : 0;
         for (int s = 0; s < steps; ++s) {
             const long long u = lo + (long long)s * kGroups + sub;
-            long long line = -1;
+            uint32_t line = kNoLine;
             if (u < hi) line = u < p.prefix_len ? prefix_line(p, (int)u, kvh) : key_line(p, q, keys.at((int)(u - p.prefix_len)), kvh);
             uint4 kr[kVec], vr[kVec];
 #pragma unroll
             for (int v = 0; v < kVec; ++v) {
                 const int piece = lane + v * kLanes;
                 kr[v] = vr[v] = make_uint4(0, 0, 0, 0);
-                if (line >= 0 && piece < pieces) {
-                    const long long at = line * p.hd + piece * kV;
+                if (line != kNoLine && piece < pieces) {
+                    const long long at = (long long)line * p.hd + piece * kV;
                     kr[v] = ldg16(GPN(p.bnd, reinterpret_cast<const T *>(p.Kc) + at, 16));
                     vr[v] = ldg16(GPN(p.bnd, reinterpret_cast<const T *>(p.Vc) + at, 16));
                 }
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_general(const __grid_consta
             }
 #pragma unroll
             for (int d = kLanes / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-            if (line < 0) continue;
+            if (line == kNoLine) continue;
             x *= p.scale_log2;
             const float mn = fmaxf(m, x), corr = m == -INFINITY ? 0.f : exp2f(m - mn), pr = exp2f(x - mn);
             l = fmaf(l, corr, pr);
@@ -131,59 +131,87 @@ __global__ void __launch_bounds__(kThreads) k_decode_general(const __grid_consta
 
 // Joins the parts of one (token, head): kW warps share them (a warp where there
 // are few; four, over shared memory, where a long context was cut into many).
-// A lane holds the channels lane, lane + 32, ...
+// A lane holds 4 adjacent channels, and 4 more of heads over 128.
 template <typename T, int kW>
 __global__ void __launch_bounds__(kThreads) k_decode_join(const __grid_constant__ DecodeArgs p) {
-    constexpr int kMaxPer = 8, kPairs = kThreads / 32 / kW;      // head_dim <= 256
-    __shared__ float so[kW > 1 ? kW : 1][kMaxPer * 32];
-    __shared__ float sl[kW];
+    constexpr int kPairs = kThreads / 32 / kW, kVecs = 2, kFlight = 8;      // head_dim <= 256
+    __shared__ float4 so[kW > 1 ? kW : 1][kVecs * 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part0 = warp % kW;
     const long long th = (long long)blockIdx.x * kPairs + warp / kW;
     const long long row = th / p.h;
     const int head = (int)(th - row * p.h);
-    pdl_wait();                                                  // the parts are there
-    if (row >= p.tokens || row >= *GP(p.bnd, p.q_start + p.batch)) return;   // with kW = 4: the whole block
+    const bool there = row < p.tokens && row < *GP(p.bnd, p.q_start + p.batch);
+    pdl_wait();                                                   // the parts are there
+    if (!there) return;                                           // with kW = 4: the whole block
     const float2 *ml = p.pml + th * p.nparts;
     const float *po = p.po + th * p.nparts * p.hd;
     float M = -INFINITY, L = 0.f;
     for (int s = lane; s < p.nparts; s += 32) M = fmaxf(M, GP(p.bnd, ml + s)->x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    float o[kMaxPer];
+    float4 o[kVecs];
 #pragma unroll
-    for (int e = 0; e < kMaxPer; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int s = part0; s < p.nparts; s += kW) {
-        const float2 v = *GP(p.bnd, ml + s);
-        const float f = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
-        L = fmaf(v.y, f, L);
+    for (int e = 0; e < kVecs; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // 32 parts at a time, a weight a lane, so that the loads of the values
+    // depend on no load before them; eight of them in flight
+    for (int s0 = 0; s0 < p.nparts; s0 += 32) {
+        const int left = min(p.nparts - s0, 32);
+        const float2 v = lane < left ? *GP(p.bnd, ml + s0 + lane) : make_float2(-INFINITY, 0.f);
+        const float mine = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
+        L = fmaf(v.y, mine, L);
+        for (int k0 = part0; k0 < left; k0 += kFlight * kW) {
 #pragma unroll
-        for (int e = 0; e < kMaxPer; ++e) {
-            const int c = lane + 32 * e;
-            if (c < p.hd) o[e] = fmaf(*GP(p.bnd, po + (long long)s * p.hd + c), f, o[e]);
+            for (int e = 0; e < kVecs; ++e) {
+                const int c = 4 * (lane + 32 * e);
+                if (32 * 4 * e >= p.hd) break;
+                float4 x[kFlight];
+                float f[kFlight];
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    const int k = k0 + i * kW;
+                    f[i] = __shfl_sync(0xffffffffu, mine, k & 31);
+                    if (k >= left) f[i] = 0.f;
+                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    // (the values of an empty part are not written)
+                    if (f[i] != 0.f && c < p.hd) x[i] = *reinterpret_cast<const float4 *>(GPN(p.bnd, po + (long long)(s0 + k) * p.hd + c, 16));
+                }
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    o[e].x = fmaf(x[i].x, f[i], o[e].x);
+                    o[e].y = fmaf(x[i].y, f[i], o[e].y);
+                    o[e].z = fmaf(x[i].z, f[i], o[e].z);
+                    o[e].w = fmaf(x[i].w, f[i], o[e].w);
+                }
+            }
         }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
     if constexpr (kW > 1) {
 #pragma unroll
-        for (int e = 0; e < kMaxPer; ++e) so[warp][lane + 32 * e] = o[e];
-        if (lane == 0) sl[warp] = L;
+        for (int e = 0; e < kVecs; ++e) so[warp][lane + 32 * e] = o[e];
         __syncthreads();
         if (warp > 0) return;
-        L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) L += sl[w];
+        for (int e = 0; e < kVecs; ++e)
 #pragma unroll
-        for (int e = 0; e < kMaxPer; ++e) {
-            o[e] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kW; ++w) o[e] += so[w][lane + 32 * e];
-        }
+            for (int w = 1; w < kW; ++w) {
+                const float4 x = so[w][lane + 32 * e];
+                o[e].x += x.x;
+                o[e].y += x.y;
+                o[e].z += x.z;
+                o[e].w += x.w;
+            }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
+    T *out = reinterpret_cast<T *>(p.O) + row * p.o_stride + (long long)head * p.hd;
 #pragma unroll
-    for (int e = 0; e < kMaxPer; ++e) {
-        const int c = lane + 32 * e;
-        if (c < p.hd) *GP(p.bnd, reinterpret_cast<T *>(p.O) + row * p.o_stride + (long long)head * p.hd + c) = Elt<T>::from_f(o[e] * inv);
+    for (int e = 0; e < kVecs; ++e) {
+        const int c = 4 * (lane + 32 * e);
+        if (c >= p.hd) break;
+        const float4 y = make_float4(o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv);
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(GPN(p.bnd, out + c, 16)) = y;
+        else *reinterpret_cast<uint2 *>(GPN(p.bnd, out + c, 8)) = make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
     }
     if (lane == 0 && p.lse) *GP(p.bnd, p.lse + th) = lse_of(M, L);
 }

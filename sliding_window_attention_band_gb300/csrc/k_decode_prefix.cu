@@ -8,14 +8,18 @@
 // reached: a block owns 128 rows of one key head and a run of 128-key chunks
 // (the prefix is split so that the blocks fill the SMs once).
 //
-// Per chunk: S = Q K^T (M = 128 rows, N = 128 keys) into one of two
-// tensor-memory buffers; eight softmax warps, two for each 32-row quarter, 64
-// keys each (thread = row), take S to registers, p = 2^(x - m) with a
-// reference m of their own that is raised only by more than 2^8, and put P,
-// 16 bits wide, back over their half of S; O_h += P V for each half h into the
-// half's own fp32 accumulator (two of them, joined at the end like two pieces
-// of a split list).  The prefix needs no mask but at its very end and for
-// absent blocks: there the scores are set to never win, and the values of
+// Two streams of work go through the tensor cores in turn, so that one stream's
+// softmax runs under the other's products: with more than 128 rows two row
+// tiles over the same chunks (kPair; K and V are fetched once for both), with
+// fewer the one tile's even and odd chunks, whose results are two parts.  Each
+// stream has a score buffer and an fp32 accumulator in tensor memory (2 x 128 +
+// 2 x hd columns, all 512 at hd 128).  Per chunk of a stream: S = Q K^T; four
+// softmax warps (thread = row) take S to registers, p = 2^(x - m) with a
+// reference m that is raised only by more than 2^8, and put P, 16 bits wide,
+// back over S; O += P V (A from tensor memory).  The next S of the stream is
+// issued once that product is done, so it may overwrite P, and the softmax may
+// rescale O without waiting.  The prefix needs no mask but at its very end and
+// for absent blocks: there the scores are set to never win, and the values of
 // those keys, which may be anything, are zeroed in shared memory.
 //
 // A block of the cache is one TMA box of `page` lines; the tiles of 128 keys,
@@ -39,13 +43,14 @@ constexpr int kThreads = 64 + 32 * kWorkers;
 constexpr uint32_t kCols = 512;                 // tensor-memory columns
 constexpr float kSlack = 8.f;
 
-template <int HD> struct Shape {
+template <int HD, bool kPair> struct Shape {
     static constexpr int kHalves = HD / 64;              // 64-channel tiles of 128-byte lines
     static constexpr int kTile = kBK * HD * 2;           // K or V of a chunk
-    static constexpr int kSlots = HD == 128 ? 6 : 8;     // ring of such tiles
-    static constexpr int kQ = kBQ * HD * 2;
+    static constexpr int kQ1 = kBQ * HD * 2;             // Q of a row tile
+    static constexpr int kQ = (kPair ? 2 : 1) * kQ1;
+    static constexpr int kSlots = HD == 64 ? 10 : kPair ? 5 : 6;   // ring of K and V tiles
     static constexpr int kSmem = kQ + kSlots * kTile + 512 + 1024;
-    static constexpr uint32_t kColS = 0, kColO = 256;    // S_b at 128 b (P_b over it), O_h at 256 + HD h
+    static constexpr uint32_t kColS = 0, kColO = 256;    // S_g at 128 g (P_g over it), O_g at 256 + HD g
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -53,30 +58,29 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-template <typename T, int HD>
+template <typename T, int HD, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     k_decode_prefix(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapV, const __grid_constant__ DecodeArgs p) {
-    using S = Shape<HD>;
+    using S = Shape<HD, kPair>;
     constexpr int kSlots = S::kSlots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t *qtile = base;                       // [HD / 64] x 128 lines
+    uint8_t *qtile = base;                       // [row tiles][HD / 64] x 128 lines
     uint8_t *ring = base + S::kQ;
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + kSlots * S::kTile);
     uint64_t *qfull = bars, *full = bars + 1, *empty = full + kSlots;
-    uint64_t *sfull = empty + kSlots;            // [2] S_b written
-    uint64_t *pfull = sfull + 2;                 // [2] P_b in place: one arrival a softmax warp
-    uint64_t *pempty = pfull + 2;                // [2] the product that read P_b is done
-    uint64_t *mlbar = pempty + 2;                // [4] per quarter, its two warps
-    uint64_t *done = mlbar + 4;
+    uint64_t *sfull = empty + kSlots;            // [2] a stream's S is written
+    uint64_t *pfull = sfull + 2;                 // [2] its P is in place: one arrival a softmax warp
+    uint64_t *odone = pfull + 2;                 // [2] its product is done
+    uint64_t *done = odone + 2;
     uint32_t *holder = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(holder + 1);
     volatile int *no_abort = abort_flag + 1;
     volatile uint32_t *okmask = holder + 4;      // [8] the pages of chunk c that are there, at c mod 8
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.x / p.npre, split = blockIdx.x - tile * p.npre, kvh = blockIdx.y;
+    const int block = blockIdx.x / p.pre_pieces, split = blockIdx.x - block * p.pre_pieces, kvh = blockIdx.y;
     const int nchunks = (p.prefix_len + kBK - 1) / kBK;
     const int c0 = split * p.pre_chunks, c1 = min(nchunks, c0 + p.pre_chunks), n = c1 - c0;
     const int ppt = 128 >> p.page_log2;          // pages of a tile
@@ -89,10 +93,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], kWorkers);
-            mbar_init(&pempty[i], 1);
+            mbar_init(&pfull[i], kWorkers / 2);
+            mbar_init(&odone[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&mlbar[i], 2);
         mbar_init(done, 1);
         *abort_flag = 0;
         *no_abort = 0;
@@ -113,14 +116,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             tma_prefetch_desc(&mapK);
             tma_prefetch_desc(&mapV);
-            mbar_arrive_expect_tx(qfull, (uint32_t)(p.pre_tokens * p.group) * 128u * S::kHalves);
-            for (int h = 0; h < S::kHalves; ++h)
-                tma_load_3d(qtile + h * (kBQ * 128), &mapQ, qfull, 64 * h, kvh * p.group, tile * p.pre_tokens);
+            mbar_arrive_expect_tx(qfull, (uint32_t)(p.pre_tokens * p.group) * 128u * S::kHalves * (kPair ? 2u : 1u));
+            for (int t = 0; t < (kPair ? 2 : 1); ++t)      // a tile past the last token reads zeros
+                for (int h = 0; h < S::kHalves; ++h)
+                    tma_load_3d(qtile + t * S::kQ1 + h * (kBQ * 128), &mapQ, qfull, 64 * h, kvh * p.group,
+                                (block * (kPair ? 2 : 1) + t) * p.pre_tokens);
         }
         __syncwarp();
         int it = 0;
         bool ok = true;
-        int id = -1;
         auto page_id = [&](int c) -> int {       // this lane's page of chunk c, -1: none
             const int j = (c * ppt + lane) << p.page_log2;
             if (lane >= ppt || c >= c1 || j >= p.prefix_len) return -1;
@@ -129,19 +133,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x != -1) atomicOr(p.err, kErrInvalid);
             return -1;
         };
-        id = page_id(c0);
+        int id = page_id(c0);
         for (int c = c0; c < c1 && ok; ++c) {
             const int ahead = page_id(c + 1);
             const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
             const uint32_t bytes = (uint32_t)__popc(there) * ((uint32_t)HD * 2u << p.page_log2);
-            for (int v = 0; v < 2 && ok; ++v, ++it) {
+            for (int v = 0; v < 2; ++v, ++it) {
                 const int slot = it % kSlots;
                 ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ((it / kSlots) & 1) ^ 1, abort_flag, p.err));
                 if (!ok) break;
                 uint8_t *dst = ring + slot * S::kTile + ((lane << p.page_log2) * 128);
                 if (lane == 0) {
-                    // (rewritten 8 chunks later, long after the softmax warps
-                    // have read it: they are at most 4 chunks behind)
+                    // (rewritten 8 chunks later, when the softmax warps, at most
+                    // kSlots / 2 chunks behind, have long read it)
                     okmask[(c - c0) & 7] = there;
                     mbar_arrive_expect_tx(&full[slot], bytes);
                 }
@@ -168,121 +172,125 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t kdesc = sdesc_sw128(smem_u32(ring), 16, 1024);
             // V as an MN-major operand: 64-channel blocks one tile half apart
             const uint64_t vdesc = sdesc_sw128(smem_u32(ring), kBK * 128, 1024);
-            bool ok = mbar_wait(qfull, 0, abort_flag, p.err);
-            auto product = [&](int c) -> bool {      // O_h += P V of chunk c (counted from 0)
-                const int b = c & 1, it = 2 * c + 1, slot = it % kSlots;
+            // job j: stream j mod 2, its chunk number j / 2, chunk `c` of the block
+            const int jobs = kPair ? 2 * n : n;
+            auto scores = [&](int j) -> bool {       // S = Q K^T
+                const int g = j & 1, c = kPair ? j >> 1 : j, it = 2 * c, slot = it % kSlots;
                 if (!mbar_wait(&full[slot], (it / kSlots) & 1, abort_flag, p.err)) return false;
-                if (!mbar_wait(&pfull[b], (c >> 1) & 1, abort_flag, p.err)) return false;
                 tc_fence_after();
-                const uint64_t va = vdesc + (uint64_t)((slot * S::kTile) >> 4);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16_ts(tmem + S::kColO + HD * h, tmem + S::kColS + kBK * b + 64 * h + 8 * k,
-                                   va + (uint64_t)((2048 * (4 * h + k)) >> 4), idesc_o, (c == 0 && k == 0) ? 0u : 1u);
-                mma_commit(&pempty[b]);
-                mma_commit(&empty[slot]);
-                return true;
-            };
-            for (int c = 0; c < n && ok; ++c) {
-                const int b = c & 1, it = 2 * c, slot = it % kSlots;
-                ok = mbar_wait(&full[slot], (it / kSlots) & 1, abort_flag, p.err);
-                if (!ok) break;
-                // S_b holds P of chunk c - 2: its product has to be done
-                if (c >= 2 && !(ok = mbar_wait(&pempty[b], ((c >> 1) & 1) ^ 1, abort_flag, p.err))) break;
-                tc_fence_after();
+                const uint64_t qa = qdesc + (uint64_t)((kPair ? g * S::kQ1 : 0) >> 4);
                 const uint64_t ka = kdesc + (uint64_t)((slot * S::kTile) >> 4);
 #pragma unroll
                 for (int h = 0; h < S::kHalves; ++h)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_f16_ss(tmem + S::kColS + kBK * b, qdesc + (uint64_t)((h * kBQ * 128) >> 4) + 2 * k,
+                        mma_f16_ss(tmem + S::kColS + kBK * g, qa + (uint64_t)((h * kBQ * 128) >> 4) + 2 * k,
                                    ka + (uint64_t)((h * kBK * 128) >> 4) + 2 * k, idesc_s, (h > 0 || k > 0) ? 1u : 0u);
-                mma_commit(&empty[slot]);
-                mma_commit(&sfull[b]);
-                if (c > 0) ok = product(c - 1);
+                if (!kPair || g == 1) mma_commit(&empty[slot]);
+                mma_commit(&sfull[g]);
+                return true;
+            };
+            auto product = [&](int j) -> bool {      // O += P V
+                const int g = j & 1, i = j >> 1, c = kPair ? i : j, it = 2 * c + 1, slot = it % kSlots;
+                if (!mbar_wait(&full[slot], (it / kSlots) & 1, abort_flag, p.err)) return false;
+                if (!mbar_wait(&pfull[g], i & 1, abort_flag, p.err)) return false;
+                tc_fence_after();
+                const uint64_t va = vdesc + (uint64_t)((slot * S::kTile) >> 4);
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                    mma_f16_ts(tmem + S::kColO + HD * g, tmem + S::kColS + kBK * g + 8 * k, va + (uint64_t)((2048 * k) >> 4), idesc_o,
+                               (i == 0 && k == 0) ? 0u : 1u);
+                if (!kPair || g == 1) mma_commit(&empty[slot]);
+                mma_commit(&odone[g]);
+                return true;
+            };
+            bool ok = mbar_wait(qfull, 0, abort_flag, p.err) && scores(0) && (jobs < 2 || scores(1));
+            for (int j = 0; j < jobs && ok; ++j) {
+                ok = product(j);
+                if (ok && j + 2 < jobs) ok = mbar_wait(&odone[j & 1], (j >> 1) & 1, abort_flag, p.err) && scores(j + 2);
             }
-            if (ok && n > 0) product(n - 1);
             mma_commit(done);                    // nothing is in flight when tensor memory is freed
             mbar_wait(done, 0, no_abort, nullptr, 100000000ull);
         }
     } else {
-        // ---------------- softmax: thread = row, half h of the keys ----------------
-        const int quarter = warp & 3, half = (warp - 2) >> 2, row = 32 * quarter + lane;
+        // ---------------- softmax: thread = row of stream g ----------------
+        const int quarter = warp & 3, g = (warp - 2) >> 2, row = 32 * quarter + lane;
+        const int mine = kPair ? n : (n - g + 1) / 2;            // chunks of the stream
         const uint32_t lane_base = tmem_addr(tmem, quarter * 32, 0);
-        const float xs = p.scale_log2;
+        const uint32_t at_s = lane_base + S::kColS + kBK * g, at_o = lane_base + S::kColO + HD * g;
+        // (scale 0: small enough for equal weights, and -inf stays -inf)
+        const float xs = p.scale_log2 == 0.f ? 1e-37f : p.scale_log2;
         const bool neg = xs < 0.f;
         const float never = neg ? INFINITY : -INFINITY;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int c = 0; c < n; ++c) {
-            const int b = c & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(&sfull[b], (c >> 1) & 1, abort_flag, p.err))) {
+        for (int i = 0; i < mine; ++i) {
+            const int c = kPair ? i : 2 * i + g;
+            if (!__all_sync(0xffffffffu, mbar_wait(&sfull[g], i & 1, abort_flag, p.err))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            // keys of this half that are there, 32 a word
-            uint32_t vm[2] = {0xffffffffu, 0xffffffffu};
+            uint32_t x[kBK];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) tmem_ld32(at_s + 32 * v, *reinterpret_cast<uint32_t (*)[32]>(x + 32 * v));
             const int j0 = (c0 + c) * kBK;
             const uint32_t there = okmask[c & 7];
             const bool whole = there == (1u << ppt) - 1u && j0 + kBK <= p.prefix_len;
-            if (!whole) {
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int j = 64 * half + 32 * w;        // in the chunk
-                    vm[w] = (((there >> (j >> p.page_log2)) & 1u) ? 0xffffu : 0u) |
-                            (((there >> ((j + 16) >> p.page_log2)) & 1u) ? 0xffff0000u : 0u);
-                    const int left = p.prefix_len - j0 - j;
-                    if (left < 32) vm[w] &= left <= 0 ? 0u : (1u << left) - 1u;
-                }
-            }
-            uint32_t x[64];
-            tmem_ld32(lane_base + S::kColS + kBK * b + 64 * half, *reinterpret_cast<uint32_t (*)[32]>(x));
-            tmem_ld32(lane_base + S::kColS + kBK * b + 64 * half + 32, *reinterpret_cast<uint32_t (*)[32]>(x + 32));
             tmem_ld_wait();
             if (!whole) {
+                // keys that are there, 32 a word
+                uint32_t vm[4];
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    if (!((vm[i >> 5] >> (i & 31)) & 1u)) x[i] = __float_as_uint(never);
-                // V lines of absent keys become zeros: this warp's quarter of the
-                // lines of its half, once the tile has landed
+                for (int w = 0; w < 4; ++w) {
+                    const int j = 32 * w, left = p.prefix_len - j0 - j;
+                    vm[w] = (((there >> (j >> p.page_log2)) & 1u) ? 0xffffu : 0u) |
+                            (((there >> ((j + 16) >> p.page_log2)) & 1u) ? 0xffff0000u : 0u);
+                    if (left < 32) vm[w] &= left <= 0 ? 0u : (1u << left) - 1u;
+                }
+#pragma unroll
+                for (int k = 0; k < kBK; ++k)
+                    if (!((vm[k >> 5] >> (k & 31)) & 1u)) x[k] = __float_as_uint(never);
+                // V lines of absent keys become zeros, once the tile has landed: a
+                // quarter of them for each warp
                 const int it = 2 * c + 1, slot = it % kSlots;
                 if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], (it / kSlots) & 1, abort_flag, p.err))) {
                     ok = false;
                     break;
                 }
-                for (int k = quarter; k < 64; k += 4) {
-                    if ((vm[k >> 5] >> (k & 31)) & 1u) continue;
-                    const int line = 64 * half + k;
-                    for (int i = lane; i < HD / 8; i += 32)
-                        *reinterpret_cast<uint4 *>(ring + slot * S::kTile + (i >> 3) * (kBK * 128) + line * 128 + (i & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    for (int k = quarter; k < 32; k += 4) {
+                        if ((vm[w] >> k) & 1u) continue;
+                        if (lane < HD / 8)
+                            *reinterpret_cast<uint4 *>(ring + slot * S::kTile + (lane >> 3) * (kBK * 128) + (32 * w + k) * 128 +
+                                                       (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
                 fence_proxy_async_smem();
             }
-            float ext[4];
+            float ext[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 8; ++k) {
                 const uint32_t *y = x + 16 * k;
                 float a = __uint_as_float(y[0]);
 #pragma unroll
-                for (int i = 1; i < 15; i += 2)
-                    a = neg ? min3(a, __uint_as_float(y[i]), __uint_as_float(y[i + 1]))
-                            : max3(a, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                for (int e = 1; e < 15; e += 2)
+                    a = neg ? min3(a, __uint_as_float(y[e]), __uint_as_float(y[e + 1]))
+                            : max3(a, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
                 ext[k] = neg ? fminf(a, __uint_as_float(y[15])) : fmaxf(a, __uint_as_float(y[15]));
             }
-            const float best = neg ? fminf(fminf(ext[0], ext[1]), fminf(ext[2], ext[3]))
-                                   : fmaxf(fmaxf(ext[0], ext[1]), fmaxf(ext[2], ext[3]));
+            const float best = neg ? fminf(min3(ext[0], ext[1], ext[2]), fminf(min3(ext[3], ext[4], ext[5]), fminf(ext[6], ext[7])))
+                                   : fmaxf(max3(ext[0], ext[1], ext[2]), fmaxf(max3(ext[3], ext[4], ext[5]), fmaxf(ext[6], ext[7])));
             const float cmax = best == never ? -INFINITY : best * xs;
             const bool raise = cmax > m + kSlack;            // the first time too: m is -inf
             const float mref = raise ? cmax : m;
             const float mb = mref == -INFINITY ? 0.f : mref;
+            const bool rescale = raise && m != -INFINITY;
+            const float corr = rescale ? ex2(m - mref) : 1.f;
             const uint64_t xs2 = f2(xs, xs), nb2 = f2(-mb, -mb);
             uint64_t ls[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
+            for (int v = 0; v < 4; ++v) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -292,71 +300,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ls[e & 1] = add2(ls[e & 1], f2(p0, p1));
                     pk[e] = pack2<T>(p0, p1);
                 }
-                tmem_st16(lane_base + S::kColS + kBK * b + 64 * half + 16 * v, pk);
+                tmem_st16(at_s + 16 * v, pk);
             }
             float l0, l1;
             f2split(add2(ls[0], ls[1]), l0, l1);
-            const bool rescale = raise && m != -INFINITY;
-            const float corr = rescale ? ex2(m - mref) : 1.f;
             l = l * corr + (l0 + l1);
             if (__any_sync(0xffffffffu, rescale)) {
-                // O_h must not move under a product: wait for chunk c - 1's
-                if (!__all_sync(0xffffffffu, mbar_wait(&pempty[b ^ 1], ((c - 1) >> 1) & 1, abort_flag, p.err))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+                // (the product before this S is done: see the issuing warp)
 #pragma unroll 1
                 for (int k = 0; k < HD / 32; ++k) {
                     uint32_t o[32];
-                    tmem_ld32(lane_base + S::kColO + HD * half + 32 * k, o);
+                    tmem_ld32(at_o + 32 * k, o);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-                    tmem_st32(lane_base + S::kColO + HD * half + 32 * k, o);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                    tmem_st32(at_o + 32 * k, o);
                 }
             }
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive_warp(&pfull[b]);
+            mbar_arrive_warp(&pfull[g]);
             m = mref;
         }
-        // the two halves of a row, then the part of this block
-        if (ok && n > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&pempty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, p.err));
-            if (ok) {
-                tc_fence_after();
-                float2 *ml = reinterpret_cast<float2 *>(qtile);      // Q is done with
-                ml[half * kBQ + row] = make_float2(m, l);
-                mbar_arrive_warp(&mlbar[quarter]);
-                ok = __all_sync(0xffffffffu, mbar_wait(&mlbar[quarter], 0, abort_flag, p.err));
-                if (ok) {
-                    const float2 e0 = ml[row], e1 = ml[kBQ + row];
-                    const float M = fmaxf(e0.x, e1.x);
-                    const float f0 = e0.x == -INFINITY ? 0.f : ex2(e0.x - M), f1 = e1.x == -INFINITY ? 0.f : ex2(e1.x - M);
-                    const int tok = tile * p.pre_tokens + row / p.group, hh = kvh * p.group + row % p.group;
-                    const bool live = row < p.pre_tokens * p.group && tok < p.tokens;
-                    const long long at = ((long long)tok * p.h + hh) * p.nparts + p.nsplit + split;
-                    if (live && half == 0) *GP(p.bnd, p.pml + at) = make_float2(M, e0.y * f0 + e1.y * f1);
+        // the stream's part
+        const int tok = (block * (kPair ? 2 : 1) + (kPair ? g : 0)) * p.pre_tokens + row / p.group;
+        const int hh = kvh * p.group + row % p.group;
+        const bool live = row < p.pre_tokens * p.group && tok < p.tokens;
+        const long long at = ((long long)tok * p.h + hh) * p.nparts + p.nsplit + (kPair ? split : 2 * split + g);
+        if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(&odone[g], (mine - 1) & 1, abort_flag, p.err));
+        if (ok) {
+            tc_fence_after();
+            if (live) *GP(p.bnd, p.pml + at) = make_float2(m, l);
+            if (mine > 0) {
 #pragma unroll 1
-                    for (int k = 0; k < HD / 32; ++k) {          // 16 channels of this half's share
-                        uint32_t o0[16], o1[16];
-                        const int ch = half * (HD / 2) + 16 * k;
-                        tmem_ld16(lane_base + S::kColO + ch, o0);
-                        tmem_ld16(lane_base + S::kColO + HD + ch, o1);
-                        tmem_ld_wait();
-                        if (live) {
-                            float *dst = p.po + at * HD + ch;
+                for (int k = 0; k < HD / 32; ++k) {
+                    uint32_t o[32];
+                    tmem_ld32(at_o + 32 * k, o);
+                    tmem_ld_wait();
+                    if (live) {
+                        float *dst = p.po + at * HD + 32 * k;
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                float4 y;
-                                y.x = fmaf(__uint_as_float(o1[4 * v]), f1, __uint_as_float(o0[4 * v]) * f0);
-                                y.y = fmaf(__uint_as_float(o1[4 * v + 1]), f1, __uint_as_float(o0[4 * v + 1]) * f0);
-                                y.z = fmaf(__uint_as_float(o1[4 * v + 2]), f1, __uint_as_float(o0[4 * v + 2]) * f0);
-                                y.w = fmaf(__uint_as_float(o1[4 * v + 3]), f1, __uint_as_float(o0[4 * v + 3]) * f0);
-                                *reinterpret_cast<float4 *>(GPN(p.bnd, dst + 4 * v, 16)) = y;
-                            }
-                        }
+                        for (int v = 0; v < 8; ++v)
+                            *reinterpret_cast<uint4 *>(GPN(p.bnd, dst + 4 * v, 16)) =
+                                make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                     }
                 }
             }
@@ -367,21 +353,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, kCols);
 }
 
-template <typename T, int HD>
+template <typename T, int HD, bool kPair>
 cudaError_t launch_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const DecodeArgs &a, cudaStream_t st) {
-    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(&k_decode_prefix<T, HD>), Shape<HD>::kSmem);
+    using S = Shape<HD, kPair>;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(&k_decode_prefix<T, HD, kPair>), S::kSmem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(a.npre * ((a.tokens + a.pre_tokens - 1) / a.pre_tokens)), (unsigned)a.hk);
-    k_decode_prefix<T, HD><<<grid, kThreads, Shape<HD>::kSmem, st>>>(mq, mk, mv, a);
+    const int tokens = a.pre_tokens * (kPair ? 2 : 1);           // of a block
+    const dim3 grid((unsigned)(a.pre_pieces * ((a.tokens + tokens - 1) / tokens)), (unsigned)a.hk);
+    k_decode_prefix<T, HD, kPair><<<grid, kThreads, S::kSmem, st>>>(mq, mk, mv, a);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_hd(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const DecodeArgs &a, cudaStream_t st) {
+    const bool pair = a.tokens > a.pre_tokens;
+    if (a.hd == 64) return pair ? launch_t<T, 64, true>(mq, mk, mv, a, st) : launch_t<T, 64, false>(mq, mk, mv, a, st);
+    return pair ? launch_t<T, 128, true>(mq, mk, mv, a, st) : launch_t<T, 128, false>(mq, mk, mv, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_prefix(DType dt, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const DecodeArgs &a,
                                  cudaStream_t st) {
-    if (dt == kF16) return a.hd == 64 ? launch_t<__half, 64>(mq, mk, mv, a, st) : launch_t<__half, 128>(mq, mk, mv, a, st);
-    return a.hd == 64 ? launch_t<__nv_bfloat16, 64>(mq, mk, mv, a, st) : launch_t<__nv_bfloat16, 128>(mq, mk, mv, a, st);
+    return dt == kF16 ? launch_hd<__half>(mq, mk, mv, a, st) : launch_hd<__nv_bfloat16>(mq, mk, mv, a, st);
 }
 
 }  // namespace swab

@@ -32,17 +32,17 @@ static constexpr unsigned kSwabFile = 15;   // site id of the bounds checks
 namespace swab {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 16;          // keys of a group
 constexpr float kSlack = 8.f;      // log2 headroom of the running maximum
 
-template <int HD> struct Shape {
-    static constexpr int kStages = HD == 128 ? 3 : 6;
+template <int HD, int NT, int kWarps> struct Shape {
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kBlocks = (NT == 1 ? 12 : 8) / kWarps;    // an SM holds, by registers and shared memory
+    static constexpr int kStages = (NT == 1 ? 2 : 3) * (HD == 128 ? 1 : 2);
     static constexpr int kTile = kKeys * HD * 2;             // bytes of 16 lines
     static constexpr int kStage = 2 * kTile;                 // K and V
-    static constexpr int kRing = kStages * kStage;           // of a warp: 24 KB
-    static constexpr int kSmem = kWarps * kRing;
+    static constexpr int kRing = kStages * kStage;           // of a warp
+    static constexpr int kSmem = kWarps * kRing + 256;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -76,14 +76,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // NT: 16-row tiles of a block.  Grid: (piece, key head and row tile, request).
-template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant__ DecodeArgs p) {
-    using S = Shape<HD>;
+// kWarps: the warps that share a piece.
+template <typename T, int HD, int NT, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k_decode_rows(const __grid_constant__ DecodeArgs p) {
+    using S = Shape<HD, NT, kWarps>;
+    constexpr int kThreads = S::kThreads;
     constexpr int kRows = 16 * NT, kSteps = HD / 16, kPieces = HD / 8;   // 16-byte pieces of a line
     constexpr int kPer = 32 / kPieces;                                   // lines of a copy instruction
     constexpr int kPad = HD + 8;                                         // floats of a row in the final exchange
     static_assert(kRows * kPad * 4 <= S::kRing, "a warp's O fits its ring");
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    // (the xors below need the rings at multiples of 256 bytes)
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 255) & ~static_cast<uintptr_t>(255));
     __shared__ float2 sml[kWarps][kRows];
     __shared__ float swt[kWarps][kRows];
     __shared__ float2 stot[kRows];
@@ -96,6 +100,19 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
     const Request q = request_of(p, r);
     uint8_t *ring = smem + warp * S::kRing;
     const uint32_t ring_s = smem_u32(ring);
+    // this lane's piece of a line in memory, where a copy of it goes, and the
+    // lines an ldmatrix reads: the place of piece 2k + b of line r is that of
+    // piece b, xor 2k
+    const char *kbase = reinterpret_cast<const char *>(p.Kc) + lane % kPieces * 16;
+    const char *vbase = reinterpret_cast<const char *>(p.Vc) + lane % kPieces * 16;
+    const uint32_t copy_row = lane / kPieces, copy_to = copy_row * (HD * 2) + (((lane % kPieces) ^ copy_row) << 4);
+    const uint32_t krow = (lane & 7) + ((lane >> 4) << 3), vrow = (lane & 7) + (((lane >> 3) & 1) << 3);
+    const uint32_t kat = krow * (HD * 2) + ((((lane >> 3) & 1) ^ (krow & 7)) << 4);
+    const uint32_t vat = S::kTile + vrow * (HD * 2) + (((lane >> 4) ^ (vrow & 7)) << 4);
+    // scores are scaled by |scale| inside the exponent; a negative one turns Q
+    // round (exact), zero clears it
+    const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    const uint32_t q_and = p.scale_log2 == 0.f ? 0u : 0xffffffffu, q_xor = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     // tiles of rows: with a key stride each token has its own
     const int per_tok = (p.group + kRows - 1) / kRows;
     const int ntiles = p.stride == 1 ? (q.m * p.group + kRows - 1) / kRows : q.m * per_tok;
@@ -118,29 +135,30 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
         const int groups = (hi - lo + kKeys - 1) / kKeys;
         const int mine = groups > warp ? (groups - warp + kWarps - 1) / kWarps : 0;   // of this warp
 
-        // line of key (lane mod 16) of the warp's group n, -1 when there is none
-        auto look_up = [&](int n) -> long long {
+        // line of key (lane mod 16) of the warp's group n
+        auto look_up = [&](int n) -> uint32_t {
             const int u = lo + kKeys * (warp + kWarps * n) + (lane & 15);
-            return n < mine && u < hi ? key_line(p, q, keys.at(u), kvh) : -1;
+            return n < mine && u < hi ? key_line(p, q, keys.at(u), kvh) : kNoLine;
         };
-        auto load = [&](int stage, long long line) {
-            const uint32_t dst = ring_s + stage * S::kStage;
-            const uint32_t there = __ballot_sync(0xffffffffu, line >= 0) & 0xffffu;
+        // the 16 lines into a stage: copy i brings lines i * kPer.. ; piece c of
+        // line r goes to place c ^ (r mod 8) of the line
+        auto load = [&](int stage, uint32_t line) {
+            const uint32_t there = __ballot_sync(0xffffffffu, line != kNoLine) & 0xffffu;
             if (lane == 0) sok[warp][stage] = there;
+            const uint32_t to = ring_s + stage * S::kStage + copy_to;
 #pragma unroll
             for (int i = 0; i < kKeys / kPer; ++i) {
-                const int row = i * kPer + lane / kPieces, piece = lane % kPieces;
-                const long long ln = __shfl_sync(0xffffffffu, line, row);
-                const uint32_t bytes = ln >= 0 ? 16u : 0u;
-                const long long at = (ln >= 0 ? ln : 0) * HD + piece * 8;
-                const uint32_t to = dst + row * (HD * 2) + ((piece ^ (row & 7)) << 4);
-                cp_async16(to, GPN(p.bnd, reinterpret_cast<const T *>(p.Kc) + at, 16), bytes);
-                cp_async16(to + S::kTile, GPN(p.bnd, reinterpret_cast<const T *>(p.Vc) + at, 16), bytes);
+                const uint32_t ln = __shfl_sync(0xffffffffu, line, i * kPer + lane / kPieces);
+                const uint32_t bytes = ln != kNoLine ? 16u : 0u;
+                const unsigned long long at = (unsigned long long)(ln != kNoLine ? ln : 0u) * (HD * 2);
+                const uint32_t dst = (to + i * kPer * HD * 2) ^ (((i * kPer) & 7) << 4);
+                cp_async16(dst, GPN(p.bnd, kbase + at, 16), bytes);
+                cp_async16(dst + S::kTile, GPN(p.bnd, vbase + at, 16), bytes);
             }
         };
 
         // fill the ring; the lines of the stage after it are looked up meanwhile
-        long long first[S::kStages];
+        uint32_t first[S::kStages];
 #pragma unroll
         for (int s = 0; s < S::kStages; ++s) first[s] = look_up(s);
 #pragma unroll
@@ -148,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
             if (s < mine) load(s, first[s]);
             cp_commit();
         }
-        long long next = first[S::kStages - 1];
+        uint32_t next = first[S::kStages - 1];
 
         // Q of the tile as A operands
         uint32_t qa[NT][kSteps][4];
@@ -164,8 +182,8 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
                 for (int k = 0; k < kSteps; ++k) {
                     const uint32_t x0 = *GP(p.bnd, reinterpret_cast<const uint32_t *>(src + 16 * k));
                     const uint32_t x1 = *GP(p.bnd, reinterpret_cast<const uint32_t *>(src + 16 * k + 8));
-                    qa[t][k][half] = live ? x0 : 0u;
-                    qa[t][k][half + 2] = live ? x1 : 0u;
+                    qa[t][k][half] = live ? (x0 & q_and) ^ q_xor : 0u;
+                    qa[t][k][half + 2] = live ? (x1 & q_and) ^ q_xor : 0u;
                 }
             }
         // positions of this lane's rows (row g + 8 e of tile t)
@@ -190,13 +208,13 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
         int stage = 0;
         for (int n = 0; n < mine; ++n) {
             // the ring's free stage takes group n + kStages - 1
-            const long long ahead = look_up(n + S::kStages);
+            const uint32_t ahead = look_up(n + S::kStages);
             if (n + S::kStages - 1 < mine) load(stage == 0 ? S::kStages - 1 : stage - 1, next);
             cp_commit();
             next = ahead;
             cp_wait<S::kStages - 1>();
             __syncwarp();
-            const uint32_t kt = ring_s + stage * S::kStage, vt = kt + S::kTile;
+            const uint32_t kt = ring_s + stage * S::kStage + kat, vt = ring_s + stage * S::kStage + vat;
 
             float c[NT][2][4];
 #pragma unroll
@@ -206,8 +224,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
                 uint32_t b[4];
-                const int row = (lane & 7) + ((lane >> 4) << 3), piece = 2 * k + ((lane >> 3) & 1);
-                ldsm4(kt + row * (HD * 2) + ((piece ^ (row & 7)) << 4), b);
+                ldsm4(kt ^ (k << 5), b);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     mma16816<T>(c[t][0], qa[t][k], b[0], b[1]);
@@ -219,34 +236,35 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
             const uint32_t ok = sok[warp][stage];
             const int j_lo = keys.at(u0), j_hi = keys.at(u0 + kKeys - 1);
             const bool all = ok == 0xffffu && j_hi <= pos_lo && (j_hi < p.n_sink || (long long)pos_hi - j_lo <= (long long)p.w * p.stride);
-            uint32_t pa[NT][4];
-            bool up = false;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
+            if (!all) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = c[t][x][e] * p.scale_log2;
-                        if (!all) {
-                            const int col = 8 * x + 2 * t4 + (e & 1);
-                            const bool see = ((ok >> col) & 1u) && attends(p, pos[t][e >> 1], keys.at(u0 + col));
-                            v = see ? v : -INFINITY;
-                        }
-                        c[t][x][e] = v;
+                    for (int e = 0; e < 2; ++e) {
+                        const int col = 8 * x + 2 * t4 + e, j = keys.at(u0 + col);
+                        const bool here = (ok >> col) & 1u;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int r2 = 0; r2 < 2; ++r2)
+                                if (!(here && attends(p, pos[t][r2], j))) c[t][x][2 * r2 + e] = -INFINITY;
                     }
+            }
+            float best[NT][2];
+            bool up = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float mx = fmaxf(fmaxf(c[t][0][2 * e], c[t][0][2 * e + 1]), fmaxf(c[t][1][2 * e], c[t][1][2 * e + 1]));
-                    up |= mx > m[t][e] + kSlack;
+                    best[t][e] = fmaxf(max3(c[t][0][2 * e], c[t][0][2 * e + 1], c[t][1][2 * e]), c[t][1][2 * e + 1]) * scale;
+                    up |= best[t][e] > m[t][e] + kSlack;
                 }
-            }
             if (__any_sync(0xffffffffu, up)) {   // raise the maxima, scale what was summed so far
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(fmaxf(c[t][0][2 * e], c[t][0][2 * e + 1]), fmaxf(c[t][1][2 * e], c[t][1][2 * e + 1]));
+                        float mx = best[t][e];
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                         const float mn = fmaxf(m[t][e], mx);
@@ -260,13 +278,14 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
                         }
                     }
             }
+            uint32_t pa[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float mb = m[t][e] == -INFINITY ? 0.f : m[t][e];
-                    const float p0 = ex2(c[t][0][2 * e] - mb), p1 = ex2(c[t][0][2 * e + 1] - mb);
-                    const float p2 = ex2(c[t][1][2 * e] - mb), p3 = ex2(c[t][1][2 * e + 1] - mb);
+                    const float p0 = ex2(fmaf(c[t][0][2 * e], scale, -mb)), p1 = ex2(fmaf(c[t][0][2 * e + 1], scale, -mb));
+                    const float p2 = ex2(fmaf(c[t][1][2 * e], scale, -mb)), p3 = ex2(fmaf(c[t][1][2 * e + 1], scale, -mb));
                     l[t][e] += (p0 + p1) + (p2 + p3);
                     pa[t][e] = pack2<T>(p0, p1);
                     pa[t][e + 2] = pack2<T>(p2, p3);
@@ -274,8 +293,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
 #pragma unroll
             for (int d = 0; d < kSteps; ++d) {
                 uint32_t b[4];
-                const int row = (lane & 7) + (((lane >> 3) & 1) << 3), piece = 2 * d + (lane >> 4);
-                ldsm4t(vt + row * (HD * 2) + ((piece ^ (row & 7)) << 4), b);
+                ldsm4t(vt ^ (d << 5), b);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     mma16816<T>(o[t][2 * d], pa[t], b[0], b[1]);
@@ -303,11 +321,22 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
                 for (int d = 0; d < HD / 8; ++d)
                     *reinterpret_cast<float2 *>(mine_o + row * kPad + 8 * d + 2 * t4) = make_float2(o[t][d][2 * e], o[t][d][2 * e + 1]);
             }
+        if (p.fold) pdl_wait();                  // the prefix's parts are there
         __syncthreads();
         if (threadIdx.x < kRows) {
             const int row = threadIdx.x;
+            const int a = (row0 + row) / p.group, hh = kvh * p.group + row0 + row - a * p.group;
+            const long long th = (long long)(q.row0 + a) * p.h + hh;
             float M = -INFINITY, L = 0.f;
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w][row].x);
+            if (p.fold && row < nrows) {
+                const float2 *ml = p.pml + th * p.nparts + 1;
+                for (int s = 0; s < p.npre; ++s) M = fmaxf(M, GP(p.bnd, ml + s)->x);
+                for (int s = 0; s < p.npre; ++s) {
+                    const float2 v = *GP(p.bnd, ml + s);
+                    if (v.x != -INFINITY) L = fmaf(v.y, ex2(v.x - M), L);
+                }
+            }
             for (int w = 0; w < kWarps; ++w) {
                 const float f = sml[w][row].x == -INFINITY ? 0.f : ex2(sml[w][row].x - M);
                 swt[w][row] = f;
@@ -315,9 +344,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
             }
             stot[row] = make_float2(M, L);
             if (row < nrows) {
-                const int a = (row0 + row) / p.group, hh = kvh * p.group + row0 + row - a * p.group;
-                const long long th = (long long)(q.row0 + a) * p.h + hh;
-                if (p.nparts > 1) *GP(p.bnd, p.pml + th * p.nparts + split) = make_float2(M, L);
+                if (p.nparts > 1 && !p.fold) *GP(p.bnd, p.pml + th * p.nparts + split) = make_float2(M, L);
                 else if (p.lse) *GP(p.bnd, p.lse + th) = lse_of(M, L);
             }
         }
@@ -336,7 +363,23 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
             }
             const int a = (row0 + row) / p.group, hh = kvh * p.group + row0 + row - a * p.group;
             const long long tok = q.row0 + a, th = tok * p.h + hh;
-            if (p.nparts > 1) {
+            if (p.fold) {
+                const float M = stot[row].x;
+                const float2 *ml = p.pml + th * p.nparts + 1;
+                const float *po = p.po + (th * p.nparts + 1) * HD + c4;
+#pragma unroll 4
+                for (int s = 0; s < p.npre; ++s) {
+                    const float ms = GP(p.bnd, ml + s)->x;
+                    if (ms == -INFINITY) continue;               // an empty part's values are not written
+                    const float f = ex2(ms - M);
+                    const float4 v = *reinterpret_cast<const float4 *>(GPN(p.bnd, po + (long long)s * HD, 16));
+                    y.x = fmaf(v.x, f, y.x);
+                    y.y = fmaf(v.y, f, y.y);
+                    y.z = fmaf(v.z, f, y.z);
+                    y.w = fmaf(v.w, f, y.w);
+                }
+            }
+            if (p.nparts > 1 && !p.fold) {
                 *reinterpret_cast<float4 *>(GPN(p.bnd, p.po + (th * p.nparts + split) * HD + c4, 16)) = y;
             } else {
                 const float inv = stot[row].y > 0.f ? 1.f / stot[row].y : 0.f;
@@ -350,16 +393,17 @@ __global__ void __launch_bounds__(kThreads) k_decode_rows(const __grid_constant_
     if (p.npre > 0) pdl_wait();
 }
 
-template <typename T, int HD, int NT>
+template <typename T, int HD, int NT, int kWarps>
 cudaError_t launch_nt(const DecodeArgs &a, int tiles, cudaStream_t st) {
-    const void *fn = reinterpret_cast<const void *>(&k_decode_rows<T, HD, NT>);
-    const cudaError_t e = ensure_smem(fn, Shape<HD>::kSmem);
+    using S = Shape<HD, NT, kWarps>;
+    const auto fn = &k_decode_rows<T, HD, NT, kWarps>;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), S::kSmem);
     if (e != cudaSuccess) return e;
     const int most = 65535 / a.hk;
     const dim3 grid((unsigned)a.nsplit, (unsigned)(a.hk * (tiles < most ? tiles : most)), (unsigned)a.batch);
     // behind the prefix kernel it may start at once: it reads nothing of it
-    if (a.npre > 0) return launch_dependent(&k_decode_rows<T, HD, NT>, grid, kThreads, Shape<HD>::kSmem, st, a);
-    k_decode_rows<T, HD, NT><<<grid, kThreads, Shape<HD>::kSmem, st>>>(a);
+    if (a.npre > 0) return launch_dependent(fn, grid, S::kThreads, S::kSmem, st, a);
+    fn<<<grid, S::kThreads, S::kSmem, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -368,8 +412,12 @@ cudaError_t launch_hd(const DecodeArgs &a, int max_q, cudaStream_t st) {
     // one 16-row tile where the rows fit it, else tiles of 32
     const long long rows = a.stride == 1 ? (long long)max_q * a.group : a.group;
     const long long each = a.stride == 1 ? 1 : max_q;
-    if (rows <= 16) return launch_nt<T, HD, 1>(a, (int)each, st);
-    return launch_nt<T, HD, 2>(a, (int)((rows + 31) / 32 * each < 65535 ? (rows + 31) / 32 * each : 65535), st);
+    if (rows <= 16) {
+        if (a.row_warps == 2) return launch_nt<T, HD, 1, 2>(a, (int)each, st);
+        if (a.row_warps == 3) return launch_nt<T, HD, 1, 3>(a, (int)each, st);
+        return launch_nt<T, HD, 1, 4>(a, (int)each, st);
+    }
+    return launch_nt<T, HD, 2, 4>(a, (int)((rows + 31) / 32 * each < 65535 ? (rows + 31) / 32 * each : 65535), st);
 }
 
 }  // namespace

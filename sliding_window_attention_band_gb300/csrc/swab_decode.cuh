@@ -85,30 +85,37 @@ __device__ __forceinline__ bool attends(const DecodeArgs &p, int i, int j) {
     return j <= i && (j < p.n_sink || (long long)i - j <= (long long)p.w * p.stride);
 }
 
-// Line (row of head_dim values) of head kvh at row `off` of block `id`, or -1:
-// an absent column, or an id outside the cache (recorded).
-__device__ __forceinline__ long long block_line(const DecodeArgs &p, int id, int off, int kvh) {
+// Line (row of head_dim values) of head kvh at row `off` of block `id`, or
+// kNoLine: an absent column, or an id outside the cache (recorded).  The lines
+// of a cache number less than 2^32 - 1 (checked by the caller).
+constexpr uint32_t kNoLine = 0xffffffffu;
+__device__ __forceinline__ uint32_t block_line(const DecodeArgs &p, int id, int off, int kvh) {
     if ((unsigned)id >= (unsigned)p.n_blocks) {
         if (id != -1) atomicOr(p.err, kErrInvalid);
-        return -1;
+        return kNoLine;
     }
-    return (((long long)id * p.hk + kvh) << p.page_log2) + off;
+    return (((uint32_t)id * (uint32_t)p.hk + (uint32_t)kvh) << p.page_log2) + (uint32_t)off;
 }
-__device__ __forceinline__ long long key_line(const DecodeArgs &p, const Request &q, int j, int kvh) {
-    [[maybe_unused]] constexpr unsigned kSwabFile = kDecodeFile;
+// Column of position j, or -1 when it has none (a context longer than its
+// table: recorded) or its block has been recycled.
+__device__ __forceinline__ int key_column(const DecodeArgs &p, const Request &q, int j) {
     const int lb = j >> p.page_log2;
     int col = lb;
     if (lb >= p.cols) {
-        if (!p.ring) {                 // a context longer than its table
+        if (!p.ring) {
             atomicOr(p.err, kErrInvalid);
             return -1;
         }
         col = p.pinned + (lb - p.pinned) % (p.cols - p.pinned);
     }
-    if (lb >= p.pinned && j < q.ring_lo) return -1;
-    return block_line(p, *GP(p.bnd, q.trow + col), j & ((1 << p.page_log2) - 1), kvh);
+    return lb >= p.pinned && j < q.ring_lo ? -1 : col;
 }
-__device__ __forceinline__ long long prefix_line(const DecodeArgs &p, int j, int kvh) {
+__device__ __forceinline__ uint32_t key_line(const DecodeArgs &p, const Request &q, int j, int kvh) {
+    [[maybe_unused]] constexpr unsigned kSwabFile = kDecodeFile;
+    const int col = key_column(p, q, j);
+    return col < 0 ? kNoLine : block_line(p, *GP(p.bnd, q.trow + col), j & ((1 << p.page_log2) - 1), kvh);
+}
+__device__ __forceinline__ uint32_t prefix_line(const DecodeArgs &p, int j, int kvh) {
     [[maybe_unused]] constexpr unsigned kSwabFile = kDecodeFile;
     return block_line(p, *GP(p.bnd, p.ptable + (j >> p.page_log2)), j & ((1 << p.page_log2) - 1), kvh);
 }

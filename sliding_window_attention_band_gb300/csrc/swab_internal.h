@@ -346,7 +346,11 @@ struct DecodeArgs {
     int page_log2, n_blocks, cols, ring, pinned;
     int nsplit, chunk;         // pieces of the key list of a query and their length
     int nparts;                // parts joined for a query (1: written directly)
-    int npre, pre_chunks, pre_tokens;   // the prefix kernel: pieces, 128-key chunks of one, tokens of a tile
+    // the prefix kernel: parts it makes of a query, pieces of the prefix, 128-key
+    // chunks of a piece, tokens of a row tile
+    int npre, pre_pieces, pre_chunks, pre_tokens;
+    int row_warps;             // warps that share a piece in the rows kernel: 2 or 4
+    int fold;                  // the rows kernel joins the prefix's parts itself
     float scale_log2;
     unsigned *err;
 #if SWAB_BOUNDS_CHECK

@@ -155,7 +155,9 @@ constexpr long long kSms = 152;      // of a GB300
 struct DecodePlan {
     bool rows;                       // tensor-core kernels (fp16 / bf16, head_dim 64 or 128)
     int nsplit, chunk, nparts;
-    int npre, pre_chunks, pre_tokens;
+    int npre, pre_pieces, pre_chunks, pre_tokens;
+    int row_warps;
+    bool fold;                       // no join launch: the rows kernel adds the prefix's parts
     size_t parts_bytes, bytes;       // workspace: the parts, then their (max, sum)
 };
 
@@ -177,6 +179,7 @@ swab_status check_decode(const swab_decode_desc *d) {
     }
     if (s != SWAB_OK) return s;
     if (d->head_dim % vec != 0 || d->head_dim > 256 || d->dilation > SWAB_MAX_DILATION) return SWAB_ERR_UNSUPPORTED;
+    if ((long long)c->n_blocks * c->page * d->hk >= 0xffffffffll) return SWAB_ERR_UNSUPPORTED;
     if (d->h / d->hk > 128 || d->h > 65535 || (long long)d->tokens * d->h > 0x7fffffffll) return SWAB_ERR_UNSUPPORTED;
     for (const int64_t rs : {d->q_row_stride, d->out_row_stride}) {
         if (rs % vec != 0) return SWAB_ERR_MISALIGNED;
@@ -200,8 +203,13 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
     // where there are fewer blocks than the GPU holds
     long long keys = most_keys(d), blocks = batch, hold, least;
     if (p.rows) {
-        blocks *= d->hk * (d->dilation == 0 ? (d->max_q * group + 31) / 32 : d->max_q * ((group + 31) / 32));
-        hold = 2 * kSms;
+        const long long rows = d->dilation == 0 ? d->max_q * group : group;
+        blocks *= d->hk * (rows <= 16 ? 1 : (rows + 31) / 32) * (d->dilation == 0 ? 1 : d->max_q);
+        // An SM holds 12 warps (8 of the 32-row tiles).  Long lists want all of
+        // them in one go: four warps a block where the blocks fit at once, else
+        // three or two
+        p.row_warps = rows > 16 || blocks <= 3 * kSms ? 4 : blocks <= 4 * kSms ? 3 : blocks <= 6 * kSms ? 2 : keys <= 256 ? 2 : 4;
+        hold = (rows <= 16 ? 3 : 2) * kSms;
         least = 256;
     } else {
         keys += d->prefix_len;
@@ -214,12 +222,16 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
     p.nsplit = (int)((keys + chunk - 1) / chunk);
     p.chunk = (int)std::min<long long>(chunk, 0x7fffffff);
     if (p.rows && d->prefix_len > 0) {
+        // one block an SM: as many pieces of the prefix as fill the SMs once
         p.pre_tokens = (int)(128 / group);
-        const long long tiles = (d->tokens + p.pre_tokens - 1) / p.pre_tokens * d->hk;
+        const bool pair = d->tokens > p.pre_tokens;
+        const long long per = p.pre_tokens * (pair ? 2 : 1), tiles = (d->tokens + per - 1) / per * d->hk;
         const long long chunks = ((long long)d->prefix_len + 127) / 128;
         const long long pieces = std::min(std::max<long long>(1, kSms / tiles), (chunks + 1) / 2);
         p.pre_chunks = (int)((chunks + pieces - 1) / pieces);
-        p.npre = (int)((chunks + p.pre_chunks - 1) / p.pre_chunks);
+        p.pre_pieces = (int)((chunks + p.pre_chunks - 1) / p.pre_chunks);
+        p.npre = p.pre_pieces * (pair ? 1 : 2);
+        p.fold = p.nsplit == 1 && p.npre <= 16;
     }
     p.nparts = p.nsplit + p.npre;
     if (p.nparts > 1) {
@@ -429,7 +441,10 @@ SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, cons
     a.chunk = plan.chunk;
     a.nparts = plan.nparts;
     a.npre = plan.npre;
+    a.pre_pieces = plan.pre_pieces;
     a.pre_chunks = plan.pre_chunks;
+    a.fold = plan.fold;
+    a.row_warps = plan.row_warps;
     a.pre_tokens = plan.pre_tokens;
     a.scale_log2 = scale * 1.4426950408889634f;
     const DType dt = static_cast<DType>(desc->dtype);
@@ -453,7 +468,7 @@ SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, cons
     }
     if (e == cudaSuccess)
         e = plan.rows ? launch_decode_rows(dt, a, desc->max_q, as_stream(stream)) : launch_decode_general(dt, a, as_stream(stream));
-    if (e == cudaSuccess && a.nparts > 1) e = launch_decode_join(dt, a, as_stream(stream));
+    if (e == cudaSuccess && a.nparts > 1 && !a.fold) e = launch_decode_join(dt, a, as_stream(stream));
     return status_of(e);
 }
 

@@ -58,6 +58,7 @@ class CacheDesc:
         self.batch, self.page, self.n_blocks, self.cols = int(batch), int(page), int(n_blocks), int(cols)
         self.ring, self.pinned = bool(ring), int(pinned)
         self.c = _CacheDesc(self.batch, self.page, self.n_blocks, self.cols, int(self.ring), self.pinned)
+        self._ref = ctypes.byref(self.c)
 
 
 class RotaryDesc:
@@ -71,15 +72,22 @@ class RotaryDesc:
         self.b, self.n, self.h, self.hk = int(b), int(n), int(h), int(hk)
         self.head_dim, self.rot_dim, self.interleaved = int(head_dim), int(rot_dim), bool(interleaved)
         self.scale, self.pos0, self.dtype = float(scale), int(pos0), dtype
-        self._structs = {}      # the C struct by the strides of a call
+        self.tokens = self.b * self.n
+        # the shapes a tensor of h or hk heads may have: tokens as [b, n] or flat
+        self._q = ((self.b, self.n, self.h, self.head_dim), (self.tokens, self.h, self.head_dim))
+        self._k = ((self.b, self.n, self.hk, self.head_dim), (self.tokens, self.hk, self.head_dim))
+        self._structs = {}      # the C struct by the strides of a call's tensors
 
     def struct(self, q=None, k=None, qo=None, ko=None, v=None):
+        """The C struct for tensors of these strides, each a tensor's own
+        stride() (3 or 4 numbers), or None."""
         key = (q, k, qo, ko, v)
         c = self._structs.get(key)
         if c is None:
-            zero = (0, 0, 0)
+            names = (("Q", q, self.h), ("K", k, self.hk), ("Qo", qo, self.h), ("Ko", ko, self.hk), ("V", v, self.hk))
+            strides = [_S3(*(_row_strides(n, s, self, heads) if s else (0, 0, 0))) for n, s, heads in names]
             c = _RotaryDesc(self.b, self.n, self.h, self.hk, self.head_dim, self.rot_dim, int(self.interleaved),
-                            _b._DTYPES[self.dtype], self.scale, self.pos0, *(_S3(*(s or zero)) for s in key))
+                            _b._DTYPES[self.dtype], self.scale, self.pos0, *strides)
             if len(self._structs) < 64:
                 self._structs[key] = c
         return ctypes.byref(c)
@@ -105,77 +113,102 @@ class DecodeDesc:
         self.c = _DecodeDesc(cache.c, self.tokens, self.h, self.hk, self.head_dim, self.w, self.dilation, self.n_sink,
                              self.max_q, self.max_len, self.prefix_len, _b._DTYPES[dtype], self.q_row_stride,
                              self.out_row_stride)
-        self.workspace_bytes = None
+        self._shape = (self.tokens, self.h, self.head_dim)
+        self._kv = (cache.n_blocks, self.hk, cache.page, self.head_dim)
+        self._batch, self._table = cache.batch, cache.batch * cache.cols
+        self._ref = ctypes.byref(self.c)
+        self._workspace = None
 
 
 # ---------------------------------------------------------------------------
-# marshalling helpers
+# marshalling helpers.  A call of a few microseconds must not wait for its
+# checks: each entry point asks all its tensors in one expression, and only
+# when that fails looks again, one by one, for the one to name in the error.
 # ---------------------------------------------------------------------------
-def _run(name, like, stream, *args):
-    """Call `name` with the stream appended, on the device of the tensor `like`."""
-    dev = like.device
+_I32, _F32, _I64 = torch.int32, torch.float32, torch.int64
+_fns = {}
+
+
+def _run(name, dev, stream, *args):
+    """Call `name` with the stream appended, on CUDA device number dev."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_b.load(), name)
     if stream is None:
-        s = torch.cuda.current_stream(dev).cuda_stream
+        s = torch._C._cuda_getCurrentRawStream(dev)
     else:
         s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    fn = getattr(_b.load(), name)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev:
         rc = fn(*args, s)
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, s)
-    if rc != _b.SWAB_OK:
+    if rc:
         raise _b.SwabError(name, rc)
 
 
-def _on(name, t, like):
+def _unnamed():
+    return ValueError("the call's tensors changed while they were checked")
+
+
+def _place(name, t, dev):
+    """The error for a tensor that is not on CUDA device dev (-1: on none)."""
     if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, the call's other tensors are on {like.device}")
+        return ValueError(f"{name}: expected a CUDA tensor")
+    return ValueError(f"{name}: on {t.device}, the call's other tensors are on cuda:{dev}")
 
 
-def _ints(name, t, n, like):
-    """Pointer of a contiguous int32 tensor of n elements (None: None)."""
-    if t is None:
-        return None
-    _on(name, t, like)
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+def _device(name, t):
+    dev = t.get_device()
+    if dev < 0:
+        raise _place(name, t, dev)
+    return dev
+
+
+def _ints(name, t, n, dev):
+    """Pointer of a contiguous int32 tensor of n elements."""
+    if t.get_device() != dev:
+        raise _place(name, t, dev)
+    if t.dtype is not _I32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous int32 tensor of {n} elements, got {tuple(t.shape)} {t.dtype}")
     return t.data_ptr()
 
 
-def _turns(d, t, like):
+def _turns(d, t, dev):
     if d.rot_dim == 0:
         return None
     if t is None:
         raise ValueError("turns: needed when rot_dim > 0")
-    _on("turns", t, like)
-    if t.dtype != torch.int64 or t.numel() != d.rot_dim // 2 or not t.is_contiguous():
+    if t.get_device() != dev:
+        raise _place("turns", t, dev)
+    if t.dtype is not _I64 or t.numel() * 2 != d.rot_dim or not t.is_contiguous():
         raise ValueError(f"turns: expected {d.rot_dim // 2} contiguous int64 values (rotary_frequencies), got "
                          f"{tuple(t.shape)} {t.dtype}")
     return t.data_ptr()
 
 
-def _rows(name, t, d, heads, like):
-    """(pointer, element strides over (b, n, head)) of a [b, n, heads, hd] or, the
-    tokens flat, [b * n, heads, hd] tensor with adjacent channels."""
-    _on(name, t, like)
-    if t.dtype != d.dtype:
+def _rows(name, t, d, shapes, dev):
+    """Pointer of a tensor of heads; its strides go through d.struct()."""
+    if t.get_device() != dev:
+        raise _place(name, t, dev)
+    if t.dtype is not d.dtype:
         raise ValueError(f"{name}: expected dtype {d.dtype}, got {t.dtype}")
-    shape, st = t.shape, t.stride()
-    if len(shape) == 3 and tuple(shape) == (d.b * d.n, heads, d.head_dim):
-        sizes, strides = (d.b, d.n, heads), (d.n * st[0], st[0], st[1])
-    elif len(shape) == 4 and tuple(shape) == (d.b, d.n, heads, d.head_dim):
-        sizes, strides = (d.b, d.n, heads), st[:3]
-    else:
-        raise ValueError(f"{name}: expected [{d.b}, {d.n}, {heads}, {d.head_dim}] (or the tokens flat), got {tuple(shape)}")
+    shape = t.shape
+    if shape != shapes[0] and shape != shapes[1]:
+        raise ValueError(f"{name}: expected {list(shapes[0])} (or the tokens flat), got {list(shape)}")
+    return t.data_ptr()
+
+
+def _row_strides(name, st, d, heads):
+    """Element strides over (b, n, head) from those of a [b, n, heads, hd] or,
+    the tokens flat, [b * n, heads, hd] tensor with adjacent channels."""
+    sizes, strides = (d.b, d.n, heads), st[:3] if len(st) == 4 else (d.n * st[0], st[0], st[1])
     if st[-1] != 1 and d.head_dim > 1:
         raise ValueError(f"{name}: the channels must be adjacent")
     strides = tuple(0 if k == 1 else s for k, s in zip(sizes, strides))   # a single element's stride says nothing
     if not any(strides) and max(sizes) > 1:
         raise ValueError(f"{name}: the same row for every token and head")
-    return t.data_ptr(), strides
+    return strides
 
 
 # ---------------------------------------------------------------------------
@@ -202,15 +235,15 @@ def rotary_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, origin
 
 
 def _rotary(fn, d, turns, Q, Qo, K, Ko, pos, stream):
-    q, sq = _rows("Q", Q, d, d.h, None)
-    qo, sqo = _rows("Qo", Qo, d, d.h, Q)
+    dev = _device("Q", Q)
+    q, qo = _rows("Q", Q, d, d._q, dev), _rows("Qo", Qo, d, d._q, dev)
     k = ko = sk = sko = None
     if d.hk > 0:
         if K is None or Ko is None:
             raise ValueError("K, Ko: needed when hk > 0")
-        k, sk = _rows("K", K, d, d.hk, Q)
-        ko, sko = _rows("Ko", Ko, d, d.hk, Q)
-    _run(fn, Q, stream, d.struct(sq, sk, sqo, sko), _turns(d, turns, Q), _ints("pos", pos, d.b * d.n, Q), q, k, qo, ko)
+        k, ko, sk, sko = _rows("K", K, d, d._k, dev), _rows("Ko", Ko, d, d._k, dev), K.stride(), Ko.stride()
+    _run(fn, dev, stream, d.struct(Q.stride(), sk, Qo.stride(), sko), _turns(d, turns, dev),
+         None if pos is None else _ints("pos", pos, d.tokens, dev), q, k, qo, ko)
 
 
 def rotary(desc: RotaryDesc, turns, Q, Qo, K=None, Ko=None, pos=None, stream=None):
@@ -233,24 +266,33 @@ def cache_slots(cache: CacheDesc, lens, n_new, table, free_list, used, lens_out,
     past the last token: -1 and 0).  lens_out [batch] (may be lens) and
     used_out [2] (may be used): lengths and blocks taken after the step, and
     how many blocks were missing (such requests get slots of -1)."""
-    B = cache.batch
-    n_free = free_list.numel()
-    tokens = slots.numel()
-    args = [_ints("lens", lens, B, None), _ints("n_new", n_new, B, lens), _ints("table", table, B * cache.cols, lens),
-            _ints("free_list", free_list, n_free, lens)]
-    _on("used", used, lens)
-    if used.dtype != torch.int32 or used.numel() < 1 or not used.is_contiguous():
-        raise ValueError("used: expected a contiguous int32 tensor")
-    outs = [_ints("lens_out", lens_out, B, lens), _ints("used_out", used_out, 2, lens), _ints("q_start", q_start, B + 1, lens),
-            _ints("slots", slots, tokens, lens), _ints("pos", pos, tokens, lens)]
-    _run("cache_slots", lens, stream, ctypes.byref(cache.c), tokens, int(pos0), *args, n_free, used.data_ptr(), *outs)
+    B, n_free, tokens, dev = cache.batch, free_list.numel(), slots.numel(), lens.get_device()
+    if not (dev >= 0 and lens.dtype is _I32 and n_new.dtype is _I32 and table.dtype is _I32 and free_list.dtype is _I32
+            and used.dtype is _I32 and lens_out.dtype is _I32 and used_out.dtype is _I32 and q_start.dtype is _I32
+            and slots.dtype is _I32 and pos.dtype is _I32 and lens.numel() == B and n_new.numel() == B
+            and table.numel() == B * cache.cols and used.numel() >= 1 and lens_out.numel() == B and used_out.numel() == 2
+            and q_start.numel() == B + 1 and pos.numel() == tokens and lens.is_contiguous() and n_new.is_contiguous()
+            and table.is_contiguous() and free_list.is_contiguous() and used.is_contiguous() and lens_out.is_contiguous()
+            and used_out.is_contiguous() and q_start.is_contiguous() and slots.is_contiguous() and pos.is_contiguous()
+            and n_new.get_device() == dev and table.get_device() == dev and free_list.get_device() == dev
+            and used.get_device() == dev and lens_out.get_device() == dev and used_out.get_device() == dev
+            and q_start.get_device() == dev and slots.get_device() == dev and pos.get_device() == dev):
+        _device("lens", lens)
+        for name, t, n in (("lens", lens, B), ("n_new", n_new, B), ("table", table, B * cache.cols),
+                           ("free_list", free_list, n_free), ("used", used, max(1, used.numel())), ("lens_out", lens_out, B),
+                           ("used_out", used_out, 2), ("q_start", q_start, B + 1), ("slots", slots, tokens), ("pos", pos, tokens)):
+            _ints(name, t, n, dev)
+        raise _unnamed()
+    _run("cache_slots", dev, stream, cache._ref, tokens, pos0, lens.data_ptr(), n_new.data_ptr(), table.data_ptr(),
+         free_list.data_ptr(), n_free, used.data_ptr(), lens_out.data_ptr(), used_out.data_ptr(), q_start.data_ptr(),
+         slots.data_ptr(), pos.data_ptr())
 
 
-def _cache(name, t, c, d, like):
-    _on(name, t, like)
-    if t.dtype != d.dtype or tuple(t.shape) != (c.n_blocks, d.hk, c.page, d.head_dim) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {d.dtype} tensor [{c.n_blocks}, {d.hk}, {c.page}, {d.head_dim}], got "
-                         f"{tuple(t.shape)} {t.dtype}")
+def _cache(name, t, shape, dtype, dev):
+    if t.get_device() != dev:
+        raise _place(name, t, dev)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)}, got {list(t.shape)} {t.dtype}")
     return t.data_ptr()
 
 
@@ -258,35 +300,46 @@ def rotary_append(desc: RotaryDesc, cache: CacheDesc, turns, Q, K, V, pos, slots
     """rotary on Q -> Qo, and K (rotated) and V into the rows slots[t] of the
     cache tensors Kc, Vc [n_blocks, hk, page, hd]; slot -1 is not written.  Q
     and Qo may both be None."""
-    q = qo = sq = sqo = None
     if (Q is None) != (Qo is None):
         raise ValueError("Q, Qo: both or neither")
+    d, dev, dt, n = desc, K.get_device(), desc.dtype, desc.tokens
+    kv, ks = (cache.n_blocks, d.hk, cache.page, d.head_dim), d._k
+    if not (dev >= 0 and K.dtype is dt and V.dtype is dt and Kc.dtype is dt and Vc.dtype is dt and slots.dtype is _I32
+            and (K.shape == ks[1] or K.shape == ks[0]) and (V.shape == ks[1] or V.shape == ks[0]) and Kc.shape == kv
+            and Vc.shape == kv and slots.numel() == n and Kc.is_contiguous() and Vc.is_contiguous() and slots.is_contiguous()
+            and V.get_device() == dev and Kc.get_device() == dev and Vc.get_device() == dev and slots.get_device() == dev):
+        if slots is None:
+            raise ValueError("slots: needed")
+        _device("K", K)
+        _rows("K", K, d, ks, dev)
+        _rows("V", V, d, ks, dev)
+        _ints("slots", slots, n, dev)
+        _cache("Kc", Kc, kv, dt, dev)
+        _cache("Vc", Vc, kv, dt, dev)
+        raise _unnamed()
+    q = qo = sq = sqo = None
     if Q is not None:
-        q, sq = _rows("Q", Q, desc, desc.h, K)
-        qo, sqo = _rows("Qo", Qo, desc, desc.h, K)
-    k, sk = _rows("K", K, desc, desc.hk, None)
-    v, sv = _rows("V", V, desc, desc.hk, K)
-    n = desc.b * desc.n
-    if slots is None:
-        raise ValueError("slots: needed")
-    _run("rotary_append", K, stream, desc.struct(sq, sk, sqo, None, sv), ctypes.byref(cache.c), _turns(desc, turns, K),
-         _ints("pos", pos, n, K), _ints("slots", slots, n, K), q, k, v, qo, _cache("Kc", Kc, cache, desc, K),
-         _cache("Vc", Vc, cache, desc, K))
+        q, qo, sq, sqo = _rows("Q", Q, d, d._q, dev), _rows("Qo", Qo, d, d._q, dev), Q.stride(), Qo.stride()
+    _run("rotary_append", dev, stream, d.struct(sq, K.stride(), sqo, None, V.stride()), cache._ref, _turns(d, turns, dev),
+         None if pos is None else _ints("pos", pos, n, dev), slots.data_ptr(), q, K.data_ptr(), V.data_ptr(), qo, Kc.data_ptr(),
+         Vc.data_ptr())
 
 
 def band_decode_workspace(desc: DecodeDesc) -> int:
     """Bytes of device workspace band_decode needs (0: none)."""
-    if desc.workspace_bytes is None:
-        desc.workspace_bytes = int(_b.load().band_decode_workspace(ctypes.byref(desc.c)))
-    return desc.workspace_bytes
+    if desc._workspace is None:
+        desc._workspace = int(_b.load().band_decode_workspace(desc._ref))
+    return desc._workspace
 
 
-def _heads(name, t, d, row_stride, like):
-    _on(name, t, like)
-    st = row_stride or d.h * d.head_dim
-    if t.dtype != d.dtype or tuple(t.shape) != (d.tokens, d.h, d.head_dim):
-        raise ValueError(f"{name}: expected [{d.tokens}, {d.h}, {d.head_dim}] {d.dtype}, got {tuple(t.shape)} {t.dtype}")
-    s = t.stride()
+def _heads(name, t, d, row_stride, dev):
+    if t.get_device() != dev:
+        raise _place(name, t, dev)
+    if t.dtype is not d.dtype or t.shape != d._shape:
+        raise ValueError(f"{name}: expected {list(d._shape)} {d.dtype}, got {list(t.shape)} {t.dtype}")
+    if row_stride == 0 and t.is_contiguous():
+        return t.data_ptr()
+    s, st = t.stride(), row_stride or d.h * d.head_dim
     if (s[0] != st and d.tokens > 1) or (s[1] != d.head_dim and d.h > 1) or (s[2] != 1 and d.head_dim > 1):
         raise ValueError(f"{name}: expected strides ({st}, {d.head_dim}, 1), got {s}")
     return t.data_ptr()
@@ -298,26 +351,47 @@ def band_decode(desc: DecodeDesc, scale, Q, Kc, Vc, table, lens, q_start, O, lse
     (and lse [tokens, h] fp32) of queries Q whose rows q_start[r]:q_start[r + 1]
     are the last positions of request r's lens[r].  With ``prefix_len`` the
     shared prefix lies in the blocks prefix_table of the same cache."""
-    c = desc.cache
-    args = [_heads("Q", Q, desc, desc.q_row_stride, None), _cache("Kc", Kc, c, desc, Q), _cache("Vc", Vc, c, desc, Q),
-            _ints("table", table, c.batch * c.cols, Q), _ints("lens", lens, c.batch, Q),
-            _ints("q_start", q_start, c.batch + 1, Q)]
-    pt = None
-    if desc.prefix_len > 0:
+    d, dev, dt, kv = desc, Q.get_device(), desc.dtype, desc._kv
+    need = d._workspace
+    if need is None:
+        need = band_decode_workspace(d)
+    if not (dev >= 0 and Q.dtype is dt and O.dtype is dt and Kc.dtype is dt and Vc.dtype is dt and table.dtype is _I32
+            and lens.dtype is _I32 and q_start.dtype is _I32 and Q.shape == d._shape and O.shape == d._shape and Kc.shape == kv
+            and Vc.shape == kv and table.numel() == d._table and lens.numel() == d._batch and q_start.numel() == d._batch + 1
+            and Kc.is_contiguous() and Vc.is_contiguous() and table.is_contiguous() and lens.is_contiguous()
+            and q_start.is_contiguous() and O.get_device() == dev and Kc.get_device() == dev and Vc.get_device() == dev
+            and table.get_device() == dev and lens.get_device() == dev and q_start.get_device() == dev):
+        _device("Q", Q)
+        _heads("Q", Q, d, d.q_row_stride, dev)
+        _heads("O", O, d, d.out_row_stride, dev)
+        _cache("Kc", Kc, kv, dt, dev)
+        _cache("Vc", Vc, kv, dt, dev)
+        _ints("table", table, d._table, dev)
+        _ints("lens", lens, d._batch, dev)
+        _ints("q_start", q_start, d._batch + 1, dev)
+        raise _unnamed()
+    if d.q_row_stride or not Q.is_contiguous():
+        _heads("Q", Q, d, d.q_row_stride, dev)
+    if d.out_row_stride or not O.is_contiguous():
+        _heads("O", O, d, d.out_row_stride, dev)
+    pt = lp = ws = None
+    if d.prefix_len > 0:
         if prefix_table is None:
             raise ValueError("prefix_table: needed when prefix_len > 0")
-        pt = _ints("prefix_table", prefix_table, -(-desc.prefix_len // c.page), Q)
-    o = _heads("O", O, desc, desc.out_row_stride, Q)
+        pt = _ints("prefix_table", prefix_table, -(-d.prefix_len // d.cache.page), dev)
     if lse is not None:
-        _on("lse", lse, Q)
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (desc.tokens, desc.h) or not lse.is_contiguous():
-            raise ValueError(f"lse: expected a contiguous float32 tensor [{desc.tokens}, {desc.h}]")
-    need = band_decode_workspace(desc)
+        if lse.get_device() != dev:
+            raise _place("lse", lse, dev)
+        if lse.dtype is not _F32 or lse.shape != d._shape[:2] or not lse.is_contiguous():
+            raise ValueError(f"lse: expected a contiguous float32 tensor [{d.tokens}, {d.h}]")
+        lp = lse.data_ptr()
     if need:
         if workspace is None:
             raise ValueError("workspace: needed (band_decode_workspace)")
-        _on("workspace", workspace, Q)
+        if workspace.get_device() != dev:
+            raise _place("workspace", workspace, dev)
         if workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
             raise ValueError(f"workspace: expected at least {need} contiguous bytes")
-    _run("band_decode", Q, stream, ctypes.byref(desc.c), float(scale), *args, pt, o,
-         lse.data_ptr() if lse is not None else None, workspace.data_ptr() if need else None)
+        ws = workspace.data_ptr()
+    _run("band_decode", dev, stream, d._ref, scale, Q.data_ptr(), Kc.data_ptr(), Vc.data_ptr(), table.data_ptr(), lens.data_ptr(),
+         q_start.data_ptr(), pt, O.data_ptr(), lp, ws)

@@ -456,6 +456,16 @@ def test_decode_with_large_scores(dtype):
     Decode(dtype, [200, 31], [1, 2], 4, 2, 64, qscale=40.0, prefix=50, seed=97).check()
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1e-4, 3.0])
+def test_decode_scales(dtype, scale):
+    """Negative scales turn the order of the scores round, zero makes the weights equal."""
+    for prefix in (0, 70):
+        c = Decode(dtype, [90, 21], [2, 1], 4, 2, 64, w=60, prefix=prefix, seed=106)
+        c.scale = scale
+        c.check()
+
+
 def test_decode_without_keys():
     """Contexts shorter than their new tokens, empty columns: rows without a key give 0 and -inf."""
     for dtype in (F16, F32):

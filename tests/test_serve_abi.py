@@ -254,29 +254,37 @@ def test_binding_checks():
 
 
 class FakeCuda:
-    """Enough of a CUDA tensor for the binding's shape checks."""
+    """Enough of a CUDA tensor for the binding's checks."""
 
-    def __init__(self, shape, strides, dtype=torch.float16, device="cuda:0", ptr=FAKE):
-        self.shape, self._s, self.dtype, self.device, self._p, self.is_cuda = shape, strides, dtype, device, ptr, True
+    def __init__(self, shape, strides, dtype=torch.float16, device=0):
+        self.shape, self._s, self.dtype, self._d, self.is_cuda, self.device = shape, strides, dtype, device, True, f"cuda:{device}"
+
+    def get_device(self):
+        return self._d
 
     def stride(self):
         return self._s
 
     def data_ptr(self):
-        return self._p
+        return FAKE
 
 
-def test_binding_strides():
+def test_binding_rows_and_strides():
     d = swab.RotaryDesc(2, 3, 4, 2, 64, 64)
-    rows = serve._rows
-    assert rows("Q", FakeCuda((2, 3, 4, 64), (768, 256, 64, 1)), d, 4, None) == (FAKE, (768, 256, 64))
-    assert rows("Q", FakeCuda((6, 4, 64), (512, 64, 1)), d, 4, None) == (FAKE, (1536, 512, 64))
-    assert rows("Q", FakeCuda((2, 3, 4, 64), (0, 256, 64, 1)), d, 4, None) == (FAKE, (0, 256, 64))
-    for bad in (FakeCuda((2, 3, 4, 64), (768, 256, 64, 2)), FakeCuda((2, 3, 4, 64), (0, 0, 0, 1)),
-                FakeCuda((2, 3, 5, 64), (960, 320, 64, 1)), FakeCuda((2, 3, 4, 64), (768, 256, 64, 1), torch.bfloat16)):
+    strides = lambda st: serve._row_strides("Q", st, d, 4)  # noqa: E731
+    assert strides((768, 256, 64, 1)) == (768, 256, 64)
+    assert strides((512, 64, 1)) == (1536, 512, 64)
+    assert strides((0, 256, 64, 1)) == (0, 256, 64)
+    for bad in ((768, 256, 64, 2), (0, 0, 0, 1)):
         with pytest.raises(ValueError):
-            rows("Q", bad, d, 4, None)
-    with pytest.raises(ValueError, match="other tensors"):
-        rows("K", FakeCuda((2, 3, 2, 64), (384, 128, 64, 1), device="cuda:1"), d, 2, FakeCuda((1,), (1,)))
+            strides(bad)
     one = swab.RotaryDesc(1, 1, 1, 0, 64, 64)
-    assert rows("Q", FakeCuda((1, 1, 1, 64), (7, 9, 3, 1)), one, 1, None) == (FAKE, (0, 0, 0))
+    assert serve._row_strides("Q", (7, 9, 3, 1), one, 1) == (0, 0, 0)
+    rows = lambda t: serve._rows("Q", t, d, d._q, 0)  # noqa: E731
+    assert rows(FakeCuda((2, 3, 4, 64), (768, 256, 64, 1))) == FAKE
+    assert rows(FakeCuda((6, 4, 64), (256, 64, 1))) == FAKE
+    for bad in (FakeCuda((2, 3, 5, 64), (960, 320, 64, 1)), FakeCuda((6, 4, 64), (256, 64, 1), torch.bfloat16)):
+        with pytest.raises(ValueError):
+            rows(bad)
+    with pytest.raises(ValueError, match="other tensors"):
+        rows(FakeCuda((6, 4, 64), (256, 64, 1), device=1))
