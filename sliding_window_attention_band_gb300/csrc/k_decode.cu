@@ -231,7 +231,7 @@ cudaError_t launch_general_t(const DecodeArgs &a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_join_t(const DecodeArgs &a, cudaStream_t st) {
     const long long pairs = (long long)a.tokens * a.h;
-    if (a.nparts > 8) return launch_dependent(&k_decode_join<T, 4>, dim3((unsigned)pairs), kThreads, 0, st, a);
+    if (a.nparts > 8 && pairs <= 2048) return launch_dependent(&k_decode_join<T, 4>, dim3((unsigned)pairs), kThreads, 0, st, a);
     return launch_dependent(&k_decode_join<T, 1>, dim3((unsigned)((pairs + 3) / 4)), kThreads, 0, st, a);
 }
 

@@ -50,6 +50,11 @@ template <int HD, bool kPair> struct Shape {
     static constexpr int kQ = (kPair ? 2 : 1) * kQ1;
     static constexpr int kSlots = HD == 64 ? 10 : kPair ? 5 : 6;   // ring of K and V tiles
     static constexpr int kSmem = kQ + kSlots * kTile + 512 + 1024;
+    // One row tile: the product of a chunk's first half starts under the
+    // exponentials of the second (32 requests' worth of rows, 8 x 32k keys: 33.8
+    // -> 32.9 us).  With two the issuing warp waits for one stream while the
+    // other is ready (42.5 -> 44.0 us), so there a chunk is signalled whole.
+    static constexpr bool kEarly = !kPair;
     static constexpr uint32_t kColS = 0, kColO = 256;    // S_g at 128 g (P_g over it), O_g at 256 + HD g
 };
 
@@ -58,6 +63,14 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// a whole 32-byte sector: rows of parts lie far apart, so a warp's store
+// fills 32 of them
+__device__ __forceinline__ void stg32(float *dst, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 template <typename T, int HD, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     k_decode_prefix(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
@@ -71,8 +84,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + kSlots * S::kTile);
     uint64_t *qfull = bars, *full = bars + 1, *empty = full + kSlots;
     uint64_t *sfull = empty + kSlots;            // [2] a stream's S is written
-    uint64_t *pfull = sfull + 2;                 // [2] its P is in place: one arrival a softmax warp
-    uint64_t *odone = pfull + 2;                 // [2] its product is done
+    uint64_t *pfull = sfull + 2;                 // [2][2] P of a chunk or its half is in place: one arrival a softmax warp
+    uint64_t *odone = pfull + 4;                 // [2] its product is done
     uint64_t *done = odone + 2;
     uint32_t *holder = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(holder + 1);
@@ -85,6 +98,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c0 = split * p.pre_chunks, c1 = min(nchunks, c0 + p.pre_chunks), n = c1 - c0;
     const int ppt = 128 >> p.page_log2;          // pages of a tile
 
+    // this lane's page of chunk c, -1: none (warp 0)
+    auto page_id = [&](int c) -> int {
+        const int j = (c * ppt + lane) << p.page_log2;
+        if (lane >= ppt || c >= c1 || j >= p.prefix_len) return -1;
+        const int x = *GP(p.bnd, p.ptable + (j >> p.page_log2));
+        if ((unsigned)x < (unsigned)p.n_blocks) return x;
+        if (x != -1) atomicOr(p.err, kErrInvalid);
+        return -1;
+    };
+    int id = warp == 0 ? page_id(c0) : -1;       // on its way during the set-up
+
     if (threadIdx.x == 0) {
         mbar_init(qfull, 1);
         for (int i = 0; i < kSlots; ++i) {
@@ -93,9 +117,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], kWorkers / 2);
             mbar_init(&odone[i], 1);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&pfull[i], kWorkers / 2);
         mbar_init(done, 1);
         *abort_flag = 0;
         *no_abort = 0;
@@ -125,15 +149,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         int it = 0;
         bool ok = true;
-        auto page_id = [&](int c) -> int {       // this lane's page of chunk c, -1: none
-            const int j = (c * ppt + lane) << p.page_log2;
-            if (lane >= ppt || c >= c1 || j >= p.prefix_len) return -1;
-            const int x = *GP(p.bnd, p.ptable + (j >> p.page_log2));
-            if ((unsigned)x < (unsigned)p.n_blocks) return x;
-            if (x != -1) atomicOr(p.err, kErrInvalid);
-            return -1;
-        };
-        int id = page_id(c0);
         for (int c = c0; c < c1 && ok; ++c) {
             const int ahead = page_id(c + 1);
             const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
@@ -193,13 +208,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto product = [&](int j) -> bool {      // O += P V
                 const int g = j & 1, i = j >> 1, c = kPair ? i : j, it = 2 * c + 1, slot = it % kSlots;
                 if (!mbar_wait(&full[slot], (it / kSlots) & 1, abort_flag, p.err)) return false;
-                if (!mbar_wait(&pfull[g], i & 1, abort_flag, p.err)) return false;
-                tc_fence_after();
                 const uint64_t va = vdesc + (uint64_t)((slot * S::kTile) >> 4);
 #pragma unroll
-                for (int k = 0; k < kBK / 16; ++k)
-                    mma_f16_ts(tmem + S::kColO + HD * g, tmem + S::kColS + kBK * g + 8 * k, va + (uint64_t)((2048 * k) >> 4), idesc_o,
-                               (i == 0 && k == 0) ? 0u : 1u);
+                for (int half = 0; half < 2; ++half) {
+                    if ((half == 0 || S::kEarly) && !mbar_wait(&pfull[2 * g + half], i & 1, abort_flag, p.err)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 4 * half; k < 4 * half + 4; ++k)
+                        mma_f16_ts(tmem + S::kColO + HD * g, tmem + S::kColS + kBK * g + 8 * k, va + (uint64_t)((2048 * k) >> 4),
+                                   idesc_o, (i == 0 && k == 0) ? 0u : 1u);
+                }
                 if (!kPair || g == 1) mma_commit(&empty[slot]);
                 mma_commit(&odone[g]);
                 return true;
@@ -231,16 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            uint32_t x[kBK];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) tmem_ld32(at_s + 32 * v, *reinterpret_cast<uint32_t (*)[32]>(x + 32 * v));
             const int j0 = (c0 + c) * kBK;
             const uint32_t there = okmask[c & 7];
             const bool whole = there == (1u << ppt) - 1u && j0 + kBK <= p.prefix_len;
-            tmem_ld_wait();
+            // keys that are there, 32 a word
+            uint32_t vm[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
             if (!whole) {
-                // keys that are there, 32 a word
-                uint32_t vm[4];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int j = 32 * w, left = p.prefix_len - j0 - j;
@@ -248,9 +262,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             (((there >> ((j + 16) >> p.page_log2)) & 1u) ? 0xffff0000u : 0u);
                     if (left < 32) vm[w] &= left <= 0 ? 0u : (1u << left) - 1u;
                 }
-#pragma unroll
-                for (int k = 0; k < kBK; ++k)
-                    if (!((vm[k >> 5] >> (k & 31)) & 1u)) x[k] = __float_as_uint(never);
                 // V lines of absent keys become zeros, once the tile has landed: a
                 // quarter of them for each warp
                 const int it = 2 * c + 1, slot = it % kSlots;
@@ -268,43 +279,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 fence_proxy_async_smem();
             }
-            float ext[8];
+            // 32 scores of this row; those of absent keys never win
+            auto take = [&](int v, uint32_t (&x)[32]) {
+                tmem_ld32(at_s + 32 * v, x);
+                tmem_ld_wait();
+                if (!whole) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t *y = x + 16 * k;
-                float a = __uint_as_float(y[0]);
+                    for (int k = 0; k < 32; ++k)
+                        if (!((vm[v] >> k) & 1u)) x[k] = __float_as_uint(never);
+                }
+            };
+            float best = never;
 #pragma unroll
-                for (int e = 1; e < 15; e += 2)
-                    a = neg ? min3(a, __uint_as_float(y[e]), __uint_as_float(y[e + 1]))
-                            : max3(a, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
-                ext[k] = neg ? fminf(a, __uint_as_float(y[15])) : fmaxf(a, __uint_as_float(y[15]));
+            for (int v = 0; v < 4; ++v) {
+                uint32_t x[32];
+                take(v, x);
+                float ext[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t *y = x + 8 * k;
+#define F(i) __uint_as_float(y[i])
+                    float a = neg ? min3(F(0), F(1), F(2)) : max3(F(0), F(1), F(2));
+                    a = neg ? min3(a, F(3), F(4)) : max3(a, F(3), F(4));
+                    a = neg ? min3(a, F(5), F(6)) : max3(a, F(5), F(6));
+                    ext[k] = neg ? fminf(a, F(7)) : fmaxf(a, F(7));
+#undef F
+                }
+                best = neg ? min3(min3(best, ext[0], ext[1]), ext[2], ext[3]) : max3(max3(best, ext[0], ext[1]), ext[2], ext[3]);
             }
-            const float best = neg ? fminf(min3(ext[0], ext[1], ext[2]), fminf(min3(ext[3], ext[4], ext[5]), fminf(ext[6], ext[7])))
-                                   : fmaxf(max3(ext[0], ext[1], ext[2]), fmaxf(max3(ext[3], ext[4], ext[5]), fmaxf(ext[6], ext[7])));
             const float cmax = best == never ? -INFINITY : best * xs;
             const bool raise = cmax > m + kSlack;            // the first time too: m is -inf
             const float mref = raise ? cmax : m;
             const float mb = mref == -INFINITY ? 0.f : mref;
             const bool rescale = raise && m != -INFINITY;
             const float corr = rescale ? ex2(m - mref) : 1.f;
-            const uint64_t xs2 = f2(xs, xs), nb2 = f2(-mb, -mb);
-            uint64_t ls[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float y0, y1;
-                    f2split(fma2(f2(__uint_as_float(x[32 * v + 2 * e]), __uint_as_float(x[32 * v + 2 * e + 1])), xs2, nb2), y0, y1);
-                    const float p0 = ex2(y0), p1 = ex2(y1);
-                    ls[e & 1] = add2(ls[e & 1], f2(p0, p1));
-                    pk[e] = pack2<T>(p0, p1);
-                }
-                tmem_st16(at_s + 16 * v, pk);
-            }
-            float l0, l1;
-            f2split(add2(ls[0], ls[1]), l0, l1);
-            l = l * corr + (l0 + l1);
             if (__any_sync(0xffffffffu, rescale)) {
                 // (the product before this S is done: see the issuing warp)
 #pragma unroll 1
@@ -317,9 +325,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st32(at_o + 32 * k, o);
                 }
             }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive_warp(&pfull[g]);
+            const uint64_t xs2 = f2(xs, xs), nb2 = f2(-mb, -mb);
+            uint64_t ls[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                uint32_t x[32], pk[16];
+                take(v, x);                      // (P of v lands where S of v and before was)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float y0, y1;
+                    f2split(fma2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), xs2, nb2), y0, y1);
+                    const float p0 = ex2(y0), p1 = ex2(y1);
+                    ls[e & 1] = add2(ls[e & 1], f2(p0, p1));
+                    pk[e] = pack2<T>(p0, p1);
+                }
+                tmem_st16(at_s + 16 * v, pk);
+                if (v == 3 || (S::kEarly && v == 1)) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive_warp(&pfull[2 * g + (S::kEarly ? v >> 1 : 0)]);
+                }
+            }
+            float l0, l1;
+            f2split(add2(ls[0], ls[1]), l0, l1);
+            l = l * corr + (l0 + l1);
             m = mref;
         }
         // the stream's part
@@ -340,9 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (live) {
                         float *dst = p.po + at * HD + 32 * k;
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            *reinterpret_cast<uint4 *>(GPN(p.bnd, dst + 4 * v, 16)) =
-                                make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                        for (int v = 0; v < 4; ++v) stg32(GPN(p.bnd, dst + 8 * v, 32), o + 8 * v);
                     }
                 }
             }

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
     __shared__ float2 sml[kWarps][kRows];
     __shared__ float swt[kWarps][kRows];
     __shared__ float2 stot[kRows];
+    __shared__ float2 spre[kMaxFold][kRows];       // the prefix's parts, joined here: (max, sum), then the weight
     __shared__ uint32_t sok[kWarps][S::kStages];   // which keys of the group in a stage are there
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int split = blockIdx.x, r = blockIdx.z;
@@ -321,7 +322,15 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
                 for (int d = 0; d < HD / 8; ++d)
                     *reinterpret_cast<float2 *>(mine_o + row * kPad + 8 * d + 2 * t4) = make_float2(o[t][d][2 * e], o[t][d][2 * e + 1]);
             }
-        if (p.fold) pdl_wait();                  // the prefix's parts are there
+        if (p.fold) {
+            pdl_wait();                          // the prefix's parts are there
+            for (int e = threadIdx.x; e < kRows * p.npre; e += kThreads) {
+                const int row = e % kRows, s = e / kRows;
+                if (row >= nrows) continue;
+                const int a = (row0 + row) / p.group, hh = kvh * p.group + row0 + row - a * p.group;
+                spre[s][row] = *GP(p.bnd, p.pml + ((long long)(q.row0 + a) * p.h + hh) * p.nparts + 1 + s);
+            }
+        }
         __syncthreads();
         if (threadIdx.x < kRows) {
             const int row = threadIdx.x;
@@ -330,11 +339,11 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
             float M = -INFINITY, L = 0.f;
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w][row].x);
             if (p.fold && row < nrows) {
-                const float2 *ml = p.pml + th * p.nparts + 1;
-                for (int s = 0; s < p.npre; ++s) M = fmaxf(M, GP(p.bnd, ml + s)->x);
+                for (int s = 0; s < p.npre; ++s) M = fmaxf(M, spre[s][row].x);
                 for (int s = 0; s < p.npre; ++s) {
-                    const float2 v = *GP(p.bnd, ml + s);
-                    if (v.x != -INFINITY) L = fmaf(v.y, ex2(v.x - M), L);
+                    const float f = spre[s][row].x == -INFINITY ? 0.f : ex2(spre[s][row].x - M);
+                    L = fmaf(spre[s][row].y, f, L);
+                    spre[s][row].x = f;
                 }
             }
             for (int w = 0; w < kWarps; ++w) {
@@ -364,15 +373,13 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
             const int a = (row0 + row) / p.group, hh = kvh * p.group + row0 + row - a * p.group;
             const long long tok = q.row0 + a, th = tok * p.h + hh;
             if (p.fold) {
-                const float M = stot[row].x;
-                const float2 *ml = p.pml + th * p.nparts + 1;
                 const float *po = p.po + (th * p.nparts + 1) * HD + c4;
-#pragma unroll 4
+#pragma unroll 8
                 for (int s = 0; s < p.npre; ++s) {
-                    const float ms = GP(p.bnd, ml + s)->x;
-                    if (ms == -INFINITY) continue;               // an empty part's values are not written
-                    const float f = ex2(ms - M);
-                    const float4 v = *reinterpret_cast<const float4 *>(GPN(p.bnd, po + (long long)s * HD, 16));
+                    const float f = spre[s][row].x;
+                    // (the values of an empty part are not written)
+                    const float4 v = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                              : *reinterpret_cast<const float4 *>(GPN(p.bnd, po + (long long)s * HD, 16));
                     y.x = fmaf(v.x, f, y.x);
                     y.y = fmaf(v.y, f, y.y);
                     y.z = fmaf(v.z, f, y.z);

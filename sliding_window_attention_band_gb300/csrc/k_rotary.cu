@@ -6,8 +6,8 @@
 // the gradient by -t.  The frequency is a 64-bit fixed-point fraction of a
 // turn, so the product with the position, taken modulo 2^64, IS the fraction
 // of the turn: one integer multiply, exact at any distance, where an fp32
-// product is off by 0.06 rad at position 10^6.  Its upper bits become the
-// argument of sincospif (relative rounding 2^-24, so at most 2^-25 pi rad).
+// product is off by 0.06 rad at position 10^6.  Its upper 32 bits (2 pi 2^-32
+// rad) become the argument of sincospif (rounded to fp32: 2^-25 pi rad).
 //
 // A block takes a few tokens.  It lists their head rows (where from, where to)
 // and fills a table of their cosines and sines in shared memory -- one sincospi
@@ -27,9 +27,9 @@ namespace swab {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBlocks = 5;           // of an SM
 constexpr int kMaxRows = 512;        // listed rows of a block at a time
 constexpr int kMaxTile = 16;        // tokens of a block (Row::token)
-constexpr int kUnroll = 4;            // rows of a thread in flight
 
 // One row of work: a head of Q or K (turned) or of V (copied).  The addresses
 // are multiples of 16, so their low bits carry the token of the tile and
@@ -71,83 +71,118 @@ __device__ __forceinline__ uint4 pack16(const float *f) {
 }
 __device__ __forceinline__ uint4 load16(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
 
-// Row `idx` of token t: heads of Q, then of K, then (append) of V.
-template <typename T, bool kAppend>
-__device__ __forceinline__ Row row_of(const RotaryArgs &p, unsigned t, int tt, int idx) {
-    const unsigned bb = t / (unsigned)p.n, i = t - bb * (unsigned)p.n;
-    const char *src;
-    char *dst;
-    bool turn = true;
-    if (idx < p.hq) {
-        src = (const char *)p.Q + ((long long)bb * p.sq[0] + (long long)i * p.sq[1] + (long long)idx * p.sq[2]) * (int)sizeof(T);
-        dst = (char *)p.Qo + ((long long)bb * p.sqo[0] + (long long)i * p.sqo[1] + (long long)idx * p.sqo[2]) * (int)sizeof(T);
+// N floats of the table, 16 or 8 bytes at a time
+template <int N>
+__device__ __forceinline__ void take(const float *src, float (&f)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src + k);
+            f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
+        }
     } else {
-        idx -= p.hq;
-        const bool is_v = kAppend && idx >= p.hk;
-        if (is_v) idx -= p.hk;
-        const long long *s = is_v ? p.sv : p.sk;
-        src = (const char *)(is_v ? p.V : p.K) + ((long long)bb * s[0] + (long long)i * s[1] + (long long)idx * s[2]) * (int)sizeof(T);
-        turn = !is_v;
-        if constexpr (kAppend) {
-            const int slot = *GP(p.bnd, p.slots + t);
-            dst = nullptr;
-            if (slot >= 0 && slot < p.n_slots) {
-                const unsigned blk = (unsigned)slot >> p.page_log2, off = (unsigned)slot & ((1u << p.page_log2) - 1u);
-                const long long line = (((long long)blk * p.hk + idx) << p.page_log2) + off;
-                dst = (char *)(is_v ? p.Vc : p.Kc) + line * p.hd * (int)sizeof(T);
-            } else if (slot != -1) {
-                atomicOr(p.err, kErrInvalid);
-            }
-        } else {
-            dst = (char *)p.Ko + ((long long)bb * p.sko[0] + (long long)i * p.sko[1] + (long long)idx * p.sko[2]) * (int)sizeof(T);
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(src + k);
+            f[k] = v.x, f[k + 1] = v.y;
         }
     }
+}
+
+// Row `idx` of token t: heads of Q, then of K, then (append) of V.  Strides
+// are in units of 16 bytes, their sums below 2^32 (checked by the caller).
+template <bool kAppend>
+__device__ __forceinline__ Row row_of(const RotaryArgs &p, unsigned t, unsigned tt, int idx) {
+    unsigned bb = 0, i = t;
+    if (p.n < p.tokens) {
+        bb = t / (unsigned)p.n;
+        i = t - bb * (unsigned)p.n;
+    }
+    const bool is_q = idx < p.hq;
+    unsigned head = is_q ? idx : idx - p.hq;
+    const bool is_v = kAppend && !is_q && head >= (unsigned)p.hk;
+    if (is_v) head -= p.hk;
+    const unsigned *s = is_q ? p.sq : is_v ? p.sv : p.sk;
+    const char *src = (const char *)(is_q ? p.Q : is_v ? p.V : p.K) + (unsigned long long)(bb * s[0] + i * s[1] + head * s[2]) * 16u;
+    char *dst;
+    if (kAppend && !is_q) {
+        const int slot = *GP(p.bnd, p.slots + t);
+        dst = nullptr;
+        if (slot >= 0 && slot < p.n_slots) {
+            const unsigned blk = (unsigned)slot >> p.page_log2, off = (unsigned)slot & ((1u << p.page_log2) - 1u);
+            const unsigned line = ((blk * (unsigned)p.hk + head) << p.page_log2) + off;     // below 2^32
+            dst = (char *)(is_v ? p.Vc : p.Kc) + (unsigned long long)line * p.row_bytes;
+        } else if (slot != -1) {
+            atomicOr(p.err, kErrInvalid);
+        }
+    } else {
+        const unsigned *so = is_q ? p.sqo : p.sko;
+        dst = (char *)(is_q ? p.Qo : p.Ko) + (unsigned long long)(bb * so[0] + i * so[1] + head * so[2]) * 16u;
+    }
     const uintptr_t d = reinterpret_cast<uintptr_t>(dst);
-    return Row{reinterpret_cast<uintptr_t>(src) + tt, d && turn ? d + 1 : d};
+    return Row{reinterpret_cast<uintptr_t>(src) + tt, d && !is_v ? d + 1 : d};
 }
 
 // kMode: 0 = halves in 16-byte pieces, 1 = interleaved in 16-byte pieces,
 // 2 = a pair a place (the pairs do not start on 16-byte pieces; the channels
 // behind them are copied 16 bytes at a time where they do).
 template <typename T, int kMode, bool kAppend>
-__global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ RotaryArgs p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_constant__ RotaryArgs p) {
     constexpr int kV = VecOf<T>::kN, kB = (int)sizeof(T);
-    constexpr int kLoads = kMode == 0 ? 2 : 1;
-    extern __shared__ float tab[];           // [tile][2][rot / 2]: cos, sin of each token
+    constexpr int kLoads = kMode == 0 ? 2 : 1, kUnroll = 4 / kLoads;   // rows of a thread in flight
+    extern __shared__ __align__(16) float tab[];       // [tile][2][rot / 2]: cos, sin of each token
     __shared__ Row list[kMaxRows];
     const int half = p.rot / 2;
-    const int rows = p.hq + p.hk * (kAppend ? 2 : 1);
     const bool vcopy = kMode != 2 || p.rot * kB % 16 == 0;
     // places of a row: those whose pairs turn, then those copied
     const int nturn = kMode == 0 ? half / kV : kMode == 1 ? p.rot / kV : half;
     const int places = nturn + (vcopy ? (p.hd - p.rot) / kV : p.hd - p.rot);
     const int per_pass = places >= kThreads ? 1 : kThreads / places;   // rows of a pass
     const int place0 = threadIdx.x % places, q0 = threadIdx.x / places;
+    const bool active = places >= kThreads || q0 < per_pass;           // not one of the threads left over
     // the block's share of the heads: gridDim.y slices
-    const int lo = (int)((long long)rows * blockIdx.y / gridDim.y), mine = (int)((long long)rows * (blockIdx.y + 1) / gridDim.y) - lo;
+    const int lo = (int)((long long)p.rows * blockIdx.y / gridDim.y), mine = (int)((long long)p.rows * (blockIdx.y + 1) / gridDim.y) - lo;
+    // x / mine and x / half for x < 2^15 by one multiplication
+    const unsigned by_mine = 0xffffffffu / mine + 1u, by_half = half > 1 ? 0xffffffffu / half + 1u : 0u;
+
+    // byte offset of a place in its row
+    auto place_at = [&](int place) {
+        return place < nturn ? 16 * place : vcopy ? (p.rot + (place - nturn) * kV) * kB : (p.rot + place - nturn) * kB;
+    };
+    auto fetch = [&](Row (&r)[kUnroll], uint4 (&v)[kUnroll][kLoads], int q, int at, bool copies, int total) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int e = q + u * per_pass;
+            r[u].d = 0;
+            if (e < total) r[u] = list[e];
+            if (!r[u].d) continue;
+            v[u][0] = load16(GPN(p.bnd, r[u].src() + at, 16));
+            if (kMode == 0 && !copies) v[u][kLoads - 1] = load16(GPN(p.bnd, r[u].src() + at + half * kB, 16));
+        }
+    };
 
     for (long long t0 = (long long)blockIdx.x * p.tile; t0 < p.tokens; t0 += (long long)gridDim.x * p.tile) {
         const int nt = (int)(p.tokens - t0 < p.tile ? p.tokens - t0 : p.tile);
         const int total = nt * mine;
         for (int e = threadIdx.x; e < total; e += kThreads) {
-            const int tt = e / mine;
-            list[e] = row_of<T, kAppend>(p, (unsigned)t0 + tt, tt, lo + e - tt * mine);
+            const unsigned tt = mine > 1 ? __umulhi(e, by_mine) : e;
+            list[e] = row_of<kAppend>(p, (unsigned)t0 + tt, tt, lo + e - tt * mine);
         }
         for (int e = threadIdx.x; e < nt * half; e += kThreads) {
-            const int tt = e / half, k = e - tt * half;
-            const unsigned t = (unsigned)t0 + tt;
+            const unsigned tt = half > 1 ? __umulhi(e, by_half) : e, k = e - tt * half, t = (unsigned)t0 + tt;
             const long long at = (p.pos ? (long long)*GP(p.bnd, p.pos + t) : (long long)(t % (unsigned)p.n)) + p.pos0;
-            const long long frac = (long long)((unsigned long long)at * *GP(p.bnd, p.turns + k));
+            // the upper 32 bits of the fraction of a turn: half turns in [-1, 1)
+            const int frac = (int)(((unsigned long long)at * *GP(p.bnd, p.turns + k)) >> 32);
             float sn, cs;
-            sincospif((float)frac * 0x1p-63f, &sn, &cs);   // in half turns: [-1, 1)
+            sincospif((float)frac * 0x1p-31f, &sn, &cs);
             tab[(2 * tt) * half + k] = cs * p.scale;
             tab[(2 * tt + 1) * half + k] = sn * (p.backward ? -p.scale : p.scale);
         }
         __syncthreads();
         for (int place = place0; place < places; place += kThreads) {
-            if (places < kThreads && q0 >= per_pass) break;      // the threads left over by a pass
+            if (!active) break;                  // the threads left over by a pass
             const bool copies = place >= nturn;
-            const int at = copies ? (vcopy ? (p.rot + (place - nturn) * kV) * kB : (p.rot + place - nturn) * kB) : 16 * place;
+            const int at = place_at(place);
             for (int q = q0; q < total; q += kUnroll * per_pass) {
                 if constexpr (kMode == 2) {
                     if (!(copies && vcopy)) {                     // element by element
@@ -176,47 +211,43 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ Rot
                         continue;
                     }
                 }
+                Row r[kUnroll];
                 uint4 v[kUnroll][kLoads];
+                fetch(r, v, q, at, copies, total);
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int e = q + u * per_pass;
-                    if (e >= total || !list[e].d) continue;
-                    v[u][0] = load16(GPN(p.bnd, list[e].src() + at, 16));
-                    if (kMode == 0 && !copies) v[u][kLoads - 1] = load16(GPN(p.bnd, list[e].src() + at + half * kB, 16));
-                }
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int e = q + u * per_pass;
-                    if (e >= total) break;
-                    const Row r = list[e];
-                    if (!r.d) continue;
-                    char *out = r.dst();
-                    if (kMode != 2 && !copies && r.turn()) {
-                        const float *cs = tab + 2 * r.token() * half, *sn = cs + half;
+                    if (!r[u].d) continue;
+                    if (kMode != 2 && !copies && (!kAppend || r[u].turn())) {
+                        constexpr int kPairs = kMode == 0 ? kV : kV / 2;
+                        const float *tc = tab + 2 * r[u].token() * half + place * kPairs;
+                        float c[kPairs], s[kPairs];
+                        take<kPairs>(tc, c);
+                        take<kPairs>(tc + half, s);
                         if constexpr (kMode == 0) {
-                            float fa[kV], fb[kV], ya[kV], yb[kV];
+                            float fa[kV], fb[kV];
                             unpack16<T>(v[u][0], fa);
-                            unpack16<T>(v[u][1], fb);
+                            unpack16<T>(v[u][kLoads - 1], fb);
 #pragma unroll
                             for (int k = 0; k < kV; ++k) {
-                                const float c = cs[place * kV + k], s = sn[place * kV + k];
-                                ya[k] = fa[k] * c - fb[k] * s;
-                                yb[k] = fb[k] * c + fa[k] * s;
+                                const float x = fa[k];
+                                fa[k] = x * c[k] - fb[k] * s[k];
+                                fb[k] = fb[k] * c[k] + x * s[k];
                             }
-                            v[u][0] = pack16<T>(ya);
-                            v[u][1] = pack16<T>(yb);
+                            v[u][0] = pack16<T>(fa);
+                            v[u][kLoads - 1] = pack16<T>(fb);
                         } else if constexpr (kMode == 1) {
-                            float f[kV], y[kV];
+                            float f[kV];
                             unpack16<T>(v[u][0], f);
 #pragma unroll
-                            for (int k = 0; k < kV / 2; ++k) {
-                                const float c = cs[place * (kV / 2) + k], s = sn[place * (kV / 2) + k];
-                                y[2 * k] = f[2 * k] * c - f[2 * k + 1] * s;
-                                y[2 * k + 1] = f[2 * k + 1] * c + f[2 * k] * s;
+                            for (int k = 0; k < kPairs; ++k) {
+                                const float x = f[2 * k];
+                                f[2 * k] = x * c[k] - f[2 * k + 1] * s[k];
+                                f[2 * k + 1] = f[2 * k + 1] * c[k] + x * s[k];
                             }
-                            v[u][0] = pack16<T>(y);
+                            v[u][0] = pack16<T>(f);
                         }
                     }
+                    char *out = r[u].dst();
                     *reinterpret_cast<uint4 *>(GPN(p.bnd, out + at, 16)) = v[u][0];
                     if (kMode == 0 && !copies) *reinterpret_cast<uint4 *>(GPN(p.bnd, out + at + half * kB, 16)) = v[u][kLoads - 1];
                 }
@@ -242,6 +273,8 @@ cudaError_t launch_rotary(DType dt, bool append, RotaryArgs a, cudaStream_t st) 
     const int es = dt == kF32 ? 4 : 2, vec = 16 / es;
     const int mode = a.rot == 0 ? 0 : a.interleaved ? (a.rot % vec == 0 ? 1 : 2) : (a.rot / 2 % vec == 0 ? 0 : 2);
     const int rows = a.hq + a.hk * (append ? 2 : 1);
+    a.rows = rows;
+    a.row_bytes = a.hd * es;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidValue;
     // tokens of a block: about four rows a thread, but blocks enough for the GPU
@@ -255,7 +288,11 @@ cudaError_t launch_rotary(DType dt, bool append, RotaryArgs a, cudaStream_t st) 
     else tile = std::max(1LL, std::min(tile, (long long)kMaxRows / rows));
     a.tile = (int)tile;
     const long long tiles = (a.tokens + a.tile - 1) / a.tile;
-    const dim3 grid((unsigned)std::min(tiles, 64LL * sms), (unsigned)slices);
+    // the GPU full once: the set-up of a block is then paid for by several tiles
+    // (12 x 1365 tokens of 24 heads of 64: 19.8 us against 21.7 with a block a
+    // tile), unless that would leave a short second round
+    const long long full = (long long)kBlocks * sms;
+    const dim3 grid((unsigned)(tiles <= 2 * full ? tiles : full), (unsigned)slices);
     const size_t smem = (size_t)a.tile * a.rot * sizeof(float);
     if (dt == kF32) return append ? launch_t<float, true>(a, mode, grid, smem, st) : launch_t<float, false>(a, mode, grid, smem, st);
     if (dt == kF16) return append ? launch_t<__half, true>(a, mode, grid, smem, st) : launch_t<__half, false>(a, mode, grid, smem, st);

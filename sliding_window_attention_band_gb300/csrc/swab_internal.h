@@ -306,15 +306,19 @@ struct RotaryArgs {
     void *Kc, *Vc;             // the cache [n_blocks, hk, page, hd]
     const unsigned long long *turns;
     const int *pos, *slots;
-    long long sq[3], sk[3], sv[3], sqo[3], sko[3];   // strides over (b, n, head)
-    long long tokens;          // b * n
-    int n, hq, hk, hd, rot;    // hq: query heads handled (0 leaves Q out)
+    unsigned sq[3], sk[3], sv[3], sqo[3], sko[3];    // strides over (b, n, head) in units of 16 bytes
+    unsigned tokens;           // b * n
+    unsigned n;
+    int hq, hk, hd, rot;       // hq: query heads handled (0 leaves Q out)
     int interleaved, backward;
     int pos0;
     float scale;
     int page_log2, n_slots;
     unsigned *err;
-    int tile;                  // tokens a block takes at a time (set by the launcher)
+    // set by the launcher: tokens a block takes at a time, head rows of a token,
+    // bytes of one
+    int tile, rows;
+    unsigned row_bytes;
 #if SWAB_BOUNDS_CHECK
     Bounds bnd;
 #endif
@@ -357,6 +361,7 @@ struct DecodeArgs {
     Bounds bnd;
 #endif
 };
+constexpr int kMaxFold = 16;    // most parts of the prefix that the rows kernel joins
 cudaError_t launch_decode_general(DType dt, const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_decode_rows(DType dt, const DecodeArgs &a, int max_q, cudaStream_t st);
 cudaError_t launch_decode_prefix(DType dt, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,

@@ -41,38 +41,48 @@ int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 
 // rotary
 // ---------------------------------------------------------------------------
 
-// Strides of a [b, n, heads, hd] tensor: the given ones, or contiguous.  An
-// output's rows must not overlap: sorted by stride, each dimension has to step
-// over all that the smaller ones span.
-swab_status take_strides(const swab_rotary_desc *d, int heads, const int64_t *given, bool output, long long *s) {
-    const long long vec = 16 / elt(d->dtype);
+// Strides of a [b, n, heads, hd] tensor in units of 16 bytes: the given ones,
+// or contiguous.  An output's rows must not overlap: sorted by stride, each
+// dimension has to step over all that the smaller ones span.
+swab_status take_strides(const swab_rotary_desc *d, int heads, const int64_t *given, bool output, unsigned *units) {
+    const long long vec = 16 / elt(d->dtype), size[3] = {d->b, d->n, heads};
+    long long s[3];
     if (given[0] == 0 && given[1] == 0 && given[2] == 0) {
         s[2] = d->head_dim;
         s[1] = s[2] * heads;
         s[0] = s[1] * d->n;
-        return SWAB_OK;
+        output = false;
+    } else {
+        for (int k = 0; k < 3; ++k) {
+            if (given[k] < 0) return SWAB_ERR_INVALID_ARG;
+            if (given[k] % vec != 0) return SWAB_ERR_MISALIGNED;
+            s[k] = given[k];
+        }
     }
-    const long long size[3] = {d->b, d->n, heads};
-    int order[3] = {0, 1, 2};
+    if (output) {
+        int order[3] = {0, 1, 2};
+        std::sort(order, order + 3, [&](int x, int y) { return s[x] < s[y]; });
+        long long span = d->head_dim;
+        for (int k : order) {
+            if (size[k] == 1) continue;
+            if (s[k] < span) return SWAB_ERR_INVALID_ARG;
+            if (s[k] > (1ll << 40)) return SWAB_ERR_UNSUPPORTED;
+            span += s[k] * (size[k] - 1);
+        }
+    }
+    long long last = 0;                      // of a row, in units of 16 bytes
     for (int k = 0; k < 3; ++k) {
-        if (given[k] < 0) return SWAB_ERR_INVALID_ARG;
-        if (given[k] % vec != 0) return SWAB_ERR_MISALIGNED;
-        if (given[k] > (1ll << 40)) return SWAB_ERR_UNSUPPORTED;
-        s[k] = given[k];
-    }
-    if (!output) return SWAB_OK;
-    std::sort(order, order + 3, [&](int x, int y) { return s[x] < s[y]; });
-    long long span = d->head_dim;
-    for (int k : order) {
-        if (size[k] == 1) continue;
-        if (s[k] < span) return SWAB_ERR_INVALID_ARG;
-        span += s[k] * (size[k] - 1);
+        const long long u = size[k] == 1 ? 0 : s[k] / vec;
+        if (u > 0xffffffffll) return SWAB_ERR_UNSUPPORTED;
+        if (size[k] > 1 && u > (0xffffffffll - last) / (size[k] - 1)) return SWAB_ERR_UNSUPPORTED;
+        last += u * (size[k] - 1);
+        units[k] = (unsigned)u;
     }
     return SWAB_OK;
 }
 
-[[maybe_unused]] size_t strided_bytes(const swab_rotary_desc *d, int heads, const long long *s) {
-    return (size_t)(s[0] * (d->b - 1) + s[1] * (d->n - 1) + s[2] * (heads - 1) + d->head_dim) * elt(d->dtype);
+[[maybe_unused]] size_t strided_bytes(const swab_rotary_desc *d, int heads, const unsigned *s) {
+    return ((size_t)s[0] * (d->b - 1) + (size_t)s[1] * (d->n - 1) + (size_t)s[2] * (heads - 1)) * 16 + d->head_dim * elt(d->dtype);
 }
 
 swab_status check_rotary(const swab_rotary_desc *d, const uint64_t *turns, const int32_t *pos, RotaryArgs *a) {
@@ -91,8 +101,8 @@ swab_status check_rotary(const swab_rotary_desc *d, const uint64_t *turns, const
     if (pos && !aligned(pos, 4)) return SWAB_ERR_MISALIGNED;
     a->turns = reinterpret_cast<const unsigned long long *>(turns);
     a->pos = pos;
-    a->tokens = (long long)d->b * d->n;
-    a->n = d->n;
+    a->tokens = (unsigned)d->b * (unsigned)d->n;
+    a->n = (unsigned)d->n;
     a->hq = d->h;
     a->hk = d->hk;
     a->hd = d->head_dim;
@@ -231,13 +241,13 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
         p.pre_chunks = (int)((chunks + pieces - 1) / pieces);
         p.pre_pieces = (int)((chunks + p.pre_chunks - 1) / p.pre_chunks);
         p.npre = p.pre_pieces * (pair ? 1 : 2);
-        p.fold = p.nsplit == 1 && p.npre <= 16;
+        p.fold = p.nsplit == 1 && p.npre <= kMaxFold;
     }
     p.nparts = p.nsplit + p.npre;
     if (p.nparts > 1) {
         const size_t lines = (size_t)d->tokens * d->h * p.nparts;
         p.parts_bytes = (lines * d->head_dim * 4 + 255) / 256 * 256;
-        p.bytes = p.parts_bytes + lines * 8;
+        p.bytes = p.parts_bytes + lines * 8 + 256;      // the parts start on a multiple of 256 bytes
     }
     return p;
 }
@@ -358,6 +368,7 @@ SWAB_API swab_status rotary_append(const swab_rotary_desc *desc, const swab_cach
     if (s != SWAB_OK) return s;
     if ((s = check_cache(cache)) != SWAB_OK) return s;
     if (desc->hk < 1 || !Q != !Qo) return SWAB_ERR_INVALID_ARG;
+    if ((long long)cache->n_blocks * cache->page * desc->hk >= 0xffffffffll) return SWAB_ERR_UNSUPPORTED;
     if (desc->rot_dim > 0 && !pos) return SWAB_ERR_INVALID_ARG;
     if (Q) {
         if ((s = take_strides(desc, desc->h, desc->q_stride, false, a.sq)) != SWAB_OK) return s;
@@ -418,8 +429,9 @@ SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, cons
     a.lens = lens;
     a.q_start = q_start;
     a.ptable = prefix_table;
-    a.po = static_cast<float *>(workspace);
-    a.pml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + plan.parts_bytes);
+    char *parts = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
+    a.po = reinterpret_cast<float *>(parts);
+    a.pml = reinterpret_cast<float2 *>(parts + plan.parts_bytes);
     a.q_stride = desc->q_row_stride ? desc->q_row_stride : (long long)desc->h * desc->head_dim;
     a.o_stride = desc->out_row_stride ? desc->out_row_stride : (long long)desc->h * desc->head_dim;
     a.batch = c->batch;

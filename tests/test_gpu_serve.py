@@ -365,7 +365,7 @@ class Decode:
     def run(self, stream=None, lse=True):
         o = torch.full_like(self.q, 7.0)
         l = torch.full(self.q.shape[:2], 7.0, dtype=F32, device="cuda") if lse else None
-        ws = torch.empty(swab.band_decode_workspace(self.desc), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(swab.band_decode_workspace(self.desc) + 16, dtype=torch.uint8, device="cuda")[16:]   # 16-byte aligned, no more
         swab.band_decode(self.desc, self.scale, self.q, self.kc, self.vc, i32(self.table), i32(self.lens), i32(self.q_start),
                          o, l, ws, i32(self.ptable) if self.prefix else None, stream=stream)
         return o, l
