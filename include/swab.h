@@ -402,8 +402,8 @@ typedef struct swab_rotary_desc {
     int32_t pos0;          /* added to every position */
     /* Element strides over (b, n, head) of Q, K, their outputs, and V
      * (rotary_append), the channels adjacent; three zeros = contiguous
-     * [b, n, heads, head_dim].  Multiples of 16 bytes; the rows of an output
-     * must not overlap. */
+     * [b, n, heads, head_dim].  Multiples of 16 bytes; a tensor spans less than
+     * 64 GB; the rows of an output must not overlap. */
     int64_t q_stride[3], k_stride[3], qo_stride[3], ko_stride[3], v_stride[3];
 } swab_rotary_desc;
 
@@ -448,7 +448,8 @@ SWAB_API swab_status rotary_bwd(const swab_rotary_desc *desc, const uint64_t *tu
 typedef struct swab_cache_desc {
     int32_t batch;     /* requests, 1..65535 */
     int32_t page;      /* positions a block: 16, 32, 64 or 128 */
-    int32_t n_blocks;  /* blocks of the cache, >= 1; n_blocks * page < 2^31 */
+    int32_t n_blocks;  /* blocks of the cache, >= 1; n_blocks * page < 2^31 - 255, and
+                          n_blocks * page * hk < 2^32 - 1 */
     int32_t cols;      /* columns of the block table, >= 1 */
     int32_t ring;      /* 1: columns from `pinned` on are recycled */
     int32_t pinned;    /* 0..cols - 1; 0 without ring */
@@ -501,7 +502,7 @@ typedef struct swab_decode_desc {
     int32_t n_sink;       /* leading positions every later query attends to, >= 0 */
     int32_t max_q;        /* most new tokens of a request, >= 1 */
     int32_t max_len;      /* longest context, >= 1 (divides the work; longer ones stay right) */
-    int32_t prefix_len;   /* positions of the shared prefix, 0: none */
+    int32_t prefix_len;   /* positions of the shared prefix, 0: none; at most n_blocks * page */
     int32_t dtype;        /* swab_dtype of Q, K, V, O */
     int64_t q_row_stride; /* elements between rows of Q, 0 = h * head_dim; multiple of 16 bytes */
     int64_t out_row_stride; /* the same of O */
@@ -519,7 +520,9 @@ SWAB_API size_t band_decode_workspace(const swab_decode_desc *desc);
  *     with prefix_len > 0 also every position of the shared prefix,
  * each once:  O = softmax(scale * q . K) . V,  lse = log of its sum of
  * exponentials ([tokens, h] fp32, may be NULL).  A query without a key (an
- * inconsistent length, absent blocks) gets O = 0 and lse = -inf.  Rows past
+ * inconsistent length, absent blocks) gets O = 0 and lse = -inf.  Without ring,
+ * positions past the table (lens[r] > cols * page) count as absent and raise
+ * SWAB_ERR_INVALID_ARG in the status word.  Rows past
  * q_start[batch] are left as they were.
  * The shared prefix lies in the same cache: positions p of it in block
  * prefix_table[p / page] ([ceil(prefix_len / page)], DEVICE int32); it comes

@@ -280,8 +280,8 @@ cudaError_t launch_rotary(DType dt, bool append, RotaryArgs a, cudaStream_t st) 
     // tokens of a block: about four rows a thread, but blocks enough for the GPU
     const int places = (mode == 0 ? a.rot / 2 : a.rot) / (mode == 2 ? 2 : vec) + (a.hd - a.rot) / vec;
     const long long items = (long long)rows * (places > 0 ? places : 1);
-    long long tile = 4LL * kThreads / items;
-    tile = std::min(tile, a.tokens / (4LL * sms));
+    const long long full = (long long)kBlocks * sms;          // blocks the GPU holds
+    long long tile = std::min(4LL * kThreads / items, (a.tokens + full - 1) / full);
     tile = std::max(1LL, std::min(tile, (long long)kMaxTile));
     int slices = 1;                          // of the heads
     if (rows > kMaxRows) slices = (rows + kMaxRows - 1) / kMaxRows, tile = 1;
@@ -289,10 +289,8 @@ cudaError_t launch_rotary(DType dt, bool append, RotaryArgs a, cudaStream_t st) 
     a.tile = (int)tile;
     const long long tiles = (a.tokens + a.tile - 1) / a.tile;
     // the GPU full once: the set-up of a block is then paid for by several tiles
-    // (12 x 1365 tokens of 24 heads of 64: 19.8 us against 21.7 with a block a
-    // tile), unless that would leave a short second round
-    const long long full = (long long)kBlocks * sms;
-    const dim3 grid((unsigned)(tiles <= 2 * full ? tiles : full), (unsigned)slices);
+    // (12 x 1365 tokens of 24 heads of 64: 19.8 us against 21.7 with a block a tile)
+    const dim3 grid((unsigned)std::min(tiles, full), (unsigned)slices);
     const size_t smem = (size_t)a.tile * a.rot * sizeof(float);
     if (dt == kF32) return append ? launch_t<float, true>(a, mode, grid, smem, st) : launch_t<float, false>(a, mode, grid, smem, st);
     if (dt == kF16) return append ? launch_t<__half, true>(a, mode, grid, smem, st) : launch_t<__half, false>(a, mode, grid, smem, st);

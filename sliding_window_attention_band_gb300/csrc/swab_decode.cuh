@@ -33,6 +33,7 @@ struct Request {
     int r, m, row0, len, i0;
     const int *trow;     // its row of the block table
     int ring_lo;         // recycled positions below this one are gone
+    int last;            // last position with a column: a context longer than its table (recorded) ends there
 };
 
 constexpr unsigned kDecodeFile = 14;   // site id of the bounds checks in this header
@@ -49,6 +50,9 @@ __device__ __forceinline__ Request request_of(const DecodeArgs &p, int r) {
     q.i0 = q.len - m_all;
     q.trow = p.table + (long long)r * p.cols;
     q.ring_lo = 0;
+    const long long room = (long long)p.cols << p.page_log2;
+    q.last = p.ring || q.len <= room ? 0x7fffffff : (int)room - 1;
+    if (q.last != 0x7fffffff && threadIdx.x == 0) atomicOr(p.err, kErrInvalid);
     if (p.ring && q.len > 0) q.ring_lo = max(((q.len - 1) >> p.page_log2) - (p.cols - p.pinned) + 1, 0) << p.page_log2;
     return q;
 }
@@ -63,7 +67,7 @@ struct KeyList {
 
 __device__ __forceinline__ KeyList keys_of(const DecodeArgs &p, const Request &q, int a_lo, int a_hi) {
     KeyList k;
-    const int lo = q.i0 + a_lo, hi = q.i0 + a_hi;
+    const int lo = q.i0 + a_lo, hi = min(q.i0 + a_hi, q.last);
     k.step = p.stride;
     k.nsink = max(min(p.n_sink, hi + 1), 0);
     int cnt = 0;
@@ -72,9 +76,8 @@ __device__ __forceinline__ KeyList keys_of(const DecodeArgs &p, const Request &q
         k.band_lo = (int)max((long long)lo - p.w, (long long)p.n_sink);
         cnt = max(hi - k.band_lo + 1, 0);
     } else if (lo >= p.n_sink) {
-        const int t = min((lo - p.n_sink) / p.stride, p.w);
-        k.band_lo = lo - t * p.stride;
-        cnt = t + 1;
+        k.band_lo = lo - min((lo - p.n_sink) / p.stride, p.w) * p.stride;
+        if (k.band_lo <= hi) cnt = (hi - k.band_lo) / p.stride + 1;
     }
     k.count = k.nsink + cnt;
     return k;
@@ -96,19 +99,11 @@ __device__ __forceinline__ uint32_t block_line(const DecodeArgs &p, int id, int 
     }
     return (((uint32_t)id * (uint32_t)p.hk + (uint32_t)kvh) << p.page_log2) + (uint32_t)off;
 }
-// Column of position j, or -1 when it has none (a context longer than its
-// table: recorded) or its block has been recycled.
+// Column of position j of a list, or -1 when its block has been recycled.
 __device__ __forceinline__ int key_column(const DecodeArgs &p, const Request &q, int j) {
     const int lb = j >> p.page_log2;
-    int col = lb;
-    if (lb >= p.cols) {
-        if (!p.ring) {
-            atomicOr(p.err, kErrInvalid);
-            return -1;
-        }
-        col = p.pinned + (lb - p.pinned) % (p.cols - p.pinned);
-    }
-    return lb >= p.pinned && j < q.ring_lo ? -1 : col;
+    if (lb >= p.pinned && j < q.ring_lo) return -1;
+    return lb < p.cols ? lb : p.pinned + (lb - p.pinned) % (p.cols - p.pinned);
 }
 __device__ __forceinline__ uint32_t key_line(const DecodeArgs &p, const Request &q, int j, int kvh) {
     [[maybe_unused]] constexpr unsigned kSwabFile = kDecodeFile;

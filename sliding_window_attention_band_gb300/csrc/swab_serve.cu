@@ -148,7 +148,7 @@ swab_status check_cache(const swab_cache_desc *c) {
     if (c->ring != 0 && c->ring != 1) return SWAB_ERR_INVALID_ARG;
     if (c->pinned < 0 || c->pinned >= (c->ring ? c->cols : 1)) return SWAB_ERR_INVALID_ARG;
     if (log2_of(c->page) < 0 || c->batch > 65535) return SWAB_ERR_UNSUPPORTED;
-    if ((long long)c->n_blocks * c->page > 0x7fffffffll) return SWAB_ERR_UNSUPPORTED;
+    if ((long long)c->n_blocks * c->page > 0x7fffff00ll) return SWAB_ERR_UNSUPPORTED;
     return SWAB_OK;
 }
 
@@ -179,6 +179,7 @@ swab_status check_decode(const swab_decode_desc *d) {
     if (d->tokens < 1 || d->h < 1 || d->hk < 1 || d->head_dim < 1 || d->max_q < 1 || d->max_len < 1) return SWAB_ERR_INVALID_ARG;
     if (d->w < 0 || d->w > (1 << 30) || d->dilation < 0 || d->n_sink < 0 || d->prefix_len < 0) return SWAB_ERR_INVALID_ARG;
     if (!good_dtype(d->dtype) || d->h % d->hk != 0) return SWAB_ERR_INVALID_ARG;
+    if (d->prefix_len > (long long)c->n_blocks * c->page) return SWAB_ERR_INVALID_ARG;
     const long long width = (long long)d->h * d->head_dim, vec = 16 / elt(d->dtype);
     for (const int64_t rs : {d->q_row_stride, d->out_row_stride})
         if (rs < 0 || (rs > 0 && rs < width)) return SWAB_ERR_INVALID_ARG;
@@ -193,7 +194,7 @@ swab_status check_decode(const swab_decode_desc *d) {
     if (d->h / d->hk > 128 || d->h > 65535 || (long long)d->tokens * d->h > 0x7fffffffll) return SWAB_ERR_UNSUPPORTED;
     for (const int64_t rs : {d->q_row_stride, d->out_row_stride}) {
         if (rs % vec != 0) return SWAB_ERR_MISALIGNED;
-        if (rs > (1ll << 40)) return SWAB_ERR_UNSUPPORTED;
+        if (rs > (1ll << 36)) return SWAB_ERR_UNSUPPORTED;
     }
     return SWAB_OK;
 }

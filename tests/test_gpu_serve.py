@@ -499,6 +499,30 @@ def test_decode_skips_and_flags_blocks_outside_the_cache():
         assert swab.device_status(reset=True) == INVALID_BIT
 
 
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("case", [dict(), dict(w=30), dict(w=3, dilation=2, n_sink=2), dict(w=20, ring=True)])
+def test_decode_of_lengths_that_make_no_sense(dtype, case):
+    """A length up to the last int32, row starts that go backwards or below zero: the call ends, the other requests are
+    right, and a length past its table is flagged."""
+    c = Decode(dtype, [40, 20, 30], [1, 2, 1], 4, 2, 64, seed=107, **case)
+    want, lse = c.run()
+    for bad in (2 ** 31 - 1, 2 ** 31 - 17, 49):
+        c.lens[0] = bad
+        o, l = c.run()
+        same_bits(o[1:], want[1:])
+        same_bits(l[1:], lse[1:])
+        assert swab.device_status(reset=True) == (0 if c.ring else INVALID_BIT)
+    c.lens[0] = 40
+    for starts in ([-5, 1, 3, 4], [-2 ** 31, 1, 3, 4], [7, 1, 3, 4]):
+        c.q_start = np.array(starts)
+        o, l = c.run()
+        same_bits(o[1:], want[1:])
+        same_bits(l[1:], lse[1:])
+    c.q_start = np.array([0, 1, 3, 2 ** 31 - 1])
+    same_bits(c.run()[0][:3], want[:3])
+    assert swab.device_status(reset=True) == 0
+
+
 def test_decode_row_strides_and_optional_lse():
     c = Decode(BF16, [70, 9], [2, 1], 4, 2, 64, seed=102)
     want, lse = c.run()

@@ -100,6 +100,8 @@ def test_rotary_pointers_and_strides(lib):
     assert rotary(lib, rotary_desc({"qo": (2048, 128, 64)})) == INVALID       # 4 heads of 64 in rows of 128
     assert rotary(lib, rotary_desc({"qo": (0, 256, 64)})) == INVALID          # both sequences in one place
     assert rotary(lib, rotary_desc({"ko": (1024, 64, 56)})) == INVALID
+    assert rotary(lib, rotary_desc({"q": (1 << 36, 256, 64)})) == UNSUPPORTED  # over 64 GB
+    assert rotary(lib, rotary_desc({"qo": (1 << 41, 256, 64)})) == UNSUPPORTED
 
 
 @needs_no_gpu
@@ -157,15 +159,17 @@ def test_append_arguments(lib):
     assert append(lib, d, c, vc=FAKE) == INVALID                              # both caches in one place
     assert append(lib, rotary_desc(hk=0), c) == INVALID
     assert append(lib, rotary_desc({"v": (1024, 128, 60)}), c) == MISALIGNED
+    assert append(lib, rotary_desc(hk=5000), cache_desc(n_blocks=1 << 20)) == UNSUPPORTED     # 2^32 lines and more
+    assert decode(lib, decode_desc(cache_desc(n_blocks=1 << 26), h=512, hk=256)) == UNSUPPORTED
 
 
 @pytest.mark.parametrize("bad,want", [
     (dict(tokens=0), INVALID), (dict(h=0), INVALID), (dict(hk=0), INVALID), (dict(hk=3), INVALID), (dict(head_dim=0), INVALID),
     (dict(max_q=0), INVALID), (dict(max_len=0), INVALID), (dict(w=-1), INVALID), (dict(w=(1 << 30) + 1), INVALID),
-    (dict(dilation=-1), INVALID), (dict(n_sink=-1), INVALID), (dict(prefix_len=-1), INVALID), (dict(dtype=9), INVALID),
+    (dict(dilation=-1), INVALID), (dict(n_sink=-1), INVALID), (dict(prefix_len=-1), INVALID), (dict(prefix_len=641), INVALID), (dict(dtype=9), INVALID),
     (dict(q_row_stride=64), INVALID), (dict(out_row_stride=-512), INVALID), (dict(head_dim=68), UNSUPPORTED),
     (dict(head_dim=264), UNSUPPORTED), (dict(dilation=16), UNSUPPORTED), (dict(h=258, hk=2), UNSUPPORTED),
-    (dict(tokens=1 << 29), UNSUPPORTED), (dict(q_row_stride=516), MISALIGNED), (dict(out_row_stride=516), MISALIGNED)])
+    (dict(tokens=1 << 29), UNSUPPORTED), (dict(q_row_stride=1 << 37), UNSUPPORTED), (dict(q_row_stride=516), MISALIGNED), (dict(out_row_stride=516), MISALIGNED)])
 def test_decode_descriptor(lib, bad, want):
     d = decode_desc(**bad)
     assert decode(lib, d) == want
