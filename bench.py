@@ -411,6 +411,27 @@ def prologue_and_globals(device, steps, flush, peaks):
     return out
 
 
+def decode_steps(wl, batch, device, steps, flush, peaks):
+    """One step of a running batch that carries the workload's window on, a token
+    for each of `batch` requests past the window (cache_slots, rotary_append,
+    band_decode, captured together)."""
+    from sliding_window_attention_band_gb300.decode_loop import DecodeLoop
+
+    loop = DecodeLoop.from_workload(wl, batch, device)
+    context = wl.w * (wl.dilation + 1) + 200
+    g = torch.Generator(device=device).manual_seed(6)
+    qkv = torch.randn(batch * context, 3 * wl.h, wl.head_dim, generator=g, device=device).to(wl.dtype)
+    loop.fill(qkv, torch.full((batch,), context, dtype=torch.int32, device=device))
+    loop.n_new.fill_(1)
+    loop.qkv.copy_(qkv[:batch])
+    ms = time_graph(loop.step, steps, 3, flush)
+    keys = wl.w + 1 + len(wl.global_idx)
+    nbytes = batch * wl.h * wl.head_dim * loop.q.element_size() * (2 * keys + 10)   # keys, values; qkv, cache, q, out
+    return {"ms": round(ms, 4), "tokens_per_s": round(batch / (ms * 1e-3)), "bound": "hbm",
+            "roofline_frac": round(nbytes / (peaks["hbm_gbs"] * 1e9) / (ms * 1e-3), 4), "bytes": nbytes,
+            "note": f"{batch} requests, one token each: cache_slots, rotary_append, band_decode"}
+
+
 def step_summary(wl, step, per_step, per_kernel, peaks):
     return {"ms_per_step": round(statistics.mean(per_step), 4),
             "ms_per_step_median": round(statistics.median(per_step), 4),
@@ -864,6 +885,8 @@ def main():
             also[f"fused+{feature.replace(' ', '_')}:{wl.name}"] = step_summary(wl, st, ps, pk, peaks)
             del st
         also.update(prologue_and_globals(device, n_also, flush, peaks))
+        for w_, batch in ((wl5, 64), (WORKLOADS[4], 64)):
+            also[f"decode:{w_.name}"] = decode_steps(w_, batch, device, n_also, flush, peaks)
         # the training workload with global tokens through the materialised calls
         w4 = WORKLOADS[4]
         st = GlobStep(w4, device)

@@ -18,6 +18,7 @@ from ._binding import (API_FUNCTIONS, Desc, SwabError, add_bias_transpose,  # no
 from .serve import (CacheDesc, DecodeDesc, RotaryDesc, band_decode,  # noqa: F401
                     band_decode_workspace, cache_slots, rotary, rotary_append, rotary_bwd,
                     rotary_frequencies)
+from .decode_loop import DecodeLoop  # noqa: F401
 from .inputs import WORKLOADS, Workload, seeded_qkvo, workload_inputs  # noqa: F401
 
 __all__ = ["Desc", "SwabError", "add_bias_transpose", "band_qk", "band_softmax",
@@ -27,7 +28,7 @@ __all__ = ["Desc", "SwabError", "add_bias_transpose", "band_qk", "band_softmax",
            "band_attention_bwd_noalloc",
            "band_attention_bwd_workspace", "band_attention_dropout_mask_bytes", "device_status", "selftest_wait_timeout", "bounds_checked", "bounds_report",
            "selftest_bounds", "load",
-           "CacheDesc", "DecodeDesc", "RotaryDesc", "rotary_frequencies", "rotary", "rotary_bwd",
+           "CacheDesc", "DecodeDesc", "DecodeLoop", "RotaryDesc", "rotary_frequencies", "rotary", "rotary_bwd",
            "cache_slots", "rotary_append", "band_decode", "band_decode_workspace",
            "library_path", "version", "status_string", "WORKLOADS", "Workload",
            "seeded_qkvo", "workload_inputs"]

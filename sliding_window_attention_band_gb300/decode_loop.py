@@ -1,0 +1,96 @@
+"""A running batch that answers with the banded attention.
+
+``DecodeLoop`` holds what a serving program keeps between steps -- the paged
+cache, the block table, the free list, lengths, descriptors, workspace -- and
+runs one step of it:
+
+    loop = DecodeLoop(batch, h, hk, head_dim, w, max_new=4)
+    loop.fill(qkv, n_new)               # prompts: into the cache
+    loop.n_new.fill_(1)                 # one token for every request
+    loop.qkv[:batch].copy_(projection)  # its Q, K, V heads side by side
+    loop.step()                         # loop.out, loop.lse: rows loop.q_start[r] ..
+
+A step needs no value on the host, so it can be captured once in a CUDA graph
+and replayed.  Every computation is one of the library's calls: cache_slots,
+rotary_append, band_decode.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import serve
+
+
+class DecodeLoop:
+    """A batch of requests of h query and hk key heads under a window of ``w``
+    keys on the left (dilation, ``n_sink`` leading global tokens), at most
+    ``max_new`` tokens a request and step.  The blocks of a request are
+    recycled as its window moves on, so the cache does not grow with the
+    context.  Rotary positions turn the whole head unless ``rot_dim`` says
+    less (0: none); ``turns`` and ``rotary_scale`` as rotary_frequencies gives
+    them."""
+
+    def __init__(self, batch, h, hk, head_dim, w, dilation=0, n_sink=0, max_new=1, page=64, rot_dim=None, turns=None,
+                 rotary_scale=1.0, dtype=torch.bfloat16, device="cuda"):
+        self.batch, self.h, self.hk, self.head_dim, self.dtype = batch, h, hk, head_dim, dtype
+        self.rot_dim, self.rotary_scale = head_dim if rot_dim is None else rot_dim, rotary_scale
+        pinned = -(-n_sink // page)
+        cols = pinned + -(-(w * (dilation + 1) + max_new - 1) // page) + 1
+        self.cache = serve.CacheDesc(batch, page, batch * cols, cols, ring=True, pinned=pinned)
+        if self.rot_dim and turns is None:
+            turns, self.rotary_scale = serve.rotary_frequencies(self.rot_dim)
+        self.turns = turns.to(device) if self.rot_dim else None
+        i32 = dict(dtype=torch.int32, device=device)
+        new = dict(dtype=dtype, device=device)
+        self.Kc = torch.zeros(batch * cols, hk, page, head_dim, **new)
+        self.Vc = torch.zeros_like(self.Kc)
+        self.table = torch.full((batch, cols), -1, **i32)
+        self.free_list = torch.arange(batch * cols, **i32)
+        self.lens, self.used, self.q_start = torch.zeros(batch, **i32), torch.zeros(2, **i32), torch.zeros(batch + 1, **i32)
+        self.tokens = batch * max_new
+        self.n_new = torch.zeros(batch, **i32)
+        self.slots, self.pos = torch.zeros(self.tokens, **i32), torch.zeros(self.tokens, **i32)
+        self.qkv = torch.zeros(self.tokens, h + 2 * hk, head_dim, **new)
+        self.q = torch.zeros(self.tokens, h, head_dim, **new)
+        self.out = torch.zeros_like(self.q)
+        self.lse = torch.zeros(self.tokens, h, dtype=torch.float32, device=device)
+        self._rotary = serve.RotaryDesc(1, self.tokens, h, hk, head_dim, self.rot_dim, scale=self.rotary_scale, dtype=dtype)
+        self._decode = serve.DecodeDesc(self.cache, self.tokens, h, hk, head_dim, w=w, dilation=dilation, n_sink=n_sink,
+                                        max_q=max_new, max_len=1 << 30, dtype=dtype)
+        need = serve.band_decode_workspace(self._decode)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        self.scale = head_dim ** -0.5
+
+    def _place(self, n_new, slots, pos):
+        serve.cache_slots(self.cache, self.lens, n_new, self.table, self.free_list, self.used, self.lens, self.used, self.q_start,
+                          slots, pos)
+
+    def fill(self, qkv, n_new):
+        """Prompts of n_new[r] tokens (int32 [batch]) into the cache: the rows of
+        qkv [tokens, h + 2 hk, head_dim] request by request.  Returns the rotated
+        queries [tokens, h, head_dim]; their attention over the whole prompt is
+        band_attention's."""
+        T = qkv.shape[0]
+        slots, pos = torch.empty(T, dtype=torch.int32, device=qkv.device), torch.empty(T, dtype=torch.int32, device=qkv.device)
+        self._place(n_new, slots, pos)
+        q, k, v = qkv.split([self.h, self.hk, self.hk], dim=1)
+        d = serve.RotaryDesc(1, T, self.h, self.hk, self.head_dim, self.rot_dim, scale=self.rotary_scale, dtype=self.dtype)
+        out = torch.empty(T, self.h, self.head_dim, dtype=self.dtype, device=qkv.device)
+        serve.rotary_append(d, self.cache, self.turns, q, k, v, pos, slots, out, self.Kc, self.Vc)
+        return out
+
+    def step(self):
+        """n_new[r] tokens for every request, their heads in the rows of ``qkv``;
+        the attention in ``out`` and ``lse``."""
+        self._place(self.n_new, self.slots, self.pos)
+        q, k, v = self.qkv.split([self.h, self.hk, self.hk], dim=1)
+        serve.rotary_append(self._rotary, self.cache, self.turns, q, k, v, self.pos, self.slots, self.q, self.Kc, self.Vc)
+        serve.band_decode(self._decode, self.scale, self.q, self.Kc, self.Vc, self.table, self.lens, self.q_start, self.out,
+                          self.lse, self.workspace)
+
+    @classmethod
+    def from_workload(cls, wl, batch=None, device="cuda"):
+        """The loop that carries a named workload's sequences on: its heads,
+        window on the left, dilation and leading global tokens."""
+        n_sink = len(wl.global_idx) if tuple(wl.global_idx) == tuple(range(len(wl.global_idx))) else 0
+        return cls(wl.b if batch is None else batch, wl.h, wl.h, wl.head_dim, wl.w, wl.dilation, n_sink, dtype=wl.dtype, device=device)

@@ -49,7 +49,7 @@ def randn(shape, dtype, seed, scale=1.0):
 
 
 def i32(x):
-    return torch.tensor(x, dtype=torch.int32).cuda()
+    return torch.tensor(np.asarray(x), dtype=torch.int32).cuda()
 
 
 def bits(t):
@@ -725,6 +725,48 @@ def test_last_rows_agree_with_the_banded_forward():
     # each side is within A (2^-11 weights + sums) + half a step of the exact value, A <= 4.5
     bound = 2 * (4.5 * (2.0 ** -11 + 2.0 ** -13) + 4.5 * 2.0 ** -11)
     assert (o.float() - O[:, -m:].transpose(0, 1).float()).abs().max().item() <= bound
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_decode_loop_matches_attention_over_the_sequences(dtype):
+    """DecodeLoop: prompts of different lengths, then steps of 0 to 2 tokens a request, dilation and sinks."""
+    B, h, hd, w, dil, sink, steps = 3, 2, 64, 9, 1, 2, 12
+    loop = swab.DecodeLoop(B, h, h, hd, w, dil, sink, max_new=2, page=16, rot_dim=0, dtype=dtype)
+    rng = np.random.default_rng(12)
+    first, news = np.array([40, 1, 17]), rng.integers(0, 3, (steps, B))
+    data = [randn((int(first[r] + news[:, r].sum()), 3 * h, hd), dtype, 500 + r) for r in range(B)]
+    loop.fill(torch.cat([data[r][:first[r]] for r in range(B)]), i32(first))
+    at, got = list(first), [[] for _ in range(B)]
+    for t in range(steps):
+        loop.n_new.copy_(i32(news[t]))
+        rows = torch.cat([data[r][at[r]:at[r] + news[t][r]] for r in range(B)])
+        loop.qkv[:len(rows)] = rows
+        loop.step()
+        pos = 0
+        for r in range(B):
+            got[r].append(loop.out[pos:pos + news[t][r]].clone())
+            pos += news[t][r]
+            at[r] += int(news[t][r])
+    assert loop.lens.tolist() == [len(x) for x in data] and loop.used.tolist()[1] == 0
+    for r in range(B):
+        x, out = f64(data[r]), f64(torch.cat(got[r]))
+        for i in range(int(first[r]), len(data[r])):
+            keys = orc.keys_of(i, w, dil, sink)
+            for hh in range(h):
+                k, v = x[keys, h + hh], x[keys, 2 * h + hh]
+                s = k @ x[i, hh] * hd ** -0.5
+                p = np.exp(s - s.max())
+                A = p @ np.abs(v) / p.sum()
+                # weights and result rounded to the type once each, fp32 sums of at most 64 products and 12 keys
+                bound = A * ((half_step(dtype) if dtype != F32 else 0) + 2.0 ** -17) + (A + 1) * half_step(dtype)
+                assert (np.abs(out[i - first[r], hh] - p @ v / p.sum()) <= bound).all()
+
+
+@pytest.mark.parametrize("name", ["tiny_fp32_n512_w32", "longformer_base_fp16_n4096_w256_d3", "train_bf16_b12_n4096_w256_g16"])
+def test_run_workload_decodes(name):
+    res = subprocess.run([sys.executable, "-m", "sliding_window_attention_band_gb300.run_workload", "--workload", name, "--call",
+                          "decode", "--repeat", "3"], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout + res.stderr[-2000:]
 
 
 @pytest.mark.skipif(os.environ.get("SWAB_BOUNDS_CHECK") == "1", reason="is that run")
