@@ -3,8 +3,8 @@
 // parts of a split key axis.
 //
 // A query's keys are a list: the shared prefix, the leading global tokens, the
-// band (ascending).  The list is cut into pieces; a block takes one (request,
-// query head, piece) and runs through it once with the running maximum m and
+// band (ascending).  The list is cut into pieces; a block takes a request, up to
+// four query heads of a key head and a piece, and runs through it once with the running maximum m and
 // sum l of the softmax, in log2 units and fp32:
 //     m' = max(m, x),  l' = l 2^(m - m') + 2^(x - m'),  o' = o 2^(m - m') + 2^(x - m') v.
 // The pieces are joined as O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
@@ -34,97 +34,145 @@ __device__ __forceinline__ void widen16(const uint4 &v, float *f) {
 
 // A key belongs to a group of kLanes lanes, 16 bytes of its row a lane (kVec
 // times when the row has more than 32 pieces); kThreads / kLanes keys at a time.
-template <typename T, int kLanes, int kVec>
+// A block answers kR query heads that share the key head, so a key is loaded
+// once for them.
+template <typename T, int kLanes, int kVec, int kR>
 __global__ void __launch_bounds__(kThreads) k_decode_general(const __grid_constant__ DecodeArgs p) {
-    constexpr int kV = 16 / sizeof(T), kE = kV * kVec, kGroups = kThreads / kLanes;
+    constexpr int kV = 16 / sizeof(T), kE = kV * kVec, kGroups = kThreads / kLanes, kU = kVec == 1 ? 4 : 2;
     __shared__ float so[kGroups][kLanes * kE];
     __shared__ float2 sml[kGroups];
-    const int split = blockIdx.x, head = blockIdx.y, r = blockIdx.z;
-    const int kvh = head / p.group, sub = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const int per = (p.group + kR - 1) / kR;                       // blocks of a key head
+    const int split = blockIdx.x, kvh = blockIdx.y / per, g0 = blockIdx.y % per * kR, r = blockIdx.z;
+    const int head0 = kvh * p.group + g0, nr = min(kR, p.group - g0);
+    const int sub = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int pieces = p.hd / kV;
     pdl_trigger();                   // k_decode_join, which waits for this grid
     const Request q = request_of(p, r);
     for (int a = 0; a < q.m; ++a) {
         const KeyList keys = keys_of(p, q, a, a);
-        const long long n = keys.count + p.prefix_len, lo = (long long)split * p.chunk;
+        const long long n = (long long)keys.count + p.prefix_len, lo = (long long)split * p.chunk;
         const long long hi = split == p.nsplit - 1 ? n : min(n, lo + p.chunk);
         const long long row = q.row0 + a;
-        const T *qrow = reinterpret_cast<const T *>(p.Q) + row * p.q_stride + (long long)head * p.hd;
-        float qf[kE], o[kE], m = -INFINITY, l = 0.f;
+        float qf[kR][kE], o[kR][kE], m[kR], l[kR];
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            const int piece = lane + v * kLanes;
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (piece < pieces) raw = *reinterpret_cast<const uint4 *>(GPN(p.bnd, qrow + piece * kV, 16));
-            widen16<T>(raw, qf + v * kV);
-        }
-#pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = 0.f;
-        // every lane group makes the same number of steps: the shuffles below
-        // need the whole warp
-        const int steps = lo < hi ? (int)((hi - lo + kGroups - 1) / kGroups) : 0;
-        for (int s = 0; s < steps; ++s) {
-            const long long u = lo + (long long)s * kGroups + sub;
-            uint32_t line = kNoLine;
-            if (u < hi) line = u < p.prefix_len ? prefix_line(p, (int)u, kvh) : key_line(p, q, keys.at((int)(u - p.prefix_len)), kvh);
-            uint4 kr[kVec], vr[kVec];
+        for (int t = 0; t < kR; ++t) {
+            m[t] = -INFINITY;
+            l[t] = 0.f;
+            const T *qrow = reinterpret_cast<const T *>(p.Q) + row * p.q_stride + (long long)(head0 + min(t, nr - 1)) * p.hd;
 #pragma unroll
             for (int v = 0; v < kVec; ++v) {
                 const int piece = lane + v * kLanes;
-                kr[v] = vr[v] = make_uint4(0, 0, 0, 0);
-                if (line != kNoLine && piece < pieces) {
-                    const long long at = (long long)line * p.hd + piece * kV;
-                    kr[v] = ldg16(GPN(p.bnd, reinterpret_cast<const T *>(p.Kc) + at, 16));
-                    vr[v] = ldg16(GPN(p.bnd, reinterpret_cast<const T *>(p.Vc) + at, 16));
+                uint4 raw = make_uint4(0, 0, 0, 0);
+                if (piece < pieces) raw = *reinterpret_cast<const uint4 *>(GPN(p.bnd, qrow + piece * kV, 16));
+                widen16<T>(raw, qf[t] + v * kV);
+            }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[t][e] = 0.f;
+        }
+        // every lane group makes the same number of steps (the shuffles below
+        // need the whole warp), kU keys a step with all their loads in flight
+        const long long span = hi - lo;
+        const int steps = span > 0 ? (int)((span + kGroups * kU - 1) / (kGroups * kU)) : 0;
+        for (int s = 0; s < steps; ++s) {
+            uint32_t line[kU];
+            uint4 kr[kU][kVec], vr[kU][kVec];
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+                const long long u = lo + ((long long)s * kU + i) * kGroups + sub;
+                line[i] = kNoLine;
+                if (u < hi) line[i] = u < p.prefix_len ? prefix_line(p, (int)u, kvh) : key_line(p, q, keys.at((int)(u - p.prefix_len)), kvh);
+            }
+#pragma unroll
+            for (int i = 0; i < kU; ++i)
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) {
+                    const int piece = lane + v * kLanes;
+                    kr[i][v] = vr[i][v] = make_uint4(0, 0, 0, 0);
+                    if (line[i] != kNoLine && piece < pieces) {
+                        const long long at = (long long)line[i] * p.hd + piece * kV;
+                        kr[i][v] = ldg16(GPN(p.bnd, reinterpret_cast<const T *>(p.Kc) + at, 16));
+                        vr[i][v] = ldg16(GPN(p.bnd, reinterpret_cast<const T *>(p.Vc) + at, 16));
+                    }
+                }
+            float x[kR][kU];
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+                float kf[kE];
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) widen16<T>(kr[i][v], kf + v * kV);
+#pragma unroll
+                for (int t = 0; t < kR; ++t) {
+                    x[t][i] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) x[t][i] = fmaf(qf[t][e], kf[e], x[t][i]);
                 }
             }
-            float x = 0.f;
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                float kf[kV];
-                widen16<T>(kr[v], kf);
+            for (int d = kLanes / 2; d > 0; d >>= 1)
 #pragma unroll
-                for (int e = 0; e < kV; ++e) x = fmaf(qf[v * kV + e], kf[e], x);
+                for (int t = 0; t < kR; ++t)
+#pragma unroll
+                    for (int i = 0; i < kU; ++i) x[t][i] += __shfl_xor_sync(0xffffffffu, x[t][i], d);
+#pragma unroll
+            for (int t = 0; t < kR; ++t) {
+                float mn = m[t];
+#pragma unroll
+                for (int i = 0; i < kU; ++i) {
+                    x[t][i] = line[i] == kNoLine ? -INFINITY : x[t][i] * p.scale_log2;
+                    mn = fmaxf(mn, x[t][i]);
+                }
+                const float mb = mn == -INFINITY ? 0.f : mn;                 // no key yet
+                const float corr = m[t] == -INFINITY ? 0.f : exp2f(m[t] - mb);
+                m[t] = mn;
+                l[t] *= corr;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) o[t][e] *= corr;
+#pragma unroll
+                for (int i = 0; i < kU; ++i) {
+                    x[t][i] = exp2f(x[t][i] - mb);                           // 0 for an absent key
+                    l[t] += x[t][i];
+                }
             }
 #pragma unroll
-            for (int d = kLanes / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-            if (line == kNoLine) continue;
-            x *= p.scale_log2;
-            const float mn = fmaxf(m, x), corr = m == -INFINITY ? 0.f : exp2f(m - mn), pr = exp2f(x - mn);
-            l = fmaf(l, corr, pr);
+            for (int i = 0; i < kU; ++i) {
+                float vf[kE];
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                float vf[kV];
-                widen16<T>(vr[v], vf);
+                for (int v = 0; v < kVec; ++v) widen16<T>(vr[i][v], vf + v * kV);
 #pragma unroll
-                for (int e = 0; e < kV; ++e) o[v * kV + e] = fmaf(pr, vf[e], o[v * kV + e] * corr);
+                for (int t = 0; t < kR; ++t)
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) o[t][e] = fmaf(x[t][i], vf[e], o[t][e]);
             }
-            m = mn;
         }
-        __syncthreads();                 // the previous query's reads of the buffers
 #pragma unroll
-        for (int e = 0; e < kE; ++e) so[sub][lane * kE + e] = o[e];
-        if (lane == 0) sml[sub] = make_float2(m, l);
-        __syncthreads();
-        float M = -INFINITY, L = 0.f;
-        for (int g = 0; g < kGroups; ++g) M = fmaxf(M, sml[g].x);
-        for (int g = 0; g < kGroups; ++g)
-            if (sml[g].x != -INFINITY) L += sml[g].y * exp2f(sml[g].x - M);
-        const long long th = row * p.h + head;
-        for (int c = threadIdx.x; c < p.hd; c += kThreads) {
-            const int piece = c / kV, at = piece % kLanes * kE + piece / kLanes * kV + c % kV;
-            float y = 0.f;
+        for (int t = 0; t < kR; ++t) {
+            if (t >= nr) break;
+            __syncthreads();             // the previous head's reads of the buffers
+#pragma unroll
+            for (int e = 0; e < kE; ++e) so[sub][lane * kE + e] = o[t][e];
+            if (lane == 0) sml[sub] = make_float2(m[t], l[t]);
+            __syncthreads();
+            float M = -INFINITY, L = 0.f;
+            for (int g = 0; g < kGroups; ++g) M = fmaxf(M, sml[g].x);
             for (int g = 0; g < kGroups; ++g)
-                if (sml[g].x != -INFINITY) y += so[g][at] * exp2f(sml[g].x - M);
-            if (p.nparts > 1)
-                *GP(p.bnd, p.po + (th * p.nparts + split) * p.hd + c) = y;
-            else
-                *GP(p.bnd, reinterpret_cast<T *>(p.O) + row * p.o_stride + (long long)head * p.hd + c) =
-                    Elt<T>::from_f(L > 0.f ? y / L : 0.f);
-        }
-        if (threadIdx.x == 0) {
-            if (p.nparts > 1) *GP(p.bnd, p.pml + th * p.nparts + split) = make_float2(M, L);
-            else if (p.lse) *GP(p.bnd, p.lse + th) = lse_of(M, L);
+                if (sml[g].x != -INFINITY) L += sml[g].y * exp2f(sml[g].x - M);
+            const int head = head0 + t;
+            const long long th = row * p.h + head;
+            for (int c = threadIdx.x; c < p.hd; c += kThreads) {
+                const int piece = c / kV, at = piece % kLanes * kE + piece / kLanes * kV + c % kV;
+                float y = 0.f;
+                for (int g = 0; g < kGroups; ++g)
+                    if (sml[g].x != -INFINITY) y += so[g][at] * exp2f(sml[g].x - M);
+                if (p.nparts > 1)
+                    *GP(p.bnd, p.po + (th * p.nparts + split) * p.hd + c) = y;
+                else
+                    *GP(p.bnd, reinterpret_cast<T *>(p.O) + row * p.o_stride + (long long)head * p.hd + c) =
+                        Elt<T>::from_f(L > 0.f ? y / L : 0.f);
+            }
+            if (threadIdx.x == 0) {
+                if (p.nparts > 1) *GP(p.bnd, p.pml + th * p.nparts + split) = make_float2(M, L);
+                else if (p.lse) *GP(p.bnd, p.lse + th) = lse_of(M, L);
+            }
         }
     }
 }
@@ -216,16 +264,21 @@ __global__ void __launch_bounds__(kThreads) k_decode_join(const __grid_constant_
     if (lane == 0 && p.lse) *GP(p.bnd, p.lse + th) = lse_of(M, L);
 }
 
+template <typename T, int kR>
+cudaError_t launch_general_r(const DecodeArgs &a, cudaStream_t st) {
+    const dim3 grid((unsigned)a.nsplit, (unsigned)(a.hk * ((a.group + kR - 1) / kR)), (unsigned)a.batch);
+    const int pieces = a.hd * (int)sizeof(T) / 16;
+    if (pieces <= 4) k_decode_general<T, 4, 1, kR><<<grid, kThreads, 0, st>>>(a);
+    else if (pieces <= 8) k_decode_general<T, 8, 1, kR><<<grid, kThreads, 0, st>>>(a);
+    else if (pieces <= 16) k_decode_general<T, 16, 1, kR><<<grid, kThreads, 0, st>>>(a);
+    else if (pieces <= 32) k_decode_general<T, 32, 1, kR><<<grid, kThreads, 0, st>>>(a);
+    else k_decode_general<T, 32, 2, kR><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_general_t(const DecodeArgs &a, cudaStream_t st) {
-    const dim3 grid((unsigned)a.nsplit, (unsigned)a.h, (unsigned)a.batch);
-    const int pieces = a.hd * (int)sizeof(T) / 16;
-    if (pieces <= 4) k_decode_general<T, 4, 1><<<grid, kThreads, 0, st>>>(a);
-    else if (pieces <= 8) k_decode_general<T, 8, 1><<<grid, kThreads, 0, st>>>(a);
-    else if (pieces <= 16) k_decode_general<T, 16, 1><<<grid, kThreads, 0, st>>>(a);
-    else if (pieces <= 32) k_decode_general<T, 32, 1><<<grid, kThreads, 0, st>>>(a);
-    else k_decode_general<T, 32, 2><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return a.group == 1 ? launch_general_r<T, 1>(a, st) : launch_general_r<T, 4>(a, st);
 }
 
 template <typename T>

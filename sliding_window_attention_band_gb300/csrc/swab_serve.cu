@@ -224,9 +224,9 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
         least = 256;
     } else {
         keys += d->prefix_len;
-        blocks *= d->h;
+        blocks *= d->hk * ((group + 3) / 4);
         hold = 8 * kSms;
-        least = 256;
+        least = 64;
     }
     const long long want = std::max<long long>(1, hold / blocks);
     const long long chunk = std::max<long long>(least, ((keys + want - 1) / want + 63) / 64 * 64);
