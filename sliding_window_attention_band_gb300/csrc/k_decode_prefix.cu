@@ -50,11 +50,6 @@ template <int HD, bool kPair> struct Shape {
     static constexpr int kQ = (kPair ? 2 : 1) * kQ1;
     static constexpr int kSlots = HD == 64 ? 10 : kPair ? 5 : 6;   // ring of K and V tiles
     static constexpr int kSmem = kQ + kSlots * kTile + 512 + 1024;
-    // One row tile: the product of a chunk's first half starts under the
-    // exponentials of the second (32 requests' worth of rows, 8 x 32k keys: 33.8
-    // -> 32.9 us).  With two the issuing warp waits for one stream while the
-    // other is ready (42.5 -> 44.0 us), so there a chunk is signalled whole.
-    static constexpr bool kEarly = !kPair;
     static constexpr uint32_t kColS = 0, kColO = 256;    // S_g at 128 g (P_g over it), O_g at 256 + HD g
 };
 
@@ -62,6 +57,18 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " elect.sync _|p, 0xffffffff;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(yes));
+    return yes != 0;
 }
 // a whole 32-byte sector: rows of parts lie far apart, so a warp's store
 // fills 32 of them
@@ -84,8 +91,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + kSlots * S::kTile);
     uint64_t *qfull = bars, *full = bars + 1, *empty = full + kSlots;
     uint64_t *sfull = empty + kSlots;            // [2] a stream's S is written
-    uint64_t *pfull = sfull + 2;                 // [2][2] P of a chunk or its half is in place: one arrival a softmax warp
-    uint64_t *odone = pfull + 4;                 // [2] its product is done
+    uint64_t *pfull = sfull + 2;                 // [2] its P is in place: one arrival a softmax warp
+    uint64_t *odone = pfull + 2;                 // [2] its product is done
     uint64_t *done = odone + 2;
     uint32_t *holder = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(holder + 1);
@@ -117,9 +124,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], kWorkers / 2);
             mbar_init(&odone[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&pfull[i], kWorkers / 2);
         mbar_init(done, 1);
         *abort_flag = 0;
         *no_abort = 0;
@@ -179,57 +186,116 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(qfull, 0, no_abort, nullptr, 100000000ull);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr bool kBf16 = !std::is_same<T, __half>::value;
-            constexpr uint32_t idesc_s = idesc_f16(kBQ, kBK, kBf16, false, false);
-            constexpr uint32_t idesc_o = idesc_f16(kBQ, HD, kBf16, false, true);
-            const uint64_t qdesc = sdesc_sw128(smem_u32(qtile), 16, 1024);
-            const uint64_t kdesc = sdesc_sw128(smem_u32(ring), 16, 1024);
-            // V as an MN-major operand: 64-channel blocks one tile half apart
-            const uint64_t vdesc = sdesc_sw128(smem_u32(ring), kBK * 128, 1024);
-            // job j: stream j mod 2, its chunk number j / 2, chunk `c` of the block
-            const int jobs = kPair ? 2 * n : n;
-            auto scores = [&](int j) -> bool {       // S = Q K^T
-                const int g = j & 1, c = kPair ? j >> 1 : j, it = 2 * c, slot = it % kSlots;
-                if (!mbar_wait(&full[slot], (it / kSlots) & 1, abort_flag, p.err)) return false;
-                tc_fence_after();
-                const uint64_t qa = qdesc + (uint64_t)((kPair ? g * S::kQ1 : 0) >> 4);
-                const uint64_t ka = kdesc + (uint64_t)((slot * S::kTile) >> 4);
+        // The whole warp walks the loop and one lane issues: descriptors and
+        // addresses then stay in uniform registers.  With the loop itself under
+        // one lane each instruction moved its six operands there first and 16 of
+        // them took 2100 cycles against the 1024 of the tensor cores.
+        constexpr bool kBf16 = !std::is_same<T, __half>::value;
+        constexpr uint32_t idesc_s = idesc_f16(kBQ, kBK, kBf16, false, false);
+        constexpr uint32_t idesc_o = idesc_f16(kBQ, HD, kBf16, false, true);
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t qdesc = sdesc_sw128(smem_u32(qtile), 16, 1024);
+        const uint64_t kdesc = sdesc_sw128(smem_u32(ring), 16, 1024);
+        // V as an MN-major operand: 64-channel blocks one tile half apart
+        const uint64_t vdesc = sdesc_sw128(smem_u32(ring), kBK * 128, 1024);
+        auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.err));
+        };
+        // ring position and phase of a tile
+        struct Place {
+            int slot;
+            uint32_t phase;
+            __device__ __forceinline__ void step(int by) {
+                slot += by;
+                if (slot >= kSlots) {
+                    slot -= kSlots;
+                    phase ^= 1u;
+                }
+            }
+        };
+        auto scores = [&](int g, const Place &k_at, bool last_use) {       // S = Q K^T
+            const uint64_t qa = qdesc + (uint64_t)((kPair ? g * S::kQ1 : 0) >> 4);
+            const uint64_t ka = kdesc + (uint64_t)((k_at.slot * S::kTile) >> 4);
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
                 for (int h = 0; h < S::kHalves; ++h)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_f16_ss(tmem + S::kColS + kBK * g, qa + (uint64_t)((h * kBQ * 128) >> 4) + 2 * k,
+                        mma_f16_ss(tm + S::kColS + kBK * g, qa + (uint64_t)((h * kBQ * 128) >> 4) + 2 * k,
                                    ka + (uint64_t)((h * kBK * 128) >> 4) + 2 * k, idesc_s, (h > 0 || k > 0) ? 1u : 0u);
-                if (!kPair || g == 1) mma_commit(&empty[slot]);
                 mma_commit(&sfull[g]);
-                return true;
-            };
-            auto product = [&](int j) -> bool {      // O += P V
-                const int g = j & 1, i = j >> 1, c = kPair ? i : j, it = 2 * c + 1, slot = it % kSlots;
-                if (!mbar_wait(&full[slot], (it / kSlots) & 1, abort_flag, p.err)) return false;
-                const uint64_t va = vdesc + (uint64_t)((slot * S::kTile) >> 4);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if ((half == 0 || S::kEarly) && !mbar_wait(&pfull[2 * g + half], i & 1, abort_flag, p.err)) return false;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 4 * half; k < 4 * half + 4; ++k)
-                        mma_f16_ts(tmem + S::kColO + HD * g, tmem + S::kColS + kBK * g + 8 * k, va + (uint64_t)((2048 * k) >> 4),
-                                   idesc_o, (i == 0 && k == 0) ? 0u : 1u);
-                }
-                if (!kPair || g == 1) mma_commit(&empty[slot]);
-                mma_commit(&odone[g]);
-                return true;
-            };
-            bool ok = mbar_wait(qfull, 0, abort_flag, p.err) && scores(0) && (jobs < 2 || scores(1));
-            for (int j = 0; j < jobs && ok; ++j) {
-                ok = product(j);
-                if (ok && j + 2 < jobs) ok = mbar_wait(&odone[j & 1], (j >> 1) & 1, abort_flag, p.err) && scores(j + 2);
+                if (last_use) mma_commit(&empty[k_at.slot]);
             }
+            __syncwarp();
+        };
+        auto product = [&](int g, const Place &v_at, uint32_t more, bool last_use) {      // O += P V
+            const uint64_t va = vdesc + (uint64_t)((v_at.slot * S::kTile) >> 4);
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                    mma_f16_ts(tm + S::kColO + HD * g, tm + S::kColS + kBK * g + 8 * k, va + (uint64_t)((2048 * k) >> 4), idesc_o,
+                               k == 0 ? more : 1u);
+                mma_commit(&odone[g]);
+                if (last_use) mma_commit(&empty[v_at.slot]);
+            }
+            __syncwarp();
+        };
+        bool ok = wait(qfull, 0);
+        if constexpr (kPair) {
+            // both streams over the chunks: a tile is waited for by the first one
+            Place k_at{0, 0}, v_at{1, 0};
+            if (ok && (ok = wait(&full[0], 0))) {
+                scores(0, k_at, false);
+                scores(1, k_at, true);
+            }
+            for (int i = 0; i < n && ok; ++i) {
+                const uint32_t par = i & 1;
+                const bool go = i + 1 < n;
+                ok = wait(&full[v_at.slot], v_at.phase) && wait(&pfull[0], par);
+                if (!ok) break;
+                product(0, v_at, i > 0, false);
+                if (go) {
+                    k_at.step(2);
+                    if (!(ok = wait(&full[k_at.slot], k_at.phase) && wait(&odone[0], par))) break;
+                    scores(0, k_at, false);
+                }
+                if (!(ok = wait(&pfull[1], par))) break;
+                product(1, v_at, i > 0, true);
+                if (go) {
+                    if (!(ok = wait(&odone[1], par))) break;
+                    scores(1, k_at, true);
+                    v_at.step(2);
+                }
+            }
+        } else {
+            // the streams take the chunks in turn
+            Place k_at{0, 0}, v_at{1, 0};        // of the next scores, of the next product
+            for (int c = 0; c < n && c < 2 && ok; ++c) {
+                if (!(ok = wait(&full[k_at.slot], k_at.phase))) break;
+                scores(c, k_at, true);
+                k_at.step(2);
+            }
+            for (int c = 0; c < n && ok; ++c) {
+                const int g = c & 1;
+                const uint32_t par = (c >> 1) & 1;
+                if (!(ok = wait(&full[v_at.slot], v_at.phase) && wait(&pfull[g], par))) break;
+                product(g, v_at, c > 1, true);
+                v_at.step(2);
+                if (c + 2 < n) {
+                    if (!(ok = wait(&full[k_at.slot], k_at.phase) && wait(&odone[g], par))) break;
+                    scores(g, k_at, true);
+                    k_at.step(2);
+                }
+            }
+        }
+        if (leader) {
             mma_commit(done);                    // nothing is in flight when tensor memory is freed
             mbar_wait(done, 0, no_abort, nullptr, 100000000ull);
         }
+        __syncwarp();
     } else {
         // ---------------- softmax: thread = row of stream g ----------------
         const int quarter = warp & 3, g = (warp - 2) >> 2, row = 32 * quarter + lane;
@@ -240,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float xs = p.scale_log2 == 0.f ? 1e-37f : p.scale_log2;
         const bool neg = xs < 0.f;
         const float never = neg ? INFINITY : -INFINITY;
+        const bool real = row < p.pre_tokens * p.group;          // not one of the tile's spare rows, which hold anything
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int i = 0; i < mine; ++i) {
@@ -289,72 +356,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!((vm[v] >> k) & 1u)) x[k] = __float_as_uint(never);
                 }
             };
-            float best = never;
+            // P of the chunk against the reference mb, its sum and largest weight
+            uint32_t pk[kBK / 2];
+            auto weigh = [&](float mb, float &sum) -> float {
+                const uint64_t xs2 = f2(xs, xs), nb2 = f2(-mb, -mb);
+                uint64_t ls[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+                float top[2] = {0.f, 0.f};
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                uint32_t x[32];
-                take(v, x);
-                float ext[4];
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t x[32];
+                    take(v, x);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t *y = x + 8 * k;
-#define F(i) __uint_as_float(y[i])
-                    float a = neg ? min3(F(0), F(1), F(2)) : max3(F(0), F(1), F(2));
-                    a = neg ? min3(a, F(3), F(4)) : max3(a, F(3), F(4));
-                    a = neg ? min3(a, F(5), F(6)) : max3(a, F(5), F(6));
-                    ext[k] = neg ? fminf(a, F(7)) : fmaxf(a, F(7));
-#undef F
+                    for (int e = 0; e < 16; ++e) {
+                        float y0, y1;
+                        f2split(fma2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), xs2, nb2), y0, y1);
+                        const float p0 = ex2(y0), p1 = ex2(y1);
+                        top[e & 1] = max3(top[e & 1], p0, p1);
+                        ls[e & 1] = add2(ls[e & 1], f2(p0, p1));
+                        pk[16 * v + e] = pack2<T>(p0, p1);
+                    }
                 }
-                best = neg ? min3(min3(best, ext[0], ext[1]), ext[2], ext[3]) : max3(max3(best, ext[0], ext[1]), ext[2], ext[3]);
+                float l0, l1;
+                f2split(add2(ls[0], ls[1]), l0, l1);
+                sum = l0 + l1;
+                return fmaxf(top[0], top[1]);
+            };
+            // Almost always no weight passes 2^8 against the reference so far, and
+            // no maximum is needed; else it is found and the weights made again.
+            float sum, corr = 1.f;
+            bool made = false;
+            if (__all_sync(0xffffffffu, m != -INFINITY || !real)) {
+                const float top = weigh(real ? m : 0.f, sum);
+                made = !__any_sync(0xffffffffu, real && top > 256.f);
             }
-            const float cmax = best == never ? -INFINITY : best * xs;
-            const bool raise = cmax > m + kSlack;            // the first time too: m is -inf
-            const float mref = raise ? cmax : m;
-            const float mb = mref == -INFINITY ? 0.f : mref;
-            const bool rescale = raise && m != -INFINITY;
-            const float corr = rescale ? ex2(m - mref) : 1.f;
-            if (__any_sync(0xffffffffu, rescale)) {
-                // (the product before this S is done: see the issuing warp)
+            if (!made) {
+                float best = never;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t x[32];
+                    take(v, x);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        best = neg ? min3(best, __uint_as_float(x[e]), __uint_as_float(x[e + 1]))
+                                   : max3(best, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                }
+                const float cmax = best == never ? -INFINITY : best * xs;
+                const bool raise = cmax > m + kSlack;        // the first time too: m is -inf
+                const bool rescale = raise && m != -INFINITY;
+                corr = rescale ? ex2(m - cmax) : 1.f;
+                if (raise) m = cmax;
+                if (__any_sync(0xffffffffu, rescale)) {
+                    // (the product before this S is done: see the issuing warp)
 #pragma unroll 1
-                for (int k = 0; k < HD / 32; ++k) {
-                    uint32_t o[32];
-                    tmem_ld32(at_o + 32 * k, o);
-                    tmem_ld_wait();
+                    for (int k = 0; k < HD / 32; ++k) {
+                        uint32_t o[32];
+                        tmem_ld32(at_o + 32 * k, o);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                    tmem_st32(at_o + 32 * k, o);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                        tmem_st32(at_o + 32 * k, o);
+                    }
                 }
+                weigh(m == -INFINITY ? 0.f : m, sum);
             }
-            const uint64_t xs2 = f2(xs, xs), nb2 = f2(-mb, -mb);
-            uint64_t ls[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                uint32_t x[32], pk[16];
-                take(v, x);                      // (P of v lands where S of v and before was)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float y0, y1;
-                    f2split(fma2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), xs2, nb2), y0, y1);
-                    const float p0 = ex2(y0), p1 = ex2(y1);
-                    ls[e & 1] = add2(ls[e & 1], f2(p0, p1));
-                    pk[e] = pack2<T>(p0, p1);
-                }
-                tmem_st16(at_s + 16 * v, pk);
-                if (v == 3 || (S::kEarly && v == 1)) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                    mbar_arrive_warp(&pfull[2 * g + (S::kEarly ? v >> 1 : 0)]);
-                }
-            }
-            float l0, l1;
-            f2split(add2(ls[0], ls[1]), l0, l1);
-            l = l * corr + (l0 + l1);
-            m = mref;
+            for (int v = 0; v < 2; ++v) tmem_st32(at_s + 32 * v, *reinterpret_cast<const uint32_t (*)[32]>(pk + 32 * v));
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive_warp(&pfull[g]);
+            l = l * corr + sum;
         }
         // the stream's part
         const int tok = (block * (kPair ? 2 : 1) + (kPair ? g : 0)) * p.pre_tokens + row / p.group;
         const int hh = kvh * p.group + row % p.group;
-        const bool live = row < p.pre_tokens * p.group && tok < p.tokens;
+        const bool live = real && tok < p.tokens;
         const long long at = ((long long)tok * p.h + hh) * p.nparts + p.nsplit + (kPair ? split : 2 * split + g);
         if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(&odone[g], (mine - 1) & 1, abort_flag, p.err));
         if (ok) {
