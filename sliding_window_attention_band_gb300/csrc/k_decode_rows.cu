@@ -5,23 +5,32 @@
 //
 // HBM-bound (4 flops a row for every 2 bytes): what counts is bytes in flight.
 // A warp owns groups of 16 keys (group g of the block's piece goes to warp
-// g mod 4) and runs on its own: it looks the 16 lines up in the block table one
-// stage ahead, brings them in with 16-byte cp.async into a ring of its own, and
-// waits for nobody until the end.  A group is 16 rows x 16 keys of mma.sync
+// g mod kWarps) and runs on its own: it looks the 16 lines up in the block table
+// one stage ahead, brings them in with 16-byte cp.async into a ring of its own,
+// and waits for nobody until the end.  A group is 16 rows x 16 keys of mma.sync
 // m16n8k16 (the rows are few: a 128-row tcgen05 tile would be 7/8 padding and
-// would need the gathered lines staged for it): S = Q K^T with Q in registers,
-// the softmax on the accumulator, O += P V with P repacked in registers (the
-// accumulator's layout is the A operand's).  The running maximum is raised only
-// when a score exceeds it by 2^8, so the usual group needs no exchange between
-// lanes; a weight is rounded to 16 bits for the product (at most 2^8, inside
-// fp16), the sums stay fp32.  Lines of 16-byte pieces are stored with the piece
-// number xor (line mod 8), so the eight lines of an ldmatrix miss each other's
-// banks.  Absent keys are zero-filled, so whatever the cache holds there cannot
-// reach a product.
+// would need the gathered lines staged for it; 32 of these instructions a group
+// are 256 cycles of an SM quarter, a fifth of what the memory takes): S = Q K^T
+// with Q in registers, the softmax on the accumulator, O += P V with P repacked
+// in registers (the accumulator's layout is the A operand's).  The running
+// maximum is raised only when a score exceeds it by 2^8, so the usual group
+// needs no exchange between lanes; a weight is rounded to 16 bits for the
+// product (at most 2^8, inside fp16; the tensor cores take no wider operand at
+// this rate), the sums stay fp32.  Piece c of line r lies at place c xor (r mod
+// 8), so the eight lines of an ldmatrix miss each other's banks.  Absent keys are
+// zero-filled, so whatever the cache holds there cannot reach a product.
 //
 // The warps' (m, l, O) are joined in shared memory; the pieces of a split key
 // list (few requests, long contexts) go to the workspace and are joined by
-// k_decode_join.
+// k_decode_join; the parts of a shared prefix, up to 16 of them, are joined here.
+//
+// 12 warps an SM (168 registers, 16 KB of ring each) in blocks that all fit at
+// once, so that no second wave pays the chain lengths -> table -> keys again:
+// 48 requests of 8 key heads of 128 under a window of 4096 take 110 us (733 MB:
+// 6.7 TB/s) with 384 blocks of 4 warps on 456 places, 128 us cut into three
+// pieces; 8 warps an SM with 3 stages took 149 us.  512 blocks of 4096 keys:
+// 154 us with 3 warps a block, 208 with 4.  One context of 131072: 80 us for
+// 57 x 8 pieces, 86 with the join.
 #include <type_traits>
 
 #include "swab_internal.h"

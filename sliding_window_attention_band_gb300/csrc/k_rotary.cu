@@ -14,9 +14,12 @@
 // for a pair and token, shared by all the heads, so the divisions and the
 // trigonometry cost one thread-step a row and a pair.  Then a thread owns one
 // place in a row (16 bytes of each member of its pairs, 16 bytes of both when
-// interleaved) and walks the rows four at a time, their loads in flight
-// together; consecutive threads cover whole lines.
-// HBM-bound: every value is read once and written once.
+// interleaved) and walks the rows with four loads in flight; consecutive threads cover whole lines.
+// HBM-bound: every value is read once and written once.  8192 tokens of 32 + 8
+// heads of 128: 28 us (168 MB, 6.0 TB/s); 12 x 1365 tokens of 24 heads of 64,
+// half turned, adjacent pairs: 19.7 us (101 MB, 5.1 TB/s); 8.9k tokens into the
+// cache: 18.9 us (82 MB).  The short rows are bound by instructions (62 % of the
+// issue slots): 16 bytes a thread carry the same addresses as 32.
 #include <algorithm>
 
 #include "swab_internal.h"
