@@ -88,6 +88,18 @@ class DecodeLoop:
         serve.band_decode(self._decode, self.scale, self.q, self.Kc, self.Vc, self.table, self.lens, self.q_start, self.out,
                           self.lse, self.workspace)
 
+    def restart(self, requests):
+        """Empty the given requests (a list of row numbers): their blocks go back
+        to the free list.  Reads the number of blocks in use from the device."""
+        rows = torch.tensor(sorted(set(requests)), dtype=torch.long, device=self.table.device)
+        held = self.table[rows]
+        left = torch.cat((self.free_list[int(self.used[0]):], held[held >= 0]))
+        start = self.free_list.numel() - left.numel()
+        self.free_list[start:] = left
+        self.used[0] = start
+        self.table[rows] = -1
+        self.lens[rows] = 0
+
     @classmethod
     def from_workload(cls, wl, batch=None, device="cuda"):
         """The loop that carries a named workload's sequences on: its heads,

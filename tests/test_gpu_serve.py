@@ -95,6 +95,7 @@ ROTARY = [  # b, n, h, hk, hd, rot, interleaved, scaling
     (1, 5000, 2, 1, 64, 32, False, "none"),
     (2, 7, 3, 1, 64, 0, False, "none"),
     (1, 12, 3, 1, 64, 2, True, "none"),
+    (1, 3, 700, 300, 64, 64, False, "none"),      # more heads than a block lists
 ]
 
 
@@ -457,6 +458,40 @@ def test_decode_with_large_scores(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 2, 128)])
+def test_decode_with_scores_that_keep_growing(heads, dtype):
+    """Keys that grow along the prefix and along the own context: the reference is raised again and again, and what was
+    summed so far scaled."""
+    c = Decode(dtype, [700, 300], [1, 2], *heads, page=64, prefix=900, qscale=2.0, seed=108)
+    for p in range(900):
+        c.kc[int(c.ptable[p // 64]), :, p % 64] *= 0.2 + p / 300
+    for r in range(2):
+        for j in range(c.lens[r]):
+            c.kc[int(c.table[r, j // 64]), :, j % 64] *= 0.2 + j / 100
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("case", [dict(h=128, hk=1, hd=64, page=16), dict(h=100, hk=1, hd=128, page=64),
+                                  dict(h=12, hk=4, hd=64, page=128), dict(h=24, hk=8, hd=128, page=32)])
+def test_prefix_row_tiles(case, dtype):
+    """Groups that leave rows of a tile over, one row tile and several, every page size."""
+    for lens, new in (([20, 5], [1, 1]), ([9] * 50, [1] * 50)):
+        Decode(dtype, lens, new, prefix=300, seed=109, **case).check()
+
+
+def test_prefix_with_absent_blocks():
+    """Columns of the prefix that are -1 are skipped without an error; all of them: the own keys alone."""
+    for dtype in (F16, F32):
+        for gone in ([1], [0, 2, 3], list(range(13))):
+            c = Decode(dtype, [20, 5, 3], [1, 1, 2], 4, 2, 64, prefix=200, seed=110)
+            c.ptable = c.ptable.copy()
+            c.ptable[gone] = -1
+            c.check()
+    assert swab.device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("scale", [0.0, -0.125, 1e-4, 3.0])
 def test_decode_scales(dtype, scale):
     """Negative scales turn the order of the scores round, zero makes the weights equal."""
@@ -760,6 +795,34 @@ def test_decode_loop_matches_attention_over_the_sequences(dtype):
                 # weights and result rounded to the type once each, fp32 sums of at most 64 products and 12 keys
                 bound = A * ((half_step(dtype) if dtype != F32 else 0) + 2.0 ** -17) + (A + 1) * half_step(dtype)
                 assert (np.abs(out[i - first[r], hh] - p @ v / p.sum()) <= bound).all()
+
+
+def test_decode_loop_restarts_requests():
+    """A request emptied and filled again answers as a fresh one, in the same captured step."""
+    h, hd, w = 2, 64, 20
+    loop = swab.DecodeLoop(2, h, h, hd, w, page=16, rot_dim=0, dtype=F16)
+    x = randn((2, 60, 3 * h, hd), F16, 600)
+    loop.fill(x[:, :50].reshape(100, 3 * h, hd), i32([50, 50]))
+    loop.n_new.fill_(1)
+    loop.qkv.copy_(x[:, 50])
+    loop.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loop.step()
+    for round_ in range(3):
+        loop.restart([1])
+        loop.fill(x[1, :8 + round_], i32([0, 8 + round_]))
+        loop.qkv[1] = x[1, 8 + round_]
+        graph.replay()
+        assert loop.used.tolist()[1] == 0 and int(loop.lens[1]) == 9 + round_
+        fresh = swab.DecodeLoop(1, h, h, hd, w, page=16, rot_dim=0, dtype=F16)
+        fresh.fill(x[1, :8 + round_], i32([8 + round_]))
+        fresh.n_new.fill_(1)
+        fresh.qkv[0] = x[1, 8 + round_]
+        fresh.step()
+        same_bits(loop.out[1], fresh.out[0])
+        live = loop.table[loop.table >= 0].tolist()
+        assert len(set(live)) == len(live)
 
 
 @pytest.mark.parametrize("name", ["tiny_fp32_n512_w32", "longformer_base_fp16_n4096_w256_d3", "train_bf16_b12_n4096_w256_g16"])
