@@ -797,6 +797,40 @@ def test_decode_loop_matches_attention_over_the_sequences(dtype):
                 assert (np.abs(out[i - first[r], hh] - p @ v / p.sum()) <= bound).all()
 
 
+@pytest.mark.parametrize("hd", [64, 80])
+def test_offsets_past_32_bits(hd):
+    """A cache of more than 2^32 elements a tensor, the blocks in use at its end: the write, decode and the prefix."""
+    page, hk, h, n = 128, 1, 2, 300
+    n_blocks = (1 << 32) // (page * hd) + 4000
+    if torch.cuda.mem_get_info()[0] < 3 * n_blocks * page * hd * 2:
+        pytest.skip("not enough memory")
+    kc, vc = (torch.empty(n_blocks, hk, page, hd, dtype=F16, device="cuda") for _ in range(2))
+    blocks = [n_blocks - 1, n_blocks - 3900, n_blocks - 7, n_blocks - 2, n_blocks - 5]
+    table, ptable = [blocks[:3]], blocks[3:]
+    x = randn((n + 200, h + 2 * hk, hd), F16, 700)
+    q, k, v = x.split([h, hk, hk], dim=1)
+    slots = [blocks[j // page] * page + j % page for j in range(n)] + [ptable[j // page] * page + j % page for j in range(200)]
+    cache = swab.CacheDesc(1, page, n_blocks, 3)
+    d = swab.RotaryDesc(1, n + 200, h, hk, hd, 0, dtype=F16)
+    swab.rotary_append(d, cache, None, None, k, v, None, i32(slots), None, kc, vc)
+    b, o = (torch.tensor(y, device="cuda") for y in ([s // page for s in slots], [s % page for s in slots]))
+    same_bits(kc[b, :, o], k)
+    same_bits(vc[b, :, o], v)
+    dd = swab.DecodeDesc(cache, 1, h, hk, hd, max_len=n, prefix_len=200, dtype=F16)
+    out, lse = torch.empty(1, h, hd, dtype=F16, device="cuda"), torch.empty(1, h, dtype=F32, device="cuda")
+    ws = torch.empty(max(1, swab.band_decode_workspace(dd)), dtype=torch.uint8, device="cuda")
+    swab.band_decode(dd, hd ** -0.5, q[n - 1:n].contiguous(), kc, vc, i32(table), i32([n]), i32([0, 1]), out, lse, ws, i32(ptable))
+    # the same over a small cache
+    small = [c[blocks].contiguous() for c in (kc, vc)]
+    del kc, vc
+    sc = swab.CacheDesc(1, page, 5, 3)
+    sd = swab.DecodeDesc(sc, 1, h, hk, hd, max_len=n, prefix_len=200, dtype=F16)
+    want, wlse = torch.empty_like(out), torch.empty_like(lse)
+    swab.band_decode(sd, hd ** -0.5, q[n - 1:n].contiguous(), *small, i32([[0, 1, 2]]), i32([n]), i32([0, 1]), want, wlse, ws, i32([3, 4]))
+    same_bits(out, want)
+    same_bits(lse, wlse)
+
+
 def test_decode_loop_restarts_requests():
     """A request emptied and filled again answers as a fresh one, in the same captured step."""
     h, hd, w = 2, 64, 20
