@@ -536,8 +536,10 @@ SWAB_API size_t band_decode_workspace(const swab_decode_desc *desc);
  * be finite; the others are never used, whatever they hold.
  * workspace: band_decode_workspace(desc) bytes of device memory, 16-byte
  * aligned (NULL if 0); its contents on entry do not matter, and calls that may
- * overlap on the GPU need one each.  The call launches up to three kernels,
- * ordered on the stream like one.  Results do not depend on timing (no
+ * overlap on the GPU need one each.  The call launches up to three kernels.
+ * They, like those of the rotary and cache calls, are programmatic dependents:
+ * set up while the kernel before them runs, they wait inside for it; for the
+ * caller a call stays ordered on the stream like any kernel launch.  Results do not depend on timing (no
  * atomics). */
 SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, const void *Q,
                                  const void *Kc, const void *Vc, const int32_t *table,

@@ -90,6 +90,8 @@ __global__ void __launch_bounds__(kThreads) k_cache_slots(const __grid_constant_
     __shared__ Chunk c;
     __shared__ unsigned long long sh_taken, sh_missing;
     const int tid = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
     const int used0 = max(*GP(p.bnd, p.used), 0);
     const long long avail = p.n_free > used0 ? p.n_free - used0 : 0;
     if (tid == 0) sh_taken = sh_missing = 0;
@@ -190,13 +192,13 @@ cudaError_t launch_cache_slots(CacheSlotsArgs a, cudaStream_t st) {
     const bool in_place = a.lens_out == a.lens || a.used_out == a.used;
     a.table_pass = 1;
     a.state = !(in_place && blocks > 1);
-    k_cache_slots<<<blocks, kThreads, 0, st>>>(a);
-    if (!a.state) {
+    cudaError_t e = launch_dependent(&k_cache_slots, dim3((unsigned)blocks), kThreads, 0, st, a);
+    if (e == cudaSuccess && !a.state) {
         a.table_pass = 0;
         a.state = 1;
-        k_cache_slots<<<1, kThreads, 0, st>>>(a);
+        e = launch_dependent(&k_cache_slots, dim3(1), kThreads, 0, st, a);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace swab

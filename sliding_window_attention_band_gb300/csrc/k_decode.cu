@@ -50,7 +50,8 @@ __global__ void __launch_bounds__(kThreads) k_decode_general(const __grid_consta
     const int head0 = kvh * p.group + g0, nr = min(kR, p.group - g0);
     const int sub = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int pieces = p.hd / kV;
-    pdl_trigger();                   // k_decode_join, which waits for this grid
+    pdl_wait();
+    pdl_trigger();
     const Request q = request_of(p, r);
     for (int a = 0; a < q.m; ++a) {
         const KeyList keys = keys_of(p, q, a, a);
@@ -192,9 +193,9 @@ __global__ void __launch_bounds__(kThreads) k_decode_join(const __grid_constant_
     const long long th = (long long)blockIdx.x * kPairs + warp / kW;
     const long long row = th / p.h;
     const int head = (int)(th - row * p.h);
-    const bool there = row < p.tokens && row < *GP(p.bnd, p.q_start + p.batch);
     pdl_wait();                                                   // the parts are there
-    if (!there) return;                                           // with kW = 4: the whole block
+    pdl_trigger();
+    if (row >= p.tokens || row >= *GP(p.bnd, p.q_start + p.batch)) return;                                           // with kW = 4: the whole block
     const float2 *ml = p.pml + th * p.nparts;
     const float *po = p.po + th * p.nparts * p.hd;
     float M = -INFINITY, L = 0.f;
@@ -272,12 +273,11 @@ template <typename T, int kR>
 cudaError_t launch_general_r(const DecodeArgs &a, cudaStream_t st) {
     const dim3 grid((unsigned)a.nsplit, (unsigned)(a.hk * ((a.group + kR - 1) / kR)), (unsigned)a.batch);
     const int pieces = a.hd * (int)sizeof(T) / 16;
-    if (pieces <= 4) k_decode_general<T, 4, 1, kR><<<grid, kThreads, 0, st>>>(a);
-    else if (pieces <= 8) k_decode_general<T, 8, 1, kR><<<grid, kThreads, 0, st>>>(a);
-    else if (pieces <= 16) k_decode_general<T, 16, 1, kR><<<grid, kThreads, 0, st>>>(a);
-    else if (pieces <= 32) k_decode_general<T, 32, 1, kR><<<grid, kThreads, 0, st>>>(a);
-    else k_decode_general<T, 32, 2, kR><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    if (pieces <= 4) return launch_dependent(&k_decode_general<T, 4, 1, kR>, grid, kThreads, 0, st, a);
+    if (pieces <= 8) return launch_dependent(&k_decode_general<T, 8, 1, kR>, grid, kThreads, 0, st, a);
+    if (pieces <= 16) return launch_dependent(&k_decode_general<T, 16, 1, kR>, grid, kThreads, 0, st, a);
+    if (pieces <= 32) return launch_dependent(&k_decode_general<T, 32, 1, kR>, grid, kThreads, 0, st, a);
+    return launch_dependent(&k_decode_general<T, 32, 2, kR>, grid, kThreads, 0, st, a);
 }
 
 template <typename T>

@@ -124,8 +124,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x != -1) atomicOr(p.err, kErrInvalid);
         return -1;
     };
-    int id = warp == 0 ? page_id(c0) : -1;       // on its way during the set-up
-
     if (threadIdx.x == 0) {
         mbar_init(qfull, 1);
         for (int i = 0; i < kSlots; ++i) {
@@ -150,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *holder;
+    pdl_wait();
     pdl_trigger();                               // the requests' own keys may start beside this
 
     if (warp == 0) {
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 (block * (kPair ? 2 : 1) + t) * p.pre_tokens);
         }
         __syncwarp();
-        int it = 0;
+        int it = 0, id = page_id(c0);
         bool ok = true;
         for (int c = c0; c < c1 && ok; ++c) {
             const int ahead = page_id(c + 1);
@@ -472,8 +471,7 @@ cudaError_t launch_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtenso
     if (e != cudaSuccess) return e;
     const int tokens = a.pre_tokens * (kPair ? 2 : 1);           // of a block
     const dim3 grid((unsigned)(a.pre_pieces * ((a.tokens + tokens - 1) / tokens)), (unsigned)a.hk);
-    k_decode_prefix<T, HD, kPair><<<grid, kThreads, S::kSmem, st>>>(mq, mk, mv, a);
-    return cudaGetLastError();
+    return launch_dependent(&k_decode_prefix<T, HD, kPair>, grid, kThreads, S::kSmem, st, mq, mk, mv, a);
 }
 
 template <typename T>

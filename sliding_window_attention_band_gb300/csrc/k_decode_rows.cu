@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
     const int split = blockIdx.x, r = blockIdx.z;
     const int kvh = (int)(blockIdx.y % (unsigned)p.hk), tile0 = (int)(blockIdx.y / (unsigned)p.hk);
     const int tiles_y = gridDim.y / p.hk;
-    pdl_trigger();                               // k_decode_join, which waits for this grid
+    if (p.npre == 0) pdl_wait();
+    pdl_trigger();
     const Request q = request_of(p, r);
     uint8_t *ring = smem + warp * S::kRing;
     const uint32_t ring_s = smem_u32(ring);
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
         }
         __syncthreads();                         // the rings are free for the next tile
     }
-    // the join waits for this grid alone: with a shared prefix, end after its kernel
+    // what follows waits for this grid alone: with a shared prefix, end after its kernel
     if (p.npre > 0) pdl_wait();
 }
 
@@ -417,10 +418,10 @@ cudaError_t launch_nt(const DecodeArgs &a, int tiles, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int most = 65535 / a.hk;
     const dim3 grid((unsigned)a.nsplit, (unsigned)(a.hk * (tiles < most ? tiles : most)), (unsigned)a.batch);
-    // behind the prefix kernel it may start at once: it reads nothing of it
-    if (a.npre > 0) return launch_dependent(fn, grid, S::kThreads, S::kSmem, st, a);
-    fn<<<grid, S::kThreads, S::kSmem, st>>>(a);
-    return cudaGetLastError();
+    // Behind the prefix kernel it starts without waiting: it reads nothing of
+    // that kernel before its end, and whatever came before is complete once
+    // that kernel's blocks have passed their wait.
+    return launch_dependent(fn, grid, S::kThreads, S::kSmem, st, a);
 }
 
 template <typename T, int HD>

@@ -164,6 +164,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_const
         }
     };
 
+    pdl_wait();
+    pdl_trigger();
     for (long long t0 = (long long)blockIdx.x * p.tile; t0 < p.tokens; t0 += (long long)gridDim.x * p.tile) {
         const int nt = (int)(p.tokens - t0 < p.tile ? p.tokens - t0 : p.tile);
         const int total = nt * mine;
@@ -262,12 +264,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_const
 
 template <typename T, bool kAppend>
 cudaError_t launch_t(const RotaryArgs &a, int mode, dim3 grid, size_t smem, cudaStream_t st) {
-    switch (mode) {
-        case 0: k_rotary<T, 0, kAppend><<<grid, kThreads, smem, st>>>(a); break;
-        case 1: k_rotary<T, 1, kAppend><<<grid, kThreads, smem, st>>>(a); break;
-        default: k_rotary<T, 2, kAppend><<<grid, kThreads, smem, st>>>(a); break;
-    }
-    return cudaGetLastError();
+    const auto fn = mode == 0 ? &k_rotary<T, 0, kAppend> : mode == 1 ? &k_rotary<T, 1, kAppend> : &k_rotary<T, 2, kAppend>;
+    return launch_dependent(fn, grid, kThreads, smem, st, a);
 }
 
 }  // namespace

@@ -297,6 +297,32 @@ swab_status call_extents(Bounds *b, std::initializer_list<Extent> ext);
 bool encode_tiled(CUtensorMap *map, DType dt, int rank, const void *base, const cuuint64_t *dims,
                   const cuuint64_t *strides, const cuuint32_t *box);
 
+// Programmatic dependents: the kernels for answering are launched so that one
+// may be set up while the kernel before it in the stream still runs.  Each
+// waits for that kernel (pdl_wait: complete, its writes visible) before it
+// touches memory and only then lets the next one be set up (pdl_trigger), so a
+// kernel that has passed its wait knows everything before it in the stream
+// complete.  It saves the launch gap, 1 to 2 us a kernel.  (The one exception, a
+// kernel that starts without waiting, is named where it is launched.)
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launches a kernel as a programmatic dependent of the stream's last one.
+template <typename... A>
+cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------------------
 // answering: rotary positions, block tables, the paged cache, decode
 // ---------------------------------------------------------------------------
