@@ -9,17 +9,20 @@
 // product is off by 0.06 rad at position 10^6.  Its upper 32 bits (2 pi 2^-32
 // rad) become the argument of sincospif (rounded to fp32: 2^-25 pi rad).
 //
-// A block takes a few tokens.  It lists their head rows (where from, where to)
-// and fills a table of their cosines and sines in shared memory -- one sincospi
-// for a pair and token, shared by all the heads, so the divisions and the
-// trigonometry cost one thread-step a row and a pair.  Then a thread owns one
+// A block takes a few tokens at a time.  It lists their head rows (where from,
+// where to) and fills a table of their cosines and sines in shared memory -- one
+// sincospi for a pair and token, shared by all the heads, so the divisions and
+// the trigonometry cost one thread-step a row and a pair.  Then a thread owns one
 // place in a row (16 bytes of each member of its pairs, 16 bytes of both when
-// interleaved) and walks the rows with four loads in flight; consecutive threads cover whole lines.
+// interleaved) and walks the rows with four loads in flight; consecutive threads
+// cover whole lines.  List and table of the next tokens are made under the first
+// loads of these (two buffers, one barrier a tile).
+//
 // HBM-bound: every value is read once and written once.  8192 tokens of 32 + 8
 // heads of 128: 28 us (168 MB, 6.0 TB/s); 12 x 1365 tokens of 24 heads of 64,
-// half turned, adjacent pairs: 19.7 us (101 MB, 5.1 TB/s); 8.9k tokens into the
-// cache: 18.9 us (82 MB).  The short rows are bound by instructions (62 % of the
-// issue slots): 16 bytes a thread carry the same addresses as 32.
+// half turned, adjacent pairs: 18.8 us (101 MB, 5.3 TB/s; 19.8 with one buffer);
+// 8.9k tokens into the cache: 17.1 us (82 MB).  The short rows are bound by
+// instructions: 16 bytes a thread carry the same addresses as 32.
 #include <algorithm>
 
 #include "swab_internal.h"
@@ -133,8 +136,8 @@ template <typename T, int kMode, bool kAppend>
 __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_constant__ RotaryArgs p) {
     constexpr int kV = VecOf<T>::kN, kB = (int)sizeof(T);
     constexpr int kLoads = kMode == 0 ? 2 : 1, kUnroll = 4 / kLoads;   // rows of a thread in flight
-    extern __shared__ __align__(16) float tab[];       // [tile][2][rot / 2]: cos, sin of each token
-    __shared__ Row list[kMaxRows];
+    extern __shared__ __align__(16) float tabs[];      // two of [tile][2][rot / 2]: cos, sin of each token
+    __shared__ Row lists[2][kMaxRows];
     const int half = p.rot / 2;
     const bool vcopy = kMode != 2 || p.rot * kB % 16 == 0;
     // places of a row: those whose pairs turn, then those copied
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_const
     auto place_at = [&](int place) {
         return place < nturn ? 16 * place : vcopy ? (p.rot + (place - nturn) * kV) * kB : (p.rot + place - nturn) * kB;
     };
-    auto fetch = [&](Row (&r)[kUnroll], uint4 (&v)[kUnroll][kLoads], int q, int at, bool copies, int total) {
+    auto fetch = [&](const Row *list, Row (&r)[kUnroll], uint4 (&v)[kUnroll][kLoads], int q, int at, bool copies, int total) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int e = q + u * per_pass;
@@ -163,19 +166,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_const
             if (kMode == 0 && !copies) v[u][kLoads - 1] = load16(GPN(p.bnd, r[u].src() + at + half * kB, 16));
         }
     };
-
-    pdl_wait();
-    pdl_trigger();
-    for (long long t0 = (long long)blockIdx.x * p.tile; t0 < p.tokens; t0 += (long long)gridDim.x * p.tile) {
+    // the rows and the table of the tile at token t0
+    auto prepare = [&](long long t0, Row *list, float *tab) {
         const int nt = (int)(p.tokens - t0 < p.tile ? p.tokens - t0 : p.tile);
-        const int total = nt * mine;
-        for (int e = threadIdx.x; e < total; e += kThreads) {
+        for (int e = threadIdx.x; e < nt * mine; e += kThreads) {
             const unsigned tt = mine > 1 ? __umulhi(e, by_mine) : e;
             list[e] = row_of<kAppend>(p, (unsigned)t0 + tt, tt, lo + e - tt * mine);
         }
-        for (int e = threadIdx.x; e < nt * half; e += kThreads) {
+        for (int e = kThreads - 1 - threadIdx.x; e < nt * half; e += kThreads) {   // (the threads without a row first)
             const unsigned tt = half > 1 ? __umulhi(e, by_half) : e, k = e - tt * half, t = (unsigned)t0 + tt;
-            const long long at = (p.pos ? (long long)*GP(p.bnd, p.pos + t) : (long long)(t % (unsigned)p.n)) + p.pos0;
+            const long long at = (p.pos ? (long long)*GP(p.bnd, p.pos + t) : (long long)(t % p.n)) + p.pos0;
             // the upper 32 bits of the fraction of a turn: half turns in [-1, 1)
             const int frac = (int)(((unsigned long long)at * *GP(p.bnd, p.turns + k)) >> 32);
             float sn, cs;
@@ -183,7 +183,24 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_const
             tab[(2 * tt) * half + k] = cs * p.scale;
             tab[(2 * tt + 1) * half + k] = sn * (p.backward ? -p.scale : p.scale);
         }
-        __syncthreads();
+    };
+
+    pdl_wait();
+    pdl_trigger();
+    const long long step = (long long)gridDim.x * p.tile;
+    int buf = 0;
+    prepare((long long)blockIdx.x * p.tile, lists[0], tabs);
+    for (long long t0 = (long long)blockIdx.x * p.tile; t0 < p.tokens; t0 += step, buf ^= 1) {
+        const int total = (int)(p.tokens - t0 < p.tile ? p.tokens - t0 : p.tile) * mine;
+        const Row *list = lists[buf];
+        const float *tab = tabs + buf * p.tile * p.rot;
+        __syncthreads();                 // this tile is prepared, the other buffer is free
+        // the next tile is prepared under this one's first loads
+        const bool ahead = active && (kMode != 2 || (place0 >= nturn && vcopy));
+        Row r[kUnroll];
+        uint4 v[kUnroll][kLoads];
+        if (ahead) fetch(list, r, v, q0, place_at(place0), place0 >= nturn, total);
+        if (t0 + step < p.tokens) prepare(t0 + step, lists[buf ^ 1], tabs + (buf ^ 1) * p.tile * p.rot);
         for (int place = place0; place < places; place += kThreads) {
             if (!active) break;                  // the threads left over by a pass
             const bool copies = place >= nturn;
@@ -216,9 +233,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_const
                         continue;
                     }
                 }
-                Row r[kUnroll];
-                uint4 v[kUnroll][kLoads];
-                fetch(r, v, q, at, copies, total);
+                if (!(ahead && place == place0 && q == q0)) fetch(list, r, v, q, at, copies, total);
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
                     if (!r[u].d) continue;
@@ -258,7 +273,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_const
                 }
             }
         }
-        __syncthreads();
     }
 }
 
@@ -284,6 +298,7 @@ cudaError_t launch_rotary(DType dt, bool append, RotaryArgs a, cudaStream_t st) 
     const long long full = (long long)kBlocks * sms;          // blocks the GPU holds
     long long tile = std::min(4LL * kThreads / items, (a.tokens + full - 1) / full);
     tile = std::max(1LL, std::min(tile, (long long)kMaxTile));
+    if (a.rot > 0) tile = std::min(tile, 32768LL / (2 * a.rot * (long long)sizeof(float)));   // two tables, 32 KB
     int slices = 1;                          // of the heads
     if (rows > kMaxRows) slices = (rows + kMaxRows - 1) / kMaxRows, tile = 1;
     else tile = std::max(1LL, std::min(tile, (long long)kMaxRows / rows));
@@ -292,7 +307,7 @@ cudaError_t launch_rotary(DType dt, bool append, RotaryArgs a, cudaStream_t st) 
     // the GPU full once: the set-up of a block is then paid for by several tiles
     // (12 x 1365 tokens of 24 heads of 64: 19.8 us against 21.7 with a block a tile)
     const dim3 grid((unsigned)std::min(tiles, full), (unsigned)slices);
-    const size_t smem = (size_t)a.tile * a.rot * sizeof(float);
+    const size_t smem = (size_t)2 * a.tile * a.rot * sizeof(float);
     if (dt == kF32) return append ? launch_t<float, true>(a, mode, grid, smem, st) : launch_t<float, false>(a, mode, grid, smem, st);
     if (dt == kF16) return append ? launch_t<__half, true>(a, mode, grid, smem, st) : launch_t<__half, false>(a, mode, grid, smem, st);
     return append ? launch_t<__nv_bfloat16, true>(a, mode, grid, smem, st) : launch_t<__nv_bfloat16, false>(a, mode, grid, smem, st);

@@ -96,6 +96,7 @@ ROTARY = [  # b, n, h, hk, hd, rot, interleaved, scaling
     (2, 7, 3, 1, 64, 0, False, "none"),
     (1, 12, 3, 1, 64, 2, True, "none"),
     (1, 3, 700, 300, 64, 64, False, "none"),      # more heads than a block lists
+    (1, 13000, 1, 0, 512, 512, True, "none"),     # the widest table
 ]
 
 
