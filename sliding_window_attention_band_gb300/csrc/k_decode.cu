@@ -193,13 +193,19 @@ __global__ void __launch_bounds__(kThreads) k_decode_join(const __grid_constant_
     const long long th = (long long)blockIdx.x * kPairs + warp / kW;
     const long long row = th / p.h;
     const int head = (int)(th - row * p.h);
-    pdl_wait();                                                   // the parts are there
-    pdl_trigger();
-    if (row >= p.tokens || row >= *GP(p.bnd, p.q_start + p.batch)) return;                                           // with kW = 4: the whole block
+    if (row >= p.tokens) return;                                  // with kW = 4: the whole block
     const float2 *ml = p.pml + th * p.nparts;
     const float *po = p.po + th * p.nparts * p.hd;
+    pdl_wait();                                                   // the parts are there
+    pdl_trigger();
+    const int live = *GP(p.bnd, p.q_start + p.batch);
     float M = -INFINITY, L = 0.f;
-    for (int s = lane; s < p.nparts; s += 32) M = fmaxf(M, GP(p.bnd, ml + s)->x);
+    const float2 none = make_float2(-INFINITY, 0.f);
+    // the first 64 parts' (max, sum), two a lane
+    const float2 near[2] = {lane < p.nparts ? *GP(p.bnd, ml + lane) : none, lane + 32 < p.nparts ? *GP(p.bnd, ml + lane + 32) : none};
+    M = fmaxf(near[0].x, near[1].x);
+    for (int s = 64 + lane; s < p.nparts; s += 32) M = fmaxf(M, GP(p.bnd, ml + s)->x);
+    if (row >= live) return;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     float4 o[kVecs];
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_join(const __grid_constant_
     // depend on no load before them; eight of them in flight
     for (int s0 = 0; s0 < p.nparts; s0 += 32) {
         const int left = min(p.nparts - s0, 32);
-        const float2 v = lane < left ? *GP(p.bnd, ml + s0 + lane) : make_float2(-INFINITY, 0.f);
+        const float2 v = s0 == 0 ? near[0] : s0 == 32 ? near[1] : lane < left ? *GP(p.bnd, ml + s0 + lane) : none;
         const float mine = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
         L = fmaf(v.y, mine, L);
         for (int k0 = part0; k0 < left; k0 += kFlight * kW) {
