@@ -20,6 +20,11 @@
 // 8), so the eight lines of an ldmatrix miss each other's banks.  Absent keys are
 // zero-filled, so whatever the cache holds there cannot reach a product.
 //
+// More than 16 rows are several tiles, in blocks of their own beside each other:
+// the keys then come out of L2 for the second one.  (Tiles of 32 rows, 255
+// registers and 8 warps an SM: 93 against 68 us for 48 requests of 4k, 32 rows
+// over 4 key heads of 128; 99 against 115 for 32 requests of 4k to 8k.)
+//
 // The warps' (m, l, O) are joined in shared memory; the pieces of a split key
 // list (few requests, long contexts) go to the workspace and are joined by
 // k_decode_join; the parts of a shared prefix, up to 16 of them, are joined here.
@@ -44,10 +49,10 @@ namespace {
 constexpr int kKeys = 16;          // keys of a group
 constexpr float kSlack = 8.f;      // log2 headroom of the running maximum
 
-template <int HD, int NT, int kWarps> struct Shape {
+template <int HD, int kWarps> struct Shape {
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kBlocks = (NT == 1 ? 12 : 8) / kWarps;    // an SM holds, by registers and shared memory
-    static constexpr int kStages = (NT == 1 ? 2 : 3) * (HD == 128 ? 1 : 2);
+    static constexpr int kBlocks = 12 / kWarps;              // an SM holds, by registers and shared memory
+    static constexpr int kStages = HD == 128 ? 2 : 4;
     static constexpr int kTile = kKeys * HD * 2;             // bytes of 16 lines
     static constexpr int kStage = 2 * kTile;                 // K and V
     static constexpr int kRing = kStages * kStage;           // of a warp
@@ -84,13 +89,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// NT: 16-row tiles of a block.  Grid: (piece, key head and row tile, request).
-// kWarps: the warps that share a piece.
-template <typename T, int HD, int NT, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k_decode_rows(const __grid_constant__ DecodeArgs p) {
-    using S = Shape<HD, NT, kWarps>;
+// Grid: (piece, key head and 16-row tile, request).  kWarps: the warps that share
+// a piece.
+template <typename T, int HD, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, Shape<HD, kWarps>::kBlocks) k_decode_rows(const __grid_constant__ DecodeArgs p) {
+    using S = Shape<HD, kWarps>;
     constexpr int kThreads = S::kThreads;
-    constexpr int kRows = 16 * NT, kSteps = HD / 16, kPieces = HD / 8;   // 16-byte pieces of a line
+    constexpr int kRows = 16, kSteps = HD / 16, kPieces = HD / 8;   // 16-byte pieces of a line
     constexpr int kPer = 32 / kPieces;                                   // lines of a copy instruction
     constexpr int kPad = HD + 8;                                         // floats of a row in the final exchange
     static_assert(kRows * kPad * 4 <= S::kRing, "a warp's O fits its ring");
@@ -180,12 +185,10 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
         uint32_t next = first[S::kStages - 1];
 
         // Q of the tile as A operands
-        uint32_t qa[NT][kSteps][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
+        uint32_t qa[kSteps][4];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int rr = 16 * t + g + 8 * half;
+                const int rr = g + 8 * half;
                 const bool live = rr < nrows;
                 const int row = row0 + (live ? rr : 0), a = row / p.group, hh = kvh * p.group + row - a * p.group;
                 const T *src = reinterpret_cast<const T *>(p.Q) + (long long)(q.row0 + a) * p.q_stride + (long long)hh * HD + 2 * t4;
@@ -193,28 +196,23 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
                 for (int k = 0; k < kSteps; ++k) {
                     const uint32_t x0 = *GP(p.bnd, reinterpret_cast<const uint32_t *>(src + 16 * k));
                     const uint32_t x1 = *GP(p.bnd, reinterpret_cast<const uint32_t *>(src + 16 * k + 8));
-                    qa[t][k][half] = live ? (x0 & q_and) ^ q_xor : 0u;
-                    qa[t][k][half + 2] = live ? (x1 & q_and) ^ q_xor : 0u;
+                    qa[k][half] = live ? (x0 & q_and) ^ q_xor : 0u;
+                    qa[k][half + 2] = live ? (x1 & q_and) ^ q_xor : 0u;
                 }
             }
-        // positions of this lane's rows (row g + 8 e of tile t)
-        int pos[NT][2];
+        // positions of this lane's rows (row g + 8 e)
+        int pos[2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) pos[t][e] = q.i0 + (row0 + min(16 * t + g + 8 * e, nrows - 1)) / p.group;
+            for (int e = 0; e < 2; ++e) pos[e] = q.i0 + (row0 + min(g + 8 * e, nrows - 1)) / p.group;
         const int pos_lo = q.i0 + a_lo, pos_hi = q.i0 + a_hi;
 
-        float o[NT][HD / 8][4], m[NT][2], l[NT][2];
+        float o[HD / 8][4], m[2], l[2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int d = 0; d < HD / 8; ++d)
 #pragma unroll
-            for (int d = 0; d < HD / 8; ++d)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[t][d][e] = 0.f;
-            m[t][0] = m[t][1] = -INFINITY;
-            l[t][0] = l[t][1] = 0.f;
-        }
+            for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
 
         int stage = 0;
         for (int n = 0; n < mine; ++n) {
@@ -227,20 +225,15 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
             __syncwarp();
             const uint32_t kt = ring_s + stage * S::kStage + kat, vt = ring_s + stage * S::kStage + vat;
 
-            float c[NT][2][4];
+            float c[2][4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c[t][0][e] = c[t][1][e] = 0.f;
+                for (int e = 0; e < 4; ++e) c[0][e] = c[1][e] = 0.f;
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
                 uint32_t b[4];
                 ldsm4(kt ^ (k << 5), b);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma16816<T>(c[t][0], qa[t][k], b[0], b[1]);
-                    mma16816<T>(c[t][1], qa[t][k], b[2], b[3]);
-                }
+                mma16816<T>(c[0], qa[k], b[0], b[1]);
+                mma16816<T>(c[1], qa[k], b[2], b[3]);
             }
             // which of the group's keys each row attends to
             const int u0 = lo + kKeys * (warp + kWarps * n);
@@ -255,61 +248,50 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
                         const int col = 8 * x + 2 * t4 + e, j = keys.at(u0 + col);
                         const bool here = (ok >> col) & 1u;
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
                             for (int r2 = 0; r2 < 2; ++r2)
-                                if (!(here && attends(p, pos[t][r2], j))) c[t][x][2 * r2 + e] = -INFINITY;
+                                if (!(here && attends(p, pos[r2], j))) c[x][2 * r2 + e] = -INFINITY;
                     }
             }
-            float best[NT][2];
+            float best[2];
             bool up = false;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    best[t][e] = fmaxf(max3(c[t][0][2 * e], c[t][0][2 * e + 1], c[t][1][2 * e]), c[t][1][2 * e + 1]) * scale;
-                    up |= best[t][e] > m[t][e] + kSlack;
+                    best[e] = fmaxf(max3(c[0][2 * e], c[0][2 * e + 1], c[1][2 * e]), c[1][2 * e + 1]) * scale;
+                    up |= best[e] > m[e] + kSlack;
                 }
             if (__any_sync(0xffffffffu, up)) {   // raise the maxima, scale what was summed so far
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = best[t][e];
+                        float mx = best[e];
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        const float mn = fmaxf(m[t][e], mx);
-                        const float f = m[t][e] == -INFINITY ? 0.f : ex2(m[t][e] - mn);
-                        m[t][e] = mn;
-                        l[t][e] *= f;
+                        const float mn = fmaxf(m[e], mx);
+                        const float f = m[e] == -INFINITY ? 0.f : ex2(m[e] - mn);
+                        m[e] = mn;
+                        l[e] *= f;
 #pragma unroll
                         for (int d = 0; d < HD / 8; ++d) {
-                            o[t][d][2 * e] *= f;
-                            o[t][d][2 * e + 1] *= f;
+                            o[d][2 * e] *= f;
+                            o[d][2 * e + 1] *= f;
                         }
                     }
             }
-            uint32_t pa[NT][4];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
+            uint32_t pa[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float mb = m[t][e] == -INFINITY ? 0.f : m[t][e];
-                    const float p0 = ex2(fmaf(c[t][0][2 * e], scale, -mb)), p1 = ex2(fmaf(c[t][0][2 * e + 1], scale, -mb));
-                    const float p2 = ex2(fmaf(c[t][1][2 * e], scale, -mb)), p3 = ex2(fmaf(c[t][1][2 * e + 1], scale, -mb));
-                    l[t][e] += (p0 + p1) + (p2 + p3);
-                    pa[t][e] = pack2<T>(p0, p1);
-                    pa[t][e + 2] = pack2<T>(p2, p3);
+                    const float mb = m[e] == -INFINITY ? 0.f : m[e];
+                    const float p0 = ex2(fmaf(c[0][2 * e], scale, -mb)), p1 = ex2(fmaf(c[0][2 * e + 1], scale, -mb));
+                    const float p2 = ex2(fmaf(c[1][2 * e], scale, -mb)), p3 = ex2(fmaf(c[1][2 * e + 1], scale, -mb));
+                    l[e] += (p0 + p1) + (p2 + p3);
+                    pa[e] = pack2<T>(p0, p1);
+                    pa[e + 2] = pack2<T>(p2, p3);
                 }
 #pragma unroll
             for (int d = 0; d < kSteps; ++d) {
                 uint32_t b[4];
                 ldsm4t(vt ^ (d << 5), b);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma16816<T>(o[t][2 * d], pa[t], b[0], b[1]);
-                    mma16816<T>(o[t][2 * d + 1], pa[t], b[2], b[3]);
-                }
+                mma16816<T>(o[2 * d], pa, b[0], b[1]);
+                mma16816<T>(o[2 * d + 1], pa, b[2], b[3]);
             }
             __syncwarp();                        // every lane has read the stage
             stage = stage + 1 == S::kStages ? 0 : stage + 1;
@@ -320,17 +302,15 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
         // join the warps: O of each into its own ring, then all threads sum
         float *mine_o = reinterpret_cast<float *>(ring);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float s = l[t][e];
+                float s = l[e];
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                const int row = 16 * t + g + 8 * e;
-                if (t4 == 0) sml[warp][row] = make_float2(m[t][e], s);
+                const int row = g + 8 * e;
+                if (t4 == 0) sml[warp][row] = make_float2(m[e], s);
 #pragma unroll
                 for (int d = 0; d < HD / 8; ++d)
-                    *reinterpret_cast<float2 *>(mine_o + row * kPad + 8 * d + 2 * t4) = make_float2(o[t][d][2 * e], o[t][d][2 * e + 1]);
+                    *reinterpret_cast<float2 *>(mine_o + row * kPad + 8 * d + 2 * t4) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
             }
         if (p.fold) {
             pdl_wait();                          // the prefix's parts are there
@@ -410,10 +390,10 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, NT, kWarps>::kBlocks) k
     if (p.npre > 0) pdl_wait();
 }
 
-template <typename T, int HD, int NT, int kWarps>
-cudaError_t launch_nt(const DecodeArgs &a, int tiles, cudaStream_t st) {
-    using S = Shape<HD, NT, kWarps>;
-    const auto fn = &k_decode_rows<T, HD, NT, kWarps>;
+template <typename T, int HD, int kWarps>
+cudaError_t launch_w(const DecodeArgs &a, int tiles, cudaStream_t st) {
+    using S = Shape<HD, kWarps>;
+    const auto fn = &k_decode_rows<T, HD, kWarps>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), S::kSmem);
     if (e != cudaSuccess) return e;
     const int most = 65535 / a.hk;
@@ -426,15 +406,11 @@ cudaError_t launch_nt(const DecodeArgs &a, int tiles, cudaStream_t st) {
 
 template <typename T, int HD>
 cudaError_t launch_hd(const DecodeArgs &a, int max_q, cudaStream_t st) {
-    // one 16-row tile where the rows fit it, else tiles of 32
-    const long long rows = a.stride == 1 ? (long long)max_q * a.group : a.group;
-    const long long each = a.stride == 1 ? 1 : max_q;
-    if (rows <= 16) {
-        if (a.row_warps == 2) return launch_nt<T, HD, 1, 2>(a, (int)each, st);
-        if (a.row_warps == 3) return launch_nt<T, HD, 1, 3>(a, (int)each, st);
-        return launch_nt<T, HD, 1, 4>(a, (int)each, st);
-    }
-    return launch_nt<T, HD, 2, 4>(a, (int)((rows + 31) / 32 * each < 65535 ? (rows + 31) / 32 * each : 65535), st);
+    const long long tiles = a.stride == 1 ? ((long long)max_q * a.group + 15) / 16 : (long long)max_q * ((a.group + 15) / 16);
+    const int t = (int)(tiles < 65535 ? tiles : 65535);
+    if (a.row_warps == 2) return launch_w<T, HD, 2>(a, t, st);
+    if (a.row_warps == 3) return launch_w<T, HD, 3>(a, t, st);
+    return launch_w<T, HD, 4>(a, t, st);
 }
 
 }  // namespace

@@ -215,12 +215,12 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
     long long keys = most_keys(d), blocks = batch, hold, least;
     if (p.rows) {
         const long long rows = d->dilation == 0 ? d->max_q * group : group;
-        blocks *= d->hk * (rows <= 16 ? 1 : (rows + 31) / 32) * (d->dilation == 0 ? 1 : d->max_q);
-        // An SM holds 12 warps (8 of the 32-row tiles).  Long lists want all of
-        // them in one go: four warps a block where the blocks fit at once, else
-        // three or two
-        p.row_warps = rows > 16 || blocks <= 3 * kSms ? 4 : blocks <= 4 * kSms ? 3 : blocks <= 6 * kSms ? 2 : keys <= 256 ? 2 : 4;
-        hold = (rows <= 16 ? 3 : 2) * kSms;
+        blocks *= d->hk * ((rows + 15) / 16) * (d->dilation == 0 ? 1 : d->max_q);
+        // An SM holds 12 warps.  Long lists want all of them in one go: four warps
+        // a block where the blocks fit at once, else three or two; with more
+        // blocks than that, four (two for lists too short to share).
+        p.row_warps = blocks <= 3 * kSms ? 4 : blocks <= 4 * kSms ? 3 : blocks <= 6 * kSms ? 2 : keys <= 256 ? 2 : 4;
+        hold = 3 * kSms;
         least = 256;
     } else {
         keys += d->prefix_len;
