@@ -218,9 +218,18 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
         blocks *= d->hk * ((rows + 15) / 16) * (d->dilation == 0 ? 1 : d->max_q);
         // An SM holds 12 warps.  Long lists want all of them in one go: four warps
         // a block where the blocks fit at once, else three or two; with more
-        // blocks than that, four (two for lists too short to share).
+        // blocks than that, four (two for lists too short to share).  Where they
+        // leave a quarter of the warps free, blocks of three or two and a list cut
+        // once more may fill them (256 blocks of 8k keys: 94 us against 111).
         p.row_warps = blocks <= 3 * kSms ? 4 : blocks <= 4 * kSms ? 3 : blocks <= 6 * kSms ? 2 : keys <= 256 ? 2 : 4;
         hold = 3 * kSms;
+        for (int w = 3; w >= 2 && keys >= 2048; --w) {
+            const long long now = std::max<long long>(1, hold / blocks) * p.row_warps, then = 12 / w * kSms / blocks * w;
+            if (4 * then >= 5 * now && blocks <= 3 * kSms) {
+                p.row_warps = w;
+                hold = 12 / w * kSms;
+            }
+        }
         least = 256;
     } else {
         keys += d->prefix_len;
