@@ -35,7 +35,7 @@
 // 6.7 TB/s) with 384 blocks of 4 warps on 456 places, 128 us cut into three
 // pieces; 8 warps an SM with 3 stages took 149 us.  512 blocks of 4096 keys:
 // 154 us with 3 warps a block, 208 with 4.  One context of 131072: 80 us for
-// 57 x 8 pieces, 86 with the join.
+// 57 x 8 pieces, 85 with the join.
 #include <type_traits>
 
 #include "swab_internal.h"

@@ -230,7 +230,11 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
                 hold = 12 / w * kSms;
             }
         }
-        least = 256;
+        // pieces of 128 keys (8 key heads of 128, a context of 2000: 7.0 us against
+        // 8.4 with 256 and 26 in one piece), but lists up to 512 whole: a second
+        // launch costs the host more than it saves (400 keys: 6.2 against 5.5 us
+        // on the GPU, 7.3 against 9.7 called eagerly)
+        least = keys <= 512 ? 512 : 128;
     } else {
         keys += d->prefix_len;
         blocks *= d->hk * ((group + 3) / 4);
