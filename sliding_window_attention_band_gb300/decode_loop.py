@@ -71,6 +71,13 @@ class DecodeLoop:
         queries [tokens, h, head_dim]; their attention over the whole prompt is
         band_attention's."""
         T = qkv.shape[0]
+        # (a refusal must come before the lengths move on)
+        if T < 1 or qkv.shape[1:] != self.qkv.shape[1:] or qkv.dtype is not self.dtype or qkv.device != self.qkv.device:
+            raise ValueError(f"qkv: expected [tokens, {self.h + 2 * self.hk}, {self.head_dim}] {self.dtype} on {self.qkv.device}, "
+                             f"got {list(qkv.shape)} {qkv.dtype} on {qkv.device}")
+        if qkv.stride(2) != 1 or qkv.stride(0) * qkv.element_size() % 16 or qkv.stride(1) * qkv.element_size() % 16 \
+                or qkv.data_ptr() % 16:
+            raise ValueError(f"qkv: adjacent channels and rows on 16 bytes expected, got strides {qkv.stride()}")
         slots, pos = torch.empty(T, dtype=torch.int32, device=qkv.device), torch.empty(T, dtype=torch.int32, device=qkv.device)
         self._place(n_new, slots, pos)
         q, k, v = qkv.split([self.h, self.hk, self.hk], dim=1)

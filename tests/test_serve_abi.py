@@ -292,3 +292,21 @@ def test_binding_rows_and_strides():
             rows(bad)
     with pytest.raises(ValueError, match="other tensors"):
         rows(FakeCuda((6, 4, 64), (256, 64, 1), device=1))
+
+
+def test_decode_loop_refuses_a_prompt_before_its_lengths_move(lib, monkeypatch):
+    loop = swab.DecodeLoop(2, 4, 2, 64, w=16, page=16, dtype=torch.float16, device="cpu")
+    called = []
+    monkeypatch.setattr(loop, "_place", lambda *a: called.append(a))
+    n_new = torch.tensor([3, 2], dtype=torch.int32)
+    wide = torch.zeros(5, 8, 72, dtype=torch.float16)
+    for qkv in (torch.zeros(5, 8, 64), torch.zeros(5, 7, 64, dtype=torch.float16), torch.zeros(0, 8, 64, dtype=torch.float16),
+                torch.zeros(5, 8, 64, dtype=torch.float16, device="meta"), torch.zeros(5, 512, dtype=torch.float16),
+                torch.zeros(5, 64, 8, dtype=torch.float16).transpose(1, 2), wide[:, :, 1:65],
+                torch.zeros(5, 8, 68, dtype=torch.float16)[:, :, :64]):
+        with pytest.raises(ValueError):
+            loop.fill(qkv, n_new)
+    assert not called
+    with pytest.raises(ValueError, match="CUDA"):     # heads side by side in a wider row: right but for the device
+        loop.fill(wide[:, :, :64], n_new)
+    assert len(called) == 1
