@@ -6,7 +6,8 @@
 // by the tensor cores above R = bf16 rate / copy rate = 281 rows, by memory
 // below.  tcgen05 with the accumulators in tensor memory, so both can be
 // reached: a block owns 128 rows of one key head and a run of 128-key chunks
-// (the prefix is split so that the blocks fill the SMs once).
+// (as many pieces as the host finds best: the SMs left over go to the requests'
+// own keys, whose kernel runs beside this one).
 //
 // Two streams of work go through the tensor cores in turn, so that one stream's
 // softmax runs under the other's products: with more than 128 rows two row
@@ -24,7 +25,7 @@
 // of those keys, which may be anything, are zeroed in shared memory.
 //
 // 128 requests x 32 heads over 8 key heads of 128, 16384 keys (34 GFLOP, 68 MB):
-// 36 us, 0.95 PFLOP/s.  5 us go to the first tiles, 5 to the parts (19 MB in
+// 36 us on 144 SMs, 0.95 PFLOP/s; 31 to the last product.  5 us go to the first tiles, 5 to the parts (19 MB in
 // whole sectors), 1.85 to a pair of chunks, of which the four products are 1.0:
 // tensor memory has no room for a second score buffer a stream, so a stream's
 // softmax, product and scores follow one another.  Steps on the way: the halves

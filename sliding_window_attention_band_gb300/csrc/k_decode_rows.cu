@@ -27,7 +27,8 @@
 //
 // The warps' (m, l, O) are joined in shared memory; the pieces of a split key
 // list (few requests, long contexts) go to the workspace and are joined by
-// k_decode_join; the parts of a shared prefix, up to 16 of them, are joined here.
+// k_decode_join; the parts of a shared prefix, up to 16 of them, are joined here
+// where all blocks fit at once.
 //
 // 12 warps an SM (168 registers, 16 KB of ring each) in blocks that all fit at
 // once, so that no second wave pays the chain lengths -> table -> keys again:
@@ -386,8 +387,9 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, kWarps>::kBlocks) k_dec
         }
         __syncthreads();                         // the rings are free for the next tile
     }
-    // what follows waits for this grid alone: with a shared prefix, end after its kernel
-    if (p.npre > 0) pdl_wait();
+    // What follows waits for this grid alone: with a shared prefix it must end
+    // after that kernel.  One block sees to it, the others make room.
+    if (p.npre > 0 && (p.fold || (blockIdx.x | blockIdx.y | blockIdx.z) == 0)) pdl_wait();
 }
 
 template <typename T, int HD, int kWarps>

@@ -206,6 +206,47 @@ long long most_keys(const swab_decode_desc *d) {
     return std::min<long long>(d->max_len, d->n_sink + band);
 }
 
+// Pieces of the prefix, and whether the rows kernel joins its parts (fold).  The
+// prefix kernel keeps an SM a block to itself; the rows kernel starts beside it
+// on the SMs left over, and takes all of them when it has ended.  More pieces
+// end sooner but leave fewer SMs and more parts to join; with fold the rows
+// kernel's blocks stay where they are until the prefix is there, without it they
+// make room for more and a third launch joins.  The time of each choice is
+// estimated (us; `blocks` of the rows kernel with `keys` keys each): a block of
+// the prefix 7 + 2 a chunk (0.7 of a single row tile; two thirds with head_dim
+// 64), a block of rows 3 + 1 every 23 KB, parts 1.9 MB a us.  Found by
+// measuring 17 shapes with 4 to 8 numbers of pieces: the choices are 3 % slower
+// than the best ones on average, 16 % faster than all SMs to the prefix and fold
+// wherever it goes (256 requests with 2048 shared keys: 49 us with one piece of a
+// tile, 54 with four, 61 with four and fold; 64 with 8192: 36 with 16 and fold, 41 without).
+void plan_prefix(const swab_decode_desc *d, long long blocks, long long keys, DecodePlan *p) {
+    const long long group = d->h / d->hk;
+    p->pre_tokens = (int)(128 / group);
+    const bool pair = d->tokens > p->pre_tokens;
+    const long long per = p->pre_tokens * (pair ? 2 : 1), tiles = (d->tokens + per - 1) / per * d->hk;
+    const long long chunks = ((long long)d->prefix_len + 127) / 128;
+    const long long most = std::min(std::max<long long>(1, kSms / tiles), (chunks + 1) / 2);
+    const double chunk_us = (pair ? 2.0 : 0.7) * (d->head_dim + 64) / 192, slots = 12 / p->row_warps;
+    const double block_us = 3.0 + (double)keys * d->head_dim * 4 / 23e3, part_us = (double)d->tokens * d->h * d->head_dim * 4 / 1.9e6;
+    double best = 0.0;
+    for (long long eighth = 8; eighth >= 1; --eighth) {
+        const long long want = std::max<long long>(1, most * eighth / 8), pre_chunks = (chunks + want - 1) / want;
+        const long long pieces = (chunks + pre_chunks - 1) / pre_chunks, npre = pieces * (pair ? 1 : 2);
+        const double pre = 7.0 + chunk_us * pre_chunks, beside = std::max<long long>(0, kSms - tiles * pieces) * slots;
+        for (int fold = p->nsplit == 1 && npre <= kMaxFold; fold >= 0; --fold) {
+            double us = part_us * (npre + p->nsplit);
+            if (blocks <= beside) us += std::max(pre, block_us);
+            else us += pre + std::max((blocks - beside * (fold ? 1.0 : pre / block_us)) / (kSms * slots), 0.7) * block_us;
+            if (best > 0.0 && us >= best) continue;
+            best = us;
+            p->pre_chunks = (int)pre_chunks;
+            p->pre_pieces = (int)pieces;
+            p->npre = (int)npre;
+            p->fold = fold;
+        }
+    }
+}
+
 DecodePlan plan_decode(const swab_decode_desc *d) {
     DecodePlan p{};
     const long long group = d->h / d->hk, batch = d->cache.batch;
@@ -245,18 +286,7 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
     const long long chunk = std::max<long long>(least, ((keys + want - 1) / want + 63) / 64 * 64);
     p.nsplit = (int)((keys + chunk - 1) / chunk);
     p.chunk = (int)std::min<long long>(chunk, 0x7fffffff);
-    if (p.rows && d->prefix_len > 0) {
-        // one block an SM: as many pieces of the prefix as fill the SMs once
-        p.pre_tokens = (int)(128 / group);
-        const bool pair = d->tokens > p.pre_tokens;
-        const long long per = p.pre_tokens * (pair ? 2 : 1), tiles = (d->tokens + per - 1) / per * d->hk;
-        const long long chunks = ((long long)d->prefix_len + 127) / 128;
-        const long long pieces = std::min(std::max<long long>(1, kSms / tiles), (chunks + 1) / 2);
-        p.pre_chunks = (int)((chunks + pieces - 1) / pieces);
-        p.pre_pieces = (int)((chunks + p.pre_chunks - 1) / p.pre_chunks);
-        p.npre = p.pre_pieces * (pair ? 1 : 2);
-        p.fold = p.nsplit == 1 && p.npre <= kMaxFold;
-    }
+    if (p.rows && d->prefix_len > 0) plan_prefix(d, blocks * p.nsplit, std::min<long long>(keys, p.chunk), &p);
     p.nparts = p.nsplit + p.npre;
     if (p.nparts > 1) {
         const size_t lines = (size_t)d->tokens * d->h * p.nparts;

@@ -559,6 +559,41 @@ def test_decode_of_lengths_that_make_no_sense(dtype, case):
     assert swab.device_status(reset=True) == 0
 
 
+@pytest.mark.parametrize("case", [
+    dict(n=16, own=20, h=32, hk=8, hd=128, prefix=4096),       # the own keys end long before the prefix, a launch of its own joins
+    dict(n=300, own=9, h=8, hk=8, hd=64, prefix=700),          # more blocks than the GPU holds at once
+    dict(n=40, own=30, h=8, hk=4, hd=128, prefix=260),         # few parts, joined by the rows kernel
+    dict(n=4, own=900, h=8, hk=2, hd=64, prefix=2000)])        # own keys cut into pieces as well
+def test_prefix_parts_of_the_call_before_are_never_joined(case):
+    """Two inputs through one workspace in turn, back to back and in a graph: each keeps its own result."""
+    n = case["n"]
+    a, b = (Decode(BF16, [case["own"] + k % 3 for k in range(n)], [1] * n, case["h"], case["hk"], case["hd"], page=64,
+                   prefix=case["prefix"], seed=seed) for seed in (120, 130))
+    ws = torch.full((swab.band_decode_workspace(a.desc) // 4,), float("nan"), device="cuda")
+    args = [(c, i32(c.table), i32(c.lens), i32(c.q_start), i32(c.ptable)) for c in (a, b)]
+    out = [[torch.empty_like(a.q) for _ in range(8)], [torch.empty(a.q.shape[:2], device="cuda") for _ in range(8)]]
+
+    def run():
+        for k in range(8):
+            c, table, lens, q_start, ptable = args[k % 2]
+            swab.band_decode(c.desc, c.scale, c.q, c.kc, c.vc, table, lens, q_start, out[0][k], out[1][k], ws, ptable)
+
+    run()
+    torch.cuda.synchronize()
+    a.check(out[0][0], out[1][0])
+    b.check(out[0][1], out[1][1])
+    first = [[t.clone() for t in x[:2]] for x in out]
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        run()
+    for again in range(3):
+        for k in range(8):
+            same_bits(out[0][k], first[0][k % 2])
+            same_bits(out[1][k], first[1][k % 2])
+        graph.replay()
+        torch.cuda.synchronize()
+
+
 def test_decode_row_strides_and_optional_lse():
     c = Decode(BF16, [70, 9], [2, 1], 4, 2, 64, seed=102)
     want, lse = c.run()
