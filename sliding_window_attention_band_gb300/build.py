@@ -4,7 +4,9 @@ Every translation unit is compiled by nvcc for sm_103a only, in parallel, and
 linked into one shared library with the CUDA runtime linked statically.  The
 same sources with SWAB_BOUNDS_CHECK=1 give libswab_bounds.so, the
 bounds-checked build (every plain global access of a kernel tested against
-the call's buffer extents); ``build_all()`` compiles both in one pool.
+the call's buffer extents); ``build_all()`` compiles both in one pool.  Beside
+them lies _serve_call.so, host code only: a Python module that takes the
+tensors of a serving call straight to the library (csrc/serve_call.cpp).
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libswab.so")
 LIB_BOUNDS = os.path.join(LIBDIR, "libswab_bounds.so")
+CALLS = os.path.join(LIBDIR, "_serve_call.so")
+CALLS_SOURCE = os.path.join(CSRC, "serve_call.cpp")
 VARIANTS = {  # variant: (library, object folder, extra nvcc flags)
     "regular": (LIB, "obj", ()),
     "bounds": (LIB_BOUNDS, "obj_bounds", ("-DSWAB_BOUNDS_CHECK=1",)),
@@ -75,6 +80,30 @@ def _compile_jobs(variant, extra_flags, verbose):
     return [(src, compile_one) for src in SOURCES]
 
 
+def calls_up_to_date() -> bool:
+    return os.path.exists(CALLS) and all(os.path.getmtime(f) <= os.path.getmtime(CALLS)
+                                         for f in (CALLS_SOURCE, os.path.join(ROOT, "include", "swab.h")))
+
+
+def _build_calls():
+    import torch
+
+    top = os.path.dirname(torch.__file__)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(top, "include"), "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
+           "-I", os.path.join(ROOT, "include"), CALLS_SOURCE, "-o", tmp, "-L", os.path.join(top, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    os.makedirs(LIBDIR, exist_ok=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
+        raise RuntimeError("g++ failed on serve_call.cpp")
+    os.replace(tmp, CALLS)
+
+
 def _link(variant, objs):
     lib = VARIANTS[variant][0]
     tmp = lib + f".tmp{os.getpid()}"
@@ -92,9 +121,13 @@ def build_variants(variants, force: bool = False, verbose: bool = False, extra_f
     them in one pool; returns their library paths."""
     todo = [v for v in variants if force or not up_to_date(v)]
     jobs = [(v, src, fn) for v in todo for src, fn in _compile_jobs(v, extra_flags, verbose)]
-    if jobs:
-        with ThreadPoolExecutor(max_workers=min(len(jobs), max(os.cpu_count() or 1, len(SOURCES)))) as ex:
+    calls = force or not calls_up_to_date()
+    if jobs or calls:
+        with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, max(os.cpu_count() or 1, len(SOURCES)))) as ex:
+            made = ex.submit(_build_calls) if calls else None
             objs = list(ex.map(lambda job: job[2](job[1]), jobs))
+            if made is not None:
+                made.result()
         for v in todo:
             _link(v, [o for (vv, _, _), o in zip(jobs, objs) if vv == v])
     return [VARIANTS[v][0] for v in variants]

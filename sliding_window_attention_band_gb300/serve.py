@@ -5,14 +5,21 @@ write, and decode over the paged cache.
 Argument marshalling and checks only, like the rest of the binding.  Every
 tensor of a call lies on one CUDA device; the call runs on that device's
 current stream (or the stream given), whichever device is current.
+
+The usual call goes through a compiled module (csrc/serve_call.cpp).  Where
+that finds anything unusual, or is not there, the call is checked and made
+here.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
 import torch
 
 from . import _binding as _b
+from . import build as _build
 
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 _S3 = ctypes.c_int64 * 3
@@ -58,7 +65,7 @@ class CacheDesc:
         self.batch, self.page, self.n_blocks, self.cols = int(batch), int(page), int(n_blocks), int(cols)
         self.ring, self.pinned = bool(ring), int(pinned)
         self.c = _CacheDesc(self.batch, self.page, self.n_blocks, self.cols, int(self.ring), self.pinned)
-        self._ref = ctypes.byref(self.c)
+        self._ref, self._addr = ctypes.byref(self.c), ctypes.addressof(self.c)
 
 
 class RotaryDesc:
@@ -76,6 +83,9 @@ class RotaryDesc:
         # the shapes a tensor of h or hk heads may have: tokens as [b, n] or flat
         self._q = ((self.b, self.n, self.h, self.head_dim), (self.tokens, self.h, self.head_dim))
         self._k = ((self.b, self.n, self.hk, self.head_dim), (self.tokens, self.hk, self.head_dim))
+        self._plain = _RotaryDesc(self.b, self.n, self.h, self.hk, self.head_dim, self.rot_dim, int(self.interleaved),
+                                  _b._DTYPES[dtype], self.scale, self.pos0)
+        self._addr = ctypes.addressof(self._plain)
         self._structs = {}      # the C struct by the strides of a call's tensors
 
     def struct(self, q=None, k=None, qo=None, ko=None, v=None):
@@ -116,17 +126,46 @@ class DecodeDesc:
         self._shape = (self.tokens, self.h, self.head_dim)
         self._kv = (cache.n_blocks, self.hk, cache.page, self.head_dim)
         self._batch, self._table = cache.batch, cache.batch * cache.cols
-        self._ref = ctypes.byref(self.c)
+        self._ref, self._addr = ctypes.byref(self.c), ctypes.addressof(self.c)
         self._workspace = None
 
 
 # ---------------------------------------------------------------------------
 # marshalling helpers.  A call of a few microseconds must not wait for its
-# checks: each entry point asks all its tensors in one expression, and only
-# when that fails looks again, one by one, for the one to name in the error.
+# checks: the compiled module asks all its tensors; where it returns -1, each
+# entry point asks them in one expression, and only when that fails looks again,
+# one by one, for the one to name in the error.
 # ---------------------------------------------------------------------------
 _I32, _F32, _I64 = torch.int32, torch.float32, torch.int64
 _fns = {}
+_calls = None
+
+
+class _NoCalls:
+    """In place of the compiled module where it has not been built."""
+
+    rotary = rotary_bwd = cache_slots = rotary_append = band_decode = staticmethod(lambda *args: -1)
+
+
+def _load_calls():
+    global _calls
+    lib = _b.load()
+    calls = _NoCalls
+    if os.path.exists(_build.CALLS):
+        spec = importlib.util.spec_from_file_location("_serve_call", _build.CALLS)
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
+        calls.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                     for name in ("rotary", "rotary_bwd", "cache_slots", "rotary_append", "band_decode")))
+    _calls = calls
+    return calls
+
+
+def _done(name, rc):
+    """True when the compiled module has made the call, False when it has to be looked at again."""
+    if rc > 0:
+        raise _b.SwabError(name, rc)
+    return rc == 0
 
 
 def _run(name, dev, stream, *args):
@@ -250,11 +289,15 @@ def rotary(desc: RotaryDesc, turns, Q, Qo, K=None, Ko=None, pos=None, stream=Non
     """Rotary positions: Q [b, n, h, hd] -> Qo and K [b, n, hk, hd] -> Ko (any
     strides with adjacent channels; an output may be its own input).  pos
     [b, n] int32, None for 0, 1, ... in every sequence."""
+    if stream is None and _done("rotary", (_calls or _load_calls()).rotary(desc._addr, turns, pos, Q, K, Qo, Ko)):
+        return
     _rotary("rotary", desc, turns, Q, Qo, K, Ko, pos, stream)
 
 
 def rotary_bwd(desc: RotaryDesc, turns, dQo, dQ, dKo=None, dK=None, pos=None, stream=None):
     """Gradient of rotary: dQo -> dQ and dKo -> dK."""
+    if stream is None and _done("rotary_bwd", (_calls or _load_calls()).rotary_bwd(desc._addr, turns, pos, dQo, dKo, dQ, dK)):
+        return
     _rotary("rotary_bwd", desc, turns, dQo, dQ, dKo, dK, pos, stream)
 
 
@@ -266,6 +309,9 @@ def cache_slots(cache: CacheDesc, lens, n_new, table, free_list, used, lens_out,
     past the last token: -1 and 0).  lens_out [batch] (may be lens) and
     used_out [2] (may be used): lengths and blocks taken after the step, and
     how many blocks were missing (such requests get slots of -1)."""
+    if stream is None and _done("cache_slots", (_calls or _load_calls()).cache_slots(
+            cache._addr, pos0, lens, n_new, table, free_list, used, lens_out, used_out, q_start, slots, pos)):
+        return
     B, n_free, tokens, dev = cache.batch, free_list.numel(), slots.numel(), lens.get_device()
     if not (dev >= 0 and lens.dtype is _I32 and n_new.dtype is _I32 and table.dtype is _I32 and free_list.dtype is _I32
             and used.dtype is _I32 and lens_out.dtype is _I32 and used_out.dtype is _I32 and q_start.dtype is _I32
@@ -300,6 +346,9 @@ def rotary_append(desc: RotaryDesc, cache: CacheDesc, turns, Q, K, V, pos, slots
     """rotary on Q -> Qo, and K (rotated) and V into the rows slots[t] of the
     cache tensors Kc, Vc [n_blocks, hk, page, hd]; slot -1 is not written.  Q
     and Qo may both be None."""
+    if stream is None and _done("rotary_append", (_calls or _load_calls()).rotary_append(
+            desc._addr, cache._addr, turns, Q, K, V, pos, slots, Qo, Kc, Vc)):
+        return
     if (Q is None) != (Qo is None):
         raise ValueError("Q, Qo: both or neither")
     d, dev, dt, n = desc, K.get_device(), desc.dtype, desc.tokens
@@ -351,10 +400,13 @@ def band_decode(desc: DecodeDesc, scale, Q, Kc, Vc, table, lens, q_start, O, lse
     (and lse [tokens, h] fp32) of queries Q whose rows q_start[r]:q_start[r + 1]
     are the last positions of request r's lens[r].  With ``prefix_len`` the
     shared prefix lies in the blocks prefix_table of the same cache."""
-    d, dev, dt, kv = desc, Q.get_device(), desc.dtype, desc._kv
-    need = d._workspace
+    need = desc._workspace
     if need is None:
-        need = band_decode_workspace(d)
+        need = band_decode_workspace(desc)
+    if stream is None and _done("band_decode", (_calls or _load_calls()).band_decode(
+            desc._addr, need, scale, Q, Kc, Vc, table, lens, q_start, prefix_table, O, lse, workspace)):
+        return
+    d, dev, dt, kv = desc, Q.get_device(), desc.dtype, desc._kv
     if not (dev >= 0 and Q.dtype is dt and O.dtype is dt and Kc.dtype is dt and Vc.dtype is dt and table.dtype is _I32
             and lens.dtype is _I32 and q_start.dtype is _I32 and Q.shape == d._shape and O.shape == d._shape and Kc.shape == kv
             and Vc.shape == kv and table.numel() == d._table and lens.numel() == d._batch and q_start.numel() == d._batch + 1

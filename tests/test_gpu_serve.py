@@ -609,6 +609,52 @@ def test_decode_row_strides_and_optional_lse():
     same_bits(c.run(lse=False)[0], want)
 
 
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_compiled_calls_and_the_binding_agree(dtype, monkeypatch):
+    """Every call through the compiled module and marshalled in Python: the same bits, on strided views as well."""
+    B, h, hk, hd, page = 5, 4, 2, 64, 16
+    turns = swab.rotary_frequencies(hd)[0].cuda()
+    cache = swab.CacheDesc(B, page, 40, 6)
+    x = randn((2 * B, h + 2 * hk, hd), dtype, 140)
+    q, k, v = x.split([h, hk, hk], dim=1)
+    desc = swab.RotaryDesc(2, B, h, hk, hd, hd, dtype=dtype)
+    dec = swab.DecodeDesc(cache, 2 * B, h, hk, hd, max_q=3, dtype=dtype, q_row_stride=(h + 1) * hd)
+    seen = []
+
+    def all_calls():
+        out = [torch.zeros(2 * B, n, hd, dtype=dtype, device="cuda") for n in (h, hk, h, hk, h)]
+        swab.rotary(desc, turns, q, out[0], k, out[1])
+        swab.rotary_bwd(desc, turns, q, out[2], k, out[3])
+        lens, new = i32([17, 3, 0, 60, 9]), i32([2, 3, 1, 1, 3])
+        lens_out, used, table = i32([0] * B), i32([0, 0]), torch.full((B, 6), -1, dtype=torch.int32, device="cuda")
+        table[:, :4] = i32(np.arange(20).reshape(B, 4))
+        slots, pos, start = i32([0] * (2 * B)), i32([0] * (2 * B)), i32([0] * (B + 1))
+        swab.cache_slots(cache, lens, new, table, i32(np.arange(20, 40)), used, lens_out, used, start, slots, pos, pos0=2)
+        kc, vc = randn((40, hk, page, hd), dtype, 141), randn((40, hk, page, hd), dtype, 142)
+        qo = torch.zeros(2 * B, h + 1, hd, dtype=dtype, device="cuda")[:, :h]
+        swab.rotary_append(swab.RotaryDesc(1, 2 * B, h, hk, hd, hd, dtype=dtype), cache, turns, q, k, v, pos, slots, qo, kc, vc)
+        lse = torch.zeros(2 * B, h, device="cuda")
+        need = swab.band_decode_workspace(dec)
+        swab.band_decode(dec, 0.125, qo, kc, vc, table, lens_out, start, out[4], lse, torch.empty(max(need, 16), dtype=torch.uint8, device="cuda"))
+        with pytest.raises(swab.SwabError, match="MISALIGNED"):
+            swab.rotary(desc, turns, x.flatten()[1:1 + 2 * B * h * hd].view(2 * B, h, hd), out[0], k, out[1])
+        with pytest.raises(ValueError, match="lse"):
+            swab.band_decode(dec, 0.125, qo, kc, vc, table, lens_out, start, out[4], lse.flatten(), None)
+        return [*out, lens_out, used, table, slots, pos, start, kc, vc, qo.contiguous(), lse]
+
+    calls = swab.serve._load_calls()
+    assert calls is not swab.serve._NoCalls
+    for name in ("rotary", "rotary_bwd", "cache_slots", "rotary_append", "band_decode"):
+        fn = getattr(calls, name)
+        monkeypatch.setattr(calls, name, lambda *a, _f=fn, _n=name: (seen.append((_n, rc := _f(*a))), rc)[1])
+    fast = all_calls()
+    assert [rc for _, rc in seen] == [0, 0, 0, 0, 0, 3, -1]
+    monkeypatch.setattr(swab.serve, "_calls", swab.serve._NoCalls)
+    slow = all_calls()
+    for a, b in zip(fast, slow):
+        same_bits(a.float(), b.float())
+
+
 def test_decode_fewer_rows_than_tokens():
     """Rows past `tokens` are neither read nor written."""
     c = Decode(F16, [30, 20], [3, 2], 4, 2, 64, seed=103)

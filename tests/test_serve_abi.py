@@ -310,3 +310,44 @@ def test_decode_loop_refuses_a_prompt_before_its_lengths_move(lib, monkeypatch):
     with pytest.raises(ValueError, match="CUDA"):     # heads side by side in a wider row: right but for the device
         loop.fill(wide[:, :, :64], n_new)
     assert len(called) == 1
+
+
+def test_compiled_calls_leave_what_is_unusual_to_the_binding(lib):
+    """Anything but the expected tensors gives -1 and no exception; the binding then names what is wrong."""
+    call = serve._calls or serve._load_calls()
+    assert call is not serve._NoCalls
+    c = swab.CacheDesc(2, 16, 8, 4)
+    r = swab.RotaryDesc(1, 2, 4, 2, 64, 64)
+    d = swab.DecodeDesc(c, 2, 4, 2, 64)
+    f16, i32 = torch.zeros(2, 4, 64, dtype=torch.float16), torch.zeros(2, dtype=torch.int32)
+    kv = torch.zeros(8, 2, 16, 64, dtype=torch.float16)
+    odd = [None, 3, -1, "x", 1.5, f16, i32, kv, kv.to("meta"), f16.to_sparse(), torch.nn.Parameter(f16), object()]
+    rng = np.random.default_rng(0)
+    for name, lead, n in (("rotary", (r._addr,), 7), ("rotary_bwd", (r._addr,), 7), ("cache_slots", (c._addr, 0), 12),
+                          ("rotary_append", (r._addr, c._addr), 11), ("band_decode", (d._addr, 0, 0.125), 13)):
+        fn = getattr(call, name)
+        assert fn() == -1 and fn(*lead) == -1 and fn(0, *[None] * (n - 1)) == -1
+        for _ in range(60):
+            assert fn(*lead, *(odd[k] for k in rng.integers(0, len(odd), n - len(lead)))) == -1
+        assert fn("descriptor", *[f16] * (n - 1)) == -1
+    for scale in ("x", None, torch.zeros(())):
+        assert call.band_decode(d._addr, 0, scale, *[f16] * 10) == -1
+    with pytest.raises(TypeError):
+        call.bind(1, 2)
+    with pytest.raises(ValueError):
+        call.bind(0, 0, 0, 0, 0)
+    with pytest.raises(ValueError, match="CUDA"):
+        swab.rotary(r, torch.zeros(32, dtype=torch.int64), f16, f16, f16[:, :2], f16[:, :2])
+
+
+def test_descriptors_of_the_compiled_calls_follow_the_header(lib):
+    """The C structs the compiled calls read by address are those the binding passes by reference."""
+    r = swab.RotaryDesc(2, 3, 4, 2, 64, 32, interleaved=True, scale=1.25, pos0=7, dtype=torch.bfloat16)
+    a = serve._RotaryDesc.from_address(r._addr)
+    assert [getattr(a, k) for k in ("b", "n", "h", "hk", "head_dim", "rot_dim", "interleaved", "dtype", "scale", "pos0")] == [
+        2, 3, 4, 2, 64, 32, 1, 2, 1.25, 7]
+    assert not any(x for k in ("q", "k", "qo", "ko", "v") for x in getattr(a, k + "_stride"))
+    c = swab.CacheDesc(2, 16, 8, 4, ring=True, pinned=1)
+    d = swab.DecodeDesc(c, 5, 4, 2, 64, w=3, q_row_stride=512)
+    assert ctypes.addressof(d.c) == d._addr and ctypes.addressof(c.c) == c._addr
+    assert d.c.q_row_stride == 512 and d.c.cache.cols == 4 and d.c.cache.pinned == 1
