@@ -271,11 +271,15 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
                 hold = 12 / w * kSms;
             }
         }
-        // pieces of 128 keys (8 key heads of 128, a context of 2000: 7.0 us against
-        // 8.4 with 256 and 26 in one piece), but lists up to 512 whole: a second
-        // launch costs the host more than it saves (400 keys: 6.2 against 5.5 us
-        // on the GPU, 7.3 against 9.7 called eagerly)
-        least = keys <= 512 ? 512 : 128;
+        // Pieces of 128 keys (8 key heads of 128, a context of 2000: 7.0 us against
+        // 8.4 with 256 and 26 in one piece); of 64 where up to 24 blocks have up to
+        // 1024 keys (8 x 600: 5.9 against 6.5 us, 8 x 1500: 7.2 against 6.5).  Lists
+        // up to 256 whole: the second launch costs as much (12 x 200: 4.7 against
+        // 4.9 in pieces of 64).  Up to 512 too where there are more than 64 blocks
+        // or a prefix whose parts could be joined without it (192 x 400: 7.3
+        // against 8.2; 32 x 400: 8.4 against 6.7).
+        const bool whole = keys <= 256 || (keys <= 512 && (blocks > 64 || d->prefix_len > 0));
+        least = whole ? 512 : keys <= 1024 && blocks <= 24 ? 64 : 128;
     } else {
         keys += d->prefix_len;
         blocks *= d->hk * ((group + 3) / 4);
