@@ -5,7 +5,7 @@ linked into one shared library with the CUDA runtime linked statically.  The
 same sources with SWAB_BOUNDS_CHECK=1 give libswab_bounds.so, the
 bounds-checked build (every plain global access of a kernel tested against
 the call's buffer extents); ``build_all()`` compiles both in one pool.  Beside
-them lies _serve_call.so, host code only: a Python module that takes the
+them lies _serve_call-*.so, host code only: a Python module that takes the
 tensors of a serving call straight to the library (csrc/serve_call.cpp).
 """
 from __future__ import annotations
@@ -17,13 +17,16 @@ import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libswab.so")
 LIB_BOUNDS = os.path.join(LIBDIR, "libswab_bounds.so")
-CALLS = os.path.join(LIBDIR, "_serve_call.so")
+# it depends on the interpreter and on PyTorch, so both are in its name
+CALLS = os.path.join(LIBDIR, f"_serve_call-py{sys.version_info[0]}.{sys.version_info[1]}-torch{torch.__version__}.so")
 CALLS_SOURCE = os.path.join(CSRC, "serve_call.cpp")
 VARIANTS = {  # variant: (library, object folder, extra nvcc flags)
     "regular": (LIB, "obj", ()),
@@ -86,8 +89,6 @@ def calls_up_to_date() -> bool:
 
 
 def _build_calls():
-    import torch
-
     top = os.path.dirname(torch.__file__)
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
