@@ -213,12 +213,14 @@ long long most_keys(const swab_decode_desc *d) {
 // kernel's blocks stay where they are until the prefix is there, without it they
 // make room for more and a third launch joins.  The time of each choice is
 // estimated (us; `blocks` of the rows kernel with `keys` keys each): a block of
-// the prefix 7 + 2 a chunk (0.7 of a single row tile; two thirds with head_dim
-// 64), a block of rows 3 + 1 every 23 KB, parts 1.9 MB a us.  Found by
-// measuring 17 shapes with 4 to 8 numbers of pieces: the choices are 3 % slower
-// than the best ones on average, 16 % faster than all SMs to the prefix and fold
-// wherever it goes (256 requests with 2048 shared keys: 49 us with one piece of a
-// tile, 54 with four, 61 with four and fold; 64 with 8192: 36 with 16 and fold, 41 without).
+// the prefix 5.6 + 1.6 a chunk (0.8 of a single row tile; two thirds with
+// head_dim 64), a block of rows 3.3 + 1 every 45 KB, parts 1 MB a us, 1.25 in
+// a launch of their own that costs 1.3 more.  The numbers come from 208 shapes (2
+// to 200 requests, prefixes of 256 to 32768, head_dim 64 and 128) measured with
+// every choice: theirs are 3 % slower than the best on average, 5 % faster than
+// all SMs to the prefix and fold wherever it goes (256 requests with 2048
+// shared keys: 49 us with one piece of a tile, 54 with four, 61 with four and
+// fold; 64 with 8192: 33 with 7 pieces, 36 with 16 and fold, 41 without).
 void plan_prefix(const swab_decode_desc *d, long long blocks, long long keys, DecodePlan *p) {
     const long long group = d->h / d->hk;
     p->pre_tokens = (int)(128 / group);
@@ -226,17 +228,18 @@ void plan_prefix(const swab_decode_desc *d, long long blocks, long long keys, De
     const long long per = p->pre_tokens * (pair ? 2 : 1), tiles = (d->tokens + per - 1) / per * d->hk;
     const long long chunks = ((long long)d->prefix_len + 127) / 128;
     const long long most = std::min(std::max<long long>(1, kSms / tiles), (chunks + 1) / 2);
-    const double chunk_us = (pair ? 2.0 : 0.7) * (d->head_dim + 64) / 192, slots = 12 / p->row_warps;
-    const double block_us = 3.0 + (double)keys * d->head_dim * 4 / 23e3, part_us = (double)d->tokens * d->h * d->head_dim * 4 / 1.9e6;
+    const double chunk_us = (pair ? 1.6 : 0.8) * (d->head_dim + 64) / 192, slots = 12 / p->row_warps;
+    const double block_us = 3.3 + (double)keys * d->head_dim * 4 / 45e3, part_us = (double)d->tokens * d->h * d->head_dim * 4 / 1e6;
     double best = 0.0;
     for (long long eighth = 8; eighth >= 1; --eighth) {
         const long long want = std::max<long long>(1, most * eighth / 8), pre_chunks = (chunks + want - 1) / want;
         const long long pieces = (chunks + pre_chunks - 1) / pre_chunks, npre = pieces * (pair ? 1 : 2);
-        const double pre = 7.0 + chunk_us * pre_chunks, beside = std::max<long long>(0, kSms - tiles * pieces) * slots;
+        const double pre = 5.6 + chunk_us * pre_chunks, beside = std::max<long long>(0, kSms - tiles * pieces) * slots;
         for (int fold = p->nsplit == 1 && npre <= kMaxFold; fold >= 0; --fold) {
-            double us = part_us * (npre + p->nsplit);
+            double us = fold ? part_us * npre : 1.3 + part_us * (npre + p->nsplit) * 0.8;
             if (blocks <= beside) us += std::max(pre, block_us);
-            else us += pre + std::max((blocks - beside * (fold ? 1.0 : pre / block_us)) / (kSms * slots), 0.7) * block_us;
+            else if (fold) us += pre + std::max((blocks - beside) / (kSms * slots), 0.8) * block_us;
+            else us += pre + std::max((blocks - beside * pre / block_us) / (kSms * slots), 0.1) * block_us;
             if (best > 0.0 && us >= best) continue;
             best = us;
             p->pre_chunks = (int)pre_chunks;
