@@ -26,7 +26,7 @@
 //
 // 128 requests x 32 heads over 8 key heads of 128, 16384 keys (34 GFLOP, 68 MB):
 // 36 us on 144 SMs, 0.95 PFLOP/s; 31 to the last product.  5 us go to the first tiles, 5 to the parts (19 MB in
-// whole sectors), 1.85 to a pair of chunks, of which the four products are 1.0:
+// whole sectors), 1.75 to a pair of chunks, of which the four products are 1.0:
 // tensor memory has no room for a second score buffer a stream, so a stream's
 // softmax, product and scores follow one another.  Steps on the way: the halves
 // of one tile's keys as streams 45 us; steps of 64 keys with two score buffers
