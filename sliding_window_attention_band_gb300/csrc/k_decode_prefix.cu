@@ -150,7 +150,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *holder;
     pdl_wait();
-    pdl_trigger();                               // the requests' own keys may start beside this
+    if (warp == 2) {
+        // The requests' own keys may start beside this: every block of their kernel
+        // finds its word set by a thread that has passed the wait above.
+        const long long blocks = (long long)gridDim.x * gridDim.y;
+        for (long long k = (long long)blockIdx.y * gridDim.x + blockIdx.x + blocks * lane; k < p.row_blocks; k += 32 * blocks)
+            store_release(GP(p.bnd, p.go + k), p.token);
+        __syncwarp();
+        if (lane == 0) pdl_trigger();
+    }
 
     if (warp == 0) {
         // ---------------- TMA: lane k fetches page k of a tile ----------------

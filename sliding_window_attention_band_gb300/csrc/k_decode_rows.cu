@@ -112,7 +112,24 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, kWarps>::kBlocks) k_dec
     const int split = blockIdx.x, r = blockIdx.z;
     const int kvh = (int)(blockIdx.y % (unsigned)p.hk), tile0 = (int)(blockIdx.y / (unsigned)p.hk);
     const int tiles_y = gridDim.y / p.hk;
-    if (p.npre == 0) pdl_wait();
+    if (p.npre == 0) {
+        pdl_wait();
+    } else {
+        // Behind the prefix kernel this block does not wait for that kernel's end.
+        // A thread of it that has passed its own wait, so that all that was written
+        // before the call is visible to it, has set the block's word (release);
+        // seen here (acquire), and past the barrier, the same holds for this block.
+        // Not seen, it waits for the end after all.  The word is cleared for the
+        // next call, which may be a replay with the same token.
+        if (threadIdx.x == 0) {
+            unsigned long long *go = GP(p.bnd, p.go + ((long long)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x);
+            bool seen = false;
+            for (int k = 0; k < 32 && !seen; ++k) seen = load_acquire(go) == p.token;
+            if (!seen) pdl_wait();
+            *go = 0;
+        }
+        __syncthreads();
+    }
     pdl_trigger();
     const Request q = request_of(p, r);
     uint8_t *ring = smem + warp * S::kRing;
@@ -393,33 +410,27 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, kWarps>::kBlocks) k_dec
 }
 
 template <typename T, int HD, int kWarps>
-cudaError_t launch_w(const DecodeArgs &a, int tiles, cudaStream_t st) {
+cudaError_t launch_w(const DecodeArgs &a, cudaStream_t st) {
     using S = Shape<HD, kWarps>;
     const auto fn = &k_decode_rows<T, HD, kWarps>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), S::kSmem);
     if (e != cudaSuccess) return e;
-    const int most = 65535 / a.hk;
-    const dim3 grid((unsigned)a.nsplit, (unsigned)(a.hk * (tiles < most ? tiles : most)), (unsigned)a.batch);
-    // Behind the prefix kernel it starts without waiting: it reads nothing of
-    // that kernel before its end, and whatever came before is complete once
-    // that kernel's blocks have passed their wait.
+    const dim3 grid((unsigned)a.nsplit, (unsigned)(a.hk * a.row_tiles), (unsigned)a.batch);
     return launch_dependent(fn, grid, S::kThreads, S::kSmem, st, a);
 }
 
 template <typename T, int HD>
-cudaError_t launch_hd(const DecodeArgs &a, int max_q, cudaStream_t st) {
-    const long long tiles = a.stride == 1 ? ((long long)max_q * a.group + 15) / 16 : (long long)max_q * ((a.group + 15) / 16);
-    const int t = (int)(tiles < 65535 ? tiles : 65535);
-    if (a.row_warps == 2) return launch_w<T, HD, 2>(a, t, st);
-    if (a.row_warps == 3) return launch_w<T, HD, 3>(a, t, st);
-    return launch_w<T, HD, 4>(a, t, st);
+cudaError_t launch_hd(const DecodeArgs &a, cudaStream_t st) {
+    if (a.row_warps == 2) return launch_w<T, HD, 2>(a, st);
+    if (a.row_warps == 3) return launch_w<T, HD, 3>(a, st);
+    return launch_w<T, HD, 4>(a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_rows(DType dt, const DecodeArgs &a, int max_q, cudaStream_t st) {
-    if (dt == kF16) return a.hd == 64 ? launch_hd<__half, 64>(a, max_q, st) : launch_hd<__half, 128>(a, max_q, st);
-    return a.hd == 64 ? launch_hd<__nv_bfloat16, 64>(a, max_q, st) : launch_hd<__nv_bfloat16, 128>(a, max_q, st);
+cudaError_t launch_decode_rows(DType dt, const DecodeArgs &a, cudaStream_t st) {
+    if (dt == kF16) return a.hd == 64 ? launch_hd<__half, 64>(a, st) : launch_hd<__half, 128>(a, st);
+    return a.hd == 64 ? launch_hd<__nv_bfloat16, 64>(a, st) : launch_hd<__nv_bfloat16, 128>(a, st);
 }
 
 }  // namespace swab

@@ -302,10 +302,19 @@ bool encode_tiled(CUtensorMap *map, DType dt, int rank, const void *base, const 
 // waits for that kernel (pdl_wait: complete, its writes visible) before it
 // touches memory and only then lets the next one be set up (pdl_trigger), so a
 // kernel that has passed its wait knows everything before it in the stream
-// complete.  It saves the launch gap, 1 to 2 us a kernel.  (The one exception, a
-// kernel that starts without waiting, is named where it is launched.)
+// complete.  It saves the launch gap, 1 to 2 us a kernel.  (The one exception is
+// k_decode_rows behind a prefix, which takes another way to what was written
+// before: store_release and load_acquire below.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void store_release(unsigned long long *p, unsigned long long v) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long load_acquire(const unsigned long long *p) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
 
 // Launches a kernel as a programmatic dependent of the stream's last one.
 template <typename... A>
@@ -379,8 +388,13 @@ struct DecodeArgs {
     // the prefix kernel: parts it makes of a query, pieces of the prefix, 128-key
     // chunks of a piece, tokens of a row tile
     int npre, pre_pieces, pre_chunks, pre_tokens;
-    int row_warps;             // warps that share a piece in the rows kernel: 2 or 4
+    int row_warps;             // warps that share a piece in the rows kernel: 2, 3 or 4
+    int row_tiles;             // tiles of a request's rows in the rows kernel's grid
     int fold;                  // the rows kernel joins the prefix's parts itself
+    // behind a prefix: a word a block of the rows kernel (row_blocks of them), which
+    // the prefix kernel sets to `token` and the block clears
+    unsigned long long *go, token;
+    long long row_blocks;
     float scale_log2;
     unsigned *err;
 #if SWAB_BOUNDS_CHECK
@@ -389,7 +403,7 @@ struct DecodeArgs {
 };
 constexpr int kMaxFold = 16;    // most parts of the prefix that the rows kernel joins
 cudaError_t launch_decode_general(DType dt, const DecodeArgs &a, cudaStream_t st);
-cudaError_t launch_decode_rows(DType dt, const DecodeArgs &a, int max_q, cudaStream_t st);
+cudaError_t launch_decode_rows(DType dt, const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_decode_prefix(DType dt, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                                  const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_decode_join(DType dt, const DecodeArgs &a, cudaStream_t st);

@@ -2,6 +2,8 @@
 // banded attention: rotary positions, block tables, the cache write, decode.
 // Arguments are validated on the host before any CUDA call.
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <cmath>
 
 #include "swab_internal.h"
@@ -168,7 +170,9 @@ struct DecodePlan {
     int npre, pre_pieces, pre_chunks, pre_tokens;
     int row_warps;
     bool fold;                       // no join launch: the rows kernel adds the prefix's parts
-    size_t parts_bytes, bytes;       // workspace: the parts, then their (max, sum)
+    int row_tiles;                   // of a request, in the rows kernel's grid
+    long long row_blocks;            // of that grid
+    size_t parts_bytes, ml_bytes, bytes;   // workspace: the parts, their (max, sum), a word a block of rows behind a prefix
 };
 
 swab_status check_decode(const swab_decode_desc *d) {
@@ -259,7 +263,9 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
     long long keys = most_keys(d), blocks = batch, hold, least;
     if (p.rows) {
         const long long rows = d->dilation == 0 ? d->max_q * group : group;
-        blocks *= d->hk * ((rows + 15) / 16) * (d->dilation == 0 ? 1 : d->max_q);
+        const long long tiles = (rows + 15) / 16 * (d->dilation == 0 ? 1 : d->max_q);
+        blocks *= d->hk * tiles;
+        p.row_tiles = (int)std::min<long long>(tiles, 65535 / d->hk);
         // An SM holds 12 warps.  Long lists want all of them in one go: four warps
         // a block where the blocks fit at once, else three or two; with more
         // blocks than that, four (two for lists too short to share).  Where they
@@ -298,9 +304,25 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
     if (p.nparts > 1) {
         const size_t lines = (size_t)d->tokens * d->h * p.nparts;
         p.parts_bytes = (lines * d->head_dim * 4 + 255) / 256 * 256;
-        p.bytes = p.parts_bytes + lines * 8 + 256;      // the parts start on a multiple of 256 bytes
+        p.ml_bytes = lines * 8;
+        p.bytes = p.parts_bytes + p.ml_bytes + 256;     // the parts start on a multiple of 256 bytes
+    }
+    if (p.npre > 0) {
+        p.row_blocks = p.nsplit * (long long)d->hk * p.row_tiles * batch;
+        p.bytes += (size_t)p.row_blocks * 8;
     }
     return p;
+}
+
+// A number that no other call of this process, nor memory by chance, holds: the
+// workspace's contents on entry do not matter, and a word left in it must not
+// be taken for one that this call's prefix kernel has set.
+unsigned long long next_token() {
+    static std::atomic<unsigned long long> count{(unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count()};
+    unsigned long long x = count.fetch_add(1, std::memory_order_relaxed) * 0x9e3779b97f4a7c15ull;   // odd: a bijection
+    x ^= x >> 32;
+    x *= 0xd6e8feb86659fd93ull;
+    return (x ^ (x >> 32)) | 1ull;
 }
 
 // Tensor maps of the prefix kernel: Q as {hd, h, tokens}, a tile the heads of a
@@ -483,6 +505,10 @@ SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, cons
     char *parts = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
     a.po = reinterpret_cast<float *>(parts);
     a.pml = reinterpret_cast<float2 *>(parts + plan.parts_bytes);
+    a.go = reinterpret_cast<unsigned long long *>(parts + plan.parts_bytes + plan.ml_bytes);
+    a.token = plan.npre > 0 ? next_token() : 0;
+    a.row_blocks = plan.row_blocks;
+    a.row_tiles = plan.row_tiles;
     a.q_stride = desc->q_row_stride ? desc->q_row_stride : (long long)desc->h * desc->head_dim;
     a.o_stride = desc->out_row_stride ? desc->out_row_stride : (long long)desc->h * desc->head_dim;
     a.batch = c->batch;
@@ -530,7 +556,7 @@ SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, cons
         e = launch_decode_prefix(dt, mq, mk, mv, a, as_stream(stream));
     }
     if (e == cudaSuccess)
-        e = plan.rows ? launch_decode_rows(dt, a, desc->max_q, as_stream(stream)) : launch_decode_general(dt, a, as_stream(stream));
+        e = plan.rows ? launch_decode_rows(dt, a, as_stream(stream)) : launch_decode_general(dt, a, as_stream(stream));
     if (e == cudaSuccess && a.nparts > 1 && !a.fold) e = launch_decode_join(dt, a, as_stream(stream));
     return status_of(e);
 }

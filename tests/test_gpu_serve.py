@@ -815,6 +815,42 @@ def test_prompt_then_steps_behind_a_shared_prefix():
         assert (np.abs(f64(torch.stack([x[r] for x in got])) - want) <= bound).all()
 
 
+@pytest.mark.parametrize("batch,prefix,steps", [(3, 50, 12), (40, 300, 6)])
+def test_replayed_steps_behind_a_shared_prefix(batch, prefix, steps):
+    """Whole steps of one captured graph, their inputs rewritten in place and the workspace filled with noise between
+    replays: the rows kernel, which starts beside the prefix kernel, sees what the calls before it have just written."""
+    s = Server(batch, 4, BF16, prefix=prefix)
+    pre = randn((prefix, s.H + 2 * s.HK, s.HD), BF16, 320)
+    slots = i32([int(s.ptable[p // s.PAGE]) * s.PAGE + p % s.PAGE for p in range(prefix)])
+    _, k, v = pre.split([s.H, s.HK, s.HK], dim=1)
+    swab.rotary_append(swab.RotaryDesc(1, prefix, s.H, s.HK, s.HD, s.HD, dtype=BF16), s.cache, s.turns, None, k, v,
+                       i32(np.arange(prefix)), slots, None, s.kc, s.vc)
+    s.buffers(batch * 4)
+    news = np.random.default_rng(7).integers(0, 5, (steps, batch))
+    data = [randn((max(1, int(news[:, r].sum())), s.H + 2 * s.HK, s.HD), BF16, 330 + r) for r in range(batch)]
+    s.step()                                           # warm up: no tokens
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.step()
+    got, at = [[] for _ in range(batch)], [0] * batch
+    for t in range(steps):
+        s.n_new.copy_(i32(news[t]))
+        rows = torch.cat([data[r][at[r]:at[r] + news[t][r]] for r in range(batch)])
+        s.qkv[:len(rows)] = rows
+        s.ws.copy_(torch.randint(0, 256, s.ws.shape, dtype=torch.uint8, device="cuda"))
+        graph.replay()
+        first = 0
+        for r in range(batch):
+            got[r].append(s.o[first:first + news[t][r]].clone())
+            first += news[t][r]
+            at[r] += int(news[t][r])
+    assert int(s.used[1]) == 0
+    for r in range(batch):
+        want, bound = full_attention(f64(data[r])[:at[r]], s.w, s.SINK, BF16, f64(pre))
+        assert (np.abs(f64(torch.cat(got[r])) - want) <= bound).all()
+
+
 def test_last_rows_agree_with_the_banded_forward():
     """rotary, then band_attention over the sequence; the cache write and band_decode give its last rows."""
     n, h, hd, w = 200, 4, 64, 40
