@@ -20,13 +20,15 @@ constexpr unsigned kDecodeFile = 14;   // site id of the bounds checks in this h
 __device__ __forceinline__ Request request_of(const DecodeArgs &p, int r) {
     [[maybe_unused]] constexpr unsigned kSwabFile = kDecodeFile;
     Request q;
-    const int a = max(*GP(p.bnd, p.q_start + r), 0), b = min(*GP(p.bnd, p.q_start + r + 1), p.tokens);
+    // (any two values: both ends are brought into 0..tokens before they are
+    // subtracted, and the difference of the values as they are takes 33 bits)
+    const int first = *GP(p.bnd, p.q_start + r), end = *GP(p.bnd, p.q_start + r + 1);
+    const int a = min(max(first, 0), p.tokens), b = min(max(end, 0), p.tokens);
     q.r = r;
     q.row0 = a;
     q.m = max(b - a, 0);
-    const int m_all = *GP(p.bnd, p.q_start + r + 1) - *GP(p.bnd, p.q_start + r);
     q.len = max(*GP(p.bnd, p.lens + r), 0);
-    q.i0 = q.len - m_all;
+    q.i0 = (int)max((long long)q.len - ((long long)end - first), -0x7fffffffLL);
     q.trow = p.table + (long long)r * p.cols;
     q.ring_lo = 0;
     const long long room = (long long)p.cols << p.page_log2;

@@ -559,6 +559,20 @@ def test_decode_of_lengths_that_make_no_sense(dtype, case):
     assert swab.device_status(reset=True) == 0
 
 
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_decode_of_row_starts_that_fall_from_above_zero_to_the_lowest_integer(dtype, prefix):
+    """Their difference does not fit 32 bits: no row belongs to the first request, the last one is right."""
+    c = Decode(dtype, [40, 20, 30], [1, 2, 1], 4, 2, 64, prefix=prefix, seed=107)
+    want, lse = c.run()
+    for starts in ([3, -2 ** 31, 3, 4], [2, -2 ** 31 + 1, 3, 4], [2 ** 31 - 1, -2 ** 31, 3, 4]):
+        c.q_start = np.array(starts)
+        o, l = c.run()
+        same_bits(o[3:], want[3:])
+        same_bits(l[3:], lse[3:])
+    assert swab.device_status(reset=True) == 0
+
+
 @pytest.mark.parametrize("case", [
     dict(n=16, own=20, h=32, hk=8, hd=128, prefix=4096),       # the own keys end long before the prefix, a launch of its own joins
     dict(n=300, own=9, h=8, hk=8, hd=64, prefix=700),          # more blocks than the GPU holds at once
