@@ -16,6 +16,8 @@ rotary_append, band_decode.
 """
 from __future__ import annotations
 
+import operator
+
 import torch
 
 from . import serve
@@ -96,9 +98,13 @@ class DecodeLoop:
                           self.lse, self.workspace)
 
     def restart(self, requests):
-        """Empty the given requests (a list of row numbers): their blocks go back
-        to the free list.  Reads the number of blocks in use from the device."""
-        rows = torch.tensor(sorted(set(requests)), dtype=torch.long, device=self.table.device)
+        """Empty the given requests (row numbers 0 .. batch - 1): their blocks go
+        back to the free list.  Reads the number of blocks in use from the device."""
+        wanted = sorted({operator.index(r) for r in requests})
+        # (a negative number would name a row a second time and free its blocks twice)
+        if wanted and not 0 <= wanted[0] <= wanted[-1] < self.batch:
+            raise ValueError(f"requests: expected row numbers 0 .. {self.batch - 1}, got {wanted}")
+        rows = torch.tensor(wanted, dtype=torch.long, device=self.table.device)
         held = self.table[rows]
         left = torch.cat((self.free_list[int(self.used[0]):], held[held >= 0]))
         start = self.free_list.numel() - left.numel()

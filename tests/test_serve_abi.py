@@ -312,6 +312,27 @@ def test_decode_loop_refuses_a_prompt_before_its_lengths_move(lib, monkeypatch):
     assert len(called) == 1
 
 
+def test_decode_loop_restart_takes_each_row_once_and_no_other(lib):
+    """A row outside the batch (a negative one too) is refused with nothing changed; one named twice is emptied once."""
+    loop = swab.DecodeLoop(2, 4, 2, 64, w=16, page=16, dtype=torch.float16, device="cpu")
+    loop.table[:] = torch.arange(loop.cache.n_blocks, dtype=torch.int32).view(2, -1)
+    loop.lens[:], loop.used[0] = 40, loop.cache.n_blocks
+    held = lambda: [t.clone() for t in (loop.table, loop.lens, loop.used, loop.free_list)]  # noqa: E731
+    before = held()
+    for bad in ([2], [-1], [0, 2], [-1, 1], [1.5], ["1"], [None]):
+        with pytest.raises((ValueError, TypeError)):
+            loop.restart(bad)
+        assert all(torch.equal(a, b) for a, b in zip(before, held()))
+    loop.restart([])
+    assert int(loop.used[0]) == loop.cache.n_blocks and torch.equal(loop.table, before[0])
+    for one in ([1, 1], [np.int64(1), 1], torch.tensor([1, 1])):
+        loop.table[1], loop.lens[1], loop.used[0] = before[0][1], 40, loop.cache.n_blocks
+        loop.restart(one)
+        assert sorted(loop.free_list[int(loop.used[0]):].tolist()) == before[0][1].tolist()
+        assert loop.table[0].tolist() == before[0][0].tolist() and loop.table[1].tolist() == [-1] * loop.cache.cols
+        assert loop.lens.tolist() == [40, 0]
+
+
 def test_compiled_calls_leave_what_is_unusual_to_the_binding(lib):
     """Anything but the expected tensors gives -1 and no exception; the binding then names what is wrong."""
     call = serve._calls or serve._load_calls()
