@@ -520,7 +520,8 @@ SWAB_API size_t band_decode_workspace(const swab_decode_desc *desc);
  *     with prefix_len > 0 also every position of the shared prefix,
  * each once:  O = softmax(scale * q . K) . V,  lse = log of its sum of
  * exponentials ([tokens, h] fp32, may be NULL).  A query without a key (an
- * inconsistent length, absent blocks) gets O = 0 and lse = -inf.  Without ring,
+ * inconsistent length, absent blocks) gets O = 0 and lse = -inf, one with a NaN
+ * score NaN in both; scores that are all -inf count as no key.  Without ring,
  * positions past the table (lens[r] > cols * page) count as absent and raise
  * SWAB_ERR_INVALID_ARG in the status word.  Rows past
  * q_start[batch] are left as they were.

@@ -159,20 +159,18 @@ __global__ void __launch_bounds__(kThreads) k_decode_general(const __grid_consta
             __syncthreads();
             float M = -INFINITY, L = 0.f;
             for (int g = 0; g < kGroups; ++g) M = fmaxf(M, sml[g].x);
-            for (int g = 0; g < kGroups; ++g)
-                if (sml[g].x != -INFINITY) L += sml[g].y * exp2f(sml[g].x - M);
+            for (int g = 0; g < kGroups; ++g) L = fmaf(sml[g].y, sml[g].x == -INFINITY ? 0.f : exp2f(sml[g].x - M), L);
             const int head = head0 + t;
             const long long th = row * p.h + head;
             for (int c = threadIdx.x; c < p.hd; c += kThreads) {
                 const int piece = c / kV, at = piece % kLanes * kE + piece / kLanes * kV + c % kV;
                 float y = 0.f;
-                for (int g = 0; g < kGroups; ++g)
-                    if (sml[g].x != -INFINITY) y += so[g][at] * exp2f(sml[g].x - M);
+                for (int g = 0; g < kGroups; ++g) y = fmaf(so[g][at], sml[g].x == -INFINITY ? 0.f : exp2f(sml[g].x - M), y);
                 if (p.nparts > 1)
                     *GP(p.bnd, p.po + (th * p.nparts + split) * p.hd + c) = y;
                 else
                     *GP(p.bnd, reinterpret_cast<T *>(p.O) + row * p.o_stride + (long long)head * p.hd + c) =
-                        Elt<T>::from_f(L > 0.f ? y / L : 0.f);
+                        Elt<T>::from_f(L == 0.f ? 0.f : y / L);
             }
             if (threadIdx.x == 0) {
                 if (p.nparts > 1) *GP(p.bnd, p.pml + th * p.nparts + split) = make_float2(M, L);
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_join(const __grid_constant_
                 o[e].w += x.w;
             }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = inverse_of(L);
     T *out = reinterpret_cast<T *>(p.O) + row * p.o_stride + (long long)head * p.hd;
 #pragma unroll
     for (int e = 0; e < kVecs; ++e) {

@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<HD, kWarps>::kBlocks) k_dec
             if (p.nparts > 1 && !p.fold) {
                 *reinterpret_cast<float4 *>(GPN(p.bnd, p.po + (th * p.nparts + split) * HD + c4, 16)) = y;
             } else {
-                const float inv = stot[row].y > 0.f ? 1.f / stot[row].y : 0.f;
+                const float inv = inverse_of(stot[row].y);
                 *reinterpret_cast<uint2 *>(GPN(p.bnd, reinterpret_cast<T *>(p.O) + tok * p.o_stride + (long long)hh * HD + c4, 8)) =
                     make_uint2(pack2<T>(y.x * inv, y.y * inv), pack2<T>(y.z * inv, y.w * inv));
             }

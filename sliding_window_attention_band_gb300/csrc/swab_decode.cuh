@@ -96,9 +96,14 @@ __device__ __forceinline__ uint32_t prefix_line(const DecodeArgs &p, int j, int 
     return block_line(p, *GP(p.bnd, p.ptable + (j >> p.page_log2)), j & ((1 << p.page_log2) - 1), kvh);
 }
 
+// A maximum leaves NaN out (fmaxf, max.f32), a sum keeps it: a row with keys
+// whose scores are NaN has m = -inf and l = NaN, one without keys m = -inf and
+// l = 0.  So it is the sum that says whether there was a key, and a part with m =
+// -inf weighs 0 but its sum is still added (NaN * 0 is NaN).
+__device__ __forceinline__ float inverse_of(float L) { return L == 0.f ? 0.f : 1.f / L; }
 // log-sum-exp from the maximum (log2 units) and the sum
 __device__ __forceinline__ float lse_of(float M, float L) {
-    return L > 0.f ? M * 0.6931471805599453f + logf(L) : -INFINITY;
+    return L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
 }
 
 }  // namespace swab

@@ -516,6 +516,36 @@ def test_decode_without_keys():
     assert swab.device_status(reset=True) == 0
 
 
+NOT_FINITE = [  # how the lists are cut: whole, pieces joined by a launch of their own, behind a prefix (folded, joined)
+    dict(lens=[40, 20, 9], new=[1, 2, 1], h=4, hk=2, hd=64),
+    dict(lens=[3000, 50], new=[1, 1], h=8, hk=2, hd=128, page=64),
+    dict(lens=[40, 20, 9], new=[1, 2, 1], h=4, hk=2, hd=64, prefix=70),
+    dict(lens=[30] * 40, new=[1] * 40, h=8, hk=4, hd=128, page=64, prefix=260),
+    dict(lens=[20] * 16, new=[1] * 16, h=32, hk=8, hd=128, page=64, prefix=4096),
+    dict(lens=[40, 20, 9], new=[1, 2, 1], h=6, hk=2, hd=80),
+    dict(lens=[2000], new=[2], h=2, hk=2, hd=80)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("case", NOT_FINITE)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_decode_of_queries_that_are_not_finite(case, dtype, bad):
+    """softmax of NaN is NaN: a query with a NaN, or with both infinities, gives NaN in O and lse, however its list is
+    cut, and leaves the other heads and tokens as they are."""
+    c = Decode(dtype, seed=111, **case)
+    want, wlse = c.run()
+    rows, heads, q = [0, c.tokens - 1], [0, c.q.shape[1] - 1], c.q.clone()
+    for t, h in zip(rows, heads):
+        c.q[t, h, 5], c.q[t, h, 6] = bad, -bad
+    o, lse = c.run()
+    hit = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    hit[rows, heads] = True
+    assert o[hit].isnan().all() and lse[hit].isnan().all()
+    # (not the same bits: an infinite score makes its warp raise the references of the rows beside it as well)
+    o[hit], lse[hit], c.q = want[hit], wlse[hit], q
+    c.check(o, lse)
+
+
 def test_decode_skips_and_flags_blocks_outside_the_cache():
     for dtype in (F16, F32):
         for prefix in (0, 40):
