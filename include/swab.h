@@ -371,8 +371,8 @@ SWAB_API swab_status band_attention_bwd_noalloc(const swab_desc *desc, float sca
  * token at a time.
  *
  * Tokens of a step are flat: row t of the [tokens, heads, head_dim] tensors
- * belongs to request r when q_start[r] <= t < q_start[r + 1]; rows from
- * q_start[batch] on are padding.
+ * belongs to request r when q_start[r] <= t < q_start[r + 1]; rows before
+ * q_start[0] (cache_slots writes 0) and from q_start[batch] on belong to none.
  *
  * The cache holds K and V as two tensors [n_blocks, hk, page, head_dim].  A
  * request's positions j = 0, 1, ... lie in blocks of `page` positions; block
@@ -523,8 +523,8 @@ SWAB_API size_t band_decode_workspace(const swab_decode_desc *desc);
  * inconsistent length, absent blocks) gets O = 0 and lse = -inf, one with a NaN
  * score NaN in both; scores that are all -inf count as no key.  Without ring,
  * positions past the table (lens[r] > cols * page) count as absent and raise
- * SWAB_ERR_INVALID_ARG in the status word.  Rows past
- * q_start[batch] are left as they were.
+ * SWAB_ERR_INVALID_ARG in the status word.  Rows of O
+ * and lse that belong to no request are left as they were.
  * The shared prefix lies in the same cache: positions p of it in block
  * prefix_table[p / page] ([ceil(prefix_len / page)], DEVICE int32); it comes
  * before position 0 of every request and is read once for all of them.  It

@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(kThreads) k_decode_join(const __grid_constant_
     const float *po = p.po + th * p.nparts * p.hd;
     pdl_wait();                                                   // the parts are there
     pdl_trigger();
+    // the requests' rows (a first start behind the second one says nothing of the others)
+    const int start = *GP(p.bnd, p.q_start), first = start <= *GP(p.bnd, p.q_start + 1) ? start : 0;
     const int live = *GP(p.bnd, p.q_start + p.batch);
     float M = -INFINITY, L = 0.f;
     const float2 none = make_float2(-INFINITY, 0.f);
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_join(const __grid_constant_
     const float2 near[2] = {lane < p.nparts ? *GP(p.bnd, ml + lane) : none, lane + 32 < p.nparts ? *GP(p.bnd, ml + lane + 32) : none};
     M = fmaxf(near[0].x, near[1].x);
     for (int s = 64 + lane; s < p.nparts; s += 32) M = fmaxf(M, GP(p.bnd, ml + s)->x);
-    if (row >= live) return;
+    if (row < first || row >= live) return;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     float4 o[kVecs];

@@ -638,6 +638,23 @@ def test_prefix_parts_of_the_call_before_are_never_joined(case):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("case", [dict(lens=[40, 20], new=[2, 1]), dict(lens=[3000, 50], new=[1, 1], page=64),
+                                  dict(lens=[40, 20], new=[2, 1], prefix=70),
+                                  dict(lens=[20] * 16, new=[1] * 16, page=64, prefix=4096)])
+def test_rows_before_the_first_request_stay_as_they_were(case, dtype):
+    """The first three rows of Q and O belong to no request (q_start[0] = 3), however the lists are cut."""
+    c = Decode(dtype, h=8, hk=2, hd=128, pad=3, seed=112, **case)
+    want, lse = c.run()
+    c.q = torch.cat((c.q[-3:], c.q[:-3])).contiguous()
+    c.q_start = c.q_start + 3
+    o, l = c.run()
+    assert (o[:3] == 7.0).all() and (l[:3] == 7.0).all()
+    n = int(c.q_start[-1])
+    same_bits(o[3:n], want[:n - 3])
+    same_bits(l[3:n], lse[:n - 3])
+
+
 def test_decode_row_strides_and_optional_lse():
     c = Decode(BF16, [70, 9], [2, 1], 4, 2, 64, seed=102)
     want, lse = c.run()
