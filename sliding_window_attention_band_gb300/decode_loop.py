@@ -69,9 +69,10 @@ class DecodeLoop:
 
     def fill(self, qkv, n_new):
         """Prompts of n_new[r] tokens (int32 [batch]) into the cache: the rows of
-        qkv [tokens, h + 2 hk, head_dim] request by request.  Returns the rotated
-        queries [tokens, h, head_dim]; their attention over the whole prompt is
-        band_attention's."""
+        qkv [tokens, h + 2 hk, head_dim] request by request, at least as many as
+        n_new adds up to (read from the device, unless the stream is being
+        captured).  Returns the rotated queries [tokens, h, head_dim]; their
+        attention over the whole prompt is band_attention's."""
         T = qkv.shape[0]
         # (a refusal must come before the lengths move on)
         if T < 1 or qkv.shape[1:] != self.qkv.shape[1:] or qkv.dtype is not self.dtype or qkv.device != self.qkv.device:
@@ -80,6 +81,9 @@ class DecodeLoop:
         if qkv.stride(2) != 1 or qkv.stride(0) * qkv.element_size() % 16 or qkv.stride(1) * qkv.element_size() % 16 \
                 or qkv.data_ptr() % 16:
             raise ValueError(f"qkv: adjacent channels and rows on 16 bytes expected, got strides {qkv.stride()}")
+        captured = n_new.is_cuda and torch.cuda.is_current_stream_capturing()
+        if not captured and int(n_new.clamp(min=0).sum()) > T:
+            raise ValueError(f"n_new: adds up to more than the {T} rows of qkv")
         slots, pos = torch.empty(T, dtype=torch.int32, device=qkv.device), torch.empty(T, dtype=torch.int32, device=qkv.device)
         self._place(n_new, slots, pos)
         q, k, v = qkv.split([self.h, self.hk, self.hk], dim=1)

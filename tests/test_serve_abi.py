@@ -312,6 +312,22 @@ def test_decode_loop_refuses_a_prompt_before_its_lengths_move(lib, monkeypatch):
     assert len(called) == 1
 
 
+def test_decode_loop_refuses_prompts_longer_than_their_rows(lib, monkeypatch):
+    """n_new may not add up to more than the rows of qkv (their positions would never be written); fewer is padding."""
+    loop = swab.DecodeLoop(3, 4, 2, 64, w=16, page=16, dtype=torch.float16, device="cpu")
+    called = []
+    monkeypatch.setattr(loop, "_place", lambda *a: called.append(a))
+    qkv = torch.zeros(5, 8, 64, dtype=torch.float16)
+    for n_new in ([3, 2, 1], [6, 0, 0], [6, -2, 0], [2 ** 31 - 1, 2 ** 31 - 1, 4]):
+        with pytest.raises(ValueError, match="n_new"):
+            loop.fill(qkv, torch.tensor(n_new, dtype=torch.int32))
+    assert not called
+    for n_new in ([3, 2, 0], [1, -7, 2], [5, -1, 0]):
+        with pytest.raises(ValueError, match="CUDA"):          # right but for the device
+            loop.fill(qkv, torch.tensor(n_new, dtype=torch.int32))
+    assert len(called) == 3
+
+
 def test_decode_loop_restart_takes_each_row_once_and_no_other(lib):
     """A row outside the batch (a negative one too) is refused with nothing changed; one named twice is emptied once."""
     loop = swab.DecodeLoop(2, 4, 2, 64, w=16, page=16, dtype=torch.float16, device="cpu")
