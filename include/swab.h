@@ -453,6 +453,8 @@ typedef struct swab_cache_desc {
     int32_t cols;      /* columns of the block table, >= 1 */
     int32_t ring;      /* 1: columns from `pinned` on are recycled */
     int32_t pinned;    /* 0..cols - 1; 0 without ring */
+    int32_t max_new;   /* cache_slots: most new tokens of a request, and every token needs a
+                          row of slots and pos; 0: no such limits */
 } swab_cache_desc;
 
 /* Block tables and slot maps from request lengths, for a step that adds
@@ -470,7 +472,10 @@ typedef struct swab_cache_desc {
  * A request whose blocks are not all there -- the list (n_free long) runs out in
  * or before it, or, without ring, its length passes cols * page -- gets none:
  * its slots are -1 and lens_out[r] = lens[r]; used_out[1] counts the blocks
- * missing (0: every request was served).  Such a request's rows of a
+ * missing (0: every request was served).  The same holds, with max_new > 0, of a
+ * request that adds more than max_new tokens or whose tokens do not all have
+ * rows (q_start[r + 1] > tokens): it counts at least one in used_out[1] and raises
+ * SWAB_ERR_INVALID_ARG in the status word.  An unserved request's rows of a
  * following band_decode are meaningless.
  * All arrays DEVICE int32, 4-byte aligned; lens_out may be lens and used_out
  * (2 elements) may be used, no other overlap. */

@@ -51,7 +51,8 @@ def column(block, cols, ring, pinned):
     return pinned + (block - pinned) % (cols - pinned) if ring else None
 
 
-def cache_slots(lens, new, table, free, used, page, cols, ring=False, pinned=0, tokens=0, pos0=0, n_blocks=1 << 30):
+def cache_slots(lens, new, table, free, used, page, cols, ring=False, pinned=0, tokens=0, pos0=0, n_blocks=1 << 30,
+                max_new=0):
     """One token at a time: (table, lens_out, used_out, q_start, slots, pos)."""
     table = np.array(table)
     lens = [max(int(x), 0) for x in lens]
@@ -62,12 +63,14 @@ def cache_slots(lens, new, table, free, used, page, cols, ring=False, pinned=0, 
     for r, (a, m) in enumerate(zip(lens, new)):
         start.append(start[-1] + m)
         have, want = min(-(-a // page), cols), -(-(a + m) // page)
-        too_long = not ring and want > cols
+        too_many = 0 < max_new < m
+        too_long = too_many or (not ring and want > cols)
         need = 0 if too_long else min(want, cols) - have
         asked += need
-        ok = not too_long and (need == 0 or asked <= len(free))
+        no_rows = max_new > 0 and m > 0 and start[-1] > tokens
+        ok = not too_long and not no_rows and (need == 0 or asked <= len(free))
         if not ok:
-            missing += want - cols if too_long else need
+            missing += max(want - cols if too_long else need, 1)
             lens_out.append(a)
             slots += [-1] * m
             pos += [a + k + pos0 for k in range(m)]

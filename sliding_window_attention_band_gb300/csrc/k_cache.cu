@@ -105,21 +105,24 @@ __global__ void __launch_bounds__(kThreads) k_cache_slots(const __grid_constant_
         const int r = r0 + tid, nr = min(kThreads, p.batch - r0);
         long long m = 0, need = 0, total = 0, over = 0;
         int len = 0, have = 0;
-        bool fits = true;
+        bool fits = true, many = false;
         if (tid < nr) {
             len = max(*GP(p.bnd, p.lens + r), 0);
             m = max(*GP(p.bnd, p.n_new + r), 0);
             total = len + m;
             const long long hb = ((long long)len + page - 1) >> p.page_log2, wb = (total + page - 1) >> p.page_log2;
             have = (int)min(hb, (long long)p.cols);
-            fits = total <= 0x7fffffffLL && (p.ring || wb <= p.cols);
+            many = p.max_new > 0 && m > p.max_new;
+            fits = total <= 0x7fffffffLL && (p.ring || wb <= p.cols) && !many;
             if (fits) need = min(wb, (long long)p.cols) - have;
             else over = max(wb - p.cols, 1LL);
         }
         long long ts = m, bs = need;
         __syncthreads();                 // the previous pass has read the chunk
         scan2(ts, bs, c, tok0, blk0);
-        const bool served = fits && (need == 0 || bs + need <= avail);
+        // (a request past the rows takes no block, and none after it does)
+        const bool rows = p.max_new == 0 || m == 0 || ts + m <= p.tokens;
+        const bool served = fits && rows && (need == 0 || bs + need <= avail);
         c.len[tid] = len;
         c.have[tid] = have;
         c.total[tid] = served ? (int)total : 0;
@@ -129,7 +132,8 @@ __global__ void __launch_bounds__(kThreads) k_cache_slots(const __grid_constant_
                 *GP(p.bnd, p.q_start + r) = clamp32(ts);
                 *GP(p.bnd, p.lens_out + r) = served ? (int)total : len;
                 if (served && need) atomicMax(&sh_taken, (unsigned long long)(bs + need));
-                if (!served) atomicAdd(&sh_missing, (unsigned long long)(need + over));
+                if (!served) atomicAdd(&sh_missing, (unsigned long long)max(need + over, 1LL));
+                if (many || !rows) atomicOr(p.err, kErrInvalid);
             }
         }
         __syncthreads();

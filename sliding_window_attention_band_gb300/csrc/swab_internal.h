@@ -363,7 +363,7 @@ cudaError_t launch_rotary(DType dt, bool append, RotaryArgs a, cudaStream_t st);
 struct CacheSlotsArgs {
     const int *lens, *n_new, *free_list, *used;
     int *table, *lens_out, *used_out, *q_start, *slots, *pos;
-    int batch, page_log2, n_blocks, cols, ring, pinned, n_free, tokens, pos0;
+    int batch, page_log2, n_blocks, cols, ring, pinned, max_new, n_free, tokens, pos0;
     int table_pass, state;     // what a launch writes (set by the launcher)
     unsigned *err;
 #if SWAB_BOUNDS_CHECK

@@ -148,7 +148,7 @@ swab_status check_cache(const swab_cache_desc *c) {
     if (!c) return SWAB_ERR_INVALID_ARG;
     if (c->batch < 1 || c->n_blocks < 1 || c->cols < 1) return SWAB_ERR_INVALID_ARG;
     if (c->ring != 0 && c->ring != 1) return SWAB_ERR_INVALID_ARG;
-    if (c->pinned < 0 || c->pinned >= (c->ring ? c->cols : 1)) return SWAB_ERR_INVALID_ARG;
+    if (c->pinned < 0 || c->pinned >= (c->ring ? c->cols : 1) || c->max_new < 0) return SWAB_ERR_INVALID_ARG;
     if (log2_of(c->page) < 0 || c->batch > 65535) return SWAB_ERR_UNSUPPORTED;
     if ((long long)c->n_blocks * c->page > 0x7fffff00ll) return SWAB_ERR_UNSUPPORTED;
     return SWAB_OK;
@@ -420,6 +420,7 @@ SWAB_API swab_status cache_slots(const swab_cache_desc *cache, int32_t tokens, i
     a.cols = cache->cols;
     a.ring = cache->ring;
     a.pinned = cache->pinned;
+    a.max_new = cache->max_new;
     a.n_free = n_free;
     a.tokens = tokens;
     a.pos0 = pos0;

@@ -26,7 +26,9 @@ from . import serve
 class DecodeLoop:
     """A batch of requests of h query and hk key heads under a window of ``w``
     keys on the left (dilation, ``n_sink`` leading global tokens), at most
-    ``max_new`` tokens a request and step.  The blocks of a request are
+    ``max_new`` tokens a request and step (one that adds more is left out of the
+    step: its length stays, used[1] is not 0, the device status word says
+    INVALID_ARG, its rows of the result mean nothing).  The blocks of a request are
     recycled as its window moves on, so the cache does not grow with the
     context.  Rotary positions turn the whole head unless ``rot_dim`` says
     less (0: none); ``turns`` and ``rotary_scale`` as rotary_frequencies gives
@@ -38,7 +40,8 @@ class DecodeLoop:
         self.rot_dim, self.rotary_scale = head_dim if rot_dim is None else rot_dim, rotary_scale
         pinned = -(-n_sink // page)
         cols = pinned + -(-(w * (dilation + 1) + max_new - 1) // page) + 1
-        self.cache = serve.CacheDesc(batch, page, batch * cols, cols, ring=True, pinned=pinned)
+        self.cache = serve.CacheDesc(batch, page, batch * cols, cols, ring=True, pinned=pinned, max_new=max_new)
+        self._prompts = serve.CacheDesc(batch, page, batch * cols, cols, ring=True, pinned=pinned, max_new=(1 << 31) - 1)
         if self.rot_dim and turns is None:
             turns, self.rotary_scale = serve.rotary_frequencies(self.rot_dim)
         self.turns = turns.to(device) if self.rot_dim else None
@@ -63,8 +66,8 @@ class DecodeLoop:
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         self.scale = head_dim ** -0.5
 
-    def _place(self, n_new, slots, pos):
-        serve.cache_slots(self.cache, self.lens, n_new, self.table, self.free_list, self.used, self.lens, self.used, self.q_start,
+    def _place(self, cache, n_new, slots, pos):
+        serve.cache_slots(cache, self.lens, n_new, self.table, self.free_list, self.used, self.lens, self.used, self.q_start,
                           slots, pos)
 
     def fill(self, qkv, n_new):
@@ -85,7 +88,7 @@ class DecodeLoop:
         if not captured and int(n_new.clamp(min=0).sum()) > T:
             raise ValueError(f"n_new: adds up to more than the {T} rows of qkv")
         slots, pos = torch.empty(T, dtype=torch.int32, device=qkv.device), torch.empty(T, dtype=torch.int32, device=qkv.device)
-        self._place(n_new, slots, pos)
+        self._place(self._prompts, n_new, slots, pos)
         q, k, v = qkv.split([self.h, self.hk, self.hk], dim=1)
         d = serve.RotaryDesc(1, T, self.h, self.hk, self.head_dim, self.rot_dim, scale=self.rotary_scale, dtype=self.dtype)
         out = torch.empty(T, self.h, self.head_dim, dtype=self.dtype, device=qkv.device)
@@ -95,7 +98,7 @@ class DecodeLoop:
     def step(self):
         """n_new[r] tokens for every request, their heads in the rows of ``qkv``;
         the attention in ``out`` and ``lse``."""
-        self._place(self.n_new, self.slots, self.pos)
+        self._place(self.cache, self.n_new, self.slots, self.pos)
         q, k, v = self.qkv.split([self.h, self.hk, self.hk], dim=1)
         serve.rotary_append(self._rotary, self.cache, self.turns, q, k, v, self.pos, self.slots, self.q, self.Kc, self.Vc)
         serve.band_decode(self._decode, self.scale, self.q, self.Kc, self.Vc, self.table, self.lens, self.q_start, self.out,

@@ -26,7 +26,7 @@ _S3 = ctypes.c_int64 * 3
 
 
 class _CacheDesc(ctypes.Structure):
-    _fields_ = [(k, ctypes.c_int32) for k in ("batch", "page", "n_blocks", "cols", "ring", "pinned")]
+    _fields_ = [(k, ctypes.c_int32) for k in ("batch", "page", "n_blocks", "cols", "ring", "pinned", "max_new")]
 
 
 class _RotaryDesc(ctypes.Structure):
@@ -59,12 +59,14 @@ def signatures():
 class CacheDesc:
     """A paged cache (swab_cache_desc): K and V as [n_blocks, hk, page, head_dim]
     and a block table [batch, cols]; with ``ring`` the columns from ``pinned``
-    on are recycled once a window has left their blocks."""
+    on are recycled once a window has left their blocks.  With ``max_new``
+    cache_slots serves no request that adds more tokens than that, or more than
+    it has rows for (0: no such limits)."""
 
-    def __init__(self, batch, page, n_blocks, cols, ring=False, pinned=0):
+    def __init__(self, batch, page, n_blocks, cols, ring=False, pinned=0, max_new=0):
         self.batch, self.page, self.n_blocks, self.cols = int(batch), int(page), int(n_blocks), int(cols)
-        self.ring, self.pinned = bool(ring), int(pinned)
-        self.c = _CacheDesc(self.batch, self.page, self.n_blocks, self.cols, int(self.ring), self.pinned)
+        self.ring, self.pinned, self.max_new = bool(ring), int(pinned), int(max_new)
+        self.c = _CacheDesc(self.batch, self.page, self.n_blocks, self.cols, int(self.ring), self.pinned, self.max_new)
         self._ref, self._addr = ctypes.byref(self.c), ctypes.addressof(self.c)
 
 

@@ -260,6 +260,26 @@ def test_cache_slots_writes_no_token_past_its_rows_and_takes_negative_counts_as_
     assert swab.device_status(reset=True) == 0
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("case", [(7, 16, 5, True, 1, 100, 6, 4, 0), (40, 16, 600, False, 0, 4000, 90, 60, 300),
+                                  (1500, 128, 90, False, 0, 9000, 5, 5, 1000), (40, 16, 600, False, 0, 4000, 900, 2 ** 31 - 1, 5000)])
+def test_cache_slots_serves_no_request_past_its_limits(case, in_place):
+    """More tokens than max_new, or than there are rows for: slots of -1, the length kept, no block lost, the status raised."""
+    batch, page, cols, ring, pinned, len_hi, new_hi, max_new, cut = case
+    cache, lens, new, table, free = slots_case(batch, page, cols, ring, pinned, len_hi, new_hi, 13)
+    cache = swab.CacheDesc(batch, page, cache.n_blocks, cols, ring, pinned, max_new=max_new)
+    tokens = int(new.sum()) - cut
+    got = run_slots(cache, lens, new, table, free, 2, tokens, pos0=13, in_place=in_place)
+    want = orc.cache_slots(lens, new, table, free, 2, page, cols, ring, pinned, tokens, 13, max_new=max_new)
+    for name, g, w in zip(("table", "lens", "used", "start", "slots", "pos"), got, want):
+        np.testing.assert_array_equal(g, w, err_msg=name)
+    assert got[2][1] > 0 and swab.device_status(reset=True) == INVALID_BIT
+    # the same within the limits raises nothing
+    within = np.minimum(new, max_new)
+    run_slots(cache, lens, within, table, free, 2, int(within.sum()), pos0=13, in_place=in_place)
+    assert swab.device_status(reset=True) == 0
+
+
 def test_cache_slots_flags_blocks_outside_the_cache():
     cache = swab.CacheDesc(2, 16, 4, 3)
     table = [[4, -1, -1], [1, -1, -1]]              # block 4 of a cache of 4
@@ -1008,6 +1028,30 @@ def test_offsets_past_32_bits(hd):
     swab.band_decode(sd, hd ** -0.5, q[n - 1:n].contiguous(), *small, i32([[0, 1, 2]]), i32([n]), i32([0, 1]), want, wlse, ws, i32([3, 4]))
     same_bits(out, want)
     same_bits(lse, wlse)
+
+
+def test_decode_loop_leaves_out_requests_that_add_too_much():
+    """A step with more tokens than max_new for one request: its length stays, the others go on, the status is raised."""
+    h, hd, w = 2, 64, 20
+    loops = [swab.DecodeLoop(3, h, h, hd, w, max_new=2, page=16, rot_dim=0, dtype=F16) for _ in range(2)]
+    x = randn((3, 40, 3 * h, hd), F16, 610)
+    for loop in loops:
+        loop.fill(x[:, :30].reshape(90, 3 * h, hd), i32([30] * 3))
+        loop.n_new.copy_(i32([1, 3, 2] if loop is loops[0] else [1, 0, 2]))
+        rows = torch.cat((x[0, 30:31], x[1, 30:33 if loop is loops[0] else 30], x[2, 30:32]))
+        loop.qkv[:len(rows)] = rows
+        loop.step()
+    assert loops[0].lens.tolist() == loops[1].lens.tolist() == [31, 30, 32]
+    assert loops[0].used.tolist()[1] > 0 and loops[1].used.tolist()[1] == 0
+    assert swab.device_status(reset=True) == INVALID_BIT
+    same_bits(loops[0].out[[0, 4, 5]], loops[1].out[[0, 1, 2]])
+    # and the left-out request goes on as if nothing had been asked of it
+    for loop in loops:
+        loop.n_new.copy_(i32([0, 2, 1]))
+        loop.qkv[:3] = torch.cat((x[1, 30:32], x[2, 32:33]))
+        loop.step()
+    same_bits(loops[0].out[:3], loops[1].out[:3])
+    assert loops[0].lens.tolist() == [31, 32, 33] and swab.device_status(reset=True) == 0
 
 
 def test_decode_loop_restarts_requests():

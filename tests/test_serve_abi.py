@@ -140,6 +140,15 @@ def test_cache_slots_arguments(lib):
     assert slots(lib, c, start=FAKE) == INVALID
 
 
+def test_cache_max_new(lib):
+    c = cache_desc()
+    c.max_new = -1
+    assert slots(lib, c) == INVALID and append(lib, rotary_desc(), c) == INVALID and decode(lib, decode_desc(c)) == INVALID
+    if not torch.cuda.is_available():
+        c.max_new = 2 ** 31 - 1
+        assert slots(lib, c) == CUDA
+
+
 @needs_no_gpu
 def test_valid_cache_calls_reach_the_launch(lib):
     assert slots(lib, cache_desc()) == CUDA

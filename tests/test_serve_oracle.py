@@ -66,6 +66,17 @@ def test_cache_slots_by_hand():
     assert lens.tolist() == [47] and used.tolist() == [0, 1] and slots.tolist() == [-1] * 3
 
 
+def test_cache_slots_limits_by_hand():
+    # at most 2 tokens a request, 4 rows: request 1 adds 3, request 3 ends at row 6; request 2 is served
+    t, lens, used, start, slots, _ = orc.cache_slots([15, 0, 0, 16], [1, 3, 0, 2], [[5, -1]] * 4, [9, 4, 2], 0, 16, 2, tokens=4,
+                                                     max_new=2)
+    assert lens.tolist() == [16, 0, 0, 16] and used.tolist() == [0, 2] and start.tolist() == [0, 1, 4, 4, 6]
+    assert slots.tolist() == [5 * 16 + 15, -1, -1, -1] and t.tolist() == [[5, -1]] * 4
+    # no limits: request 1 takes block 9, request 3 block 4, rows or not
+    _, lens, used, _, slots, _ = orc.cache_slots([15, 0, 0, 16], [1, 3, 0, 2], [[5, -1]] * 4, [9, 4, 2], 0, 16, 2, tokens=4)
+    assert lens.tolist() == [16, 3, 0, 18] and used.tolist() == [2, 0] and slots.tolist() == [95, 144, 145, 146]
+
+
 def paged(x, page, perm):
     """[n, hk, hd] -> cache blocks in the order perm."""
     n, hk, hd = x.shape
