@@ -56,6 +56,19 @@ def signatures():
     }
 
 
+def _number(name, value, bits=32):
+    """value as an int; ctypes would cut it down to the field's bits without a word."""
+    value = int(value)
+    if not -(1 << (bits - 1)) <= value < 1 << (bits - 1):
+        raise ValueError(f"{name}: {value} does not fit {bits} bits")
+    return value
+
+
+def _take_numbers(self, bits=32, **values):
+    for name, value in values.items():
+        setattr(self, name, _number(name, value, bits))
+
+
 class CacheDesc:
     """A paged cache (swab_cache_desc): K and V as [n_blocks, hk, page, head_dim]
     and a block table [batch, cols]; with ``ring`` the columns from ``pinned``
@@ -64,8 +77,8 @@ class CacheDesc:
     it has rows for (0: no such limits)."""
 
     def __init__(self, batch, page, n_blocks, cols, ring=False, pinned=0, max_new=0):
-        self.batch, self.page, self.n_blocks, self.cols = int(batch), int(page), int(n_blocks), int(cols)
-        self.ring, self.pinned, self.max_new = bool(ring), int(pinned), int(max_new)
+        _take_numbers(self, batch=batch, page=page, n_blocks=n_blocks, cols=cols, pinned=pinned, max_new=max_new)
+        self.ring = bool(ring)
         self.c = _CacheDesc(self.batch, self.page, self.n_blocks, self.cols, int(self.ring), self.pinned, self.max_new)
         self._ref, self._addr = ctypes.byref(self.c), ctypes.addressof(self.c)
 
@@ -78,9 +91,8 @@ class RotaryDesc:
     def __init__(self, b, n, h, hk, head_dim, rot_dim, interleaved=False, scale=1.0, pos0=0, dtype=torch.float16):
         if dtype not in _b._DTYPES:
             raise ValueError(f"unsupported dtype {dtype}")
-        self.b, self.n, self.h, self.hk = int(b), int(n), int(h), int(hk)
-        self.head_dim, self.rot_dim, self.interleaved = int(head_dim), int(rot_dim), bool(interleaved)
-        self.scale, self.pos0, self.dtype = float(scale), int(pos0), dtype
+        _take_numbers(self, b=b, n=n, h=h, hk=hk, head_dim=head_dim, rot_dim=rot_dim, pos0=pos0)
+        self.interleaved, self.scale, self.dtype = bool(interleaved), float(scale), dtype
         self.tokens = self.b * self.n
         # the shapes a tensor of h or hk heads may have: tokens as [b, n] or flat
         self._q = ((self.b, self.n, self.h, self.head_dim), (self.tokens, self.h, self.head_dim))
@@ -116,12 +128,11 @@ class DecodeDesc:
                  dtype=torch.float16, q_row_stride=0, out_row_stride=0):
         if dtype not in _b._DTYPES:
             raise ValueError(f"unsupported dtype {dtype}")
-        self.cache, self.tokens, self.h, self.hk, self.head_dim = cache, int(tokens), int(h), int(hk), int(head_dim)
-        self.w = 1 << 30 if w is None else int(w)
-        self.dilation, self.n_sink, self.max_q = int(dilation), int(n_sink), int(max_q)
-        self.max_len = cache.cols * cache.page if max_len is None else int(max_len)
-        self.prefix_len, self.dtype = int(prefix_len), dtype
-        self.q_row_stride, self.out_row_stride = int(q_row_stride), int(out_row_stride)
+        _take_numbers(self, tokens=tokens, h=h, hk=hk, head_dim=head_dim, w=1 << 30 if w is None else w, dilation=dilation,
+                      n_sink=n_sink, max_q=max_q, prefix_len=prefix_len,
+                      max_len=min(cache.cols * cache.page, 0x7fffffff) if max_len is None else max_len)
+        _take_numbers(self, 64, q_row_stride=q_row_stride, out_row_stride=out_row_stride)
+        self.cache, self.dtype = cache, dtype
         self.c = _DecodeDesc(cache.c, self.tokens, self.h, self.hk, self.head_dim, self.w, self.dilation, self.n_sink,
                              self.max_q, self.max_len, self.prefix_len, _b._DTYPES[dtype], self.q_row_stride,
                              self.out_row_stride)
@@ -266,9 +277,10 @@ def rotary_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, origin
         raise ValueError(f"scaling: expected one of {sorted(_SCALING)}, got {scaling!r}")
     if high_turns is None:
         high_turns = 32.0 if scaling == "yarn" else 4.0
-    turns = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.int64)
+    rot_dim = _number("rot_dim", rot_dim)
+    turns = torch.empty(max(rot_dim, 0) // 2, dtype=torch.int64)
     scale = ctypes.c_float(1.0)
-    rc = _b.load().rotary_frequencies(int(rot_dim), float(base), _SCALING[scaling], float(factor), float(original),
+    rc = _b.load().rotary_frequencies(rot_dim, float(base), _SCALING[scaling], float(factor), float(original),
                                       float(low_turns), float(high_turns), turns.data_ptr(), ctypes.byref(scale))
     if rc != _b.SWAB_OK:
         raise _b.SwabError("rotary_frequencies", rc)
@@ -315,6 +327,9 @@ def cache_slots(cache: CacheDesc, lens, n_new, table, free_list, used, lens_out,
             cache._addr, pos0, lens, n_new, table, free_list, used, lens_out, used_out, q_start, slots, pos)):
         return
     B, n_free, tokens, dev = cache.batch, free_list.numel(), slots.numel(), lens.get_device()
+    if max(n_free, tokens) > 0x7fffffff:
+        raise ValueError(f"free_list, slots: at most 2^31 - 1 elements, got {n_free} and {tokens}")
+    pos0 = _number("pos0", pos0)
     if not (dev >= 0 and lens.dtype is _I32 and n_new.dtype is _I32 and table.dtype is _I32 and free_list.dtype is _I32
             and used.dtype is _I32 and lens_out.dtype is _I32 and used_out.dtype is _I32 and q_start.dtype is _I32
             and slots.dtype is _I32 and pos.dtype is _I32 and lens.numel() == B and n_new.numel() == B

@@ -266,6 +266,34 @@ def test_binding_checks():
         swab.rotary_append(d, c, None, x, x, x, None, None, None, x, x)
 
 
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 16, -2 ** 31 - 1, 2 ** 64 + 16])
+def test_numbers_past_32_bits_are_refused_not_wrapped(big):
+    """A window of 2^32 + 16 is no window of 16."""
+    c = swab.CacheDesc(1, 16, 2, 2)
+    for k in ("batch", "page", "n_blocks", "cols", "pinned", "max_new"):
+        with pytest.raises(ValueError, match=k):
+            swab.CacheDesc(**{**dict(batch=1, page=16, n_blocks=2, cols=2), k: big})
+    for k in ("b", "n", "h", "hk", "head_dim", "rot_dim", "pos0"):
+        with pytest.raises(ValueError, match=k):
+            swab.RotaryDesc(**{**dict(b=1, n=4, h=2, hk=1, head_dim=64, rot_dim=64), k: big})
+    for k in ("tokens", "h", "hk", "head_dim", "w", "dilation", "n_sink", "max_q", "max_len", "prefix_len"):
+        with pytest.raises(ValueError, match=k):
+            swab.DecodeDesc(c, **{**dict(tokens=1, h=2, hk=1, head_dim=64), k: big})
+    for k in ("q_row_stride", "out_row_stride"):
+        with pytest.raises(ValueError, match=k):
+            swab.DecodeDesc(c, 1, 2, 1, 64, **{k: big << 33})
+    with pytest.raises(ValueError, match="rot_dim"):
+        swab.rotary_frequencies(big)
+    names = ("lens", "n_new", "table", "free_list", "used", "lens_out", "used_out", "q_start", "slots", "pos")
+    sizes = dict(table=2, used_out=2, q_start=2)
+    with pytest.raises(ValueError, match="pos0"):
+        swab.cache_slots(c, *[FakeInts(sizes.get(k, 1)) for k in names], pos0=big)
+    for name in ("free_list", "slots"):
+        with pytest.raises(ValueError, match=name):
+            swab.cache_slots(c, *[FakeInts(2 ** 32 + 1 if k == name or (k, name) == ("pos", "slots") else sizes.get(k, 1))
+                                  for k in names])
+
+
 class FakeCuda:
     """Enough of a CUDA tensor for the binding's checks."""
 
@@ -280,6 +308,17 @@ class FakeCuda:
 
     def data_ptr(self):
         return FAKE
+
+
+class FakeInts(FakeCuda):
+    def __init__(self, n):
+        super().__init__((n,), (1,), torch.int32)
+
+    def numel(self):
+        return self.shape[0]
+
+    def is_contiguous(self):
+        return True
 
 
 def test_binding_rows_and_strides():
