@@ -44,7 +44,16 @@ class DecodeLoop:
         self._prompts = serve.CacheDesc(batch, page, batch * cols, cols, ring=True, pinned=pinned, max_new=(1 << 31) - 1)
         if self.rot_dim and turns is None:
             turns, self.rotary_scale = serve.rotary_frequencies(self.rot_dim)
-        self.turns = turns.to(device) if self.rot_dim else None
+        if self.rot_dim and (turns.dtype is not torch.int64 or turns.shape != (self.rot_dim // 2,)):
+            raise ValueError(f"turns: expected {self.rot_dim // 2} int64 values (rotary_frequencies), got {tuple(turns.shape)} "
+                             f"{turns.dtype}")
+        self.tokens = batch * max_new
+        self._rotary = serve.RotaryDesc(1, self.tokens, h, hk, head_dim, self.rot_dim, scale=self.rotary_scale, dtype=dtype)
+        self._decode = serve.DecodeDesc(self.cache, self.tokens, h, hk, head_dim, w=w, dilation=dilation, n_sink=n_sink,
+                                        max_q=max_new, max_len=1 << 30, dtype=dtype)
+        # (what the calls of a step would refuse is refused here: there the lengths would have moved on)
+        serve.check_step(self.cache, self._rotary, self._decode)
+        self.turns = turns.contiguous().to(device) if self.rot_dim else None
         i32 = dict(dtype=torch.int32, device=device)
         new = dict(dtype=dtype, device=device)
         self.Kc = torch.zeros(batch * cols, hk, page, head_dim, **new)
@@ -52,16 +61,12 @@ class DecodeLoop:
         self.table = torch.full((batch, cols), -1, **i32)
         self.free_list = torch.arange(batch * cols, **i32)
         self.lens, self.used, self.q_start = torch.zeros(batch, **i32), torch.zeros(2, **i32), torch.zeros(batch + 1, **i32)
-        self.tokens = batch * max_new
         self.n_new = torch.zeros(batch, **i32)
         self.slots, self.pos = torch.zeros(self.tokens, **i32), torch.zeros(self.tokens, **i32)
         self.qkv = torch.zeros(self.tokens, h + 2 * hk, head_dim, **new)
         self.q = torch.zeros(self.tokens, h, head_dim, **new)
         self.out = torch.zeros_like(self.q)
         self.lse = torch.zeros(self.tokens, h, dtype=torch.float32, device=device)
-        self._rotary = serve.RotaryDesc(1, self.tokens, h, hk, head_dim, self.rot_dim, scale=self.rotary_scale, dtype=dtype)
-        self._decode = serve.DecodeDesc(self.cache, self.tokens, h, hk, head_dim, w=w, dilation=dilation, n_sink=n_sink,
-                                        max_q=max_new, max_len=1 << 30, dtype=dtype)
         need = serve.band_decode_workspace(self._decode)
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         self.scale = head_dim ** -0.5

@@ -464,3 +464,18 @@ def band_decode(desc: DecodeDesc, scale, Q, Kc, Vc, table, lens, q_start, O, lse
         ws = workspace.data_ptr()
     _run("band_decode", dev, stream, d._ref, scale, Q.data_ptr(), Kc.data_ptr(), Vc.data_ptr(), table.data_ptr(), lens.data_ptr(),
          q_start.data_ptr(), pt, O.data_ptr(), lp, ws)
+
+
+def check_step(cache: CacheDesc, rotary: RotaryDesc, decode: DecodeDesc):
+    """Raises the error with which cache_slots, rotary_append or band_decode would
+    refuse these descriptors.  The library looks at them before it looks at
+    pointers, so a call with good ones is stopped by a pointer off its alignment:
+    nothing is launched, no GPU is needed."""
+    ok, odd = 16, 2
+    calls = {"cache_slots": (cache._ref, 0, 0, odd, odd, odd, odd, 0, odd, odd, odd, odd, odd, odd, None),
+             "rotary_append": (ctypes.byref(rotary._plain), cache._ref, ok, ok, ok, odd, odd, odd, odd, odd, odd, None),
+             "band_decode": (decode._ref, 1.0, odd, odd, odd, odd, odd, odd, odd, odd, odd, odd, None)}
+    for name, args in calls.items():
+        rc = getattr(_b.load(), name)(*args)
+        if rc != _b.STATUS_NAMES.index("SWAB_ERR_MISALIGNED"):
+            raise _b.SwabError(name, rc)

@@ -360,6 +360,17 @@ def test_decode_loop_refuses_a_prompt_before_its_lengths_move(lib, monkeypatch):
     assert len(called) == 1
 
 
+@pytest.mark.parametrize("bad", [
+    dict(head_dim=68), dict(head_dim=264), dict(h=3), dict(h=256, hk=1), dict(dilation=16), dict(dilation=-1), dict(page=48),
+    dict(max_new=0), dict(w=-1), dict(w=(1 << 30) + 1), dict(n_sink=-1), dict(batch=0), dict(batch=70000), dict(hk=0), dict(rot_dim=31),
+    dict(rot_dim=66), dict(rot_dim=-2), dict(turns=torch.zeros(31, dtype=torch.int64)),
+    dict(turns=torch.zeros(32)), dict(dtype=torch.int8)])
+def test_decode_loop_refuses_when_it_is_made_what_its_calls_would(lib, bad):
+    """Not at its first step, when the lengths have moved on."""
+    with pytest.raises((ValueError, B.SwabError)):
+        swab.DecodeLoop(**{**dict(batch=2, h=4, hk=2, head_dim=64, w=16, page=16, dtype=torch.float16, device="cpu"), **bad})
+
+
 def test_decode_loop_refuses_prompts_longer_than_their_rows(lib, monkeypatch):
     """n_new may not add up to more than the rows of qkv (their positions would never be written); fewer is padding."""
     loop = swab.DecodeLoop(3, 4, 2, 64, w=16, page=16, dtype=torch.float16, device="cpu")
