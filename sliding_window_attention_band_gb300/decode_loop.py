@@ -43,7 +43,7 @@ class DecodeLoop:
         self.cache = serve.CacheDesc(batch, page, batch * cols, cols, ring=True, pinned=pinned, max_new=max_new)
         self._prompts = serve.CacheDesc(batch, page, batch * cols, cols, ring=True, pinned=pinned, max_new=(1 << 31) - 1)
         if self.rot_dim and turns is None:
-            turns, self.rotary_scale = serve.rotary_frequencies(self.rot_dim)
+            turns, _ = serve.rotary_frequencies(self.rot_dim)
         if self.rot_dim and (turns.dtype is not torch.int64 or turns.shape != (self.rot_dim // 2,)):
             raise ValueError(f"turns: expected {self.rot_dim // 2} int64 values (rotary_frequencies), got {tuple(turns.shape)} "
                              f"{turns.dtype}")

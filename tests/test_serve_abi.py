@@ -371,6 +371,16 @@ def test_decode_loop_refuses_when_it_is_made_what_its_calls_would(lib, bad):
         swab.DecodeLoop(**{**dict(batch=2, h=4, hk=2, head_dim=64, w=16, page=16, dtype=torch.float16, device="cpu"), **bad})
 
 
+def test_decode_loop_keeps_the_rotary_scale_it_is_given(lib):
+    make = lambda **kw: swab.DecodeLoop(2, 4, 2, 64, w=16, page=16, dtype=torch.float16, device="cpu", **kw)  # noqa: E731
+    turns, scale = swab.rotary_frequencies(64, scaling="yarn", factor=4.0, original=4096)
+    for loop, want in ((make(), 1.0), (make(rotary_scale=1.25), 1.25), (make(turns=turns, rotary_scale=scale), scale)):
+        assert loop.rotary_scale == want and loop._rotary.scale == want and abs(loop._rotary._plain.scale - want) < 1e-7
+    assert torch.equal(make(turns=turns).turns, turns) and not torch.equal(make().turns, turns)
+    with pytest.raises(B.SwabError):
+        make(rotary_scale=math.inf)
+
+
 def test_decode_loop_refuses_prompts_longer_than_their_rows(lib, monkeypatch):
     """n_new may not add up to more than the rows of qkv (their positions would never be written); fewer is padding."""
     loop = swab.DecodeLoop(3, 4, 2, 64, w=16, page=16, dtype=torch.float16, device="cpu")
