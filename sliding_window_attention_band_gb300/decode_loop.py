@@ -128,6 +128,9 @@ class DecodeLoop:
     @classmethod
     def from_workload(cls, wl, batch=None, device="cuda"):
         """The loop that carries a named workload's sequences on: its heads,
-        window on the left, dilation and leading global tokens."""
-        n_sink = len(wl.global_idx) if tuple(wl.global_idx) == tuple(range(len(wl.global_idx))) else 0
+        window on the left, dilation and global tokens, which have to be the
+        leading ones."""
+        n_sink = len(set(wl.global_idx))
+        if sorted(set(wl.global_idx)) != list(range(n_sink)):
+            raise ValueError(f"global tokens other than the leading ones: {tuple(wl.global_idx)}")
         return cls(wl.b if batch is None else batch, wl.h, wl.h, wl.head_dim, wl.w, wl.dilation, n_sink, dtype=wl.dtype, device=device)

@@ -381,6 +381,15 @@ def test_decode_loop_keeps_the_rotary_scale_it_is_given(lib):
         make(rotary_scale=math.inf)
 
 
+def test_decode_loop_of_a_workload_takes_leading_global_tokens_only(lib):
+    wl = lambda idx: swab.Workload(9, "w", 2, 2, 64, 64, 8, 8, 0, torch.float16, idx)  # noqa: E731
+    for idx, sinks in (((), 0), ((0,), 1), ((0, 1, 2), 3), ((2, 0, 1), 3)):
+        assert swab.DecodeLoop.from_workload(wl(idx), device="cpu")._decode.n_sink == sinks
+    for idx in ((1,), (0, 2), (0, 1, 63), (5, 6)):
+        with pytest.raises(ValueError, match="leading"):
+            swab.DecodeLoop.from_workload(wl(idx), device="cpu")
+
+
 def test_decode_loop_refuses_prompts_longer_than_their_rows(lib, monkeypatch):
     """n_new may not add up to more than the rows of qkv (their positions would never be written); fewer is padding."""
     loop = swab.DecodeLoop(3, 4, 2, 64, w=16, page=16, dtype=torch.float16, device="cpu")
