@@ -6,7 +6,8 @@ same sources with SWAB_BOUNDS_CHECK=1 give libswab_bounds.so, the
 bounds-checked build (every plain global access of a kernel tested against
 the call's buffer extents); ``build_all()`` compiles both in one pool.  Beside
 them lies _serve_call-*.so, host code only: a Python module that takes the
-tensors of a serving call straight to the library (csrc/serve_call.cpp).
+tensors of a serving call straight to the library (csrc/serve_call.cpp).  The
+library does without it: where it cannot be built, a warning says so.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 import torch
@@ -127,10 +129,13 @@ def build_variants(variants, force: bool = False, verbose: bool = False, extra_f
         with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, max(os.cpu_count() or 1, len(SOURCES)))) as ex:
             made = ex.submit(_build_calls) if calls else None
             objs = list(ex.map(lambda job: job[2](job[1]), jobs))
-            if made is not None:
-                made.result()
         for v in todo:
             _link(v, [o for (vv, _, _), o in zip(jobs, objs) if vv == v])
+        # (the same calls go through Python where the module is not there)
+        if made is not None and made.exception() is not None:
+            if os.path.exists(CALLS):
+                os.unlink(CALLS)             # made from older sources
+            warnings.warn(f"the compiled serving calls were not built, they take some microseconds more: {made.exception()}")
     return [VARIANTS[v][0] for v in variants]
 
 

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -166,10 +167,14 @@ def _load_calls():
     calls = _NoCalls
     if os.path.exists(_build.CALLS):
         spec = importlib.util.spec_from_file_location("_serve_call", _build.CALLS)
-        calls = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(calls)
-        calls.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-                     for name in ("rotary", "rotary_bwd", "cache_slots", "rotary_append", "band_decode")))
+        try:
+            calls = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(calls)
+            calls.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                         for name in ("rotary", "rotary_bwd", "cache_slots", "rotary_append", "band_decode")))
+        except ImportError as e:
+            warnings.warn(f"the compiled serving calls do not load, they take some microseconds more: {e}")
+            calls = _NoCalls
     _calls = calls
     return calls
 

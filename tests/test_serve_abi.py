@@ -455,6 +455,31 @@ def test_compiled_calls_leave_what_is_unusual_to_the_binding(lib):
         swab.rotary(r, torch.zeros(32, dtype=torch.int64), f16, f16, f16[:, :2], f16[:, :2])
 
 
+def test_library_is_built_and_called_without_the_compiled_calls(lib, monkeypatch, tmp_path):
+    """A compiler that cannot make the module, or a module that does not load: a warning, and the calls go through Python."""
+    linked = []
+    monkeypatch.setattr(swab_build, "CALLS", str(tmp_path / "_serve_call.so"))
+    (tmp_path / "_serve_call.so").write_bytes(b"of another machine")
+    monkeypatch.setattr(serve, "_calls", None)
+    with pytest.warns(UserWarning, match="compiled"):
+        assert serve._load_calls() is serve._NoCalls
+    with pytest.raises(ValueError, match="CUDA"):
+        z = torch.zeros(1, dtype=torch.int32)
+        swab.cache_slots(swab.CacheDesc(1, 16, 2, 2), z, z, z, z, z, z, z, z, z, z)
+
+    def no_compiler():
+        raise RuntimeError("g++ failed")
+    monkeypatch.setattr(swab_build, "_build_calls", no_compiler)
+    monkeypatch.setattr(swab_build, "calls_up_to_date", lambda: False)
+    monkeypatch.setattr(swab_build, "up_to_date", lambda v: False)
+    monkeypatch.setattr(swab_build, "_compile_jobs", lambda *a: [("x.cu", lambda src: "x.o")])
+    monkeypatch.setattr(swab_build, "_link", lambda v, objs: linked.append((v, objs)))
+    with pytest.warns(UserWarning, match="compiled"):
+        assert swab_build.build_variants(("regular",)) == [swab_build.LIB]
+    assert linked == [("regular", ["x.o"])]
+    assert not (tmp_path / "_serve_call.so").exists()          # one of older sources must not be loaded
+
+
 def test_descriptors_of_the_compiled_calls_follow_the_header(lib):
     """The C structs the compiled calls read by address are those the binding passes by reference."""
     r = swab.RotaryDesc(2, 3, 4, 2, 64, 32, interleaved=True, scale=1.25, pos0=7, dtype=torch.bfloat16)
