@@ -238,7 +238,7 @@ def _turns(d, t, dev):
         raise ValueError("turns: needed when rot_dim > 0")
     if t.get_device() != dev:
         raise _place("turns", t, dev)
-    if t.dtype is not _I64 or t.numel() * 2 != d.rot_dim or not t.is_contiguous():
+    if t.dtype is not _I64 or t.numel() != d.rot_dim // 2 or not t.is_contiguous():
         raise ValueError(f"turns: expected {d.rot_dim // 2} contiguous int64 values (rotary_frequencies), got "
                          f"{tuple(t.shape)} {t.dtype}")
     return t.data_ptr()

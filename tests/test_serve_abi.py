@@ -310,6 +310,18 @@ class FakeCuda:
         return FAKE
 
 
+def test_an_odd_rot_dim_is_the_librarys_error_on_either_way(lib, monkeypatch):
+    """The binding's own check of turns lets through what the compiled module lets through."""
+    d = swab.RotaryDesc(1, 1, 2, 1, 64, 31)
+    t = FakeInts(15)
+    t.dtype = torch.int64
+    assert serve._turns(d, t, 0) == FAKE
+    t.shape = (16,)
+    with pytest.raises(ValueError, match="turns"):
+        serve._turns(d, t, 0)
+    assert rotary(lib, d._plain) == INVALID
+
+
 class FakeInts(FakeCuda):
     def __init__(self, n):
         super().__init__((n,), (1,), torch.int32)
