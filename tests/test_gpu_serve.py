@@ -465,6 +465,55 @@ def test_decode_long_and_wide(case, dtype):
     Decode(dtype, seed=90, **case).check()
 
 
+def check_some(c, o, lse, requests):
+    """Decode.check for the named requests of a large batch: each against the oracle over its own blocks."""
+    for r in requests:
+        pre = len(c.ptable) if c.prefix else 0
+        used = c.table[r][c.table[r] >= 0]
+        blocks = torch.tensor(np.concatenate([c.ptable[:pre], used]).astype(np.int64), device="cuda")
+        one = Decode.__new__(Decode)
+        one.__dict__.update(c.__dict__)
+        rows = slice(int(c.q_start[r]), int(c.q_start[r + 1]))
+        one.q, one.kc, one.vc, one.tokens = c.q[rows], c.kc[blocks], c.vc[blocks], rows.stop - rows.start
+        one.table, one.ptable = np.full((1, c.table.shape[1]), -1), np.arange(pre)
+        one.table[0, :len(used)] = pre + np.arange(len(used))
+        one.lens, one.q_start = [c.lens[r]], np.array([0, one.tokens])
+        one.check(o[rows], lse[rows])
+
+
+# 12 warps an SM come as blocks of four, three or two by how many blocks there are (152 SMs: 456 of four, 608 of
+# three, 912 of two fit at once) and, for lists of 2048 keys and more, by how well the pieces fill them
+BLOCKS = [  # requests, most keys, and: how the rows kernel runs
+    dict(n=60, keys=600, h=16, hk=8),                        # 480 blocks: three warps, lists whole
+    dict(n=60, keys=600, h=16, hk=8, prefix=260),            # three warps, the prefix's parts folded in
+    dict(n=60, keys=600, h=8, hk=8, m=2, w=300, n_sink=5),   # three warps under a window
+    dict(n=100, keys=500, h=8, hk=8),                        # 800 blocks: two warps
+    dict(n=100, keys=500, h=16, hk=8, prefix=300),           # two warps, the prefix's parts folded in
+    dict(n=32, keys=2600, h=8, hk=8),                        # 256 long lists: three warps, two pieces
+    dict(n=32, keys=2600, h=8, hk=8, prefix=700),            # three warps, two pieces and the prefix's parts joined
+    dict(n=45, keys=2600, h=8, hk=4, m=2),                   # 180 long lists: two warps, five pieces
+    dict(n=45, keys=2600, h=8, hk=4, m=2, prefix=300),       # two warps, five pieces and the prefix's parts joined
+    dict(n=130, keys=400, h=8, hk=8),                        # 1040 blocks: four warps, more than fit at once
+    dict(n=130, keys=400, h=8, hk=8, prefix=300)]
+
+
+@pytest.mark.parametrize("dtype,hd", [(F16, 64), (BF16, 128), (F16, 128), (BF16, 64)])
+@pytest.mark.parametrize("case", BLOCKS)
+def test_decode_in_blocks_of_four_three_and_two_warps(case, dtype, hd):
+    n, keys, m = case["n"], case["keys"], case.get("m", 1)
+    rng = np.random.default_rng(113)
+    lens, new = rng.integers(m, keys + 1, n), rng.integers(0, m + 1, n)
+    lens[n // 2], new[n // 2], new[0], new[n - 1] = keys, m, m, 1
+    if keys > 2000:
+        lens[rng.random(n) < 0.7] //= 16             # (few of the long ones are filled in)
+        lens, lens[n // 2] = np.maximum(lens, m), keys
+    c = Decode(dtype, lens.tolist(), new.tolist(), case["h"], case["hk"], hd, page=64, w=case.get("w"),
+               n_sink=case.get("n_sink", 0), prefix=case.get("prefix", 0), pad=2, seed=114)
+    o, lse = c.run()
+    assert (o[int(c.q_start[-1]):] == 7.0).all() and not o.isnan().any()
+    check_some(c, o, lse, sorted({0, 1, n // 3, n // 2, n - 2, n - 1}))
+
+
 def test_decode_of_contexts_longer_than_announced():
     """max_len divides the work only."""
     for dtype in (F16, F32):
