@@ -9,9 +9,9 @@
 //     m' = max(m, x),  l' = l 2^(m - m') + 2^(x - m'),  o' = o 2^(m - m') + 2^(x - m') v.
 // The pieces are joined as O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
 // fp32 is exact to fp32 rounding here (no tf32).  HBM-bound with a head of its
-// own (16 requests of 4k, 12 heads of 64, fp32: 67 us, 5.6 TB/s), bound by
+// own (16 requests of 3 to 5k, 12 heads of 64, fp32: 62 us, 6.0 TB/s), bound by
 // instructions where a key serves several heads (24 heads of 96 over 8, bf16:
-// 135 us, a fifth of the copy rate); joining 57 parts of 32 heads takes 5 us.
+// 122 us, a quarter of the copy rate); joining 57 parts of 32 heads takes 5 us.
 #include "swab_internal.h"
 #include "swab_decode.cuh"
 
@@ -40,8 +40,17 @@ __device__ __forceinline__ void widen16(const uint4 &v, float *f) {
 // times when the row has more than 32 pieces); kThreads / kLanes keys at a time.
 // A block answers kR query heads that share the key head, so a key is loaded
 // once for them.
+// Blocks an SM holds: the plan cuts the lists for 8.  Left to itself the compiler
+// gave one query head 52 to 72 registers and four of them 96 to 168, by what the
+// code around the loop happened to be, and the loads in flight went with them (16
+// requests of 3 to 5k, 12 heads of 64, fp32: 67 to 83 us, 62 with 8 blocks; 12
+// of 96 in 16 bits 83 to 104, 69; 24 over 8 of 96 in 16 bits 120 to 134, 122 with 4).
+// Fewer where that would spill: 4 lanes a key are 32 keys at a time.
+template <typename T, int kLanes, int kR>
+constexpr int kResident = kR == 1 ? (kLanes == 4 ? 6 : 8) : sizeof(T) == 2 && kLanes == 4 ? 3 : 4;
+
 template <typename T, int kLanes, int kVec, int kR>
-__global__ void __launch_bounds__(kThreads) k_decode_general(const __grid_constant__ DecodeArgs p) {
+__global__ void __launch_bounds__(kThreads, kResident<T, kLanes, kR>) k_decode_general(const __grid_constant__ DecodeArgs p) {
     constexpr int kV = 16 / sizeof(T), kE = kV * kVec, kGroups = kThreads / kLanes, kU = kVec == 1 ? 4 : 2;
     __shared__ float so[kGroups][kLanes * kE];
     __shared__ float2 sml[kGroups];
@@ -282,8 +291,9 @@ cudaError_t launch_general_r(const DecodeArgs &a, cudaStream_t st) {
     if (pieces <= 4) return launch_dependent(&k_decode_general<T, 4, 1, kR>, grid, kThreads, 0, st, a);
     if (pieces <= 8) return launch_dependent(&k_decode_general<T, 8, 1, kR>, grid, kThreads, 0, st, a);
     if (pieces <= 16) return launch_dependent(&k_decode_general<T, 16, 1, kR>, grid, kThreads, 0, st, a);
-    if (pieces <= 32) return launch_dependent(&k_decode_general<T, 32, 1, kR>, grid, kThreads, 0, st, a);
-    return launch_dependent(&k_decode_general<T, 32, 2, kR>, grid, kThreads, 0, st, a);
+    if constexpr (sizeof(T) == 4)
+        if (pieces > 32) return launch_dependent(&k_decode_general<T, 32, 2, kR>, grid, kThreads, 0, st, a);
+    return launch_dependent(&k_decode_general<T, 32, 1, kR>, grid, kThreads, 0, st, a);
 }
 
 template <typename T>
