@@ -434,7 +434,8 @@ SWAB_API swab_status rotary_frequencies(int32_t rot_dim, double base, int32_t sc
 /* Rotary positions: with t = 2 pi * frac(p * turns[k] / 2^64) for the position
  * p = pos[bb, i] + pos0 (pos NULL: p = i + pos0) and pair k = (a, b) of a head,
  *     y_a = scale * (x_a cos t - x_b sin t),  y_b = scale * (x_b cos t + x_a sin t),
- * channels from rot_dim on copied; fp32, rounded once.  Q -> Qo and, with
+ * channels from rot_dim on copied; fp32, rounded once (the angle is off by at most
+ * 2^-25 pi).  Q -> Qo and, with
  * hk > 0, K -> Ko.  turns: DEVICE array of rot_dim / 2 (NULL when rot_dim is
  * 0); pos: DEVICE int32 [b, n].  An output may be its own input (same pointer
  * and strides), no other overlap. */
@@ -490,7 +491,8 @@ SWAB_API swab_status cache_slots(const swab_cache_desc *cache, int32_t tokens, i
  * tokens, slots and pos as written by cache_slots; a token with slot -1 is not
  * written (its Q still turns).  rot_dim 0: a plain append (turns, pos may be
  * NULL; Q and Qo both NULL leave Q out).  hk >= 1.  Slots other than -1 must
- * differ from each other.  cache->batch, cols, ring, pinned are not used. */
+ * differ from each other.  cache->batch, cols, ring, pinned, max_new are not
+ * used. */
 SWAB_API swab_status rotary_append(const swab_rotary_desc *desc, const swab_cache_desc *cache,
                                    const uint64_t *turns, const int32_t *pos, const int32_t *slots,
                                    const void *Q, const void *K, const void *V, void *Qo, void *Kc,
@@ -532,21 +534,28 @@ SWAB_API size_t band_decode_workspace(const swab_decode_desc *desc);
  * and lse that belong to no request are left as they were.
  * The shared prefix lies in the same cache: positions p of it in block
  * prefix_table[p / page] ([ceil(prefix_len / page)], DEVICE int32); it comes
- * before position 0 of every request and is read once for all of them.  It
- * stays visible whatever the window, like the global tokens of the banded
- * calls.
+ * before position 0 of every request.  For fp16 / bf16 with head_dim 64 or 128
+ * it is read from memory once for all of them; with other types and head sizes
+ * it is a part of every request's key list, read again for each request and
+ * every four heads.  It stays visible whatever the window, like the global
+ * tokens of the banded calls.
+ * Scores, sums, lse and the parts of a cut list are fp32.  With fp16 / bf16 and
+ * head_dim 64 or 128 the products run on the tensor cores: a weight, at most 2^8
+ * relative to the running reference, is rounded to dtype before it multiplies
+ * V (its sum is not); elsewhere weights are fp32.
  * With ring, the recycled columns must hold a step's window:
  * w * (dilation + 1) + max_q <= (cols - pinned - 1) * page + 1, and the pinned
  * ones the sinks: n_sink <= pinned * page (else SWAB_ERR_INVALID_ARG).
  * Every key and value that some query of the same request attends to has to
  * be finite; the others are never used, whatever they hold.
+ * cache.max_new is not used.
  * workspace: band_decode_workspace(desc) bytes of device memory, 16-byte
  * aligned (NULL if 0); its contents on entry do not matter, and calls that may
  * overlap on the GPU need one each.  The call launches up to three kernels.
  * They, like those of the rotary and cache calls, are programmatic dependents:
- * set up while the kernel before them runs, they wait inside for it; for the
- * caller a call stays ordered on the stream like any kernel launch.  Results do not depend on timing (no
- * atomics). */
+ * set up while the kernel before them runs, they wait inside for what it
+ * writes; for the caller a call stays ordered on the stream like any kernel
+ * launch.  Results do not depend on timing (no atomics). */
 SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, const void *Q,
                                  const void *Kc, const void *Vc, const int32_t *table,
                                  const int32_t *lens, const int32_t *q_start,

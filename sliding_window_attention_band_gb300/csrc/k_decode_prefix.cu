@@ -24,14 +24,15 @@
 // and for absent blocks: there the scores are set to never win, and the values
 // of those keys, which may be anything, are zeroed in shared memory.
 //
-// 128 requests x 32 heads over 8 key heads of 128, 16384 keys (34 GFLOP, 68 MB):
-// 36 us on 144 SMs, 0.95 PFLOP/s; 31 to the last product.  5 us go to the first tiles, 5 to the parts (19 MB in
-// whole sectors), 1.75 to a pair of chunks, of which the four products are 1.0:
-// tensor memory has no room for a second score buffer a stream, so a stream's
-// softmax, product and scores follow one another.  Steps on the way: the halves
-// of one tile's keys as streams 45 us; steps of 64 keys with two score buffers
-// 60 (N = 64 costs the tensor cores as much as N = 128); the issuing loop under
-// one lane 45.
+// 128 requests x 32 heads over 8 key heads of 128, 16384 keys (34 GFLOP, 68 MB)
+// with all SMs to it: 36 us on 144, 0.95 PFLOP/s; 31 to the last product.  5 us
+// go to the first tiles, 5 to the parts (19 MB in whole sectors), 1.75 to a pair
+// of chunks, of which the four products are 1.0.  (The plan gives it 96 there, 42
+// us, and the rest to the requests' own keys.)  Tensor memory has no room for a
+// second score buffer a stream, so a stream's softmax, product and scores follow
+// one another.  Steps on the way: the halves of one tile's keys as
+// streams 45 us; steps of 64 keys with two score buffers 60 (N = 64 costs the
+// tensor cores as much as N = 128); the issuing loop under one lane 45.
 //
 // A block of the cache is one TMA box of `page` lines; the tiles of 128 keys,
 // K and V in turn, run through a ring.  Warps: 0 = TMA (each lane fetches one

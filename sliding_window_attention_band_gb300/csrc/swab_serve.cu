@@ -162,7 +162,7 @@ swab_status check_cache(const swab_cache_desc *c) {
 // ---------------------------------------------------------------------------
 // decode
 // ---------------------------------------------------------------------------
-constexpr long long kSms = 152;      // of a GB300
+constexpr long long kSms = 152;      // of a GB300 (the plan sizes the workspace, and that needs no device)
 
 struct DecodePlan {
     bool rows;                       // tensor-core kernels (fp16 / bf16, head_dim 64 or 128)
@@ -219,10 +219,11 @@ long long most_keys(const swab_decode_desc *d) {
 // estimated (us; `blocks` of the rows kernel with `keys` keys each): a block of
 // the prefix 5.6 + 1.6 a chunk (0.8 of a single row tile; two thirds with
 // head_dim 64), a block of rows 3.3 + 1 every 45 KB, parts 1 MB a us, 1.25 in
-// a launch of their own that costs 1.3 more.  The numbers come from 208 shapes (2
-// to 200 requests, prefixes of 256 to 32768, head_dim 64 and 128) measured with
-// every choice: theirs are 3 % slower than the best on average, 5 % faster than
-// all SMs to the prefix and fold wherever it goes (256 requests with 2048
+// a launch of their own that costs 1.3 more.  The numbers were fitted to shapes
+// measured with every choice; on 162 of them (2 to 256 requests, prefixes of 256
+// to 32768, head_dim 64 and 128; profiles/prefix_plan.md) theirs are 3.8 %
+// slower than the best on average, all SMs to the prefix and fold wherever it
+// goes 9.0 % (256 requests with 2048
 // shared keys: 49 us with one piece of a tile, 54 with four, 61 with four and
 // fold; 64 with 8192: 33 with 7 pieces, 36 with 16 and fold, 41 without).
 void plan_prefix(const swab_decode_desc *d, long long blocks, long long keys, DecodePlan *p) {

@@ -80,7 +80,8 @@ class DecodeLoop:
         qkv [tokens, h + 2 hk, head_dim] request by request, at least as many as
         n_new adds up to (read from the device, unless the stream is being
         captured).  Returns the rotated queries [tokens, h, head_dim]; their
-        attention over the whole prompt is band_attention's."""
+        attention over the whole prompt is left to the caller (band_attention
+        where it takes the heads: hk = h and, in 16 bits, head_dim 64)."""
         T = qkv.shape[0]
         # (a refusal must come before the lengths move on)
         if T < 1 or qkv.shape[1:] != self.qkv.shape[1:] or qkv.dtype is not self.dtype or qkv.device != self.qkv.device:
