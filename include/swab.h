@@ -435,7 +435,7 @@ SWAB_API swab_status rotary_frequencies(int32_t rot_dim, double base, int32_t sc
  * p = pos[bb, i] + pos0 (pos NULL: p = i + pos0) and pair k = (a, b) of a head,
  *     y_a = scale * (x_a cos t - x_b sin t),  y_b = scale * (x_b cos t + x_a sin t),
  * channels from rot_dim on copied; fp32, rounded once (the angle is off by at most
- * 2^-25 pi).  Q -> Qo and, with
+ * 2^-26 pi).  Q -> Qo and, with
  * hk > 0, K -> Ko.  turns: DEVICE array of rot_dim / 2 (NULL when rot_dim is
  * 0); pos: DEVICE int32 [b, n].  An output may be its own input (same pointer
  * and strides), no other overlap. */

@@ -7,7 +7,8 @@
 // turn, so the product with the position, taken modulo 2^64, IS the fraction
 // of the turn: one integer multiply, exact at any distance, where an fp32
 // product is off by 0.06 rad at position 10^6.  Its upper 32 bits (2 pi 2^-32
-// rad) become the argument of sincospif (rounded to fp32: 2^-25 pi rad).
+// rad), the nearest quarter turn taken off, become the argument of sincospif
+// (rounded to fp32: 2^-27 pi rad at most, a small angle relatively).
 //
 // A block takes a few tokens at a time.  It lists their head rows (where from,
 // where to) and fills a table of their cosines and sines in shared memory -- one
@@ -176,10 +177,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_const
         for (int e = kThreads - 1 - threadIdx.x; e < nt * half; e += kThreads) {   // (the threads without a row first)
             const unsigned tt = half > 1 ? __umulhi(e, by_half) : e, k = e - tt * half, t = (unsigned)t0 + tt;
             const long long at = (p.pos ? (long long)*GP(p.bnd, p.pos + t) : (long long)(t % p.n)) + p.pos0;
-            // the upper 32 bits of the fraction of a turn: half turns in [-1, 1)
-            const int frac = (int)(((unsigned long long)at * *GP(p.bnd, p.turns + k)) >> 32);
+            // the upper 32 bits of the fraction of a turn, less the nearest quarter:
+            // at most an eighth of a turn is rounded to a float, not the whole angle
+            const unsigned frac = (unsigned)(((unsigned long long)at * *GP(p.bnd, p.turns + k)) >> 32);
+            const unsigned quarter = (frac + 0x20000000u) >> 30;
             float sn, cs;
-            sincospif((float)frac * 0x1p-31f, &sn, &cs);
+            sincospif((float)(int)(frac - (quarter << 30)) * 0x1p-31f, &sn, &cs);
+            if (quarter & 1u) {
+                const float x = cs;
+                cs = -sn;
+                sn = x;
+            }
+            if (quarter & 2u) {
+                cs = -cs;
+                sn = -sn;
+            }
             tab[(2 * tt) * half + k] = cs * p.scale;
             tab[(2 * tt + 1) * half + k] = sn * (p.backward ? -p.scale : p.scale);
         }

@@ -142,6 +142,31 @@ def test_rotary_positions_at_the_ends_of_their_range(dtype):
 
 
 @pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rotary_angles_next_to_quarter_turns(inter, sign):
+    """x = (1, 0) gives (cos t, sin t) themselves.  The turns are cut to 2^-32 (2 pi 2^-32 rad); what is left of the
+    quarter turn is then rounded relatively (2^-24) and its sine and cosine are within 2 ulp (2^-22), so a small value
+    keeps its bits: nothing of the size of the whole angle's rounding (2^-25 pi) may show."""
+    N = 256
+    rng = np.random.default_rng(40)
+    quarter, off = rng.integers(0, 4, N), (2.0 ** rng.uniform(33, 61, N)).astype(np.int64) * rng.choice([-1, 1], N)
+    turns = ((quarter.astype(object) << 62) + off.astype(object)) % (1 << 64)
+    t64 = torch.tensor([int(t) - (1 << 64) if t >= 1 << 63 else int(t) for t in turns], dtype=torch.int64).cuda()
+    x = torch.zeros(1, 1, 1, 2 * N, dtype=F32, device="cuda")
+    (x[..., 0::2] if inter else x[..., :N]).fill_(1.0)
+    y = torch.empty_like(x)
+    swab.rotary(swab.RotaryDesc(1, 1, 1, 0, 2 * N, 2 * N, inter, dtype=F32), t64, x, y, pos=i32([[sign]]))
+    a = off.astype(np.float64) * 2 * np.pi * 2.0 ** -64          # the part past the quarter turns
+    c, s = np.cos(a), np.sin(a)
+    cos = np.choose(quarter, [c, -s, -c, s])
+    sin = np.choose(quarter, [s, c, -s, -c]) * sign
+    got = f64(y).reshape(-1)
+    got_c, got_s = (got[0::2], got[1::2]) if inter else (got[:N], got[N:])
+    for g, w in ((got_c, cos), (got_s, sin)):
+        assert (np.abs(g - w) <= 2 * np.pi * 2.0 ** -32 + np.abs(w) * (2.0 ** -24 + 2.0 ** -22)).all(), np.abs(g - w).max()
+
+
+@pytest.mark.parametrize("inter", [False, True])
 def test_rotary_on_strided_views_and_in_place(inter):
     """Q, K inside a merged projection, outputs head-major; then in place, which gives the same bits."""
     b, n, h, hk, hd, rot = 2, 37, 4, 2, 64, 32
