@@ -498,6 +498,93 @@ SWAB_API swab_status rotary_append(const swab_rotary_desc *desc, const swab_cach
                                    const void *Q, const void *K, const void *V, void *Qo, void *Kc,
                                    void *Vc, void *stream);
 
+/* RMS norm of a head, before its rotary positions. */
+typedef struct swab_norm_desc {
+    float eps;             /* > 0 */
+    float offset;          /* added to every weight (1 where a model stores w - 1) */
+    int64_t q_stride[3], k_stride[3]; /* norm_rotary_bwd: element strides of Q and K, as those of swab_rotary_desc */
+} swab_norm_desc;
+
+/* Norms of queries and keys, a head at a time, and rotary positions in the same
+ * pass: a row x of head_dim channels becomes the rotation (as `rotary`, by the
+ * same desc, turns and pos) of
+ *     x_c r (w_c + offset),   r = 1 / sqrt(mean_c x_c^2 + eps),
+ * fp32, rounded once.  Q -> Qo with the weights wq and, with hk > 0, K -> Ko with
+ * wk ([head_dim] of the tensors' dtype, 16-byte aligned; NULL: every weight and
+ * the offset together count as 1).  An output may be its own input (same pointer
+ * and strides), no other overlap.  The squares are summed in fp32: a row whose sum
+ * passes its range gives 0, one with a NaN gives NaN. */
+SWAB_API swab_status norm_rotary(const swab_rotary_desc *desc, const swab_norm_desc *norm, const uint64_t *turns,
+                                 const int32_t *pos, const void *Q, const void *K, const void *wq,
+                                 const void *wk, void *Qo, void *Ko, void *stream);
+
+/* Bytes of workspace norm_rotary_bwd needs (0 if desc is bad). */
+SWAB_API size_t norm_rotary_bwd_workspace(const swab_rotary_desc *desc);
+
+/* Gradient of norm_rotary.  With g the gradient dQo turned back (rotary_bwd),
+ *     dQ_c = r (g_c v_c - x_c r^2 mean_k(g_k v_k x_k)),   v = w + offset,
+ *     dwq_c = sum over all rows of g_c x_c r,
+ * the same for K.  Strides: q_stride, k_stride of desc are those of dQo, dKo,
+ * qo_stride, ko_stride those of dQ, dK, and norm's those of Q, K.  dwq, dwk
+ * [head_dim] fp32, 16-byte aligned; NULL leaves them out (they need wq, wk).  dQ
+ * may be dQo or Q (same pointer and strides), dK likewise, no other overlap.  fp32,
+ * the sums over rows in a fixed order (results repeat bitwise on one GPU).
+ * workspace: norm_rotary_bwd_workspace(desc) bytes, 16-byte aligned, needed where
+ * dwq or dwk is given; its contents on entry do not matter, calls that may overlap on
+ * the GPU need one each. */
+SWAB_API swab_status norm_rotary_bwd(const swab_rotary_desc *desc, const swab_norm_desc *norm,
+                                     const uint64_t *turns, const int32_t *pos, const void *dQo,
+                                     const void *dKo, const void *Q, const void *K, const void *wq,
+                                     const void *wk, void *dQ, void *dK, float *dwq, float *dwk,
+                                     void *workspace, void *stream);
+
+/* norm_rotary fused with the cache write: rotary_append with Q and K normed
+ * first (V as it is). */
+SWAB_API swab_status norm_rotary_append(const swab_rotary_desc *desc, const swab_norm_desc *norm,
+                                        const swab_cache_desc *cache, const uint64_t *turns,
+                                        const int32_t *pos, const int32_t *slots, const void *Q,
+                                        const void *K, const void *V, const void *wq, const void *wk,
+                                        void *Qo, void *Kc, void *Vc, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The cache in 4 bits.  K and V are two tensors of codes each with one of scales:
+ *     codes  [n_blocks, hk, page, head_dim / 2] bytes, channel 2c in the low half
+ *            of byte c, channel 2c + 1 in the high half,
+ *     scales [n_blocks, hk, page, head_dim / 32] of the tensors' dtype;
+ * blocks, slots and the block table as above, head_dim a multiple of 32, at most
+ * 256.  Code c (0..15) of a channel stands for s (c - 8), s the scale of its 32
+ * adjacent channels.  A group x is written as
+ *     the values rounded to dtype (as the cache of that type would hold them),
+ *     m = the value of largest magnitude (of two, the positive one),
+ *     s = m / -8 rounded to 5 significant bits, but to a multiple of at least 2^-24
+ *         (fp16) or 2^-120 (bf16, fp32), and at most 1.25 * 2^11 or 1.25 * 2^123,
+ *     c = min(max(rint(x / s), -8), 7) + 8   (ties to even; 8 where s is 0),
+ * so that s (c - 8) has at most 8 significant bits: fp16 and bf16 hold it as
+ * it is.  m's own code is 0, its value within 1/32 of m; the others are off by at
+ * most |s| / 2, or 1.25 |s| next to -m.  A group with a NaN or infinity has a NaN scale,
+ * codes 8: all its values are NaN.  4.5 bits a value in 16-bit types.
+ * ------------------------------------------------------------------------- */
+
+/* rotary_append into a cache in 4 bits (codes Kc, Vc; scales Ks, Vs): Q -> Qo
+ * rotated; K rotated and V as it is, quantised, into row slots[t].  With norm Q
+ * and K are normed first (norm_rotary); NULL: not (wq, wk are not used).  pos and
+ * turns may be NULL with rot_dim 0; Q and Qo both NULL leave Q out.  Codes
+ * 16-byte aligned, scales 16-byte aligned. */
+SWAB_API swab_status rotary_append4(const swab_rotary_desc *desc, const swab_norm_desc *norm,
+                                    const swab_cache_desc *cache, const uint64_t *turns,
+                                    const int32_t *pos, const int32_t *slots, const void *Q,
+                                    const void *K, const void *V, const void *wq, const void *wk,
+                                    void *Qo, void *Kc, void *Ks, void *Vc, void *Vs, void *stream);
+
+/* The values of rows slots[0..tokens) of a cache in 4 bits: K, V [tokens, hk,
+ * head_dim] contiguous, of dtype (the scales' too).  Rows with slot -1 stay as they
+ * are; other slots outside the cache likewise, recorded as SWAB_ERR_INVALID_ARG in the
+ * status word.  tokens >= 1.  cache->batch, cols, ring, pinned, max_new are not used. */
+SWAB_API swab_status cache_read4(const swab_cache_desc *cache, int32_t tokens, int32_t hk,
+                                 int32_t head_dim, int32_t dtype, const int32_t *slots,
+                                 const void *Kc, const void *Ks, const void *Vc, const void *Vs,
+                                 void *K, void *V, void *stream);
+
 typedef struct swab_decode_desc {
     swab_cache_desc cache;
     int32_t tokens;       /* rows of Q, O, lse, >= 1 */
@@ -561,6 +648,21 @@ SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, cons
                                  const int32_t *lens, const int32_t *q_start,
                                  const int32_t *prefix_table, void *O, float *lse, void *workspace,
                                  void *stream);
+
+/* Bytes of workspace band_decode4 needs (0 if it needs none, or desc is bad). */
+SWAB_API size_t band_decode4_workspace(const swab_decode_desc *desc);
+
+/* band_decode over a cache in 4 bits: the same key set, results, rows left alone,
+ * handling of absent blocks, limits, workspace rules and launches, with K and V the
+ * values of the codes Kc, Vc under the scales Ks, Vs.  head_dim a multiple of 32, at
+ * most 256; no shared prefix (prefix_len must be 0), else SWAB_ERR_UNSUPPORTED.  The
+ * values are exact in fp16 and bf16, so with head_dim 64 or 128 the products run on
+ * the tensor cores as those of band_decode do (a weight, at most 2^8 relative to the
+ * running reference, is rounded to dtype before it multiplies V); elsewhere in fp32. */
+SWAB_API swab_status band_decode4(const swab_decode_desc *desc, float scale, const void *Q,
+                                  const void *Kc, const void *Ks, const void *Vc, const void *Vs,
+                                  const int32_t *table, const int32_t *lens, const int32_t *q_start,
+                                  void *O, float *lse, void *workspace, void *stream);
 
 /* Human-readable name of a status code (static string). */
 SWAB_API const char *swab_status_string(swab_status status);

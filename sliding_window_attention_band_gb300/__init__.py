@@ -18,6 +18,10 @@ from ._binding import (API_FUNCTIONS, Desc, SwabError, add_bias_transpose,  # no
 from .serve import (CacheDesc, DecodeDesc, RotaryDesc, band_decode,  # noqa: F401
                     band_decode_workspace, cache_slots, rotary, rotary_append, rotary_bwd,
                     rotary_frequencies)
+from .norm import (NormDesc, norm_rotary, norm_rotary_append, norm_rotary_bwd,  # noqa: F401
+                   norm_rotary_bwd_workspace)
+from .cache4 import (band_decode4, band_decode4_workspace, cache4_shapes, cache_read4,  # noqa: F401
+                     rotary_append4)
 from .decode_loop import DecodeLoop  # noqa: F401
 from .inputs import WORKLOADS, Workload, seeded_qkvo, workload_inputs  # noqa: F401
 
@@ -30,5 +34,7 @@ __all__ = ["Desc", "SwabError", "add_bias_transpose", "band_qk", "band_softmax",
            "selftest_bounds", "load",
            "CacheDesc", "DecodeDesc", "DecodeLoop", "RotaryDesc", "rotary_frequencies", "rotary", "rotary_bwd",
            "cache_slots", "rotary_append", "band_decode", "band_decode_workspace",
+           "NormDesc", "norm_rotary", "norm_rotary_bwd", "norm_rotary_bwd_workspace", "norm_rotary_append",
+           "rotary_append4", "cache_read4", "cache4_shapes", "band_decode4", "band_decode4_workspace",
            "library_path", "version", "status_string", "WORKLOADS", "Workload",
            "seeded_qkvo", "workload_inputs"]

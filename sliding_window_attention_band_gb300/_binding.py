@@ -32,6 +32,8 @@ API_FUNCTIONS = ("add_bias_transpose", "global_attention", "global_attention_bwd
                  "band_attention_dropout_mask_bytes",
                  "rotary_frequencies", "rotary", "rotary_bwd", "cache_slots", "rotary_append",
                  "band_decode", "band_decode_workspace",
+                 "norm_rotary", "norm_rotary_bwd", "norm_rotary_bwd_workspace", "norm_rotary_append",
+                 "rotary_append4", "cache_read4", "band_decode4", "band_decode4_workspace",
                  "swab_status_string", "swab_device_status",
                  "swab_selftest_wait_timeout", "swab_bounds_checked", "swab_bounds_report",
                  "swab_selftest_bounds", "swab_version")
@@ -161,9 +163,10 @@ def load():
                 "swab_bounds_report": [ctypes.POINTER(ctypes.c_uint64), i32],
                 "swab_selftest_bounds": [P],
             }
-            from . import serve
+            from . import cache4, norm, serve
 
-            sigs.update(serve.signatures())
+            for part in (serve, norm, cache4):
+                sigs.update(part.signatures())
             for name, args in sigs.items():
                 fn = getattr(lib, name)
                 fn.argtypes = args
@@ -174,8 +177,11 @@ def load():
             lib.band_attention_bwd_workspace.restype = ctypes.c_size_t
             lib.band_attention_dropout_mask_bytes.argtypes = [D]
             lib.band_attention_dropout_mask_bytes.restype = ctypes.c_size_t
-            lib.band_decode_workspace.argtypes = [ctypes.POINTER(serve._DecodeDesc)]
-            lib.band_decode_workspace.restype = ctypes.c_size_t
+            for name in ("band_decode_workspace", "band_decode4_workspace"):
+                getattr(lib, name).argtypes = [ctypes.POINTER(serve._DecodeDesc)]
+                getattr(lib, name).restype = ctypes.c_size_t
+            lib.norm_rotary_bwd_workspace.argtypes = [ctypes.POINTER(serve._RotaryDesc)]
+            lib.norm_rotary_bwd_workspace.restype = ctypes.c_size_t
             lib.swab_status_string.restype = ctypes.c_char_p
             lib.swab_status_string.argtypes = [ctypes.c_int]
             lib.swab_version.restype = ctypes.c_char_p

@@ -37,8 +37,8 @@ VARIANTS = {  # variant: (library, object folder, extra nvcc flags)
 SOURCES = ["swab_api.cu", "k_band_qk.cu", "k_band_gather.cu", "k_softmax.cu", "k_attention.cu", "k_attention_bwd.cu",
            "k_global.cu", "k_bias_transpose.cu", "k_global_proj.cu",
            "k_global_tc.cu", "swab_serve.cu", "k_rotary.cu", "k_cache.cu", "k_decode.cu",
-           "k_decode_rows.cu", "k_decode_prefix.cu"]
-HEADERS = ["swab_common.cuh", "swab_internal.h", "swab_decode.cuh"]
+           "k_decode_rows.cu", "k_decode_prefix.cu", "k_norm.cu", "k_decode4.cu"]
+HEADERS = ["swab_common.cuh", "swab_internal.h", "swab_decode.cuh", "swab_rows.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
           "--expt-relaxed-constexpr"]

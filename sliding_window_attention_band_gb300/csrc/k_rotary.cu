@@ -26,7 +26,7 @@
 // instructions: 16 bytes a thread carry the same addresses as 32.
 #include <algorithm>
 
-#include "swab_internal.h"
+#include "swab_rows.cuh"
 
 static constexpr unsigned kSwabFile = 11;   // site id of the bounds checks
 
@@ -48,53 +48,6 @@ struct Row {
     __device__ __forceinline__ int token() const { return (int)(s & 15u); }
     __device__ __forceinline__ bool turn() const { return d & 1u; }
 };
-
-template <typename T> struct VecOf {
-    static constexpr int kN = 16 / sizeof(T);   // elements of 16 bytes
-};
-
-template <typename T>
-__device__ __forceinline__ void unpack16(const uint4 &v, float *f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if constexpr (sizeof(T) == 4) {
-            f[k] = __uint_as_float(w[k]);
-        } else {
-            f[2 * k] = lo16<T>(w[k]);
-            f[2 * k + 1] = hi16<T>(w[k]);
-        }
-    }
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack16(const float *f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if constexpr (sizeof(T) == 4) w[k] = __float_as_uint(f[k]);
-        else w[k] = pack2<T>(f[2 * k], f[2 * k + 1]);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint4 load16(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
-
-// N floats of the table, 16 or 8 bytes at a time
-template <int N>
-__device__ __forceinline__ void take(const float *src, float (&f)[N]) {
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int k = 0; k < N; k += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(src + k);
-            f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; k += 2) {
-            const float2 v = *reinterpret_cast<const float2 *>(src + k);
-            f[k] = v.x, f[k + 1] = v.y;
-        }
-    }
-}
 
 // Row `idx` of token t: heads of Q, then of K, then (append) of V.  Strides
 // are in units of 16 bytes, their sums below 2^32 (checked by the caller).
@@ -177,21 +130,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_rotary(const __grid_const
         for (int e = kThreads - 1 - threadIdx.x; e < nt * half; e += kThreads) {   // (the threads without a row first)
             const unsigned tt = half > 1 ? __umulhi(e, by_half) : e, k = e - tt * half, t = (unsigned)t0 + tt;
             const long long at = (p.pos ? (long long)*GP(p.bnd, p.pos + t) : (long long)(t % p.n)) + p.pos0;
-            // the upper 32 bits of the fraction of a turn, less the nearest quarter:
-            // at most an eighth of a turn is rounded to a float, not the whole angle
-            const unsigned frac = (unsigned)(((unsigned long long)at * *GP(p.bnd, p.turns + k)) >> 32);
-            const unsigned quarter = (frac + 0x20000000u) >> 30;
             float sn, cs;
-            sincospif((float)(int)(frac - (quarter << 30)) * 0x1p-31f, &sn, &cs);
-            if (quarter & 1u) {
-                const float x = cs;
-                cs = -sn;
-                sn = x;
-            }
-            if (quarter & 2u) {
-                cs = -cs;
-                sn = -sn;
-            }
+            cos_sin(at, *GP(p.bnd, p.turns + k), cs, sn);
             tab[(2 * tt) * half + k] = cs * p.scale;
             tab[(2 * tt + 1) * half + k] = sn * (p.backward ? -p.scale : p.scale);
         }

@@ -25,6 +25,13 @@ decltype(&rotary_bwd) fn_rotary_bwd;
 decltype(&cache_slots) fn_cache_slots;
 decltype(&rotary_append) fn_rotary_append;
 decltype(&band_decode) fn_band_decode;
+decltype(&norm_rotary) fn_norm_rotary;
+decltype(&norm_rotary_bwd) fn_norm_rotary_bwd;
+decltype(&norm_rotary_bwd_workspace) fn_norm_rotary_bwd_workspace;
+decltype(&norm_rotary_append) fn_norm_rotary_append;
+decltype(&rotary_append4) fn_rotary_append4;
+decltype(&cache_read4) fn_cache_read4;
+decltype(&band_decode4) fn_band_decode4;
 
 // thrown (and caught at the entry) when a call has to be looked at again
 struct Again {};
@@ -52,10 +59,17 @@ struct Call {
     }
     int32_t *ints(PyObject *o, int64_t n, bool at_least = false) { return contiguous<int32_t>(o, at::kInt, n, at_least); }
     // a cache tensor [n_blocks, hk, page, hd]
-    void *cache(PyObject *o, const swab_cache_desc &c, int hk, int hd, int32_t dtype) {
+    void *cache(PyObject *o, const swab_cache_desc &c, int hk, int hd, int32_t dtype) { return cells(o, c, hk, hd, type_of(dtype)); }
+    // and of a cache in 4 bits
+    void *codes(PyObject *o, const swab_cache_desc &c, int hk, int hd) {
+        if (hd % 32) throw Again();
+        return cells(o, c, hk, hd / 2, at::kByte);
+    }
+    void *scales(PyObject *o, const swab_cache_desc &c, int hk, int hd, int32_t dtype) { return cells(o, c, hk, hd / 32, type_of(dtype)); }
+    void *cells(PyObject *o, const swab_cache_desc &c, int hk, int hd, at::ScalarType type) {
         const at::TensorBase &t = tensor(o);
         const auto s = t.sizes();
-        if (t.scalar_type() != type_of(dtype) || s.size() != 4 || s[0] != c.n_blocks || s[1] != hk || s[2] != c.page || s[3] != hd ||
+        if (t.scalar_type() != type || s.size() != 4 || s[0] != c.n_blocks || s[1] != hk || s[2] != c.page || s[3] != hd ||
             !t.is_contiguous())
             throw Again();
         return t.data_ptr();
@@ -97,6 +111,13 @@ struct Call {
             if ((st[0] != row_stride && s[0] > 1) || (st[1] != d.head_dim && s[1] > 1) || (st[2] != 1 && s[2] > 1)) throw Again();
         }
         return t.data_ptr();
+    }
+    // a weight [hd] or its gradient, None: null
+    template <typename P> P *vector(PyObject *o, at::ScalarType type, int64_t n) {
+        if (o == Py_None) return nullptr;
+        P *p = contiguous<P>(o, type, n);
+        if (THPVariable_Unpack(o).dim() != 1) throw Again();
+        return p;
     }
     uint64_t *turns(PyObject *o, const swab_rotary_desc &d) {
         return d.rot_dim == 0 ? nullptr : contiguous<uint64_t>(o, at::kLong, d.rot_dim / 2);
@@ -199,6 +220,139 @@ PyObject *py_rotary_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// (desc, norm, turns, pos, Q, K, wq, wk, Qo, Ko)
+PyObject *py_norm_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry(n, 10, [&] {
+        swab_rotary_desc d = desc<swab_rotary_desc>(a[0]);
+        const swab_norm_desc &norm = desc<swab_norm_desc>(a[1]);
+        Call c;
+        void *q = c.rows(a[4], d, d.h, d.q_stride), *qo = c.rows(a[8], d, d.h, d.qo_stride), *k = nullptr, *ko = nullptr;
+        if (d.hk > 0) {
+            k = c.rows(a[5], d, d.hk, d.k_stride);
+            ko = c.rows(a[9], d, d.hk, d.ko_stride);
+        }
+        const uint64_t *turns = c.turns(a[2], d);
+        const int32_t *pos = a[3] == Py_None ? nullptr : c.ints(a[3], (int64_t)d.b * d.n);
+        const void *wq = c.vector<void>(a[6], type_of(d.dtype), d.head_dim), *wk = c.vector<void>(a[7], type_of(d.dtype), d.head_dim);
+        void *st = c.stream();
+        return without_gil([&] { return fn_norm_rotary(&d, &norm, turns, pos, q, k, wq, wk, qo, ko, st); });
+    });
+}
+
+// (desc, norm, turns, pos, dQo, dKo, Q, K, wq, wk, dQ, dK, dwq, dwk, workspace)
+PyObject *py_norm_rotary_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry(n, 15, [&] {
+        swab_rotary_desc d = desc<swab_rotary_desc>(a[0]);
+        swab_norm_desc norm = desc<swab_norm_desc>(a[1]);
+        Call c;
+        void *go = c.rows(a[4], d, d.h, d.q_stride), *q = c.rows(a[6], d, d.h, norm.q_stride), *dq = c.rows(a[10], d, d.h, d.qo_stride);
+        void *gk = nullptr, *k = nullptr, *dk = nullptr;
+        if (d.hk > 0) {
+            gk = c.rows(a[5], d, d.hk, d.k_stride);
+            k = c.rows(a[7], d, d.hk, norm.k_stride);
+            dk = c.rows(a[11], d, d.hk, d.ko_stride);
+        }
+        const uint64_t *turns = c.turns(a[2], d);
+        const int32_t *pos = a[3] == Py_None ? nullptr : c.ints(a[3], (int64_t)d.b * d.n);
+        const void *wq = c.vector<void>(a[8], type_of(d.dtype), d.head_dim), *wk = c.vector<void>(a[9], type_of(d.dtype), d.head_dim);
+        float *dwq = c.vector<float>(a[12], at::kFloat, d.head_dim), *dwk = c.vector<float>(a[13], at::kFloat, d.head_dim);
+        void *ws = nullptr;
+        if (a[14] != Py_None) {
+            const at::TensorBase &t = c.tensor(a[14]);
+            if (t.nbytes() < fn_norm_rotary_bwd_workspace(&d) || !t.is_contiguous()) throw Again();
+            ws = t.data_ptr();
+        } else if (dwq || dwk) {
+            throw Again();
+        }
+        void *st = c.stream();
+        return without_gil([&] { return fn_norm_rotary_bwd(&d, &norm, turns, pos, go, gk, q, k, wq, wk, dq, dk, dwq, dwk, ws, st); });
+    });
+}
+
+// (desc, norm, cache, turns, pos, slots, Q, K, V, wq, wk, Qo, Kc, Vc); in 4 bits norm may be 0 and the last are Kc, Ks, Vc, Vs
+template <bool kBits4> PyObject *py_norm_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry(n, kBits4 ? 16 : 14, [&] {
+        swab_rotary_desc d = desc<swab_rotary_desc>(a[0]);
+        const swab_norm_desc *norm = nullptr;
+        if (!kBits4 || !PyLong_Check(a[1]) || PyLong_AsVoidPtr(a[1])) norm = &desc<swab_norm_desc>(a[1]);
+        const swab_cache_desc &cache = desc<swab_cache_desc>(a[2]);
+        if ((a[6] == Py_None) != (a[11] == Py_None) || (!norm && (a[9] != Py_None || a[10] != Py_None))) throw Again();
+        Call c;
+        void *k = c.rows(a[7], d, d.hk, d.k_stride), *v = c.rows(a[8], d, d.hk, d.v_stride), *q = nullptr, *qo = nullptr;
+        if (a[6] != Py_None) {
+            q = c.rows(a[6], d, d.h, d.q_stride);
+            qo = c.rows(a[11], d, d.h, d.qo_stride);
+        }
+        const uint64_t *turns = c.turns(a[3], d);
+        const int64_t tokens = (int64_t)d.b * d.n;
+        const int32_t *pos = a[4] == Py_None ? nullptr : c.ints(a[4], tokens), *slots = c.ints(a[5], tokens);
+        const void *wq = c.vector<void>(a[9], type_of(d.dtype), d.head_dim), *wk = c.vector<void>(a[10], type_of(d.dtype), d.head_dim);
+        if constexpr (kBits4) {
+            void *kc = c.codes(a[12], cache, d.hk, d.head_dim), *ks = c.scales(a[13], cache, d.hk, d.head_dim, d.dtype);
+            void *vc = c.codes(a[14], cache, d.hk, d.head_dim), *vs = c.scales(a[15], cache, d.hk, d.head_dim, d.dtype);
+            void *st = c.stream();
+            return without_gil([&] { return fn_rotary_append4(&d, norm, &cache, turns, pos, slots, q, k, v, wq, wk, qo, kc, ks, vc, vs, st); });
+        } else {
+            void *kc = c.cache(a[12], cache, d.hk, d.head_dim, d.dtype), *vc = c.cache(a[13], cache, d.hk, d.head_dim, d.dtype);
+            void *st = c.stream();
+            return without_gil([&] { return fn_norm_rotary_append(&d, norm, &cache, turns, pos, slots, q, k, v, wq, wk, qo, kc, vc, st); });
+        }
+    });
+}
+
+// (cache, slots, Kc, Ks, Vc, Vs, K, V)
+PyObject *py_cache_read4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry(n, 8, [&] {
+        const swab_cache_desc &cache = desc<swab_cache_desc>(a[0]);
+        Call c;
+        const at::TensorBase &t = c.tensor(a[6]);
+        const auto s = t.sizes();
+        if (s.size() != 3 || s[0] > 0x7fffffff || s[1] > 0x7fffffff || s[2] > 0x7fffffff) throw Again();
+        const at::ScalarType type = t.scalar_type();
+        const int32_t dtype = type == at::kFloat ? SWAB_F32 : type == at::kHalf ? SWAB_F16 : type == at::kBFloat16 ? SWAB_BF16 : -1;
+        if (dtype < 0 || c.tensor(a[7]).sizes() != s) throw Again();
+        const int32_t tokens = (int32_t)s[0], hk = (int32_t)s[1], hd = (int32_t)s[2];
+        const int32_t *slots = c.ints(a[1], tokens);
+        void *kc = c.codes(a[2], cache, hk, hd), *ks = c.scales(a[3], cache, hk, hd, dtype), *vc = c.codes(a[4], cache, hk, hd),
+             *vs = c.scales(a[5], cache, hk, hd, dtype);
+        void *k = c.contiguous<void>(a[6], type, t.numel()), *v = c.contiguous<void>(a[7], type, t.numel());
+        void *st = c.stream();
+        return without_gil([&] { return fn_cache_read4(&cache, tokens, hk, hd, dtype, slots, kc, ks, vc, vs, k, v, st); });
+    });
+}
+
+// (desc, need, scale, Q, Kc, Ks, Vc, Vs, table, lens, q_start, O, lse, workspace); need: bytes of workspace
+PyObject *py_band_decode4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry(n, 14, [&] {
+        const swab_decode_desc &d = desc<swab_decode_desc>(a[0]);
+        const long long need = PyLong_AsLongLong(a[1]);
+        if (!PyFloat_Check(a[2]) && !PyLong_Check(a[2])) throw Again();
+        const double scale = PyFloat_AsDouble(a[2]);
+        if (PyErr_Occurred()) throw Again();
+        const swab_cache_desc &cd = d.cache;
+        Call c;
+        void *q = c.heads(a[3], d, d.q_row_stride), *o = c.heads(a[11], d, d.out_row_stride);
+        void *kc = c.codes(a[4], cd, d.hk, d.head_dim), *ks = c.scales(a[5], cd, d.hk, d.head_dim, d.dtype);
+        void *vc = c.codes(a[6], cd, d.hk, d.head_dim), *vs = c.scales(a[7], cd, d.hk, d.head_dim, d.dtype);
+        const int32_t *table = c.ints(a[8], (int64_t)cd.batch * cd.cols), *lens = c.ints(a[9], cd.batch),
+                      *q_start = c.ints(a[10], (int64_t)cd.batch + 1);
+        float *lse = nullptr;
+        if (a[12] != Py_None) {
+            lse = c.contiguous<float>(a[12], at::kFloat, (int64_t)d.tokens * d.h);
+            const auto s = c.tensor(a[12]).sizes();
+            if (s.size() != 2 || s[0] != d.tokens) throw Again();
+        }
+        void *ws = nullptr;
+        if (need > 0) {
+            const at::TensorBase &t = c.tensor(a[13]);
+            if ((long long)t.nbytes() < need || !t.is_contiguous()) throw Again();
+            ws = t.data_ptr();
+        }
+        void *st = c.stream();
+        return without_gil([&] { return fn_band_decode4(&d, (float)scale, q, kc, ks, vc, vs, table, lens, q_start, o, lse, ws, st); });
+    });
+}
+
 // (desc, need, scale, Q, Kc, Vc, table, lens, q_start, prefix_table, O, lse, workspace); need: bytes of workspace
 PyObject *py_band_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return entry(n, 13, [&] {
@@ -251,6 +405,28 @@ PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// bind_more(norm_rotary, norm_rotary_bwd, norm_rotary_bwd_workspace, norm_rotary_append, rotary_append4, cache_read4, band_decode4)
+PyObject *py_bind_more(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 7) {
+        PyErr_SetString(PyExc_TypeError, "bind_more: seven addresses expected");
+        return nullptr;
+    }
+    void *p[7];
+    for (int k = 0; k < 7; ++k)
+        if (!(p[k] = PyLong_AsVoidPtr(a[k]))) {
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_more: an address is null");
+            return nullptr;
+        }
+    fn_norm_rotary = reinterpret_cast<decltype(fn_norm_rotary)>(p[0]);
+    fn_norm_rotary_bwd = reinterpret_cast<decltype(fn_norm_rotary_bwd)>(p[1]);
+    fn_norm_rotary_bwd_workspace = reinterpret_cast<decltype(fn_norm_rotary_bwd_workspace)>(p[2]);
+    fn_norm_rotary_append = reinterpret_cast<decltype(fn_norm_rotary_append)>(p[3]);
+    fn_rotary_append4 = reinterpret_cast<decltype(fn_rotary_append4)>(p[4]);
+    fn_cache_read4 = reinterpret_cast<decltype(fn_cache_read4)>(p[5]);
+    fn_band_decode4 = reinterpret_cast<decltype(fn_band_decode4)>(p[6]);
+    Py_RETURN_NONE;
+}
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr
 PyMethodDef methods[] = {{"bind", FAST(py_bind)},
                          {"rotary", FAST(py_rotary<false>)},
@@ -258,6 +434,13 @@ PyMethodDef methods[] = {{"bind", FAST(py_bind)},
                          {"cache_slots", FAST(py_cache_slots)},
                          {"rotary_append", FAST(py_rotary_append)},
                          {"band_decode", FAST(py_band_decode)},
+                         {"bind_more", FAST(py_bind_more)},
+                         {"norm_rotary", FAST(py_norm_rotary)},
+                         {"norm_rotary_bwd", FAST(py_norm_rotary_bwd)},
+                         {"norm_rotary_append", FAST(py_norm_append<false>)},
+                         {"rotary_append4", FAST(py_norm_append<true>)},
+                         {"cache_read4", FAST(py_cache_read4)},
+                         {"band_decode4", FAST(py_band_decode4)},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -360,6 +360,42 @@ struct RotaryArgs {
 };
 cudaError_t launch_rotary(DType dt, bool append, RotaryArgs a, cudaStream_t st);
 
+// Rows of a cache in 4 bits: 32 channels share a scale.
+constexpr int kGroup4 = 32;
+struct NormArgs {
+    RotaryArgs r;              // rows, turns, positions, cache (Kc, Vc: the codes with `bits4`)
+    const void *wq, *wk;       // weights [hd], or null (1)
+    float eps, offset;
+    int norm;                  // 0: rotary alone
+    void *Ks, *Vs;             // scales of a cache in 4 bits
+    int lanes;                 // of a row (set by the launcher, like the rest)
+    int by_pairs;              // pairs off 16-byte pieces
+    int sum_lanes, sum_turn;   // a warp a row: the lanes that would own pieces, those that turn (0: none could)
+    // backward: r.Q, r.K are dQo, dKo (strides r.sq, r.sk), r.Qo, r.Ko are dQ, dK
+    const void *X[2];          // Q, K
+    unsigned sx[2][3];         // their strides
+    float *dw[2];              // dwq, dwk, or null
+    float *part;               // partial sums: [blocks][hd]
+    int blocks_q, blocks;      // of the grid: of Q, of both
+    int tiles[2], tile[2], slices[2];
+};
+// kind: 0 = Q, K -> Qo, Ko; 1 = into the cache; 2 = into the cache in 4 bits
+cudaError_t launch_norm(DType dt, int kind, NormArgs a, cudaStream_t st);
+constexpr int kNormBlocks = 608;     // most blocks of the backward, rows of its partial sums
+cudaError_t launch_norm_bwd(DType dt, NormArgs a, cudaStream_t st);
+
+struct Read4Args {
+    const int *slots;
+    const void *Kc, *Ks, *Vc, *Vs;
+    void *K, *V;
+    int tokens, hk, hd, page_log2, n_slots;
+    unsigned *err;
+#if SWAB_BOUNDS_CHECK
+    Bounds bnd;
+#endif
+};
+cudaError_t launch_read4(DType dt, const Read4Args &a, cudaStream_t st);
+
 struct CacheSlotsArgs {
     const int *lens, *n_new, *free_list, *used;
     int *table, *lens_out, *used_out, *q_start, *slots, *pos;
@@ -374,6 +410,7 @@ cudaError_t launch_cache_slots(CacheSlotsArgs a, cudaStream_t st);
 
 struct DecodeArgs {
     const void *Q, *Kc, *Vc;
+    const void *Ks, *Vs;       // scales of a cache in 4 bits (Kc, Vc: its codes)
     void *O;
     float *lse;                // or null
     const int *table, *lens, *q_start, *ptable;
@@ -390,6 +427,7 @@ struct DecodeArgs {
     int npre, pre_pieces, pre_chunks, pre_tokens;
     int row_warps;             // warps that share a piece in the rows kernel: 2, 3 or 4
     int row_tiles;             // tiles of a request's rows in the rows kernel's grid
+    int tile_rows;             // rows of such a tile (4 bits: 8 or 16)
     int fold;                  // the rows kernel joins the prefix's parts itself
     // behind a prefix: a word a block of the rows kernel (row_blocks of them), which
     // the prefix kernel sets to `token` and the block clears
@@ -407,6 +445,9 @@ cudaError_t launch_decode_rows(DType dt, const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_decode_prefix(DType dt, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                                  const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_decode_join(DType dt, const DecodeArgs &a, cudaStream_t st);
+// over a cache in 4 bits
+cudaError_t launch_decode4_general(DType dt, const DecodeArgs &a, cudaStream_t st);
+cudaError_t launch_decode4_rows(DType dt, const DecodeArgs &a, cudaStream_t st);
 
 // rows of one dense [BH, n, 64] tile box: band_qk loads 128-row boxes,
 // the gather kernels 64-row boxes.

@@ -115,28 +115,38 @@ swab_status check_rotary(const swab_rotary_desc *d, const uint64_t *turns, const
     return SWAB_OK;
 }
 
+// Q, K and their outputs: strides and pointers
+swab_status check_heads(const swab_rotary_desc *d, const void *Q, const void *K, void *Qo, void *Ko, RotaryArgs *a) {
+    swab_status s;
+    if ((s = take_strides(d, d->h, d->q_stride, false, a->sq)) != SWAB_OK) return s;
+    if ((s = take_strides(d, d->h, d->qo_stride, true, a->sqo)) != SWAB_OK) return s;
+    if ((s = check_tensors({Q, Qo})) != SWAB_OK) return s;
+    if (d->hk > 0) {
+        if ((s = take_strides(d, d->hk, d->k_stride, false, a->sk)) != SWAB_OK) return s;
+        if ((s = take_strides(d, d->hk, d->ko_stride, true, a->sko)) != SWAB_OK) return s;
+        if ((s = check_tensors({K, Ko})) != SWAB_OK) return s;
+    }
+    a->Q = Q;
+    a->K = K;
+    a->Qo = Qo;
+    a->Ko = Ko;
+    return SWAB_OK;
+}
+[[maybe_unused]] Extent turns_extent(const swab_rotary_desc *d, const uint64_t *turns) {
+    return {d->rot_dim ? turns : nullptr, (size_t)d->rot_dim / 2 * 8};
+}
+
 swab_status rotary_common(const swab_rotary_desc *d, const uint64_t *turns, const int32_t *pos, const void *Q,
                           const void *K, void *Qo, void *Ko, bool backward, void *stream) {
     RotaryArgs a{};
     swab_status s = check_rotary(d, turns, pos, &a);
     if (s != SWAB_OK) return s;
-    if ((s = take_strides(d, d->h, d->q_stride, false, a.sq)) != SWAB_OK) return s;
-    if ((s = take_strides(d, d->h, d->qo_stride, true, a.sqo)) != SWAB_OK) return s;
-    if ((s = check_tensors({Q, Qo})) != SWAB_OK) return s;
-    if (d->hk > 0) {
-        if ((s = take_strides(d, d->hk, d->k_stride, false, a.sk)) != SWAB_OK) return s;
-        if ((s = take_strides(d, d->hk, d->ko_stride, true, a.sko)) != SWAB_OK) return s;
-        if ((s = check_tensors({K, Ko})) != SWAB_OK) return s;
-    }
-    a.Q = Q;
-    a.K = K;
-    a.Qo = Qo;
-    a.Ko = Ko;
+    if ((s = check_heads(d, Q, K, Qo, Ko, &a)) != SWAB_OK) return s;
     a.backward = backward;
     if ((s = SERVE_BOUNDS(&a.bnd, {Q, strided_bytes(d, d->h, a.sq)}, {Qo, strided_bytes(d, d->h, a.sqo)},
                           {d->hk ? K : nullptr, strided_bytes(d, d->hk, a.sk)},
-                          {d->hk ? Ko : nullptr, strided_bytes(d, d->hk, a.sko)},
-                          {d->rot_dim ? turns : nullptr, (size_t)d->rot_dim / 2 * 8}, {pos, (size_t)a.tokens * 4})) != SWAB_OK)
+                          {d->hk ? Ko : nullptr, strided_bytes(d, d->hk, a.sko)}, turns_extent(d, turns),
+                          {pos, (size_t)a.tokens * 4})) != SWAB_OK)
         return s;
     return status_of(launch_rotary(static_cast<DType>(d->dtype), false, a, as_stream(stream)));
 }
@@ -159,6 +169,71 @@ swab_status check_cache(const swab_cache_desc *c) {
 }
 [[maybe_unused]] size_t table_bytes(const swab_cache_desc *c) { return (size_t)c->batch * c->cols * 4; }
 
+// codes and scales of a cache in 4 bits
+[[maybe_unused]] size_t codes_bytes(const swab_cache_desc *c, int hk, int hd) { return (size_t)c->n_blocks * c->page * hk * hd / 2; }
+[[maybe_unused]] size_t scales_bytes(const swab_cache_desc *c, int hk, int hd, int dtype) {
+    return (size_t)c->n_blocks * c->page * hk * (hd / kGroup4) * elt(dtype);
+}
+
+// rotary_append and its kin: rows, cache and slots
+swab_status check_append(const swab_rotary_desc *desc, const swab_cache_desc *cache, const uint64_t *turns, const int32_t *pos,
+                         const int32_t *slots, const void *Q, const void *K, const void *V, void *Qo, void *Kc, void *Vc,
+                         RotaryArgs *a) {
+    swab_status s = check_rotary(desc, turns, pos, a);
+    if (s != SWAB_OK) return s;
+    if ((s = check_cache(cache)) != SWAB_OK) return s;
+    if (desc->hk < 1 || !Q != !Qo) return SWAB_ERR_INVALID_ARG;
+    if ((long long)cache->n_blocks * cache->page * desc->hk >= 0xffffffffll) return SWAB_ERR_UNSUPPORTED;
+    if (desc->rot_dim > 0 && !pos) return SWAB_ERR_INVALID_ARG;
+    if (Q) {
+        if ((s = take_strides(desc, desc->h, desc->q_stride, false, a->sq)) != SWAB_OK) return s;
+        if ((s = take_strides(desc, desc->h, desc->qo_stride, true, a->sqo)) != SWAB_OK) return s;
+        if ((s = check_tensors({Q, Qo})) != SWAB_OK) return s;
+    } else {
+        a->hq = 0;
+    }
+    if ((s = take_strides(desc, desc->hk, desc->k_stride, false, a->sk)) != SWAB_OK) return s;
+    if ((s = take_strides(desc, desc->hk, desc->v_stride, false, a->sv)) != SWAB_OK) return s;
+    if ((s = check_tensors({K, V, Kc, Vc})) != SWAB_OK) return s;
+    if ((s = check_ints({slots})) != SWAB_OK) return s;
+    if (Kc == Vc) return SWAB_ERR_INVALID_ARG;
+    a->Q = Q;
+    a->K = K;
+    a->V = V;
+    a->Qo = Qo;
+    a->Kc = Kc;
+    a->Vc = Vc;
+    a->slots = slots;
+    a->page_log2 = log2_of(cache->page);
+    a->n_slots = cache->n_blocks * cache->page;
+    return SWAB_OK;
+}
+swab_status append_bounds([[maybe_unused]] const swab_rotary_desc *desc, const swab_cache_desc *, [[maybe_unused]] const RotaryArgs &a,
+                          [[maybe_unused]] Extent kc, [[maybe_unused]] Extent vc, [[maybe_unused]] Extent ks,
+                          [[maybe_unused]] Extent vs, [[maybe_unused]] Extent wq, [[maybe_unused]] Extent wk,
+                          [[maybe_unused]] RotaryArgs *to) {
+    return SERVE_BOUNDS(&to->bnd, {a.Q, strided_bytes(desc, desc->h, a.sq)}, {a.Qo, strided_bytes(desc, desc->h, a.sqo)},
+                        {a.K, strided_bytes(desc, desc->hk, a.sk)}, {a.V, strided_bytes(desc, desc->hk, a.sv)}, kc, vc, ks, vs, wq, wk,
+                        turns_extent(desc, reinterpret_cast<const uint64_t *>(a.turns)), {a.pos, (size_t)a.tokens * 4},
+                        {a.slots, (size_t)a.tokens * 4});
+}
+
+// ---------------------------------------------------------------------------
+// norms
+// ---------------------------------------------------------------------------
+swab_status check_norm(const swab_norm_desc *norm, const void *wq, const void *wk, NormArgs *a) {
+    if (!norm || !(norm->eps > 0.f) || !std::isfinite(norm->eps) || !std::isfinite(norm->offset)) return SWAB_ERR_INVALID_ARG;
+    if (!aligned(wq, 16) || !aligned(wk, 16)) return SWAB_ERR_MISALIGNED;      // (NULL is)
+    a->norm = 1;
+    a->eps = norm->eps;
+    a->offset = norm->offset;
+    a->wq = wq;
+    a->wk = wk;
+    return SWAB_OK;
+}
+[[maybe_unused]] Extent weight_extent(const swab_rotary_desc *d, const void *w) { return {w, (size_t)d->head_dim * elt(d->dtype)}; }
+size_t norm_workspace(const swab_rotary_desc *d) { return (size_t)kNormBlocks * d->head_dim * 4; }
+
 // ---------------------------------------------------------------------------
 // decode
 // ---------------------------------------------------------------------------
@@ -171,6 +246,7 @@ struct DecodePlan {
     int row_warps;
     bool fold;                       // no join launch: the rows kernel adds the prefix's parts
     int row_tiles;                   // of a request, in the rows kernel's grid
+    int tile_rows;                   // of such a tile (4 bits)
     long long row_blocks;            // of that grid
     size_t parts_bytes, ml_bytes, bytes;   // workspace: the parts, their (max, sum), a word a block of rows behind a prefix
 };
@@ -201,6 +277,13 @@ swab_status check_decode(const swab_decode_desc *d) {
         if (rs > (1ll << 36)) return SWAB_ERR_UNSUPPORTED;
     }
     return SWAB_OK;
+}
+
+// band_decode4: codes of 32 channels share a scale, and no shared prefix.
+swab_status check_decode4(const swab_decode_desc *d) {
+    const swab_status s = check_decode(d);
+    if (s != SWAB_OK) return s;
+    return d->head_dim % kGroup4 != 0 || d->prefix_len > 0 ? SWAB_ERR_UNSUPPORTED : SWAB_OK;
 }
 
 // How many of its own positions a query (a request's queries, undilated) can
@@ -315,6 +398,38 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
     return p;
 }
 
+// The same over a cache in 4 bits: tiles of 8 or 16 rows in blocks of four warps (16
+// or 12 of them an SM), lists cut in pieces of 128 keys and more.
+DecodePlan plan_decode4(const swab_decode_desc *d) {
+    DecodePlan p{};
+    const long long group = d->h / d->hk, batch = d->cache.batch, keys = most_keys(d);
+    p.rows = d->dtype != SWAB_F32 && (d->head_dim == 64 || d->head_dim == 128);
+    long long blocks = batch * d->hk, hold = 8 * kSms, least = 64;
+    if (p.rows) {
+        const long long rows = d->dilation == 0 ? d->max_q * group : group;
+        p.tile_rows = rows <= 8 ? 8 : 16;
+        const long long tiles = (rows + p.tile_rows - 1) / p.tile_rows * (d->dilation == 0 ? 1 : d->max_q);
+        blocks *= tiles;
+        p.row_tiles = (int)std::min<long long>(tiles, 65535 / d->hk);
+        hold = (p.tile_rows == 8 ? 4 : 3) * kSms;
+        least = keys <= 256 ? 256 : 128;
+    } else {
+        blocks *= (group + 3) / 4;
+    }
+    const long long want = std::max<long long>(1, hold / blocks);
+    const long long chunk = std::max<long long>(least, ((keys + want - 1) / want + 63) / 64 * 64);
+    p.nsplit = (int)((keys + chunk - 1) / chunk);
+    p.chunk = (int)std::min<long long>(chunk, 0x7fffffff);
+    p.nparts = p.nsplit;
+    if (p.nparts > 1) {
+        const size_t lines = (size_t)d->tokens * d->h * p.nparts;
+        p.parts_bytes = (lines * d->head_dim * 4 + 255) / 256 * 256;
+        p.ml_bytes = lines * 8;
+        p.bytes = p.parts_bytes + p.ml_bytes + 256;
+    }
+    return p;
+}
+
 // A number that no other call of this process, nor memory by chance, holds: the
 // workspace's contents on entry do not matter, and a word left in it must not
 // be taken for one that this call's prefix kernel has set.
@@ -324,6 +439,59 @@ unsigned long long next_token() {
     x ^= x >> 32;
     x *= 0xd6e8feb86659fd93ull;
     return (x ^ (x >> 32)) | 1ull;
+}
+
+// What the kernels take of a call, but for the scales of a cache in 4 bits.
+DecodeArgs decode_args(const swab_decode_desc *desc, const DecodePlan &plan, float scale, const void *Q, const void *Kc,
+                       const void *Vc, const int32_t *table, const int32_t *lens, const int32_t *q_start,
+                       const int32_t *prefix_table, void *O, float *lse, void *workspace) {
+    const swab_cache_desc *c = &desc->cache;
+    DecodeArgs a{};
+    a.Q = Q;
+    a.Kc = Kc;
+    a.Vc = Vc;
+    a.O = O;
+    a.lse = lse;
+    a.table = table;
+    a.lens = lens;
+    a.q_start = q_start;
+    a.ptable = prefix_table;
+    char *parts = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
+    a.po = reinterpret_cast<float *>(parts);
+    a.pml = reinterpret_cast<float2 *>(parts + plan.parts_bytes);
+    a.go = reinterpret_cast<unsigned long long *>(parts + plan.parts_bytes + plan.ml_bytes);
+    a.token = plan.npre > 0 ? next_token() : 0;
+    a.row_blocks = plan.row_blocks;
+    a.row_tiles = plan.row_tiles;
+    a.tile_rows = plan.tile_rows;
+    a.q_stride = desc->q_row_stride ? desc->q_row_stride : (long long)desc->h * desc->head_dim;
+    a.o_stride = desc->out_row_stride ? desc->out_row_stride : (long long)desc->h * desc->head_dim;
+    a.batch = c->batch;
+    a.tokens = desc->tokens;
+    a.h = desc->h;
+    a.hk = desc->hk;
+    a.group = desc->h / desc->hk;
+    a.hd = desc->head_dim;
+    a.w = desc->w;
+    a.stride = desc->dilation + 1;
+    a.n_sink = desc->n_sink;
+    a.prefix_len = desc->prefix_len;
+    a.page_log2 = log2_of(c->page);
+    a.n_blocks = c->n_blocks;
+    a.cols = c->cols;
+    a.ring = c->ring;
+    a.pinned = c->pinned;
+    a.nsplit = plan.nsplit;
+    a.chunk = plan.chunk;
+    a.nparts = plan.nparts;
+    a.npre = plan.npre;
+    a.pre_pieces = plan.pre_pieces;
+    a.pre_chunks = plan.pre_chunks;
+    a.fold = plan.fold;
+    a.row_warps = plan.row_warps;
+    a.pre_tokens = plan.pre_tokens;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return a;
 }
 
 // Tensor maps of the prefix kernel: Q as {hd, h, tokens}, a tile the heads of a
@@ -439,42 +607,145 @@ SWAB_API swab_status rotary_append(const swab_rotary_desc *desc, const swab_cach
                                    const int32_t *pos, const int32_t *slots, const void *Q, const void *K, const void *V,
                                    void *Qo, void *Kc, void *Vc, void *stream) {
     RotaryArgs a{};
-    swab_status s = check_rotary(desc, turns, pos, &a);
+    swab_status s = check_append(desc, cache, turns, pos, slots, Q, K, V, Qo, Kc, Vc, &a);
     if (s != SWAB_OK) return s;
-    if ((s = check_cache(cache)) != SWAB_OK) return s;
-    if (desc->hk < 1 || !Q != !Qo) return SWAB_ERR_INVALID_ARG;
-    if ((long long)cache->n_blocks * cache->page * desc->hk >= 0xffffffffll) return SWAB_ERR_UNSUPPORTED;
-    if (desc->rot_dim > 0 && !pos) return SWAB_ERR_INVALID_ARG;
-    if (Q) {
-        if ((s = take_strides(desc, desc->h, desc->q_stride, false, a.sq)) != SWAB_OK) return s;
-        if ((s = take_strides(desc, desc->h, desc->qo_stride, true, a.sqo)) != SWAB_OK) return s;
-        if ((s = check_tensors({Q, Qo})) != SWAB_OK) return s;
-    } else {
-        a.hq = 0;
-    }
-    if ((s = take_strides(desc, desc->hk, desc->k_stride, false, a.sk)) != SWAB_OK) return s;
-    if ((s = take_strides(desc, desc->hk, desc->v_stride, false, a.sv)) != SWAB_OK) return s;
-    if ((s = check_tensors({K, V, Kc, Vc})) != SWAB_OK) return s;
-    if ((s = check_ints({slots})) != SWAB_OK) return s;
-    if (Kc == Vc) return SWAB_ERR_INVALID_ARG;
-    a.Q = Q;
-    a.K = K;
-    a.V = V;
-    a.Qo = Qo;
-    a.Kc = Kc;
-    a.Vc = Vc;
-    a.slots = slots;
-    a.page_log2 = log2_of(cache->page);
-    a.n_slots = cache->n_blocks * cache->page;
-    if ((s = SERVE_BOUNDS(&a.bnd, {Q, strided_bytes(desc, desc->h, a.sq)}, {Qo, strided_bytes(desc, desc->h, a.sqo)},
-                          {K, strided_bytes(desc, desc->hk, a.sk)}, {V, strided_bytes(desc, desc->hk, a.sv)},
-                          {Kc, cache_bytes(cache, desc->hk, desc->head_dim, desc->dtype)},
-                          {Vc, cache_bytes(cache, desc->hk, desc->head_dim, desc->dtype)},
-                          {desc->rot_dim ? turns : nullptr, (size_t)desc->rot_dim / 2 * 8}, {pos, (size_t)a.tokens * 4},
-                          {slots, (size_t)a.tokens * 4})) != SWAB_OK)
+    if ((s = append_bounds(desc, cache, a, {Kc, cache_bytes(cache, desc->hk, desc->head_dim, desc->dtype)},
+                           {Vc, cache_bytes(cache, desc->hk, desc->head_dim, desc->dtype)}, {}, {}, {}, {}, &a)) != SWAB_OK)
         return s;
     if (!(a.err = device_status_word())) return SWAB_ERR_CUDA;
     return status_of(launch_rotary(static_cast<DType>(desc->dtype), true, a, as_stream(stream)));
+}
+
+SWAB_API swab_status norm_rotary(const swab_rotary_desc *desc, const swab_norm_desc *norm, const uint64_t *turns,
+                                 const int32_t *pos, const void *Q, const void *K, const void *wq, const void *wk, void *Qo,
+                                 void *Ko, void *stream) {
+    NormArgs a{};
+    swab_status s = check_rotary(desc, turns, pos, &a.r);
+    if (s != SWAB_OK) return s;
+    if ((s = check_norm(norm, wq, desc->hk > 0 ? wk : nullptr, &a)) != SWAB_OK) return s;
+    if ((s = check_heads(desc, Q, K, Qo, Ko, &a.r)) != SWAB_OK) return s;
+    if ((s = SERVE_BOUNDS(&a.r.bnd, {Q, strided_bytes(desc, desc->h, a.r.sq)}, {Qo, strided_bytes(desc, desc->h, a.r.sqo)},
+                          {desc->hk ? K : nullptr, strided_bytes(desc, desc->hk, a.r.sk)},
+                          {desc->hk ? Ko : nullptr, strided_bytes(desc, desc->hk, a.r.sko)}, turns_extent(desc, turns),
+                          {pos, (size_t)a.r.tokens * 4}, weight_extent(desc, a.wq), weight_extent(desc, a.wk))) != SWAB_OK)
+        return s;
+    return status_of(launch_norm(static_cast<DType>(desc->dtype), 0, a, as_stream(stream)));
+}
+
+SWAB_API size_t norm_rotary_bwd_workspace(const swab_rotary_desc *desc) {
+    RotaryArgs a{};
+    const uint64_t *turns = reinterpret_cast<const uint64_t *>(16);     // (not looked at)
+    return check_rotary(desc, turns, nullptr, &a) == SWAB_OK ? norm_workspace(desc) : 0;
+}
+
+SWAB_API swab_status norm_rotary_bwd(const swab_rotary_desc *desc, const swab_norm_desc *norm, const uint64_t *turns,
+                                     const int32_t *pos, const void *dQo, const void *dKo, const void *Q, const void *K,
+                                     const void *wq, const void *wk, void *dQ, void *dK, float *dwq, float *dwk,
+                                     void *workspace, void *stream) {
+    NormArgs a{};
+    swab_status s = check_rotary(desc, turns, pos, &a.r);
+    if (s != SWAB_OK) return s;
+    const bool keys = desc->hk > 0;
+    if ((s = check_norm(norm, wq, keys ? wk : nullptr, &a)) != SWAB_OK) return s;
+    if ((dwq && !wq) || (keys && dwk && !wk)) return SWAB_ERR_INVALID_ARG;
+    if ((s = check_heads(desc, dQo, dKo, dQ, dK, &a.r)) != SWAB_OK) return s;
+    if ((s = take_strides(desc, desc->h, norm->q_stride, false, a.sx[0])) != SWAB_OK) return s;
+    if ((s = check_tensors({Q})) != SWAB_OK) return s;
+    if (keys) {
+        if ((s = take_strides(desc, desc->hk, norm->k_stride, false, a.sx[1])) != SWAB_OK) return s;
+        if ((s = check_tensors({K})) != SWAB_OK) return s;
+    }
+    a.X[0] = Q;
+    a.X[1] = keys ? K : nullptr;
+    a.dw[0] = dwq;
+    a.dw[1] = keys ? dwk : nullptr;
+    for (const float *w : a.dw)
+        if (w && !aligned(w, 16)) return SWAB_ERR_MISALIGNED;
+    if (a.dw[0] && a.dw[0] == a.dw[1]) return SWAB_ERR_INVALID_ARG;
+    const bool sums = a.dw[0] || a.dw[1];
+    if (sums && (s = check_tensors({workspace})) != SWAB_OK) return s;
+    a.part = static_cast<float *>(workspace);
+    if ((s = SERVE_BOUNDS(&a.r.bnd, {dQo, strided_bytes(desc, desc->h, a.r.sq)}, {dQ, strided_bytes(desc, desc->h, a.r.sqo)},
+                          {Q, strided_bytes(desc, desc->h, a.sx[0])}, {keys ? dKo : nullptr, strided_bytes(desc, desc->hk, a.r.sk)},
+                          {keys ? dK : nullptr, strided_bytes(desc, desc->hk, a.r.sko)},
+                          {a.X[1], strided_bytes(desc, desc->hk, a.sx[1])}, turns_extent(desc, turns), {pos, (size_t)a.r.tokens * 4},
+                          weight_extent(desc, a.wq), weight_extent(desc, a.wk), {a.dw[0], (size_t)desc->head_dim * 4},
+                          {a.dw[1], (size_t)desc->head_dim * 4}, {sums ? workspace : nullptr, norm_workspace(desc)})) != SWAB_OK)
+        return s;
+    return status_of(launch_norm_bwd(static_cast<DType>(desc->dtype), a, as_stream(stream)));
+}
+
+SWAB_API swab_status norm_rotary_append(const swab_rotary_desc *desc, const swab_norm_desc *norm, const swab_cache_desc *cache,
+                                        const uint64_t *turns, const int32_t *pos, const int32_t *slots, const void *Q,
+                                        const void *K, const void *V, const void *wq, const void *wk, void *Qo, void *Kc,
+                                        void *Vc, void *stream) {
+    NormArgs a{};
+    swab_status s = check_append(desc, cache, turns, pos, slots, Q, K, V, Qo, Kc, Vc, &a.r);
+    if (s != SWAB_OK) return s;
+    if ((s = check_norm(norm, Q ? wq : nullptr, wk, &a)) != SWAB_OK) return s;
+    if ((s = append_bounds(desc, cache, a.r, {Kc, cache_bytes(cache, desc->hk, desc->head_dim, desc->dtype)},
+                           {Vc, cache_bytes(cache, desc->hk, desc->head_dim, desc->dtype)}, {}, {}, weight_extent(desc, a.wq),
+                           weight_extent(desc, a.wk), &a.r)) != SWAB_OK)
+        return s;
+    if (!(a.r.err = device_status_word())) return SWAB_ERR_CUDA;
+    return status_of(launch_norm(static_cast<DType>(desc->dtype), 1, a, as_stream(stream)));
+}
+
+SWAB_API swab_status rotary_append4(const swab_rotary_desc *desc, const swab_norm_desc *norm, const swab_cache_desc *cache,
+                                    const uint64_t *turns, const int32_t *pos, const int32_t *slots, const void *Q, const void *K,
+                                    const void *V, const void *wq, const void *wk, void *Qo, void *Kc, void *Ks, void *Vc,
+                                    void *Vs, void *stream) {
+    NormArgs a{};
+    swab_status s = check_append(desc, cache, turns, pos, slots, Q, K, V, Qo, Kc, Vc, &a.r);
+    if (s != SWAB_OK) return s;
+    if (desc->head_dim % kGroup4 != 0 || desc->head_dim > 256) return SWAB_ERR_UNSUPPORTED;
+    if (norm && (s = check_norm(norm, Q ? wq : nullptr, wk, &a)) != SWAB_OK) return s;
+    if ((s = check_tensors({Ks, Vs})) != SWAB_OK) return s;
+    if (Ks == Vs || Ks == Kc || Ks == Vc || Vs == Kc || Vs == Vc) return SWAB_ERR_INVALID_ARG;
+    a.Ks = Ks;
+    a.Vs = Vs;
+    const size_t codes = codes_bytes(cache, desc->hk, desc->head_dim), scales = scales_bytes(cache, desc->hk, desc->head_dim, desc->dtype);
+    if ((s = append_bounds(desc, cache, a.r, {Kc, codes}, {Vc, codes}, {Ks, scales}, {Vs, scales}, weight_extent(desc, a.wq),
+                           weight_extent(desc, a.wk), &a.r)) != SWAB_OK)
+        return s;
+    if (!(a.r.err = device_status_word())) return SWAB_ERR_CUDA;
+    return status_of(launch_norm(static_cast<DType>(desc->dtype), 2, a, as_stream(stream)));
+}
+
+SWAB_API swab_status cache_read4(const swab_cache_desc *cache, int32_t tokens, int32_t hk, int32_t head_dim, int32_t dtype,
+                                 const int32_t *slots, const void *Kc, const void *Ks, const void *Vc, const void *Vs, void *K,
+                                 void *V, void *stream) {
+    swab_status s = check_cache(cache);
+    if (s != SWAB_OK) return s;
+    if (tokens < 1 || hk < 1 || head_dim < 1 || !good_dtype(dtype)) return SWAB_ERR_INVALID_ARG;
+    if (head_dim % kGroup4 != 0 || head_dim > 256 || hk > 65535) return SWAB_ERR_UNSUPPORTED;
+    if ((long long)cache->n_blocks * cache->page * hk >= 0xffffffffll) return SWAB_ERR_UNSUPPORTED;
+    if ((s = check_tensors({Kc, Ks, Vc, Vs, K, V})) != SWAB_OK) return s;
+    if ((s = check_ints({slots})) != SWAB_OK) return s;
+    if (K == V) return SWAB_ERR_INVALID_ARG;
+    Read4Args a{};
+    a.slots = slots;
+    a.Kc = Kc;
+    a.Ks = Ks;
+    a.Vc = Vc;
+    a.Vs = Vs;
+    a.K = K;
+    a.V = V;
+    a.tokens = tokens;
+    a.hk = hk;
+    a.hd = head_dim;
+    a.page_log2 = log2_of(cache->page);
+    a.n_slots = cache->n_blocks * cache->page;
+    const size_t codes = codes_bytes(cache, hk, head_dim), scales = scales_bytes(cache, hk, head_dim, dtype);
+    const size_t rows = (size_t)tokens * hk * head_dim * elt(dtype);
+    (void)codes;
+    (void)scales;
+    (void)rows;
+    if ((s = SERVE_BOUNDS(&a.bnd, {slots, (size_t)tokens * 4}, {Kc, codes}, {Vc, codes}, {Ks, scales}, {Vs, scales}, {K, rows},
+                          {V, rows})) != SWAB_OK)
+        return s;
+    if (!(a.err = device_status_word())) return SWAB_ERR_CUDA;
+    return status_of(launch_read4(static_cast<DType>(dtype), a, as_stream(stream)));
 }
 
 SWAB_API size_t band_decode_workspace(const swab_decode_desc *desc) {
@@ -494,52 +765,10 @@ SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, cons
     if (lse && !aligned(lse, 16)) return SWAB_ERR_MISALIGNED;
     const DecodePlan plan = plan_decode(desc);
     if (plan.bytes > 0 && (s = check_tensors({workspace})) != SWAB_OK) return s;
-    DecodeArgs a{};
-    a.Q = Q;
-    a.Kc = Kc;
-    a.Vc = Vc;
-    a.O = O;
-    a.lse = lse;
-    a.table = table;
-    a.lens = lens;
-    a.q_start = q_start;
-    a.ptable = prefix_table;
-    char *parts = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
-    a.po = reinterpret_cast<float *>(parts);
-    a.pml = reinterpret_cast<float2 *>(parts + plan.parts_bytes);
-    a.go = reinterpret_cast<unsigned long long *>(parts + plan.parts_bytes + plan.ml_bytes);
-    a.token = plan.npre > 0 ? next_token() : 0;
-    a.row_blocks = plan.row_blocks;
-    a.row_tiles = plan.row_tiles;
-    a.q_stride = desc->q_row_stride ? desc->q_row_stride : (long long)desc->h * desc->head_dim;
-    a.o_stride = desc->out_row_stride ? desc->out_row_stride : (long long)desc->h * desc->head_dim;
-    a.batch = c->batch;
-    a.tokens = desc->tokens;
-    a.h = desc->h;
-    a.hk = desc->hk;
-    a.group = desc->h / desc->hk;
-    a.hd = desc->head_dim;
-    a.w = desc->w;
-    a.stride = desc->dilation + 1;
-    a.n_sink = desc->n_sink;
-    a.prefix_len = desc->prefix_len;
-    a.page_log2 = log2_of(c->page);
-    a.n_blocks = c->n_blocks;
-    a.cols = c->cols;
-    a.ring = c->ring;
-    a.pinned = c->pinned;
-    a.nsplit = plan.nsplit;
-    a.chunk = plan.chunk;
-    a.nparts = plan.nparts;
-    a.npre = plan.npre;
-    a.pre_pieces = plan.pre_pieces;
-    a.pre_chunks = plan.pre_chunks;
-    a.fold = plan.fold;
-    a.row_warps = plan.row_warps;
-    a.pre_tokens = plan.pre_tokens;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    DecodeArgs a = decode_args(desc, plan, scale, Q, Kc, Vc, table, lens, q_start, prefix_table, O, lse, workspace);
     const DType dt = static_cast<DType>(desc->dtype);
     const size_t es = (size_t)elt(desc->dtype), width = (size_t)desc->h * desc->head_dim;
+    (void)c;
     (void)es;
     (void)width;
     if ((s = SERVE_BOUNDS(&a.bnd, {Q, ((size_t)(desc->tokens - 1) * a.q_stride + width) * es},
@@ -560,6 +789,43 @@ SWAB_API swab_status band_decode(const swab_decode_desc *desc, float scale, cons
     if (e == cudaSuccess)
         e = plan.rows ? launch_decode_rows(dt, a, as_stream(stream)) : launch_decode_general(dt, a, as_stream(stream));
     if (e == cudaSuccess && a.nparts > 1 && !a.fold) e = launch_decode_join(dt, a, as_stream(stream));
+    return status_of(e);
+}
+
+SWAB_API size_t band_decode4_workspace(const swab_decode_desc *desc) {
+    return check_decode4(desc) == SWAB_OK ? plan_decode4(desc).bytes : 0;
+}
+
+SWAB_API swab_status band_decode4(const swab_decode_desc *desc, float scale, const void *Q, const void *Kc, const void *Ks,
+                                  const void *Vc, const void *Vs, const int32_t *table, const int32_t *lens,
+                                  const int32_t *q_start, void *O, float *lse, void *workspace, void *stream) {
+    swab_status s = check_decode4(desc);
+    if (s != SWAB_OK) return s;
+    const swab_cache_desc *c = &desc->cache;
+    if (!std::isfinite(scale)) return SWAB_ERR_INVALID_ARG;
+    if ((s = check_tensors({Q, Kc, Ks, Vc, Vs, O})) != SWAB_OK) return s;
+    if ((s = check_ints({table, lens, q_start})) != SWAB_OK) return s;
+    if (lse && !aligned(lse, 16)) return SWAB_ERR_MISALIGNED;
+    const DecodePlan plan = plan_decode4(desc);
+    if (plan.bytes > 0 && (s = check_tensors({workspace})) != SWAB_OK) return s;
+    DecodeArgs a = decode_args(desc, plan, scale, Q, Kc, Vc, table, lens, q_start, nullptr, O, lse, workspace);
+    a.Ks = Ks;
+    a.Vs = Vs;
+    const DType dt = static_cast<DType>(desc->dtype);
+    const size_t es = (size_t)elt(desc->dtype), width = (size_t)desc->h * desc->head_dim;
+    const size_t codes = codes_bytes(c, desc->hk, desc->head_dim), scales = scales_bytes(c, desc->hk, desc->head_dim, desc->dtype);
+    (void)es;
+    (void)width;
+    (void)codes;
+    (void)scales;
+    if ((s = SERVE_BOUNDS(&a.bnd, {Q, ((size_t)(desc->tokens - 1) * a.q_stride + width) * es},
+                          {O, ((size_t)(desc->tokens - 1) * a.o_stride + width) * es}, {Kc, codes}, {Vc, codes}, {Ks, scales},
+                          {Vs, scales}, {table, table_bytes(c)}, {lens, (size_t)c->batch * 4}, {q_start, (size_t)(c->batch + 1) * 4},
+                          {lse, (size_t)desc->tokens * desc->h * 4}, {plan.bytes ? workspace : nullptr, plan.bytes})) != SWAB_OK)
+        return s;
+    if (!(a.err = device_status_word())) return SWAB_ERR_CUDA;
+    cudaError_t e = plan.rows ? launch_decode4_rows(dt, a, as_stream(stream)) : launch_decode4_general(dt, a, as_stream(stream));
+    if (e == cudaSuccess && a.nparts > 1) e = launch_decode_join(dt, a, as_stream(stream));
     return status_of(e);
 }
 

@@ -12,7 +12,8 @@ runs one step of it:
 
 A step needs no value on the host, so it can be captured once in a CUDA graph
 and replayed.  Every computation is one of the library's calls: cache_slots,
-rotary_append, band_decode.
+rotary_append, band_decode (with ``norm`` norm_rotary_append; with ``bits=4``
+rotary_append4, band_decode4).
 """
 from __future__ import annotations
 
@@ -20,7 +21,7 @@ import operator
 
 import torch
 
-from . import serve
+from . import cache4, norm as normed, serve
 
 
 class DecodeLoop:
@@ -32,10 +33,18 @@ class DecodeLoop:
     recycled as its window moves on, so the cache does not grow with the
     context.  Rotary positions turn the whole head unless ``rot_dim`` says
     less (0: none); ``turns`` and ``rotary_scale`` as rotary_frequencies gives
-    them."""
+    them.  ``norm`` (a NormDesc; weights ``wq``, ``wk`` [head_dim], None: 1): queries
+    and keys are normed first.  ``bits=4``: the cache holds K and V in 4 bits (codes
+    Kc, Vc, scales Ks, Vs), head_dim a multiple of 32."""
 
     def __init__(self, batch, h, hk, head_dim, w, dilation=0, n_sink=0, max_new=1, page=64, rot_dim=None, turns=None,
-                 rotary_scale=1.0, dtype=torch.bfloat16, device="cuda"):
+                 rotary_scale=1.0, dtype=torch.bfloat16, device="cuda", bits=None, norm=None, wq=None, wk=None):
+        if bits not in (None, 4):
+            raise ValueError(f"bits: expected 4, or None for a cache of the tensors' type, got {bits!r}")
+        for name, x in (("wq", wq), ("wk", wk)):
+            if x is not None and (norm is None or x.dtype is not dtype or x.shape != (head_dim,)):
+                raise ValueError(f"{name}: expected [{head_dim}] {dtype} with a norm, got {list(x.shape)} {x.dtype}")
+        self.bits, self.norm = bits, norm
         self.batch, self.h, self.hk, self.head_dim, self.dtype = batch, h, hk, head_dim, dtype
         self.rot_dim, self.rotary_scale = head_dim if rot_dim is None else rot_dim, rotary_scale
         pinned = -(-n_sink // page)
@@ -53,11 +62,19 @@ class DecodeLoop:
                                         max_q=max_new, max_len=1 << 30, dtype=dtype)
         # (what the calls of a step would refuse is refused here: there the lengths would have moved on)
         serve.check_step(self.cache, self._rotary, self._decode)
+        normed.check_norm(self._rotary, norm)
+        cache4.check_step4(self.cache, self._rotary, self._decode, bits)
         self.turns = turns.contiguous().to(device) if self.rot_dim else None
         i32 = dict(dtype=torch.int32, device=device)
         new = dict(dtype=dtype, device=device)
-        self.Kc = torch.zeros(batch * cols, hk, page, head_dim, **new)
-        self.Vc = torch.zeros_like(self.Kc)
+        self.wq, self.wk = (None if x is None else x.contiguous().to(device) for x in (wq, wk))
+        if bits == 4:
+            codes, scales = cache4.cache4_shapes(self.cache, hk, head_dim)
+            self.Kc, self.Vc = (torch.zeros(codes, dtype=torch.uint8, device=device) for _ in range(2))
+            self.Ks, self.Vs = (torch.zeros(scales, **new) for _ in range(2))
+        else:
+            self.Kc = torch.zeros(batch * cols, hk, page, head_dim, **new)
+            self.Vc = torch.zeros_like(self.Kc)
         self.table = torch.full((batch, cols), -1, **i32)
         self.free_list = torch.arange(batch * cols, **i32)
         self.lens, self.used, self.q_start = torch.zeros(batch, **i32), torch.zeros(2, **i32), torch.zeros(batch + 1, **i32)
@@ -67,13 +84,23 @@ class DecodeLoop:
         self.q = torch.zeros(self.tokens, h, head_dim, **new)
         self.out = torch.zeros_like(self.q)
         self.lse = torch.zeros(self.tokens, h, dtype=torch.float32, device=device)
-        need = serve.band_decode_workspace(self._decode)
+        need = cache4.band_decode4_workspace(self._decode) if bits == 4 else serve.band_decode_workspace(self._decode)
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         self.scale = head_dim ** -0.5
 
     def _place(self, cache, n_new, slots, pos):
         serve.cache_slots(cache, self.lens, n_new, self.table, self.free_list, self.used, self.lens, self.used, self.q_start,
                           slots, pos)
+
+    def _append(self, d, qkv, pos, slots, out):
+        q, k, v = qkv.split([self.h, self.hk, self.hk], dim=1)
+        if self.bits == 4:
+            cache4.rotary_append4(d, self.cache, self.turns, q, k, v, pos, slots, out, self.Kc, self.Ks, self.Vc, self.Vs, self.norm,
+                                  self.wq, self.wk)
+        elif self.norm is not None:
+            normed.norm_rotary_append(d, self.norm, self.cache, self.turns, q, k, v, pos, slots, out, self.Kc, self.Vc, self.wq, self.wk)
+        else:
+            serve.rotary_append(d, self.cache, self.turns, q, k, v, pos, slots, out, self.Kc, self.Vc)
 
     def fill(self, qkv, n_new):
         """Prompts of n_new[r] tokens (int32 [batch]) into the cache: the rows of
@@ -95,18 +122,20 @@ class DecodeLoop:
             raise ValueError(f"n_new: adds up to more than the {T} rows of qkv")
         slots, pos = torch.empty(T, dtype=torch.int32, device=qkv.device), torch.empty(T, dtype=torch.int32, device=qkv.device)
         self._place(self._prompts, n_new, slots, pos)
-        q, k, v = qkv.split([self.h, self.hk, self.hk], dim=1)
         d = serve.RotaryDesc(1, T, self.h, self.hk, self.head_dim, self.rot_dim, scale=self.rotary_scale, dtype=self.dtype)
         out = torch.empty(T, self.h, self.head_dim, dtype=self.dtype, device=qkv.device)
-        serve.rotary_append(d, self.cache, self.turns, q, k, v, pos, slots, out, self.Kc, self.Vc)
+        self._append(d, qkv, pos, slots, out)
         return out
 
     def step(self):
         """n_new[r] tokens for every request, their heads in the rows of ``qkv``;
         the attention in ``out`` and ``lse``."""
         self._place(self.cache, self.n_new, self.slots, self.pos)
-        q, k, v = self.qkv.split([self.h, self.hk, self.hk], dim=1)
-        serve.rotary_append(self._rotary, self.cache, self.turns, q, k, v, self.pos, self.slots, self.q, self.Kc, self.Vc)
+        self._append(self._rotary, self.qkv, self.pos, self.slots, self.q)
+        if self.bits == 4:
+            cache4.band_decode4(self._decode, self.scale, self.q, self.Kc, self.Ks, self.Vc, self.Vs, self.table, self.lens, self.q_start,
+                                self.out, self.lse, self.workspace)
+            return
         serve.band_decode(self._decode, self.scale, self.q, self.Kc, self.Vc, self.table, self.lens, self.q_start, self.out,
                           self.lse, self.workspace)
 
@@ -127,11 +156,12 @@ class DecodeLoop:
         self.lens[rows] = 0
 
     @classmethod
-    def from_workload(cls, wl, batch=None, device="cuda"):
+    def from_workload(cls, wl, batch=None, device="cuda", **more):
         """The loop that carries a named workload's sequences on: its heads,
         window on the left, dilation and global tokens, which have to be the
-        leading ones."""
+        leading ones.  ``more``: bits, norm, wq, wk."""
         n_sink = len(set(wl.global_idx))
         if sorted(set(wl.global_idx)) != list(range(n_sink)):
             raise ValueError(f"global tokens other than the leading ones: {tuple(wl.global_idx)}")
-        return cls(wl.b if batch is None else batch, wl.h, wl.h, wl.head_dim, wl.w, wl.dilation, n_sink, dtype=wl.dtype, device=device)
+        return cls(wl.b if batch is None else batch, wl.h, wl.h, wl.head_dim, wl.w, wl.dilation, n_sink, dtype=wl.dtype, device=device,
+                   **more)

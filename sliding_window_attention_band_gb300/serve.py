@@ -141,7 +141,7 @@ class DecodeDesc:
         self._kv = (cache.n_blocks, self.hk, cache.page, self.head_dim)
         self._batch, self._table = cache.batch, cache.batch * cache.cols
         self._ref, self._addr = ctypes.byref(self.c), ctypes.addressof(self.c)
-        self._workspace = None
+        self._workspace = self._workspace4 = None
 
 
 # ---------------------------------------------------------------------------
@@ -159,6 +159,7 @@ class _NoCalls:
     """In place of the compiled module where it has not been built."""
 
     rotary = rotary_bwd = cache_slots = rotary_append = band_decode = staticmethod(lambda *args: -1)
+    norm_rotary = norm_rotary_bwd = norm_rotary_append = rotary_append4 = cache_read4 = band_decode4 = rotary
 
 
 def _load_calls():
@@ -172,6 +173,9 @@ def _load_calls():
             spec.loader.exec_module(calls)
             calls.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
                          for name in ("rotary", "rotary_bwd", "cache_slots", "rotary_append", "band_decode")))
+            calls.bind_more(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                              for name in ("norm_rotary", "norm_rotary_bwd", "norm_rotary_bwd_workspace", "norm_rotary_append",
+                                           "rotary_append4", "cache_read4", "band_decode4")))
         except ImportError as e:
             warnings.warn(f"the compiled serving calls do not load, they take some microseconds more: {e}")
             calls = _NoCalls
