@@ -38,16 +38,16 @@ static constexpr unsigned kSwabFile = 18;   // site id of the bounds checks
 namespace swab {
 namespace {
 
-constexpr int kKeys = 32;          // keys of a group
+constexpr int kGroup = 64;         // keys of a group, which a warp takes at a time
 constexpr float kSlack = 8.f;      // log2 headroom of the running maximum
 
 template <int HD, int kN, int kWarps> struct Shape4 {
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kBlocks = (kN == 1 ? 16 : 12) / kWarps;   // an SM holds, by registers and shared memory
-    static constexpr int kStages = HD == 128 ? 3 : 4;
+    static constexpr int kBlocks = (HD == 64 && kN == 1 ? 16 : 12) / kWarps;   // an SM holds, by registers and shared memory
+    static constexpr int kStages = HD == 128 ? 2 : 3;
     static constexpr int kLine = HD / 2;                            // bytes of codes of a key
     static constexpr int kScale = HD / 16;                          // bytes of its scales
-    static constexpr int kCodes = kKeys * kLine, kScales = kKeys * kScale;
+    static constexpr int kCodes = kGroup * kLine, kScales = kGroup * kScale;
     static constexpr int kStage = 2 * (kCodes + kScales);          // codes of K, of V, scales of K, of V
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kWarps * kRing + 128;
@@ -85,56 +85,85 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Codes to values, two at a time.
-template <typename T> struct Two;
-template <> struct Two<__half> {
-    // codes n and n + 4 of a word as 16 + c: bits 6..9 of a half behind the exponent of 16
-    template <int n> __device__ static __forceinline__ uint32_t biased(uint32_t w) {
-        const uint32_t x = n == 0 ? w << 6 : n == 1 ? w << 2 : n == 2 ? w >> 2 : w >> 6;
-        return (x & 0x03c003c0u) | 0x4c004c00u;
-    }
-    __device__ static __forceinline__ uint32_t fma(uint32_t x, uint32_t s, uint32_t b) {
-        uint32_t y;
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(s), "r"(b));
-        return y;
-    }
-    __device__ static __forceinline__ uint32_t bias(uint32_t s) {       // -24 s, exact
-        uint32_t y;
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(s), "r"(0xce00ce00u));
-        return y;
-    }
+// Codes to values, two at a time.  (x & mask) | magic is one instruction when both
+// constants are in registers: an immediate for each makes two of it, so they are
+// held where the compiler does not see what they are.
+struct Masks {
+    uint32_t mask, magic;
 };
-template <> struct Two<__nv_bfloat16> {
-    template <int n> __device__ static __forceinline__ uint32_t biased(uint32_t w) {     // bits 3..6
-        const uint32_t x = n == 0 ? w << 3 : n == 1 ? w >> 1 : n == 2 ? w >> 5 : w >> 9;
-        return (x & 0x00780078u) | 0x41804180u;
-    }
-    __device__ static __forceinline__ uint32_t fma(uint32_t x, uint32_t s, uint32_t b) {
-        uint32_t y;
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(s), "r"(b));
-        return y;
-    }
-    __device__ static __forceinline__ uint32_t bias(uint32_t s) {
-        uint32_t y;
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(s), "r"(0xc1c0c1c0u));
-        return y;
-    }
-};
+template <typename T> __device__ __forceinline__ Masks masks_of() {
+    constexpr bool kHalf = std::is_same<T, __half>::value;      // 16 + c: bits 6..9 of a half, or 3..6
+    Masks k;
+    asm volatile("mov.b32 %0, %2;\n mov.b32 %1, %3;" : "=r"(k.mask), "=r"(k.magic)
+                 : "n"(kHalf ? 0x03c003c0 : 0x00780078), "n"(kHalf ? 0x4c004c00 : 0x41804180));
+    return k;
+}
+// codes n and n + 4 of a word as 16 + c
+template <typename T, int n> __device__ __forceinline__ uint32_t biased(uint32_t w, const Masks &k) {
+    constexpr int left = std::is_same<T, __half>::value ? 6 - 4 * n : 3 - 4 * n;
+    const uint32_t x = left >= 0 ? w << (left & 31) : w >> (-left & 31);
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(k.mask), "r"(k.magic));
+    return y;
+}
+template <typename T> __device__ __forceinline__ uint32_t fma_two(uint32_t x, uint32_t s, uint32_t b) {
+    uint32_t y;
+    if constexpr (std::is_same<T, __half>::value) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(s), "r"(b));
+    else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(s), "r"(b));
+    return y;
+}
+template <typename T> __device__ __forceinline__ uint32_t bias_of(uint32_t s) {       // -24 s, exact
+    uint32_t y;
+    if constexpr (std::is_same<T, __half>::value) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(s), "r"(0xce00ce00u));
+    else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(s), "r"(0xc1c0c1c0u));
+    return y;
+}
 // word -> {value n, value n + 4} for n = 0..3
-template <typename T> __device__ __forceinline__ void values(uint32_t w, uint32_t s, uint32_t b, uint32_t (&v)[4]) {
-    v[0] = Two<T>::fma(Two<T>::template biased<0>(w), s, b);
-    v[1] = Two<T>::fma(Two<T>::template biased<1>(w), s, b);
-    v[2] = Two<T>::fma(Two<T>::template biased<2>(w), s, b);
-    v[3] = Two<T>::fma(Two<T>::template biased<3>(w), s, b);
+template <typename T> __device__ __forceinline__ void values(uint32_t w, uint32_t s, uint32_t b, const Masks &k, uint32_t (&v)[4]) {
+    v[0] = fma_two<T>(biased<T, 0>(w, k), s, b);
+    v[1] = fma_two<T>(biased<T, 1>(w, k), s, b);
+    v[2] = fma_two<T>(biased<T, 2>(w, k), s, b);
+    v[3] = fma_two<T>(biased<T, 3>(w, k), s, b);
 }
 
 // Key (of 8) in row p of a product: the even rows take the first four, the odd ones
 // the others backwards.
 __device__ __forceinline__ int slot_of(int p) { return (p & 1) ? 4 + ((p >> 1) ^ 3) : p >> 1; }
 
+// A warp's copies of one stage have arrived: bounded, never trapping (the context
+// stays usable, the status word says so).
+struct Waiter {
+    volatile int *abort_flag;
+    unsigned *err;
+    __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity) const { mbar_wait(bar, parity, abort_flag, err); }
+};
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// The positions that a tile's rows attend to, undilated, as halves of 16: those with
+// sinks, then those of the band.
+struct Halves {
+    int count, nsink, band_lo, hi, sink_halves, band_half;
+    __device__ __forceinline__ int at(int u) const { return (u < sink_halves ? u : band_half + (u - sink_halves)) << 4; }
+    __device__ __forceinline__ bool has(int j) const { return j < nsink || (j >= band_lo && j <= hi); }
+};
+__device__ __forceinline__ Halves halves_of(const DecodeArgs &p, const Request &q, int a_lo, int a_hi) {
+    Halves k;
+    const int lo = q.i0 + a_lo;
+    k.hi = min(q.i0 + a_hi, q.last);
+    k.nsink = max(min(p.n_sink, k.hi + 1), 0);
+    k.band_lo = (int)max((long long)lo - p.w, (long long)p.n_sink);
+    k.sink_halves = (int)(((unsigned)k.nsink + 15u) >> 4);
+    k.band_half = max(k.band_lo >> 4, k.sink_halves);
+    k.count = k.sink_halves + max((k.hi >> 4) - k.band_half + 1, 0);
+    return k;
+}
+
 // Grid: (piece, key head and tile of 8 kN rows, request).  kWarps: the warps that
-// share a piece.
-template <typename T, int HD, int kN, int kWarps>
+// share a piece.  kRun: undilated, whole halves of a block at a time.
+template <typename T, int HD, int kN, int kWarps, bool kRun>
 __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) k_decode4_rows(const __grid_constant__ DecodeArgs p) {
     using S = Shape4<HD, kN, kWarps>;
     constexpr int kThreads = S::kThreads, kRows = 8 * kN;
@@ -148,97 +177,176 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
     __shared__ float2 sml[kWarps][kRows];
     __shared__ float swt[kWarps][kRows];
     __shared__ float2 stot[kRows];
-    __shared__ uint32_t sok[kWarps][S::kStages];           // which keys of the group in a stage are there
+    __shared__ uint2 sok[kRun ? 1 : kWarps][S::kStages];   // which keys of the group in a stage are there
+    __shared__ uint64_t sbar[kRun ? kWarps : 1][S::kStages];
+    __shared__ int sabort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int split = blockIdx.x, r = blockIdx.z;
     const int kvh = (int)(blockIdx.y % (unsigned)p.hk), tile0 = (int)(blockIdx.y / (unsigned)p.hk);
     const int tiles_y = gridDim.y / p.hk;
+    if constexpr (kRun) {
+        if (threadIdx.x == 0) sabort = 0;
+        if (lane < S::kStages) mbar_init(&sbar[warp][lane], 1);
+        fence_barrier_init();
+        __syncthreads();
+    }
+    const Waiter waiter{&sabort, p.err};
     pdl_wait();
     pdl_trigger();
     const Request q = request_of(p, r);
     uint8_t *ring = smem + warp * S::kRing;
     const uint32_t ring_s = smem_u32(ring);
-    const char *kbase = reinterpret_cast<const char *>(p.Kc) + lane % kChunks * 16;
-    const char *vbase = reinterpret_cast<const char *>(p.Vc) + lane % kChunks * 16;
-    // where a copied piece goes: piece c of line i at c ^ (2 (i / 2 mod 2)) of the line
-    // (64-byte lines; 32-byte ones as they are)
-    const uint32_t copy_row = lane / kChunks;
-    const uint32_t copy_to = copy_row * S::kLine + ((lane % kChunks) ^ (HD == 128 ? (copy_row & 2) : 0)) * 16;
     // what this lane reads: in K keys slot_of(g) and + 8 of each 16, in V keys t4 and 7 - t4 and + 8
     const int k_slot = slot_of(g), v_even = t4, v_odd = 4 + (t4 ^ 3);
-    const uint32_t k_at = k_slot * S::kLine + (HD == 128 ? (t4 ^ (k_slot & 2)) * 16 : t4 * 8);
-    auto v_place = [&](int slot) { return (uint32_t)(slot * S::kLine + (HD == 128 ? ((g >> 1) ^ (slot & 2)) * 16 + (g & 1) * 8 : g * 4)); };
-    const uint32_t ve_at = S::kCodes + v_place(v_even), vo_at = S::kCodes + v_place(v_odd);
-    const uint32_t ks_at = 2 * S::kCodes + k_slot * S::kScale + (HD == 128 ? t4 : t4 >> 1) * 2;
+    const uint32_t k_at = k_slot * S::kLine + t4 * (HD / 8);
+    const uint32_t ve_at = S::kCodes + v_even * S::kLine + g * (HD / 16), vo_at = S::kCodes + v_odd * S::kLine + g * (HD / 16);
+    const uint32_t ks_at = k_slot * S::kScale + (HD == 128 ? t4 : t4 >> 1) * 2;
     const int v_group = HD == 128 ? g >> 1 : g >> 2;
-    const uint32_t ves_at = 2 * S::kCodes + S::kScales + v_even * S::kScale + v_group * 2;
-    const uint32_t vos_at = 2 * S::kCodes + S::kScales + v_odd * S::kScale + v_group * 2;
+    const uint32_t ves_at = S::kScales + v_even * S::kScale + v_group * 2;
+    const uint32_t vos_at = S::kScales + v_odd * S::kScale + v_group * 2;
     // scores are scaled by |scale| inside the exponent; a negative one turns Q
     // round (exact), zero clears it
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
     const uint32_t q_and = p.scale_log2 == 0.f ? 0u : 0xffffffffu, q_xor = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     // tiles of rows: with a key stride each token has its own
     const int per_tok = (p.group + kRows - 1) / kRows;
-    const int ntiles = p.stride == 1 ? (q.m * p.group + kRows - 1) / kRows : q.m * per_tok;
+    const int ntiles = kRun ? (q.m * p.group + kRows - 1) / kRows : q.m * per_tok;
+    const Masks masks = masks_of<T>();
+    int to_fill = 0, to_read = 0;                          // stages
+    uint32_t phase = 0;                                    // of the barriers (kRun)
+    // kRun: lane 4 half + what copies codes of K, of V, scales of K, of V (what) of a half
+    const uint32_t copy_unit = t4 < 2 ? S::kLine : S::kScale, copy_half = (lane >> 2) & 3;
+    const char *copy_from = reinterpret_cast<const char *>(t4 == 0 ? p.Kc : t4 == 1 ? p.Vc : t4 == 2 ? p.Ks : p.Vs);
+    const uint32_t copy_to = ring_s + (t4 < 2 ? t4 * S::kCodes : 2 * S::kCodes + (t4 - 2) * S::kScales) + copy_half * 16 * copy_unit;
 
-    for (int tile = tile0; tile < ntiles; tile += tiles_y) {
-        int row0, nrows;
-        if (p.stride == 1) {
-            row0 = tile * kRows;
-            nrows = min(kRows, q.m * p.group - row0);
-        } else {
-            const int part = tile % per_tok;
-            row0 = tile / per_tok * p.group + part * kRows;
-            nrows = min(kRows, p.group - part * kRows);
-        }
+    // a tile of rows row0 .. row0 + nrows - 1, at most 8 N
+    auto run = [&](auto tag, int row0, int nrows) {
+        constexpr int N = decltype(tag)::value;
         const int a_lo = row0 / p.group, a_hi = (row0 + nrows - 1) / p.group;
-        const KeyList keys = keys_of(p, q, a_lo, a_hi);
-        const int lo = min((long long)split * p.chunk, (long long)keys.count);
-        const int hi = split == p.nsplit - 1 ? keys.count : (int)min((long long)lo + p.chunk, (long long)keys.count);
-        const int groups = (int)(((long long)hi - lo + kKeys - 1) / kKeys);
+        Halves halves;
+        KeyList keys;
+        int lo, hi;                                        // of the list of halves, or of keys
+        if constexpr (kRun) {
+            halves = halves_of(p, q, a_lo, a_hi);
+            const int per = p.chunk >> 4;
+            lo = (int)min((long long)split * per, (long long)halves.count);
+            hi = split == p.nsplit - 1 ? halves.count : (int)min((long long)lo + per, (long long)halves.count);
+        } else {
+            keys = keys_of(p, q, a_lo, a_hi);
+            lo = (int)min((long long)split * p.chunk, (long long)keys.count);
+            hi = split == p.nsplit - 1 ? keys.count : (int)min((long long)lo + p.chunk, (long long)keys.count);
+        }
+        constexpr int kUnit = kRun ? kGroup / 16 : kGroup;   // entries of the list a group takes
+        const int groups = (int)(((long long)hi - lo + kUnit - 1) / kUnit);
         const int mine = groups > warp ? (groups - warp + kWarps - 1) / kWarps : 0;   // of this warp
 
-        // line of key `lane` of the warp's group n
-        auto look_up = [&](int n) -> uint32_t {
+        const int pos_lo = q.i0 + a_lo, pos_hi = q.i0 + a_hi;
+
+        // kRun.  The warp's halves are looked up 32 at a time, a lane a half (8 groups),
+        // the block ids of the next ones while these are used: their lines, and
+        // which are there and attended to by every row.
+        int next_id = -1, batch = 0;
+        uint32_t lines = kNoLine, there = 0, full = 0, there_before = 0, full_before = 0;
+        auto half_of = [&](int batch_, int &j0) -> bool {
             // (unsigned: past the end of the longest list the sum passes 2^31)
-            const unsigned u = (unsigned)kKeys * (unsigned)(warp + kWarps * n) + (unsigned)lane;
-            return n < mine && u < (unsigned)(hi - lo) ? key_line(p, q, keys.at(lo + (int)u), kvh) : kNoLine;
+            const int n = 8 * batch_ + (lane >> 2);
+            const unsigned u = 4u * (unsigned)(warp + kWarps * n) + (unsigned)(lane & 3);
+            if (!(n < mine && u < (unsigned)(hi - lo))) return false;
+            j0 = halves.at(lo + (int)u);
+            return true;
         };
-        auto load = [&](int stage, uint32_t line) {
-            const uint32_t there = __ballot_sync(0xffffffffu, line != kNoLine);
-            if (lane == 0) sok[warp][stage] = there;
-            const uint32_t at = ring_s + stage * S::kStage, to = at + copy_to;
+        auto fetch_ids = [&](int batch_) {
+            int j0 = 0, col = -1;
+            if (half_of(batch_, j0)) col = key_column(p, q, j0);
+            next_id = col < 0 ? -1 : *GP(p.bnd, q.trow + col);
+        };
+        auto take_ids = [&](int batch_) {
+            int j0 = 0;
+            const bool in = half_of(batch_, j0);
+            lines = in ? block_line(p, next_id, j0 & ((1 << p.page_log2) - 1), kvh) : kNoLine;
+            bool here = lines != kNoLine;
+#if SWAB_BOUNDS_CHECK
+            // (a copy that would leave its buffer is left out)
+            const unsigned long long ln = lines;
+            auto inside = [&](const void *base, int unit) {
+                const char *src = reinterpret_cast<const char *>(base) + ln * unit;
+                return GPN(p.bnd, src, 16 * unit) == src;
+            };
+            if (here && !(inside(p.Kc, S::kLine) && inside(p.Vc, S::kLine) && inside(p.Ks, S::kScale) && inside(p.Vs, S::kScale))) here = false;
+#endif
+            there_before = there;
+            full_before = full;
+            there = __ballot_sync(0xffffffffu, here);
+            full = __ballot_sync(0xffffffffu, here && j0 + 15 <= pos_lo && (j0 + 15 < p.n_sink || (long long)pos_hi - j0 <= p.w));
+            batch = batch_;
+            fetch_ids(batch_ + 1);
+        };
+        // lines of keys `lane` and `lane` + 32 of the warp's group n
+        auto look_up = [&](int n) -> uint2 {
+            const unsigned u = (unsigned)kGroup * (unsigned)(warp + kWarps * n) + (unsigned)lane;
+            uint2 line = make_uint2(kNoLine, kNoLine);
+            if (n < mine && u < (unsigned)(hi - lo)) line.x = key_line(p, q, keys.at(lo + (int)u), kvh);
+            if (n < mine && u + 32u < (unsigned)(hi - lo)) line.y = key_line(p, q, keys.at(lo + (int)u + 32), kvh);
+            return line;
+        };
+        // the warp's group n into the next stage; `line`: of its keys (not kRun)
+        auto issue = [&](int n, const uint2 &line) {
+            if (n < mine) {
+                if constexpr (kRun) {
+                    if ((n & 7) == 0) take_ids(n >> 3);
+                    const uint32_t have = there >> (4 * (n & 7)) & 15u;
+                    const uint32_t ln = __shfl_sync(0xffffffffu, lines, 4 * (n & 7) + copy_half);
+                    uint64_t *bar = &sbar[warp][to_fill];
+                    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * (S::kStage / 4));
+                    __syncwarp();
+                    if (lane < 16 && (have >> copy_half & 1u))
+                        bulk_load(copy_to + to_fill * S::kStage, copy_from + (unsigned long long)ln * copy_unit, 16 * copy_unit, bar);
+                } else {
+                    const uint2 have = make_uint2(__ballot_sync(0xffffffffu, line.x != kNoLine), __ballot_sync(0xffffffffu, line.y != kNoLine));
+                    if (lane == 0) sok[warp][to_fill] = have;
+                    const uint32_t at = ring_s + to_fill * S::kStage, to = at + lane * 16;
 #pragma unroll
-            for (int i = 0; i < kKeys / kPer; ++i) {
-                const uint32_t ln = __shfl_sync(0xffffffffu, line, i * kPer + lane / kChunks);
-                const uint32_t bytes = ln != kNoLine ? 16u : 0u;
-                const unsigned long long from = (unsigned long long)(ln != kNoLine ? ln : 0u) * S::kLine;
-                cp_async16(to + i * kPer * S::kLine, GPN(p.bnd, kbase + from, 16), bytes);
-                cp_async16(to + i * kPer * S::kLine + S::kCodes, GPN(p.bnd, vbase + from, 16), bytes);
+                    for (int i = 0; i < kGroup / kPer; ++i) {
+                        const uint32_t ln = __shfl_sync(0xffffffffu, i * kPer < 32 ? line.x : line.y, (i * kPer & 31) + lane / kChunks);
+                        const uint32_t bytes = ln != kNoLine ? 16u : 0u;
+                        const unsigned long long from = (unsigned long long)(ln != kNoLine ? ln : 0u) * S::kLine + lane % kChunks * 16;
+                        cp_async16(to + i * kPer * S::kLine, GPN(p.bnd, reinterpret_cast<const char *>(p.Kc) + from, 16), bytes);
+                        cp_async16(to + i * kPer * S::kLine + S::kCodes, GPN(p.bnd, reinterpret_cast<const char *>(p.Vc) + from, 16), bytes);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t ln = i ? line.y : line.x, bytes = ln != kNoLine ? (uint32_t)S::kScale : 0u;
+                        const unsigned long long from = (unsigned long long)(ln != kNoLine ? ln : 0u) * S::kScale;
+                        const uint32_t sc = at + 2 * S::kCodes + (32 * i + lane) * S::kScale;
+                        cp_async_small<S::kScale>(sc, GPN(p.bnd, reinterpret_cast<const char *>(p.Ks) + from, S::kScale), bytes);
+                        cp_async_small<S::kScale>(sc + S::kScales, GPN(p.bnd, reinterpret_cast<const char *>(p.Vs) + from, S::kScale), bytes);
+                    }
+                }
+                to_fill = to_fill + 1 == S::kStages ? 0 : to_fill + 1;
             }
-            const uint32_t bytes = line != kNoLine ? (uint32_t)S::kScale : 0u;
-            const unsigned long long from = (unsigned long long)(line != kNoLine ? line : 0u) * S::kScale;
-            const uint32_t sc = at + 2 * S::kCodes + lane * S::kScale;
-            cp_async_small<S::kScale>(sc, GPN(p.bnd, reinterpret_cast<const char *>(p.Ks) + from, S::kScale), bytes);
-            cp_async_small<S::kScale>(sc + S::kScales, GPN(p.bnd, reinterpret_cast<const char *>(p.Vs) + from, S::kScale), bytes);
+            if constexpr (!kRun) cp_commit();
         };
 
         // fill the ring; the lines of the stage after it are looked up meanwhile
-        uint32_t first[S::kStages];
+        uint2 next = make_uint2(kNoLine, kNoLine);
+        if constexpr (kRun) {
+            fetch_ids(0);
 #pragma unroll
-        for (int s = 0; s < S::kStages; ++s) first[s] = look_up(s);
+            for (int s = 0; s < S::kStages - 1; ++s) issue(s, next);
+        } else {
+            uint2 first[S::kStages];
 #pragma unroll
-        for (int s = 0; s < S::kStages - 1; ++s) {
-            if (s < mine) load(s, first[s]);
-            cp_commit();
+            for (int s = 0; s < S::kStages; ++s) first[s] = look_up(s);
+#pragma unroll
+            for (int s = 0; s < S::kStages - 1; ++s) issue(s, first[s]);
+            next = first[S::kStages - 1];
         }
-        uint32_t next = first[S::kStages - 1];
 
         // Q of the tile as B operands: row 8 n + g, in the k order of a lane's words (8 w +
         // {2 e, 2 e + 4}, {2 e + 1, 2 e + 5} of its channels in step 2 w + e)
-        uint32_t qb[kN][kSteps][2];
+        uint32_t qb[N][kSteps][2];
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
+        for (int n = 0; n < N; ++n) {
             const int rr = 8 * n + g;
             const bool live = rr < nrows;
             const int row = row0 + (live ? rr : 0), a = row / p.group, hh = kvh * p.group + row - a * p.group;
@@ -255,18 +363,11 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
                 }
             }
         }
-        // positions of this lane's rows (row 8 n + 2 t4 + e)
-        int pos[kN][2];
-#pragma unroll
-        for (int n = 0; n < kN; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) pos[n][e] = q.i0 + (row0 + min(8 * n + 2 * t4 + e, nrows - 1)) / p.group;
-        const int pos_lo = q.i0 + a_lo, pos_hi = q.i0 + a_hi;
 
         // O^T: channels kTiles g' .. of row 2 t4 + e: o[n][i][e] is channel 2 i, o[n][i][2 + e] 2 i + 1
-        float o[kN][kTiles][4], m[kN][2], l[kN][2];
+        float o[N][kTiles][4], m[N][2], l[N][2];
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
+        for (int n = 0; n < N; ++n) {
 #pragma unroll
             for (int d = 0; d < kTiles; ++d)
 #pragma unroll
@@ -275,181 +376,241 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
             l[n][0] = l[n][1] = 0.f;
         }
 
-        int stage = 0;
         for (int n_it = 0; n_it < mine; ++n_it) {
             // the ring's free stage takes group n_it + kStages - 1
-            const uint32_t ahead = look_up(n_it + S::kStages);
-            if (n_it + S::kStages - 1 < mine) load(stage == 0 ? S::kStages - 1 : stage - 1, next);
-            cp_commit();
+            uint2 ahead = make_uint2(kNoLine, kNoLine);
+            if constexpr (!kRun) ahead = look_up(n_it + S::kStages);
+            issue(n_it + S::kStages - 1, next);
             next = ahead;
-            cp_wait<S::kStages - 1>();
-            __syncwarp();
-            const uint8_t *st = ring + stage * S::kStage;
-
-            // scores: c[n][x]: keys 16 x + slot_of(g) (e = 0, 1: rows) and + 8 (e = 2, 3)
-            float c[kN][2][4];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[n][x][e] = 0.f;
-                uint32_t w[2][kWords], s[2], b[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t *at = st + (16 * x + 8 * h) * S::kLine + k_at;
-                    if constexpr (HD == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(at);
-                        w[h][0] = v.x, w[h][1] = v.y, w[h][kWords - 2] = v.z, w[h][kWords - 1] = v.w;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(at);
-                        w[h][0] = v.x, w[h][1] = v.y;
-                    }
-                    const uint32_t sc = *reinterpret_cast<const uint16_t *>(st + (16 * x + 8 * h) * S::kScale + ks_at);
-                    s[h] = sc | sc << 16;
-                    b[h] = Two<T>::bias(s[h]);
-                }
-#pragma unroll
-                for (int k = 0; k < kWords; ++k) {
-                    uint32_t va[4], vb[4];
-                    values<T>(w[0][k], s[0], b[0], va);
-                    values<T>(w[1][k], s[1], b[1], vb);
-#pragma unroll
-                    for (int n = 0; n < kN; ++n) {
-                        mma16816<T>(c[n][x], va[0], vb[0], va[1], vb[1], qb[n][2 * k][0], qb[n][2 * k][1]);
-                        mma16816<T>(c[n][x], va[2], vb[2], va[3], vb[3], qb[n][2 * k + 1][0], qb[n][2 * k + 1][1]);
-                    }
-                }
+            const uint8_t *stage = ring + to_read * S::kStage;
+            // which of the group's halves (not kRun: keys) are there; halves that every row attends to
+            uint32_t there4 = 0, full4 = 0;
+            uint2 there64 = make_uint2(0u, 0u);
+            if constexpr (kRun) {
+                const bool now = n_it >> 3 == batch;
+                there4 = (now ? there : there_before) >> (4 * (n_it & 7)) & 15u;
+                full4 = (now ? full : full_before) >> (4 * (n_it & 7)) & 15u;
+                waiter.wait(&sbar[warp][to_read], phase);
+            } else {
+                cp_wait<S::kStages - 1>();
+                __syncwarp();
+                there64 = sok[warp][to_read];
             }
-            // which of the group's keys each row attends to
-            const int u0 = lo + kKeys * (warp + kWarps * n_it);
-            const uint32_t ok = sok[warp][stage];
-            const int j_lo = keys.at(u0), j_hi = keys.at(u0 + kKeys - 1);
-            const bool all = ok == 0xffffffffu && j_hi <= pos_lo && (j_hi < p.n_sink || (long long)pos_hi - j_lo <= (long long)p.w * p.stride);
-            if (!all) {
+            if (++to_read == S::kStages) {
+                to_read = 0;
+                phase ^= 1u;
+            }
+
+            // kX blocks of 16 keys at a time: all four for 8 rows (more products in flight),
+            // two for 16 (registers)
+            constexpr int kX = N == 1 ? 4 : 2;
+#pragma unroll 1
+            for (int x0 = 0; x0 < 4; x0 += kX) {
+                const int u0 = lo + kUnit * (warp + kWarps * n_it) + x0 * (kUnit / 4);
+                const uint8_t *st = stage + x0 * 16 * S::kLine, *sc = stage + 2 * S::kCodes + x0 * 16 * S::kScale;
+                uint32_t ok[kX / 2];                       // which keys are there, 32 at a time
+                bool all;
+                if constexpr (kRun) {
+                    const uint32_t have = there4 >> x0 & ((1u << kX) - 1u);
+                    if (have == 0u) break;
+                    all = (full4 >> x0 & ((1u << kX) - 1u)) == (1u << kX) - 1u;
+                    if (!all) {
+                        // scales of the values that no row attends to: 0, whatever is there
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                        for (int i = 0; i < kX / 2; ++i) {
+                            const int x = 2 * i + (lane >> 4);
+                            const bool here = (have >> x & 1u) && halves.has(halves.at(u0 + x) + (lane & 15));
+                            ok[i] = __ballot_sync(0xffffffffu, here);
+                            if (!here) {
+                                uint8_t *zero = const_cast<uint8_t *>(sc) + S::kScales + (32 * i + lane) * S::kScale;
+                                if constexpr (HD == 128) *reinterpret_cast<uint2 *>(zero) = make_uint2(0u, 0u);
+                                else *reinterpret_cast<uint32_t *>(zero) = 0u;
+                            }
+                        }
+                        fence_proxy_async_smem();          // (before the stage's next copies)
+                        __syncwarp();
+                    }
+                } else {
+                    if (kX == 4) ok[0] = there64.x, ok[kX / 2 - 1] = there64.y;
+                    else ok[0] = x0 ? there64.y : there64.x;
+                    uint32_t every = ok[0];
+                    if (kX == 4) every &= ok[kX / 2 - 1];
+                    const int j_lo = keys.at(u0), j_hi = keys.at(u0 + 16 * kX - 1);
+                    all = every == 0xffffffffu && j_hi <= pos_lo && (j_hi < p.n_sink || (long long)pos_hi - j_lo <= (long long)p.w * p.stride);
+                }
+
+                // scores: c[n][x]: keys 16 x + slot_of(g) (e = 0, 1: rows) and + 8 (e = 2, 3)
+                float c[N][kX][4];
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int x = 0; x < kX; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[n][x][e] = 0.f;
+                uint32_t w[kX][2][kWords], s[kX][2], b[kX][2];
+#pragma unroll
+                for (int x = 0; x < kX; ++x)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int slot = 16 * x + 8 * h + k_slot, j = keys.at(u0 + slot);
-                        const bool here = (ok >> slot) & 1u;
-#pragma unroll
-                        for (int n = 0; n < kN; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (!(here && attends(p, pos[n][e], j))) c[n][x][2 * h + e] = -INFINITY;
+                        const uint8_t *at = st + (16 * x + 8 * h) * S::kLine + k_at;
+                        if constexpr (HD == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(at);
+                            w[x][h][0] = v.x, w[x][h][1] = v.y, w[x][h][kWords - 2] = v.z, w[x][h][kWords - 1] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                            w[x][h][0] = v.x, w[x][h][1] = v.y;
+                        }
+                        const uint32_t one = *reinterpret_cast<const uint16_t *>(sc + (16 * x + 8 * h) * S::kScale + ks_at);
+                        s[x][h] = __byte_perm(one, one, 0x1010);
+                        b[x][h] = bias_of<T>(s[x][h]);
                     }
-            }
-            float best[kN][2];
-            bool up = false;
 #pragma unroll
-            for (int n = 0; n < kN; ++n)
+                for (int k = 0; k < kWords; ++k)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    best[n][e] = fmaxf(max3(c[n][0][e], c[n][0][2 + e], c[n][1][e]), c[n][1][2 + e]) * scale;
-                    up |= best[n][e] > m[n][e] + kSlack;
+                    for (int x = 0; x < kX; ++x) {
+                        uint32_t va[4], vb[4];
+                        values<T>(w[x][0][k], s[x][0], b[x][0], masks, va);
+                        values<T>(w[x][1][k], s[x][1], b[x][1], masks, vb);
+#pragma unroll
+                        for (int n = 0; n < N; ++n) mma16816<T>(c[n][x], va[0], vb[0], va[1], vb[1], qb[n][2 * k][0], qb[n][2 * k][1]);
+#pragma unroll
+                        for (int n = 0; n < N; ++n) mma16816<T>(c[n][x], va[2], vb[2], va[3], vb[3], qb[n][2 * k + 1][0], qb[n][2 * k + 1][1]);
+                    }
+                if (!all) {
+                    __syncwarp();                          // (a branch: predicated, this costs every group 70 instructions)
+                    // positions of this lane's rows (row 8 n + 2 t4 + e)
+                    int pos[N][2];
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) pos[n][e] = q.i0 + (row0 + min(8 * n + 2 * t4 + e, nrows - 1)) / p.group;
+#pragma unroll
+                    for (int x = 0; x < kX; ++x)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int slot = 16 * x + 8 * h + k_slot;
+                            const int j = kRun ? halves.at(u0 + x) + 8 * h + k_slot : keys.at(u0 + slot);
+                            const bool here = (ok[x / 2] >> (slot & 31)) & 1u;
+#pragma unroll
+                            for (int n = 0; n < N; ++n)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (!(here && attends(p, pos[n][e], j))) c[n][x][2 * h + e] = -INFINITY;
+                        }
                 }
-            if (__any_sync(0xffffffffu, up)) {   // raise the maxima, scale what was summed so far
+                float best[N][2];
+                bool up = false;
 #pragma unroll
-                for (int n = 0; n < kN; ++n)
+                for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = best[n][e];
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float mn = fmaxf(m[n][e], mx);
-                        const float f = m[n][e] == -INFINITY ? 0.f : ex2(m[n][e] - mn);
-                        m[n][e] = mn;
-                        l[n][e] *= f;
+                        float mx = c[n][0][e];
 #pragma unroll
-                        for (int d = 0; d < kTiles; ++d) {
-                            o[n][d][e] *= f;
-                            o[n][d][2 + e] *= f;
+                        for (int x = 0; x < kX; ++x) mx = x == 0 ? fmaxf(mx, c[n][0][2 + e]) : max3(mx, c[n][x][e], c[n][x][2 + e]);
+                        best[n][e] = mx * scale;
+                        up |= best[n][e] > m[n][e] + kSlack;
+                    }
+                if (__any_sync(0xffffffffu, up)) {   // raise the maxima, scale what was summed so far
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float mx = best[n][e];
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                            const float mn = fmaxf(m[n][e], mx);
+                            const float f = m[n][e] == -INFINITY ? 0.f : ex2(m[n][e] - mn);
+                            m[n][e] = mn;
+                            l[n][e] *= f;
+#pragma unroll
+                            for (int d = 0; d < kTiles; ++d) {
+                                o[n][d][e] *= f;
+                                o[n][d][2 + e] *= f;
+                            }
                         }
-                    }
-            }
-            // weights, as B operands: keys 2 t4, 2 t4 + 1 (rows of the first product) of row g
-            uint32_t pb[kN][2][2];
+                }
+                // weights, as B operands: keys 2 t4, 2 t4 + 1 (rows of the first product) of row g
+                uint32_t pb[N][kX][2];
 #pragma unroll
-            for (int n = 0; n < kN; ++n) {
-                const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+                for (int n = 0; n < N; ++n) {
+                    const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                    for (int x = 0; x < kX; ++x)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float p0 = ex2(fmaf(c[n][x][2 * h], scale, -m0)), p1 = ex2(fmaf(c[n][x][2 * h + 1], scale, -m1));
-                        l[n][0] += p0;
-                        l[n][1] += p1;
-                        pb[n][x][h] = transpose8(pack2<T>(p0, p1));
-                    }
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                // v[h]: keys 16 x + 8 h + v_even, v_odd
-                uint32_t we[2][HD / 64], wo[2][HD / 64], s[2], b[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t *at = st + (16 * x + 8 * h) * S::kLine;
-                    if constexpr (HD == 128) {
-                        const uint2 ve = *reinterpret_cast<const uint2 *>(at + ve_at), vo = *reinterpret_cast<const uint2 *>(at + vo_at);
-                        we[h][0] = ve.x, we[h][HD / 64 - 1] = ve.y;
-                        wo[h][0] = vo.x, wo[h][HD / 64 - 1] = vo.y;
-                    } else {
-                        we[h][0] = *reinterpret_cast<const uint32_t *>(at + ve_at);
-                        wo[h][0] = *reinterpret_cast<const uint32_t *>(at + vo_at);
-                    }
-                    const uint8_t *sc = st + (16 * x + 8 * h) * S::kScale;
-                    s[h] = *reinterpret_cast<const uint16_t *>(sc + ves_at) | (uint32_t)*reinterpret_cast<const uint16_t *>(sc + vos_at) << 16;
-                    b[h] = Two<T>::bias(s[h]);
+                        for (int h = 0; h < 2; ++h) {
+                            const float p0 = ex2(fmaf(c[n][x][2 * h], scale, -m0)), p1 = ex2(fmaf(c[n][x][2 * h + 1], scale, -m1));
+                            l[n][0] += p0;
+                            l[n][1] += p1;
+                            pb[n][x][h] = transpose8(pack2<T>(p0, p1));
+                        }
                 }
 #pragma unroll
-                for (int k = 0; k < HD / 64; ++k)
+                for (int x = 0; x < kX; ++x) {
+                    // keys 16 x + 8 h + v_even, v_odd
+                    uint32_t we[2][HD / 64], wo[2][HD / 64], vs[2], vb[2];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        // four channels (8 k + 4 half + 0..3 of the lane's) of two keys
-                        uint32_t va[4], vb[4];
-                        values<T>(__byte_perm(we[0][k], wo[0][k], half ? 0x7632 : 0x5410), s[0], b[0], va);
-                        values<T>(__byte_perm(we[1][k], wo[1][k], half ? 0x7632 : 0x5410), s[1], b[1], vb);
-                        const int i = 4 * k + 2 * half;
-#pragma unroll
-                        for (int n = 0; n < kN; ++n) {
-                            mma16816<T>(o[n][i], va[0], va[1], vb[0], vb[1], pb[n][x][0], pb[n][x][1]);
-                            mma16816<T>(o[n][i + 1], va[2], va[3], vb[2], vb[3], pb[n][x][0], pb[n][x][1]);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint8_t *at = st + (16 * x + 8 * h) * S::kLine;
+                        if constexpr (HD == 128) {
+                            const uint2 ve = *reinterpret_cast<const uint2 *>(at + ve_at), vo = *reinterpret_cast<const uint2 *>(at + vo_at);
+                            we[h][0] = ve.x, we[h][HD / 64 - 1] = ve.y;
+                            wo[h][0] = vo.x, wo[h][HD / 64 - 1] = vo.y;
+                        } else {
+                            we[h][0] = *reinterpret_cast<const uint32_t *>(at + ve_at);
+                            wo[h][0] = *reinterpret_cast<const uint32_t *>(at + vo_at);
                         }
+                        const uint8_t *of = sc + (16 * x + 8 * h) * S::kScale;
+                        vs[h] = __byte_perm(*reinterpret_cast<const uint16_t *>(of + ves_at), *reinterpret_cast<const uint16_t *>(of + vos_at), 0x5410);
+                        vb[h] = bias_of<T>(vs[h]);
                     }
+#pragma unroll
+                    for (int k = 0; k < HD / 64; ++k)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            // four channels (8 k + 4 half + 0..3 of the lane's) of two keys
+                            uint32_t a0[4], a1[4];
+                            values<T>(__byte_perm(we[0][k], wo[0][k], half ? 0x7632 : 0x5410), vs[0], vb[0], masks, a0);
+                            values<T>(__byte_perm(we[1][k], wo[1][k], half ? 0x7632 : 0x5410), vs[1], vb[1], masks, a1);
+                            const int i = 4 * k + 2 * half;
+#pragma unroll
+                            for (int n = 0; n < N; ++n) {
+                                mma16816<T>(o[n][i], a0[0], a0[1], a1[0], a1[1], pb[n][x][0], pb[n][x][1]);
+                                mma16816<T>(o[n][i + 1], a0[2], a0[3], a1[2], a1[3], pb[n][x][0], pb[n][x][1]);
+                            }
+                        }
+                }
             }
             __syncwarp();                        // every lane has read the stage
-            stage = stage + 1 == S::kStages ? 0 : stage + 1;
         }
-        cp_wait<0>();
+        if constexpr (!kRun) cp_wait<0>();
         __syncwarp();
 
         // join the warps: O of each into its own ring, then all threads sum
         float *mine_o = reinterpret_cast<float *>(ring);
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
+        for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float s = l[n][e];
-                s += __shfl_xor_sync(0xffffffffu, s, 4);
-                s += __shfl_xor_sync(0xffffffffu, s, 8);
-                s += __shfl_xor_sync(0xffffffffu, s, 16);
+                float sum = l[n][e];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 const int row = 8 * n + 2 * t4 + e;
-                if (g == 0) sml[warp][row] = make_float2(m[n][e], s);
+                if (g == 0) sml[warp][row] = make_float2(m[n][e], sum);
 #pragma unroll
                 for (int d = 0; d < kTiles; ++d)
                     *reinterpret_cast<float2 *>(mine_o + row * kPad + g * (HD / 8) + 2 * d) = make_float2(o[n][d][e], o[n][d][2 + e]);
             }
         __syncthreads();
-        if (threadIdx.x < kRows) {
+        if (threadIdx.x < 8 * N) {
             const int row = threadIdx.x;
             float M = -INFINITY, L = 0.f;
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w][row].x);
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = sml[w][row].x == -INFINITY ? 0.f : ex2(sml[w][row].x - M);
-                swt[w][row] = f;
-                L = fmaf(sml[w][row].y, f, L);
+            for (int w2 = 0; w2 < kWarps; ++w2) M = fmaxf(M, sml[w2][row].x);
+            for (int w2 = 0; w2 < kWarps; ++w2) {
+                const float f = sml[w2][row].x == -INFINITY ? 0.f : ex2(sml[w2][row].x - M);
+                swt[w2][row] = f;
+                L = fmaf(sml[w2][row].y, f, L);
             }
             stot[row] = make_float2(M, L);
             if (row < nrows) {
@@ -464,9 +625,9 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
             const int row = e / (HD / 4), c4 = e % (HD / 4) * 4;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = swt[w][row];
-                const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<float *>(smem + w * S::kRing) + row * kPad + c4);
+            for (int w2 = 0; w2 < kWarps; ++w2) {
+                const float f = swt[w2][row];
+                const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<float *>(smem + w2 * S::kRing) + row * kPad + c4);
                 y.x = fmaf(v.x, f, y.x);
                 y.y = fmaf(v.y, f, y.y);
                 y.z = fmaf(v.z, f, y.z);
@@ -482,7 +643,22 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
                     make_uint2(pack2<T>(y.x * inv, y.y * inv), pack2<T>(y.z * inv, y.w * inv));
             }
         }
+        if constexpr (kRun) fence_proxy_async_smem();
         __syncthreads();                         // the rings are free for the next tile
+    };
+
+    for (int tile = tile0; tile < ntiles; tile += tiles_y) {
+        int row0, nrows;
+        if constexpr (kRun) {
+            row0 = tile * kRows;
+            nrows = min(kRows, q.m * p.group - row0);
+        } else {
+            const int part = tile % per_tok;
+            row0 = tile / per_tok * p.group + part * kRows;
+            nrows = min(kRows, p.group - part * kRows);
+        }
+        if (kN == 1 || nrows <= 8) run(std::integral_constant<int, 1>{}, row0, nrows);
+        else run(std::integral_constant<int, kN>{}, row0, nrows);
     }
 }
 
@@ -632,7 +808,7 @@ __global__ void __launch_bounds__(kThreadsG, kR == 1 ? 8 : 4) k_decode4_general(
 template <typename T, int HD, int kN, int kWarps>
 cudaError_t launch_w(const DecodeArgs &a, cudaStream_t st) {
     using S = Shape4<HD, kN, kWarps>;
-    const auto fn = &k_decode4_rows<T, HD, kN, kWarps>;
+    const auto fn = a.stride == 1 ? &k_decode4_rows<T, HD, kN, kWarps, true> : &k_decode4_rows<T, HD, kN, kWarps, false>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), S::kSmem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)a.nsplit, (unsigned)(a.hk * a.row_tiles), (unsigned)a.batch);

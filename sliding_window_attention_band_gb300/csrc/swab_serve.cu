@@ -411,7 +411,7 @@ DecodePlan plan_decode4(const swab_decode_desc *d) {
         const long long tiles = (rows + p.tile_rows - 1) / p.tile_rows * (d->dilation == 0 ? 1 : d->max_q);
         blocks *= tiles;
         p.row_tiles = (int)std::min<long long>(tiles, 65535 / d->hk);
-        hold = (p.tile_rows == 8 ? 4 : 3) * kSms;
+        hold = (p.tile_rows == 8 && d->head_dim == 64 ? 4 : 3) * kSms;
         least = keys <= 256 ? 256 : 128;
     } else {
         blocks *= (group + 3) / 4;
