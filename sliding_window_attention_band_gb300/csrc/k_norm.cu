@@ -9,11 +9,14 @@
 // warp, each with 16 bytes of either member of its pairs (any two pieces where
 // the pairs are adjacent channels), so the rotation stays inside a lane and the
 // sum is log2(lanes) shuffles.  Rows whose pairs do not start on 16 bytes, or wider
-// than 32 lanes hold, go a warp a row through shared memory (kMode 2).
+// than 32 lanes hold, go a warp a row through shared memory.
 //
-// A block takes a few tokens at a time: it lists their rows and fills a table of
-// cosines and sines shared by all the heads, one buffer ahead (as k_rotary does);
-// the weights lie in shared memory as floats.
+// A warp takes a token at a time (or a slice of its heads, where there are fewer
+// tokens than warps): it makes the token's cosines and sines once, each lane keeps those
+// of its pairs in registers for all the heads, and rows are loaded some
+// steps ahead, across tokens.  No block-wide barrier, no list of rows.  (With a block a
+// tile of tokens, rows listed and tables in shared memory, the gradient of 12 x 1365
+// tokens took 48 us: every tile waited for its list, its table and its first rows.)
 //
 // 4 bits.  A group of 32 channels is four pieces of 16-bit values, so four lanes:
 // the value of largest magnitude is a maximum over the integers (bits << 1 | sign
@@ -125,33 +128,83 @@ template <typename T> __device__ __forceinline__ float scale_of(unsigned rank) {
     s = fminf(s, Scale4<T>::kMost);
     return (rank & 1u) && s != 0.f ? -s : s;
 }
-// Code of x under scale s: inv = 1 / s, or 0 (code 8) where s is 0 or NaN.
-__device__ __forceinline__ int code_of(float x, float inv) {
-    const float t = __fsub_rn(__fmaf_rn(x, inv, 768.f), 768.f);     // |x / s| < 26: a multiple of 2^-14
-    const int n = (int)(__float_as_uint(__fadd_rn(t, 12582912.f)) - 0x4b400000u);   // to the nearest, ties to even
-    return min(max(n, -8), 7) + 8;
+// Two fp32 at a time (fma.rn.f32x2 and its kin): the rows are bound by instructions
+// before they are by memory where each value is handled alone.
+template <typename T> __device__ __forceinline__ void unpack2(const uint4 &v, uint64_t (&f)[VecOf<T>::kN / 2]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(T) == 4) {
+        f[0] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        f[1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = f2(lo16<T>(w[k]), hi16<T>(w[k]));
+    }
+}
+template <typename T> __device__ __forceinline__ uint4 repack2(const uint64_t (&f)[VecOf<T>::kN / 2]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < VecOf<T>::kN / 2; ++k) {
+        float lo, hi;
+        f2split(f[k], lo, hi);
+        if constexpr (sizeof(T) == 4) w[2 * k] = __float_as_uint(lo), w[2 * k + 1] = __float_as_uint(hi);
+        else w[k] = pack2<T>(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// N pairs from shared memory
+template <int N> __device__ __forceinline__ void take2(const float *src, uint64_t (&f)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(src + 2 * k);
+            f[k] = v.x, f[k + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) f[k] = *reinterpret_cast<const unsigned long long *>(src + 2 * k);
+    }
+}
+__device__ __forceinline__ uint64_t negate2(uint64_t x) { return x ^ 0x8000000080000000ull; }
+__device__ __forceinline__ float sum2(uint64_t x) {
+    float lo, hi;
+    f2split(x, lo, hi);
+    return lo + hi;
 }
 
-// A lane's 16 bytes of a group as 16-bit values (already rounded): eight codes as a
-// word, and the group's scale.  Four adjacent lanes hold the group.
+// A lane's 16 bytes of a group of 16-bit values (already rounded): eight codes as a
+// word, and the group's scale.  Four adjacent lanes hold the group.  The rank is
+// taken on the 16 bits of two values at a time; a quotient is rounded to a multiple of
+// 2^-14 by the fma and to the nearest whole number, plus 8, by the addition (12582920 =
+// 1.5 * 2^23 + 8, even as 8 is, so that ties stay with the even quotient).
 template <typename T>
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float &s) {
-    unsigned rank = 0;
+__device__ __forceinline__ uint32_t quantise8(const uint4 &y, float &s) {
+    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+    uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) rank = max(rank, rank_of(x[k]));
+    for (int k = 0; k < 4; ++k) top = __vmaxu2(top, ((w[k] << 1) & 0xfffefffeu) | ((~w[k] >> 15) & 0x00010001u));
+    uint32_t rank = max(top & 0xffffu, top >> 16);
     rank = max(rank, __shfl_xor_sync(0xffffffffu, rank, 1));
     rank = max(rank, __shfl_xor_sync(0xffffffffu, rank, 2));
-    s = scale_of<T>(rank);
+    s = scale_of<T>((__float_as_uint(lo16<T>(rank >> 1)) << 1) | (rank & 1u));
     const bool none = !(fabsf(s) > 0.f);                             // 0 or NaN
     const float inv = none ? 0.f : __frcp_rn(s);
-    uint32_t w = 0;
+    const uint64_t by = f2(inv, inv), far = f2(768.f, 768.f), near = f2(12582920.f - 768.f, 12582920.f - 768.f);
+    uint64_t x[4];
+    unpack2<T>(y, x);
+    uint32_t u[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w |= (uint32_t)code_of(none ? 0.f : x[k], inv) << (4 * k);
-    return w;
+    for (int k = 0; k < 4; ++k) {
+        float lo, hi;
+        f2split(add2(fma2(x[k], by, far), near), lo, hi);
+        const uint32_t n = __vimin_s16x2_relu(__byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410), 0x000f000fu);   // into 0..15
+        u[k] = n | n >> 12;
+    }
+    const uint32_t codes = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    return none ? 0x88888888u : codes;
 }
 
-// 1 / sqrt(mean of squares + eps)
-__device__ __forceinline__ float inverse_norm(float sum, float hd, float eps) { return __frsqrt_rn(__fdiv_rn(sum, hd) + eps); }
+// 1 / sqrt(mean of squares + eps), within 2 ulp
+__device__ __forceinline__ float inverse_norm(float sum, float by_hd, float eps) { return rsqrtf(__fmaf_rn(sum, by_hd, eps)); }
 
 // A pair turned, rounded as k_rotary does (so that the cache holds the same bits
 // with and without norms, in either width): pieces, and pair by pair.
@@ -160,29 +213,279 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s, bool 
     a = __fmaf_rn(x, c, -__fmul_rn(b, s));
     b = by_pairs ? __fmaf_rn(b, c, __fmul_rn(x, s)) : __fmaf_rn(x, s, __fmul_rn(b, c));
 }
+// the same for two pairs (pieces)
+__device__ __forceinline__ void turn2(uint64_t &a, uint64_t &b, uint64_t c, uint64_t s) {
+    const uint64_t x = a;
+    a = fma2(x, c, negate2(mul2(b, s)));
+    b = fma2(x, s, mul2(b, c));
+}
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-// kMode: 0 = halves in 16-byte pieces, 1 = adjacent pairs in 16-byte pieces, 2 = a
-// warp a row.  kKind: 0 = Q, K -> Qo, Ko; 1 = into the cache; 2 = into the cache in
-// 4 bits (kMode 0, 1: 16-bit types, groups on four lanes).
-template <typename T, int kMode, int kKind>
-__global__ void __launch_bounds__(kThreads, kBlocks) k_norm(const __grid_constant__ NormArgs a) {
-    constexpr int kV = VecOf<T>::kN, kUnroll = 2;
+// Rows on lane groups: kInter: adjacent pairs in 16-byte pieces, else halves.  kKind: 0
+// = Q, K -> Qo, Ko; 1 = into the cache; 2 = into the cache in 4 bits (16-bit types,
+// groups on four lanes).
+constexpr int kWarps = 4;
+constexpr int kAhead = 2;            // rows of a lane group loaded ahead
+
+// This lane's two pieces of a row, and its place in the row group.
+struct Lane {
+    int sub, row, pa, pb;
+    bool active, turns;
+};
+template <bool kInter> __device__ __forceinline__ Lane lane_of(int lanes, int pieces, int turning) {
+    const int lane = threadIdx.x & 31, nturn = kInter ? 0 : turning;
+    Lane l;
+    l.sub = lane & (lanes - 1);
+    l.row = lane / lanes;
+    l.active = l.sub < pieces / 2;
+    l.pa = l.sub < nturn ? l.sub : nturn + l.sub;
+    l.pb = l.sub < nturn ? l.sub + nturn : pieces / 2 + l.sub;
+    l.turns = l.active && (kInter || l.sub < nturn);
+    return l;
+}
+// A token's cosines and sines by the warp, then those of this lane's pairs: c, s.
+template <typename T, bool kInter>
+__device__ __forceinline__ void token_turns(const RotaryArgs &p, const Lane &l, long long at, const unsigned long long *turns, float *cs,
+                                            uint64_t (&c)[VecOf<T>::kN / 2], uint64_t (&s)[VecOf<T>::kN / 2]) {
+    constexpr int kV = VecOf<T>::kN, kH = kV / 2;
+    const int half = p.rot / 2;
+    __syncwarp();                        // (the token before is done with the table)
+    for (int k = threadIdx.x & 31; k < half; k += 32) {
+        float x, y;
+        cos_sin(at, turns[k], x, y);
+        cs[k] = x * p.scale;
+        cs[half + k] = y * p.scale;
+    }
+    __syncwarp();
+    if (!l.turns) return;
+    if constexpr (kInter) {
+        // kH pairs of either piece
+        uint64_t *to[2] = {c, s};
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int k = 0; k < kH / 2; ++k) {
+                if (l.pa * kV < p.rot) to[w][k] = *reinterpret_cast<const unsigned long long *>(cs + w * half + l.pa * kH + 2 * k);
+                if (l.pb * kV < p.rot) to[w][kH / 2 + k] = *reinterpret_cast<const unsigned long long *>(cs + w * half + l.pb * kH + 2 * k);
+            }
+    } else {
+        take2<kH>(cs + l.pa * kV, c);
+        take2<kH>(cs + half + l.pa * kV, s);
+    }
+}
+// Position of token t.
+__device__ __forceinline__ long long position_of(const RotaryArgs &p, unsigned t) {
+    return (p.pos ? (long long)*GP(p.bnd, p.pos + t) : (long long)(t % p.n)) + p.pos0;
+}
+// Offset of token t in a tensor with these strides, in units of 16 bytes.
+__device__ __forceinline__ unsigned token_units(const RotaryArgs &p, unsigned t, const unsigned *s) {
+    if (p.n == p.tokens) return t * s[1];
+    const unsigned bb = t / p.n;
+    return bb * s[0] + (t - bb * p.n) * s[1];
+}
+
+template <typename T, bool kInter, int kKind>
+__global__ void __launch_bounds__(32 * kWarps, 5) k_norm(const __grid_constant__ NormArgs a) {
+    constexpr int kV = VecOf<T>::kN, kH = kV / 2;
+    constexpr unsigned kNever = 0xffffffffu;
     const RotaryArgs &p = a.r;
-    extern __shared__ __align__(16) float smem[];      // two tables [tile][2][rot / 2]; weights [2][hd]; (mode 2) a row a warp
+    extern __shared__ __align__(16) float smem[];      // turns [rot / 2]; weights [2][hd]; [rot] a warp
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, L = a.lanes, pad = (p.rot + 3) / 4 * 4;
+    const unsigned group = 32 / L, hq = p.hq, hqk = p.hq + p.hk, rows = p.rows;
+    unsigned long long *turns = reinterpret_cast<unsigned long long *>(smem);
+    float *wtab = smem + pad, *cs = wtab + 2 * p.hd + warp * pad;
+    const Lane l = lane_of<kInter>(L, p.hd / kV, p.rot / 2 / kV);
+    const float by_hd = 1.f / (float)p.hd;
+    // units of work: the `its` row groups of slice u % split of token u / split
+    const unsigned split = a.split, its = a.its, units = p.tokens * split, step = gridDim.x * kWarps;
+    unsigned u = blockIdx.x * kWarps + warp;
+
+    // A lane's row e of a token moves on by a row group at a time: its address by a
+    // fixed step until it passes `bound`, into the heads of the next tensor.
+    // The loads run kAhead row groups ahead: row le at `from`.
+    unsigned lu = u, li = 0, le = 0, lbound = 0, lstep = 0;
+    const char *from = nullptr;
+    auto aim_row = [&]() {
+        const unsigned t = lu / split;
+        const bool is_q = le < hq, is_v = kKind > 0 && le >= hqk;
+        const unsigned *s = is_q ? p.sq : is_v ? p.sv : p.sk;
+        const unsigned at = token_units(p, t, s) + (is_q ? le : is_v ? le - hqk : le - hq) * s[2];
+        from = (const char *)(is_q ? p.Q : is_v ? p.V : p.K) + (unsigned long long)at * 16u;
+        lstep = s[2] * group;
+        lbound = le >= rows || !l.active ? 0 : is_q ? hq : is_v || kKind == 0 ? rows : hqk;     // 0: no row
+    };
+    auto aim = [&]() {                                 // the loads at unit lu
+        lbound = 0;
+        if (lu >= units) return;
+        le = (lu % split) * its * group + l.row;
+        aim_row();
+    };
+    auto load = [&](uint4 &va, uint4 &vb) {
+        va = vb = make_uint4(0, 0, 0, 0);
+        if (lbound) {
+            va = load16(GPN(p.bnd, from + l.pa * 16, 16));
+            vb = load16(GPN(p.bnd, from + l.pb * 16, 16));
+            le += group;
+            from += (unsigned long long)lstep * 16u;
+            if (le >= lbound) aim_row();
+        }
+        if (++li == its) {
+            li = 0;
+            lu += step;
+            aim();
+        }
+    };
+
+    pdl_wait();
+    pdl_trigger();
+    uint4 va[kAhead], vb[kAhead];
+    aim();
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load(va[k], vb[k]);
+    long long at = u < units ? position_of(p, u / split) : 0;
+    int slot = kKind > 0 && u < units ? *GP(p.bnd, p.slots + u / split) : -1;
+    for (int k = threadIdx.x; k < p.rot / 2; k += 32 * kWarps) turns[k] = *GP(p.bnd, p.turns + k);
+    for (int c = threadIdx.x; c < 2 * p.hd; c += 32 * kWarps) {
+        const T *w = reinterpret_cast<const T *>(c < p.hd ? a.wq : a.wk);
+        wtab[c] = w ? Elt<T>::to_f(*GP(p.bnd, w + (c < p.hd ? c : c - p.hd))) + a.offset : 1.f;
+    }
+    __syncthreads();
+
+    for (; u < units; u += step) {
+        const unsigned t = u / split;
+        unsigned e = (u - t * split) * its * group + l.row;
+        uint64_t c[kH], s[kH];
+        token_turns<T, kInter>(p, l, at, turns, cs, c, s);
+        const int here = slot;
+        if (u + step < units) {
+            at = position_of(p, (u + step) / split);
+            if (kKind > 0) slot = *GP(p.bnd, p.slots + (u + step) / split);
+        }
+        const bool kept = kKind == 0 || (here >= 0 && here < p.n_slots);
+        if (kKind > 0 && !kept && here != -1 && lane == 0) atomicOr(p.err, kErrInvalid);
+
+        // the same for what is written: row e to `dst` (4 bits: its codes), scales to `sc`
+        unsigned bound = 0;
+        char *dst = nullptr;
+        unsigned long long dstep = 0;
+        T *sc = nullptr;
+        auto aim_out = [&]() {
+            bound = kNever;                            // (rows past the last one move nowhere)
+            if (e >= rows) return;
+            const bool is_q = e < hq, is_v = kKind > 0 && e >= hqk;
+            bound = is_q ? hq : is_v || kKind == 0 ? rows : hqk;
+            if (is_q || kKind == 0) {
+                const unsigned *so = is_q ? p.sqo : p.sko;
+                dst = (char *)(is_q ? p.Qo : p.Ko) + (unsigned long long)(token_units(p, t, so) + (is_q ? e : e - hq) * so[2]) * 16u;
+                dstep = (unsigned long long)(so[2] * group) * 16u;
+            } else {
+                const unsigned blk = (unsigned)here >> p.page_log2, off = (unsigned)here & ((1u << p.page_log2) - 1u), head = e - (is_v ? hqk : hq);
+                const unsigned long long line = ((blk * (unsigned)p.hk + head) << p.page_log2) + off;     // below 2^32
+                const unsigned width = kKind == 2 ? p.hd / 2 : p.row_bytes;
+                dst = (char *)(is_v ? p.Vc : p.Kc) + line * width;
+                dstep = (unsigned long long)(group << p.page_log2) * width;
+                if (kKind == 2) sc = (T *)(is_v ? a.Vs : a.Ks) + line * (p.hd / kGroup4);
+            }
+        };
+        aim_out();
+
+        for (unsigned i = 0; i < its; ++i) {
+            const bool there = e < rows && l.active, is_q = e < hq, as_is = kKind > 0 && e >= hqk;
+            const uint4 xa = va[0], xb = vb[0];
+#pragma unroll
+            for (int m = 0; m + 1 < kAhead; ++m) va[m] = va[m + 1], vb[m] = vb[m + 1];
+            load(va[kAhead - 1], vb[kAhead - 1]);
+            uint64_t fa[kH], fb[kH];
+            unpack2<T>(xa, fa);
+            unpack2<T>(xb, fb);
+            if (a.norm) {
+                uint64_t squares = 0;
+#pragma unroll
+                for (int m = 0; m < kH; ++m) squares = fma2(fa[m], fa[m], fma2(fb[m], fb[m], squares));
+                float sum = sum2(squares);
+                for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (!as_is && l.active) {
+                    const float rn = inverse_norm(sum, by_hd, a.eps);
+                    const uint64_t rn2 = f2(rn, rn);
+                    const float *w = wtab + (is_q ? 0 : p.hd);
+                    uint64_t v[kH];
+                    take2<kH>(w + l.pa * kV, v);
+#pragma unroll
+                    for (int m = 0; m < kH; ++m) fa[m] = mul2(fa[m], mul2(rn2, v[m]));
+                    take2<kH>(w + l.pb * kV, v);
+#pragma unroll
+                    for (int m = 0; m < kH; ++m) fb[m] = mul2(fb[m], mul2(rn2, v[m]));
+                }
+            }
+            if (l.turns && !as_is) {
+                if constexpr (kInter) {
+                    auto turn_piece = [&](uint64_t (&f)[kH], int piece, int first) {
+                        if (piece * kV >= p.rot) return;
+#pragma unroll
+                        for (int m = 0; m < kH; ++m) {
+                            float x, y, c0, c1, s0, s1;
+                            f2split(f[m], x, y);
+                            f2split(c[first + m / 2], c0, c1);
+                            f2split(s[first + m / 2], s0, s1);
+                            turn(x, y, m & 1 ? c1 : c0, m & 1 ? s1 : s0);
+                            f[m] = f2(x, y);
+                        }
+                    };
+                    turn_piece(fa, l.pa, 0);
+                    turn_piece(fb, l.pb, kH / 2);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < kH; ++m) turn2(fa[m], fb[m], c[m], s[m]);
+                }
+            }
+            const uint4 ya = as_is ? xa : repack2<T>(fa), yb = as_is ? xb : repack2<T>(fb);
+            bool whole = there && (is_q || kept);      // a row of the tensors' type to write
+            if constexpr (kKind == 2 && sizeof(T) == 2) {
+                if (__any_sync(0xffffffffu, there && !is_q)) {
+                    float s0, s1;                      // (ya, yb: as the cache of this type would hold them)
+                    const uint32_t wa = quantise8<T>(ya, s0), wb = quantise8<T>(yb, s1);
+                    if (there && !is_q && kept) {
+                        *reinterpret_cast<uint32_t *>(GPN(p.bnd, dst + l.pa * 4, 4)) = wa;
+                        *reinterpret_cast<uint32_t *>(GPN(p.bnd, dst + l.pb * 4, 4)) = wb;
+                        if ((l.sub & 3) == 0) {
+                            *GP(p.bnd, sc + l.pa / 4) = Elt<T>::from_f(s0);
+                            *GP(p.bnd, sc + l.pb / 4) = Elt<T>::from_f(s1);
+                        }
+                    }
+                    sc += (unsigned long long)(group << p.page_log2) * (p.hd / kGroup4);
+                }
+                whole = there && is_q;
+            }
+            if (whole) {
+                *reinterpret_cast<uint4 *>(GPN(p.bnd, dst + l.pa * 16, 16)) = ya;
+                *reinterpret_cast<uint4 *>(GPN(p.bnd, dst + l.pb * 16, 16)) = yb;
+            }
+            e += group;
+            dst += dstep;
+            if (e >= bound) aim_out();
+        }
+    }
+}
+
+// The rows that do not lie on lane groups: a warp a row, through shared memory.  A block
+// takes a few tokens at a time: it lists their rows and fills a table of cosines and
+// sines shared by all the heads, one buffer ahead.
+template <typename T, int kKind>
+__global__ void __launch_bounds__(kThreads, kBlocks) k_norm_rows(const __grid_constant__ NormArgs a) {
+    constexpr int kV = VecOf<T>::kN;
+    const RotaryArgs &p = a.r;
+    const float by_hd = 1.f / (float)p.hd;
+    extern __shared__ __align__(16) float smem[];      // two tables [tile][2][rot / 2]; weights [2][hd]; a row a warp
     __shared__ Row lists[2][kMaxRows];
     const int half = p.rot / 2;
     float *wtab = smem + 2 * p.tile * p.rot;
     const int lo = (int)((long long)p.rows * blockIdx.y / gridDim.y), mine = (int)((long long)p.rows * (blockIdx.y + 1) / gridDim.y) - lo;
     const unsigned by_mine = 0xffffffffu / mine + 1u, by_half = half > 1 ? 0xffffffffu / half + 1u : 0u;   // x / mine, x / half for x < 2^15
 
-    // the lanes of a row and this lane's two pieces of it
-    const int L = a.lanes, sub = threadIdx.x & (L - 1), q0 = threadIdx.x / L, per_pass = kThreads / L;
-    const int pieces = p.hd / kV, nturn = kMode == 0 ? half / kV : 0;
-    const bool active = sub < pieces / 2;
-    const int pa = sub < nturn ? sub : nturn + sub, pb = sub < nturn ? sub + nturn : pieces / 2 + sub;
+    const int pieces = p.hd / kV, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float *x = wtab + 2 * p.hd + warp * p.hd;
 
     // the rows and the table of the tile at token t0
     auto prepare = [&](long long t0, Row *list, float *tab) {
@@ -215,162 +518,72 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(const __grid_constan
         const Row *list = lists[buf];
         const float *tab = smem + buf * p.tile * p.rot;
         __syncthreads();                 // this tile is prepared, the other buffer is free
-        if constexpr (kMode < 2) {
-            Row r[kUnroll];
-            uint4 va[kUnroll], vb[kUnroll];
-            auto fetch = [&](int q) {
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int e = q + q0 + u * per_pass;
-                    r[u].s = r[u].d = 0;
-                    va[u] = vb[u] = make_uint4(0, 0, 0, 0);
-                    if (e < total) r[u] = list[e];
-                    if (!r[u].d || !active) continue;
-                    va[u] = load16(GPN(p.bnd, r[u].src() + pa * 16, 16));
-                    vb[u] = load16(GPN(p.bnd, r[u].src() + pb * 16, 16));
-                }
-            };
-            // the next tile is prepared under this one's first loads
-            fetch(0);
-            if (t0 + step < p.tokens) prepare(t0 + step, lists[buf ^ 1], smem + (buf ^ 1) * p.tile * p.rot);
-            for (int q = 0; q < total; q += kUnroll * per_pass) {
-                if (q > 0) fetch(q);
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int kind = r[u].kind();
-                    float fa[kV], fb[kV];
-                    unpack16<T>(va[u], fa);
-                    unpack16<T>(vb[u], fb);
-                    if (a.norm) {
-                        float sum = 0.f;
-#pragma unroll
-                        for (int k = 0; k < kV; ++k) sum = fmaf(fa[k], fa[k], fmaf(fb[k], fb[k], sum));
-                        for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                        if (kKind == 0 || kind != kIsV) {
-                            const float rn = inverse_norm(sum, (float)p.hd, a.eps);
-                            const float *w = wtab + (kind == kIsQ ? 0 : p.hd);
-                            if (active) {
-                                float c[kV];
-                                take<kV>(w + pa * kV, c);
-#pragma unroll
-                                for (int k = 0; k < kV; ++k) fa[k] *= rn * c[k];
-                                take<kV>(w + pb * kV, c);
-#pragma unroll
-                                for (int k = 0; k < kV; ++k) fb[k] *= rn * c[k];
+        if (t0 + step < p.tokens) prepare(t0 + step, lists[buf ^ 1], smem + (buf ^ 1) * p.tile * p.rot);
+        for (int e = warp; e < total; e += kThreads / 32) {
+            const Row r = list[e];
+            if (!r.d) continue;
+            const int kind = r.kind();
+            const T *src = reinterpret_cast<const T *>(r.src());
+            for (int c = lane; c < p.hd; c += 32) x[c] = Elt<T>::to_f(*GP(p.bnd, src + c));
+            if (kind != kIsV) {
+                if (a.norm) {
+                    __syncwarp();
+                    float sum = 0.f;
+                    if (a.sum_lanes) {               // in the order of the lanes that own pieces
+                        const int na = a.sum_turn, la = lane < na ? lane : na + lane, lb = lane < na ? lane + na : pieces / 2 + lane;
+                        if (lane < pieces / 2) {
+                            float odd = 0.f;
+                            for (int k = 0; k < kV; k += 2) {
+                                const float *xa = x + la * kV + k, *xb = x + lb * kV + k;
+                                sum = __fmaf_rn(xa[0], xa[0], __fmaf_rn(xb[0], xb[0], sum));
+                                odd = __fmaf_rn(xa[1], xa[1], __fmaf_rn(xb[1], xb[1], odd));
                             }
+                            sum += odd;
                         }
-                    }
-                    if (active && (kKind == 0 || kind != kIsV)) {
-                        const float *cs = tab + 2 * r[u].token() * half;
-                        if constexpr (kMode == 0) {
-                            if (sub < nturn) {
-                                float c[kV], s[kV];
-                                take<kV>(cs + pa * kV, c);
-                                take<kV>(cs + half + pa * kV, s);
+                        for (int d = a.sum_lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                        sum = __shfl_sync(0xffffffffu, sum, 0);
+                    } else {
+                        for (int c = lane; c < p.hd; c += 32) sum = fmaf(x[c], x[c], sum);
 #pragma unroll
-                                for (int k = 0; k < kV; ++k) turn(fa[k], fb[k], c[k], s[k]);
-                            }
-                        } else {
-                            auto turn_piece = [&](float (&f)[kV], int piece) {
-                                if (piece * kV >= p.rot) return;
-                                float c[kV / 2], s[kV / 2];
-                                take<kV / 2>(cs + piece * (kV / 2), c);
-                                take<kV / 2>(cs + half + piece * (kV / 2), s);
-#pragma unroll
-                                for (int k = 0; k < kV / 2; ++k) turn(f[2 * k], f[2 * k + 1], c[k], s[k]);
-                            };
-                            turn_piece(fa, pa);
-                            turn_piece(fb, pb);
-                        }
-                    }
-                    const uint4 ya = pack16<T>(fa), yb = pack16<T>(fb);
-                    if constexpr (kKind == 2 && sizeof(T) == 2) {
-                        if (__any_sync(0xffffffffu, kind >= kIsK)) {
-                            float s0, s1;
-                            unpack16<T>(ya, fa);                     // as the cache of this type would hold them
-                            unpack16<T>(yb, fb);
-                            const uint32_t wa = quantise8<T>(fa, s0), wb = quantise8<T>(fb, s1);
-                            if (kind >= kIsK && active) {
-                                const unsigned long long line = r[u].line();
-                                char *codes = (char *)(kind == kIsV ? p.Vc : p.Kc) + line * (p.hd / 2);
-                                T *sc = (T *)(kind == kIsV ? a.Vs : a.Ks) + line * (p.hd / kGroup4);
-                                *reinterpret_cast<uint32_t *>(GPN(p.bnd, codes + pa * 4, 4)) = wa;
-                                *reinterpret_cast<uint32_t *>(GPN(p.bnd, codes + pb * 4, 4)) = wb;
-                                if ((sub & 3) == 0) {
-                                    *GP(p.bnd, sc + pa / 4) = Elt<T>::from_f(s0);
-                                    *GP(p.bnd, sc + pb / 4) = Elt<T>::from_f(s1);
-                                }
-                            }
-                        }
-                    }
-                    if (!r[u].d || !active || (kKind == 2 && kind != kIsQ)) continue;
-                    *reinterpret_cast<uint4 *>(GPN(p.bnd, r[u].dst() + pa * 16, 16)) = ya;
-                    *reinterpret_cast<uint4 *>(GPN(p.bnd, r[u].dst() + pb * 16, 16)) = yb;
-                }
-            }
-        } else {
-            if (t0 + step < p.tokens) prepare(t0 + step, lists[buf ^ 1], smem + (buf ^ 1) * p.tile * p.rot);
-            const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-            float *x = wtab + 2 * p.hd + warp * p.hd;
-            for (int e = warp; e < total; e += kThreads / 32) {
-                const Row r = list[e];
-                if (!r.d) continue;
-                const int kind = r.kind();
-                const T *src = reinterpret_cast<const T *>(r.src());
-                for (int c = lane; c < p.hd; c += 32) x[c] = Elt<T>::to_f(*GP(p.bnd, src + c));
-                if (kind != kIsV) {
-                    if (a.norm) {
-                        __syncwarp();
-                        float sum = 0.f;
-                        if (a.sum_lanes) {               // in the order of the lanes that own pieces
-                            const int na = a.sum_turn, la = lane < na ? lane : na + lane, lb = lane < na ? lane + na : pieces / 2 + lane;
-                            if (lane < pieces / 2)
-                                for (int k = 0; k < kV; ++k) sum = fmaf(x[la * kV + k], x[la * kV + k], fmaf(x[lb * kV + k], x[lb * kV + k], sum));
-                            for (int d = a.sum_lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                            sum = __shfl_sync(0xffffffffu, sum, 0);
-                        } else {
-                            for (int c = lane; c < p.hd; c += 32) sum = fmaf(x[c], x[c], sum);
-#pragma unroll
-                            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                        }
-                        __syncwarp();
-                        const float rn = inverse_norm(sum, (float)p.hd, a.eps);
-                        const float *w = wtab + (kind == kIsQ ? 0 : p.hd);
-                        for (int c = lane; c < p.hd; c += 32) x[c] *= rn * w[c];
+                        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                     }
                     __syncwarp();
-                    const float *cs = tab + 2 * r.token() * half;
-                    for (int k = lane; k < half; k += 32) {
-                        const int one = p.interleaved ? 2 * k : k, two = p.interleaved ? 2 * k + 1 : k + half;
-                        float xa = x[one], xb = x[two];
-                        turn(xa, xb, cs[k], cs[half + k], a.by_pairs);
-                        x[one] = xa;
-                        x[two] = xb;
-                    }
+                    const float rn = inverse_norm(sum, by_hd, a.eps);
+                    const float *w = wtab + (kind == kIsQ ? 0 : p.hd);
+                    for (int c = lane; c < p.hd; c += 32) x[c] *= rn * w[c];
                 }
                 __syncwarp();
-                if (kKind == 2 && kind != kIsQ) {
-                    const unsigned long long line = r.line();
-                    char *codes = (char *)(kind == kIsV ? p.Vc : p.Kc) + line * (p.hd / 2);
-                    T *sc = (T *)(kind == kIsV ? a.Vs : a.Ks) + line * (p.hd / kGroup4);
-                    for (int g = 0; g < p.hd / kGroup4; ++g) {       // a lane a channel
-                        const float f = Elt<T>::to_f(Elt<T>::from_f(x[g * kGroup4 + lane]));
-                        const float s = scale_of<T>(__reduce_max_sync(0xffffffffu, rank_of(f)));
-                        // (fp32 quotients have ties of their own: divided as they are)
-                        const float y = fabsf(s) > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(f, s)), -8.f), 7.f) : 0.f;
-                        uint32_t w = (uint32_t)((int)y + 8) << (4 * (lane & 7));
-                        w |= __shfl_xor_sync(0xffffffffu, w, 1);
-                        w |= __shfl_xor_sync(0xffffffffu, w, 2);
-                        w |= __shfl_xor_sync(0xffffffffu, w, 4);
-                        if ((lane & 7) == 0) *reinterpret_cast<uint32_t *>(GPN(p.bnd, codes + g * 16 + lane / 2, 4)) = w;
-                        if (lane == 0) *GP(p.bnd, sc + g) = Elt<T>::from_f(s);
-                    }
-                } else {
-                    T *dst = reinterpret_cast<T *>(r.dst());
-                    for (int c = lane; c < p.hd; c += 32) *GP(p.bnd, dst + c) = Elt<T>::from_f(x[c]);
+                const float *cs = tab + 2 * r.token() * half;
+                for (int k = lane; k < half; k += 32) {
+                    const int one = p.interleaved ? 2 * k : k, two = p.interleaved ? 2 * k + 1 : k + half;
+                    float xa = x[one], xb = x[two];
+                    turn(xa, xb, cs[k], cs[half + k], a.by_pairs);
+                    x[one] = xa;
+                    x[two] = xb;
                 }
-                __syncwarp();
             }
+            __syncwarp();
+            if (kKind == 2 && kind != kIsQ) {
+                const unsigned long long line = r.line();
+                char *codes = (char *)(kind == kIsV ? p.Vc : p.Kc) + line * (p.hd / 2);
+                T *sc = (T *)(kind == kIsV ? a.Vs : a.Ks) + line * (p.hd / kGroup4);
+                for (int g = 0; g < p.hd / kGroup4; ++g) {       // a lane a channel
+                    const float f = Elt<T>::to_f(Elt<T>::from_f(x[g * kGroup4 + lane]));
+                    const float s = scale_of<T>(__reduce_max_sync(0xffffffffu, rank_of(f)));
+                    // (fp32 quotients have ties of their own: divided as they are)
+                    const float y = fabsf(s) > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(f, s)), -8.f), 7.f) : 0.f;
+                    uint32_t w = (uint32_t)((int)y + 8) << (4 * (lane & 7));
+                    w |= __shfl_xor_sync(0xffffffffu, w, 1);
+                    w |= __shfl_xor_sync(0xffffffffu, w, 2);
+                    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+                    if ((lane & 7) == 0) *reinterpret_cast<uint32_t *>(GPN(p.bnd, codes + g * 16 + lane / 2, 4)) = w;
+                    if (lane == 0) *GP(p.bnd, sc + g) = Elt<T>::from_f(s);
+                }
+            } else {
+                T *dst = reinterpret_cast<T *>(r.dst());
+                for (int c = lane; c < p.hd; c += 32) *GP(p.bnd, dst + c) = Elt<T>::from_f(x[c]);
+            }
+            __syncwarp();
         }
     }
 }
@@ -378,31 +591,187 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(const __grid_constan
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
+// Blocks 0 .. blocks_q - 1 take the rows of Q, the others those of K: each has the
+// weight gradient of one of them.
+constexpr int kBwdAhead = 2;
+
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(32 * kWarps, 4) k_norm_bwd(const __grid_constant__ NormArgs a) {
+    constexpr int kV = VecOf<T>::kN, kH = kV / 2;
+    const RotaryArgs &p = a.r;
+    extern __shared__ __align__(16) float smem[];      // turns [rot / 2]; [rot] a warp; sums [32 kWarps / lanes][hd]
+    const int which = blockIdx.x >= a.blocks_q, heads = which ? p.hk : p.hq;
+    const int warp = threadIdx.x >> 5, L = a.lanes, group = 32 / L, pad = (p.rot + 3) / 4 * 4;
+    unsigned long long *turns = reinterpret_cast<unsigned long long *>(smem);
+    float *cs = smem + pad + warp * pad, *sums = smem + pad + kWarps * pad;
+    const Lane l = lane_of<kInter>(L, p.hd / kV, p.rot / 2 / kV);
+    const float by_hd = 1.f / (float)p.hd;
+    const unsigned split = a.slices[which], its = a.tile[which], units = p.tokens * split;
+    const unsigned step = (which ? a.blocks - a.blocks_q : a.blocks_q) * kWarps;
+    unsigned u = (which ? blockIdx.x - a.blocks_q : blockIdx.x) * kWarps + warp;
+    const unsigned *sg = which ? p.sk : p.sq, *sx = a.sx[which], *sd = which ? p.sko : p.sqo;
+    const char *base_g = (const char *)(which ? p.K : p.Q), *base_x = (const char *)a.X[which];
+    char *base_d = (char *)(which ? p.Ko : p.Qo);
+
+    struct Raw {
+        uint4 xa, xb, ga, gb;
+    };
+    unsigned lu = u, li = 0, lrow = 0, og = 0, ox = 0;
+    auto aim = [&]() {
+        if (lu >= units) return;
+        const unsigned t = lu / split;
+        lrow = (lu - t * split) * its * group + l.row;
+        og = token_units(p, t, sg);
+        ox = token_units(p, t, sx);
+    };
+    auto load = [&](Raw &r) {
+        r.xa = r.xb = r.ga = r.gb = make_uint4(0, 0, 0, 0);
+        if (lu >= units) return;
+        const unsigned e = lrow + li * group;
+        if (e < (unsigned)heads && l.active) {
+            const char *x = base_x + (unsigned long long)(ox + e * sx[2]) * 16u, *g = base_g + (unsigned long long)(og + e * sg[2]) * 16u;
+            r.xa = load16(GPN(p.bnd, x + l.pa * 16, 16));
+            r.xb = load16(GPN(p.bnd, x + l.pb * 16, 16));
+            r.ga = load16(GPN(p.bnd, g + l.pa * 16, 16));
+            r.gb = load16(GPN(p.bnd, g + l.pb * 16, 16));
+        }
+        if (++li == its) {
+            li = 0;
+            lu += step;
+            aim();
+        }
+    };
+
+    pdl_wait();
+    pdl_trigger();
+    Raw raw[kBwdAhead];
+    aim();
+#pragma unroll
+    for (int k = 0; k < kBwdAhead; ++k) load(raw[k]);
+    long long at = u < units ? position_of(p, u / split) : 0;
+    for (int k = threadIdx.x; k < p.rot / 2; k += 32 * kWarps) turns[k] = *GP(p.bnd, p.turns + k);
+    uint64_t wa[kH], wb[kH], da[kH], db[kH];           // this lane's weights, and its share of dw
+    const T *w = reinterpret_cast<const T *>(which ? a.wk : a.wq);
+#pragma unroll
+    for (int k = 0; k < kH; ++k) {
+        da[k] = db[k] = 0;
+        wa[k] = wb[k] = f2(1.f, 1.f);
+        if (w && l.active) {
+            auto of = [&](int c) { return Elt<T>::to_f(*GP(p.bnd, w + c)) + a.offset; };
+            wa[k] = f2(of(l.pa * kV + 2 * k), of(l.pa * kV + 2 * k + 1));
+            wb[k] = f2(of(l.pb * kV + 2 * k), of(l.pb * kV + 2 * k + 1));
+        }
+    }
+    __syncthreads();
+
+    for (; u < units; u += step) {
+        const unsigned t = u / split, row0 = (u - t * split) * its * group + l.row;
+        uint64_t c[kH], s[kH];
+        token_turns<T, kInter>(p, l, at, turns, cs, c, s);
+        if (u + step < units) at = position_of(p, (u + step) / split);
+        const unsigned od = token_units(p, t, sd);
+        for (unsigned i = 0; i < its; ++i) {
+            const unsigned e = row0 + i * group;
+            uint64_t fa[kH], fb[kH], ya[kH], yb[kH], va[kH], vb[kH];
+            unpack2<T>(raw[0].xa, fa);
+            unpack2<T>(raw[0].xb, fb);
+            unpack2<T>(raw[0].ga, ya);
+            unpack2<T>(raw[0].gb, yb);
+#pragma unroll
+            for (int m = 0; m + 1 < kBwdAhead; ++m) raw[m] = raw[m + 1];
+            load(raw[kBwdAhead - 1]);
+            if (l.turns) {                             // R^T
+                if constexpr (kInter) {
+                    auto turn_back = [&](uint64_t (&f)[kH], int piece, int from) {
+                        if (piece * kV >= p.rot) return;
+#pragma unroll
+                        for (int m = 0; m < kH; ++m) {
+                            float x, y, c0, c1, s0, s1;
+                            f2split(f[m], x, y);
+                            f2split(c[from + m / 2], c0, c1);
+                            f2split(s[from + m / 2], s0, s1);
+                            const float co = m & 1 ? c1 : c0, si = m & 1 ? s1 : s0;
+                            f[m] = f2(x * co + y * si, y * co - x * si);
+                        }
+                    };
+                    turn_back(ya, l.pa, 0);
+                    turn_back(yb, l.pb, kH / 2);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < kH; ++m) {
+                        const uint64_t x = ya[m];
+                        ya[m] = fma2(x, c[m], mul2(yb[m], s[m]));
+                        yb[m] = fma2(yb[m], c[m], negate2(mul2(x, s[m])));
+                    }
+                }
+            }
+            uint64_t squares = 0, products = 0;
+#pragma unroll
+            for (int m = 0; m < kH; ++m) {
+                squares = fma2(fa[m], fa[m], fma2(fb[m], fb[m], squares));
+                va[m] = mul2(wa[m], ya[m]);
+                vb[m] = mul2(wb[m], yb[m]);
+                products = fma2(va[m], fa[m], fma2(vb[m], fb[m], products));
+            }
+            float sum = sum2(squares), dot = sum2(products);
+            for (int d = L / 2; d > 0; d >>= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                dot += __shfl_xor_sync(0xffffffffu, dot, d);
+            }
+            if (e >= (unsigned)heads || !l.active) continue;
+            const float rn = inverse_norm(sum, by_hd, a.eps), c2 = dot * by_hd * rn * rn;
+            const uint64_t rn2 = f2(rn, rn), less = f2(-c2, -c2);
+#pragma unroll
+            for (int m = 0; m < kH; ++m) {
+                da[m] = fma2(ya[m], mul2(fa[m], rn2), da[m]);
+                db[m] = fma2(yb[m], mul2(fb[m], rn2), db[m]);
+                fa[m] = mul2(rn2, fma2(less, fa[m], va[m]));
+                fb[m] = mul2(rn2, fma2(less, fb[m], vb[m]));
+            }
+            char *d = base_d + (unsigned long long)(od + e * sd[2]) * 16u;
+            *reinterpret_cast<uint4 *>(GPN(p.bnd, d + l.pa * 16, 16)) = repack2<T>(fa);
+            *reinterpret_cast<uint4 *>(GPN(p.bnd, d + l.pb * 16, 16)) = repack2<T>(fb);
+        }
+    }
+    if (!a.dw[which]) return;
+    // the block's sums, in the order of its row groups
+    if (l.active) {
+        float *mine = sums + (warp * group + l.row) * p.hd;
+#pragma unroll
+        for (int k = 0; k < kH; ++k) {
+            *reinterpret_cast<unsigned long long *>(mine + l.pa * kV + 2 * k) = da[k];
+            *reinterpret_cast<unsigned long long *>(mine + l.pb * kV + 2 * k) = db[k];
+        }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.hd; c += 32 * kWarps) {
+        float sum = 0.f;
+        for (int q = 0; q < kWarps * group; ++q) sum += sums[q * p.hd + c];
+        *GP(p.bnd, a.part + (long long)blockIdx.x * p.hd + c) = sum;
+    }
+}
+
+// The rows that do not lie on lane groups: a warp a row.
 struct BwdRow {
     uintptr_t g, x, d;         // of dy (low bits: the token of the tile), x, dx (0: none)
 };
 constexpr int kBwdRows = 256;
 
-// Blocks 0 .. blocks_q - 1 take the rows of Q, the others those of K: each has the
-// weight gradient of one of them.  kMode as above.
-template <typename T, int kMode>
-__global__ void __launch_bounds__(kThreads, 2) k_norm_bwd(const __grid_constant__ NormArgs a) {
-    constexpr int kV = VecOf<T>::kN, kUnroll = sizeof(T) == 2 && kMode < 2 ? 2 : 1;
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) k_norm_bwd_rows(const __grid_constant__ NormArgs a) {
     const RotaryArgs &p = a.r;
-    extern __shared__ __align__(16) float smem[];      // two tables [tile][2][rot / 2]; weights [hd]; sums [kThreads / L][hd] or, mode 2, rows
+    const float by_hd = 1.f / (float)p.hd;
+    extern __shared__ __align__(16) float smem[];      // two tables [tile][2][rot / 2]; weights [hd]; sums, x, g [3][hd] a warp
     __shared__ BwdRow lists[2][kBwdRows];
     const int which = blockIdx.x >= a.blocks_q, heads = which ? p.hk : p.hq;
     const int first = which ? blockIdx.x - a.blocks_q : blockIdx.x, nblocks = which ? a.blocks - a.blocks_q : a.blocks_q;
     const int tile = a.tile[which], slices = a.slices[which];
     const long long work = (long long)a.tiles[which] * slices;
     const int half = p.rot / 2;
+    const unsigned by_half = half > 1 ? 0xffffffffu / half + 1u : 0u;      // x / half for x < 2^15
     const int table = 2 * max(a.tile[0], a.tile[1]) * p.rot;
     float *wtab = smem + table, *sums = wtab + p.hd;
 
-    const int L = a.lanes, sub = threadIdx.x & (L - 1), q0 = threadIdx.x / L, per_pass = kThreads / L;
-    const int pieces = p.hd / kV, nturn = kMode == 0 ? half / kV : 0;
-    const bool active = sub < pieces / 2;
-    const int pa = sub < nturn ? sub : nturn + sub, pb = sub < nturn ? sub + nturn : pieces / 2 + sub;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     // unit of work u: the heads of slice u % slices of the tokens of tile u / slices
@@ -411,14 +780,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_bwd(const __grid_constant_
         const long long t0 = u / slices * tile;
         const int nt = (int)(p.tokens - t0 < tile ? p.tokens - t0 : tile);
         const unsigned *sg = which ? p.sk : p.sq, *sd = which ? p.sko : p.sqo;
+        const unsigned by_mine = 0xffffffffu / mine + 1u;  // x / mine for x < 2^15
         for (int e = threadIdx.x; e < nt * mine; e += kThreads) {
-            const unsigned tt = e / mine, head = lo + e - tt * mine, t = (unsigned)t0 + tt;
+            const unsigned tt = mine > 1 ? __umulhi(e, by_mine) : e, head = lo + e - tt * mine, t = (unsigned)t0 + tt;
             list[e].g = reinterpret_cast<uintptr_t>((const char *)(which ? p.K : p.Q) + row_units(p, t, sg, head)) + tt;
             list[e].x = reinterpret_cast<uintptr_t>((const char *)a.X[which] + row_units(p, t, a.sx[which], head));
             list[e].d = reinterpret_cast<uintptr_t>((char *)(which ? p.Ko : p.Qo) + row_units(p, t, sd, head));
         }
         for (int e = kThreads - 1 - threadIdx.x; e < nt * half; e += kThreads) {
-            const unsigned tt = e / half, k = e - tt * half, t = (unsigned)t0 + tt;
+            const unsigned tt = half > 1 ? __umulhi(e, by_half) : e, k = e - tt * half, t = (unsigned)t0 + tt;
             const long long at = (p.pos ? (long long)*GP(p.bnd, p.pos + t) : (long long)(t % p.n)) + p.pos0;
             float cs, sn;
             cos_sin(at, *GP(p.bnd, p.turns + k), cs, sn);
@@ -427,48 +797,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_bwd(const __grid_constant_
         }
         return nt * mine;
     };
-    // R^T on a lane's pieces
-    auto back = [&](const float *cs, float (&ga)[kV], float (&gb)[kV]) {
-        if constexpr (kMode == 0) {
-            if (sub < nturn) {
-                float c[kV], s[kV];
-                take<kV>(cs + pa * kV, c);
-                take<kV>(cs + half + pa * kV, s);
-#pragma unroll
-                for (int k = 0; k < kV; ++k) {
-                    const float x = ga[k];
-                    ga[k] = x * c[k] + gb[k] * s[k];
-                    gb[k] = gb[k] * c[k] - x * s[k];
-                }
-            }
-        } else {
-            auto turn = [&](float (&f)[kV], int piece) {
-                if (piece * kV >= p.rot) return;
-                float c[kV / 2], s[kV / 2];
-                take<kV / 2>(cs + piece * (kV / 2), c);
-                take<kV / 2>(cs + half + piece * (kV / 2), s);
-#pragma unroll
-                for (int k = 0; k < kV / 2; ++k) {
-                    const float x = f[2 * k];
-                    f[2 * k] = x * c[k] + f[2 * k + 1] * s[k];
-                    f[2 * k + 1] = f[2 * k + 1] * c[k] - x * s[k];
-                }
-            };
-            turn(ga, pa);
-            turn(gb, pb);
-        }
-    };
-
     pdl_wait();
     pdl_trigger();
     const T *w = reinterpret_cast<const T *>(which ? a.wk : a.wq);
     for (int c = threadIdx.x; c < p.hd; c += kThreads) wtab[c] = w ? Elt<T>::to_f(*GP(p.bnd, w + c)) + a.offset : 1.f;
-    float da[kV], db[kV];              // this lane's share of dw (mode 2: in shared memory, a row a warp)
-#pragma unroll
-    for (int k = 0; k < kV; ++k) da[k] = db[k] = 0.f;
-    float *dsum = sums + warp * 3 * p.hd, *sx = dsum + p.hd, *sg = sx + p.hd;     // mode 2
-    if constexpr (kMode == 2)
-        for (int c = lane; c < p.hd; c += 32) dsum[c] = 0.f;
+    float *dsum = sums + warp * 3 * p.hd, *sx = dsum + p.hd, *sg = sx + p.hd;
+    for (int c = lane; c < p.hd; c += 32) dsum[c] = 0.f;
 
     int buf = 0, total = prepare(first, lists[0], smem);
     for (long long u0 = first; u0 < work; u0 += nblocks, buf ^= 1) {
@@ -477,124 +811,48 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_bwd(const __grid_constant_
         const bool more = u0 + nblocks < work;
         int next = 0;
         __syncthreads();                 // this tile is prepared, the other buffer is free
-        if constexpr (kMode < 2) {
-            BwdRow r[kUnroll];
-            uint4 xa[kUnroll], xb[kUnroll], ga[kUnroll], gb[kUnroll];
-            auto fetch = [&](int q) {
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int e = q + q0 + u * per_pass;
-                    r[u].d = r[u].g = 0;
-                    xa[u] = xb[u] = ga[u] = gb[u] = make_uint4(0, 0, 0, 0);
-                    if (e >= total || !active) continue;
-                    r[u] = list[e];
-                    const char *x = reinterpret_cast<const char *>(r[u].x), *g = reinterpret_cast<const char *>(r[u].g & ~(uintptr_t)15);
-                    xa[u] = load16(GPN(p.bnd, x + pa * 16, 16));
-                    xb[u] = load16(GPN(p.bnd, x + pb * 16, 16));
-                    ga[u] = load16(GPN(p.bnd, g + pa * 16, 16));
-                    gb[u] = load16(GPN(p.bnd, g + pb * 16, 16));
-                }
-            };
-            fetch(0);
-            if (more) next = prepare(u0 + nblocks, lists[buf ^ 1], smem + (buf ^ 1) * (table / 2));
-            for (int q = 0; q < total; q += kUnroll * per_pass) {
-                if (q > 0) fetch(q);
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    float fa[kV], fb[kV], ya[kV], yb[kV], va[kV], vb[kV];
-                    unpack16<T>(xa[u], fa);
-                    unpack16<T>(xb[u], fb);
-                    unpack16<T>(ga[u], ya);
-                    unpack16<T>(gb[u], yb);
-#pragma unroll
-                    for (int k = 0; k < kV; ++k) va[k] = vb[k] = 0.f;
-                    if (active) {
-                        back(tab + 2 * (int)(r[u].g & 15u) * half, ya, yb);
-                        take<kV>(wtab + pa * kV, va);
-                        take<kV>(wtab + pb * kV, vb);
-                    }
-                    float sum = 0.f, dot = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kV; ++k) {
-                        sum = fmaf(fa[k], fa[k], fmaf(fb[k], fb[k], sum));
-                        va[k] *= ya[k];
-                        vb[k] *= yb[k];
-                        dot = fmaf(va[k], fa[k], fmaf(vb[k], fb[k], dot));
-                    }
-                    for (int d = L / 2; d > 0; d >>= 1) {
-                        sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                        dot += __shfl_xor_sync(0xffffffffu, dot, d);
-                    }
-                    if (!r[u].d) continue;
-                    const float rn = inverse_norm(sum, (float)p.hd, a.eps), c2 = dot / (float)p.hd * rn * rn;
-#pragma unroll
-                    for (int k = 0; k < kV; ++k) {
-                        da[k] = fmaf(ya[k], fa[k] * rn, da[k]);
-                        db[k] = fmaf(yb[k], fb[k] * rn, db[k]);
-                        fa[k] = rn * fmaf(-c2, fa[k], va[k]);
-                        fb[k] = rn * fmaf(-c2, fb[k], vb[k]);
-                    }
-                    char *d = reinterpret_cast<char *>(r[u].d);
-                    *reinterpret_cast<uint4 *>(GPN(p.bnd, d + pa * 16, 16)) = pack16<T>(fa);
-                    *reinterpret_cast<uint4 *>(GPN(p.bnd, d + pb * 16, 16)) = pack16<T>(fb);
-                }
+        if (more) next = prepare(u0 + nblocks, lists[buf ^ 1], smem + (buf ^ 1) * (table / 2));
+        for (int e = warp; e < total; e += kThreads / 32) {
+            const BwdRow r = list[e];
+            const T *x = reinterpret_cast<const T *>(r.x), *g = reinterpret_cast<const T *>(r.g & ~(uintptr_t)15);
+            const float *cs = tab + 2 * (int)(r.g & 15u) * half;
+            float sum = 0.f, dot = 0.f;
+            for (int c = lane; c < p.hd; c += 32) {
+                const float f = Elt<T>::to_f(*GP(p.bnd, x + c));
+                sum = fmaf(f, f, sum);
+                sx[c] = f;
+                sg[c] = Elt<T>::to_f(*GP(p.bnd, g + c));
             }
-        } else {
-            if (more) next = prepare(u0 + nblocks, lists[buf ^ 1], smem + (buf ^ 1) * (table / 2));
-            for (int e = warp; e < total; e += kThreads / 32) {
-                const BwdRow r = list[e];
-                const T *x = reinterpret_cast<const T *>(r.x), *g = reinterpret_cast<const T *>(r.g & ~(uintptr_t)15);
-                const float *cs = tab + 2 * (int)(r.g & 15u) * half;
-                float sum = 0.f, dot = 0.f;
-                for (int c = lane; c < p.hd; c += 32) {
-                    const float f = Elt<T>::to_f(*GP(p.bnd, x + c));
-                    sum = fmaf(f, f, sum);
-                    sx[c] = f;
-                    sg[c] = Elt<T>::to_f(*GP(p.bnd, g + c));
-                }
-                __syncwarp();
-                for (int k = lane; k < half; k += 32) {
-                    const int one = p.interleaved ? 2 * k : k, two = p.interleaved ? 2 * k + 1 : k + half;
-                    const float y1 = sg[one], y2 = sg[two], c = cs[k], s = cs[half + k];
-                    sg[one] = y1 * c + y2 * s;
-                    sg[two] = y2 * c - y1 * s;
-                }
-                __syncwarp();
-                for (int c = lane; c < p.hd; c += 32) dot = fmaf(sg[c] * wtab[c], sx[c], dot);
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) {
-                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                    dot += __shfl_xor_sync(0xffffffffu, dot, d);
-                }
-                const float rn = inverse_norm(sum, (float)p.hd, a.eps), c2 = dot / (float)p.hd * rn * rn;
-                T *d = reinterpret_cast<T *>(r.d);
-                for (int c = lane; c < p.hd; c += 32) {
-                    dsum[c] = fmaf(sg[c], sx[c] * rn, dsum[c]);
-                    *GP(p.bnd, d + c) = Elt<T>::from_f(rn * fmaf(-c2, sx[c], sg[c] * wtab[c]));
-                }
-                __syncwarp();
+            __syncwarp();
+            for (int k = lane; k < half; k += 32) {
+                const int one = p.interleaved ? 2 * k : k, two = p.interleaved ? 2 * k + 1 : k + half;
+                const float y1 = sg[one], y2 = sg[two], c = cs[k], s = cs[half + k];
+                sg[one] = y1 * c + y2 * s;
+                sg[two] = y2 * c - y1 * s;
             }
+            __syncwarp();
+            for (int c = lane; c < p.hd; c += 32) dot = fmaf(sg[c] * wtab[c], sx[c], dot);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                dot += __shfl_xor_sync(0xffffffffu, dot, d);
+            }
+            const float rn = inverse_norm(sum, by_hd, a.eps), c2 = dot * by_hd * rn * rn;
+            T *d = reinterpret_cast<T *>(r.d);
+            for (int c = lane; c < p.hd; c += 32) {
+                dsum[c] = fmaf(sg[c], sx[c] * rn, dsum[c]);
+                *GP(p.bnd, d + c) = Elt<T>::from_f(rn * fmaf(-c2, sx[c], sg[c] * wtab[c]));
+            }
+            __syncwarp();
         }
         total = next;
     }
     if (!a.dw[which]) return;
-    // the block's sums, in the order of its row groups
-    int rows = kThreads / 32, stride = 3 * p.hd;
-    if constexpr (kMode < 2) {
-        rows = per_pass;
-        stride = p.hd;
-        if (active) {
-#pragma unroll
-            for (int k = 0; k < kV; ++k) {
-                sums[q0 * p.hd + pa * kV + k] = da[k];
-                sums[q0 * p.hd + pb * kV + k] = db[k];
-            }
-        }
-    }
+    // the block's sums, in the order of its warps
     __syncthreads();
     for (int c = threadIdx.x; c < p.hd; c += kThreads) {
         float s = 0.f;
-        for (int q = 0; q < rows; ++q) s += sums[q * stride + c];
+        for (int q = 0; q < kThreads / 32; ++q) s += sums[q * 3 * p.hd + c];
         *GP(p.bnd, a.part + (long long)blockIdx.x * p.hd + c) = s;
     }
 }
@@ -626,32 +884,58 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const __grid_constant__ NormAr
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_read4(const __grid_constant__ Read4Args p) {
-    const int words = p.hd / 8;
-    const long long per_token = 2LL * p.hk * words, items = per_token * p.tokens;
+    constexpr int kFlight = 4;                           // words of a thread in flight: slot -> codes is a chain
+    const unsigned words = p.hd / 8, per_kind = p.hk * words, per_token = 2 * per_kind;   // at most 2^23
+    const unsigned by_words = 0xffffffffu / words + 1u;  // for x / words
+    const long long step = (long long)gridDim.x * kThreads, first = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const unsigned step_t = (unsigned)(step / per_token), step_in = (unsigned)(step - (long long)step_t * per_token);
+    long long t = first / per_token;
+    unsigned in = (unsigned)(first - t * per_token);
     pdl_wait();
     pdl_trigger();
-    for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < items; e += (long long)gridDim.x * kThreads) {
-        const long long t = e / per_token;
-        const int in = (int)(e - t * per_token), is_v = in >= p.hk * words, row = (is_v ? in - p.hk * words : in) / words;
-        const int word = in % words;
-        const int slot = *GP(p.bnd, p.slots + t);
-        if (slot < 0 || slot >= p.n_slots) {
-            if (slot != -1 && in == 0) atomicOr(p.err, kErrInvalid);
-            continue;
-        }
-        const unsigned blk = (unsigned)slot >> p.page_log2, off = (unsigned)slot & ((1u << p.page_log2) - 1u);
-        const unsigned long long line = ((blk * (unsigned)p.hk + row) << p.page_log2) + off;
-        const uint32_t w = *GP(p.bnd, reinterpret_cast<const uint32_t *>(is_v ? p.Vc : p.Kc) + line * words + word);
-        const float s = Elt<T>::to_f(*GP(p.bnd, reinterpret_cast<const T *>(is_v ? p.Vs : p.Ks) + line * (p.hd / kGroup4) + word / 4));
-        float f[8];
+    while (t < p.tokens) {
+        uint32_t w[kFlight];
+        T scale[kFlight];
+        T *dst[kFlight];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = s * (float)((int)((w >> (4 * k)) & 15u) - 8);
-        T *dst = reinterpret_cast<T *>(is_v ? p.V : p.K) + (t * p.hk + row) * p.hd + word * 8;
-        if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<uint4 *>(GPN(p.bnd, dst, 16)) = pack16<T>(f);
-            *reinterpret_cast<uint4 *>(GPN(p.bnd, dst + 4, 16)) = pack16<T>(f + 4);
-        } else {
-            *reinterpret_cast<uint4 *>(GPN(p.bnd, dst, 16)) = pack16<T>(f);
+        for (int i = 0; i < kFlight; ++i) {
+            dst[i] = nullptr;
+            if (t < p.tokens) {
+                const int slot = *GP(p.bnd, p.slots + t);
+                if (slot >= 0 && slot < p.n_slots) {
+                    const bool is_v = in >= per_kind;
+                    const unsigned x = is_v ? in - per_kind : in;
+                    unsigned row = __umulhi(x, by_words);
+                    if (row * words > x) --row;          // (the product may be one too large past 2^32 / words)
+                    const unsigned word = x - row * words, blk = (unsigned)slot >> p.page_log2, off = (unsigned)slot & ((1u << p.page_log2) - 1u);
+                    const unsigned long long line = ((blk * (unsigned)p.hk + row) << p.page_log2) + off;
+                    w[i] = *GP(p.bnd, reinterpret_cast<const uint32_t *>(is_v ? p.Vc : p.Kc) + line * words + word);
+                    scale[i] = *GP(p.bnd, reinterpret_cast<const T *>(is_v ? p.Vs : p.Ks) + line * (words / 4) + word / 4);
+                    dst[i] = reinterpret_cast<T *>(is_v ? p.V : p.K) + (t * p.hk + row) * p.hd + word * 8;
+                } else if (slot != -1 && in == 0) {
+                    atomicOr(p.err, kErrInvalid);
+                }
+                t += step_t;
+                in += step_in;
+                if (in >= per_token) {
+                    in -= per_token;
+                    ++t;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            if (!dst[i]) continue;
+            const float s = Elt<T>::to_f(scale[i]);
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = s * (float)((int)((w[i] >> (4 * k)) & 15u) - 8);
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<uint4 *>(GPN(p.bnd, dst[i], 16)) = pack16<T>(f);
+                *reinterpret_cast<uint4 *>(GPN(p.bnd, dst[i] + 4, 16)) = pack16<T>(f + 4);
+            } else {
+                *reinterpret_cast<uint4 *>(GPN(p.bnd, dst[i], 16)) = pack16<T>(f);
+            }
         }
     }
 }
@@ -679,11 +963,11 @@ int mode_of(const RotaryArgs &r, int es, bool bits4, int *lanes, NormArgs *a = n
 
 template <typename T, int kKind>
 cudaError_t launch_t(const NormArgs &a, int mode, dim3 grid, size_t smem, cudaStream_t st) {
-    if constexpr (kKind == 2 && sizeof(T) == 4) return launch_dependent(&k_norm<T, 2, kKind>, grid, kThreads, smem, st, a);
-    else {
-        const auto fn = mode == 0 ? &k_norm<T, 0, kKind> : mode == 1 ? &k_norm<T, 1, kKind> : &k_norm<T, 2, kKind>;
-        return launch_dependent(fn, grid, kThreads, smem, st, a);
+    if constexpr (kKind < 2 || sizeof(T) == 2) {
+        if (mode == 0) return launch_dependent(&k_norm<T, false, kKind>, grid, 32 * kWarps, smem, st, a);
+        if (mode == 1) return launch_dependent(&k_norm<T, true, kKind>, grid, 32 * kWarps, smem, st, a);
     }
+    return launch_dependent(&k_norm_rows<T, kKind>, grid, kThreads, smem, st, a);
 }
 template <typename T>
 cudaError_t launch_kind(int kind, const NormArgs &a, int mode, dim3 grid, size_t smem, cudaStream_t st) {
@@ -706,6 +990,24 @@ void tile_of(const RotaryArgs &r, int rows, int lanes, long long full, int most_
     *slices_out = slices;
 }
 
+// Slices of a token's `all` row groups, and row groups of a slice: more than one slice
+// where there are fewer tokens than warps.
+void split_of(const RotaryArgs &r, long long all, long long warps, int *split, int *its) {
+    const long long want = std::max(1LL, std::min(all, warps / r.tokens));
+    *its = (int)((all + want - 1) / want);
+    *split = (int)((all + *its - 1) / *its);
+}
+
+template <typename T>
+cudaError_t launch_bwd_t(const NormArgs &a, int mode, size_t smem, cudaStream_t st) {
+    if (mode == 0) return launch_dependent(&k_norm_bwd<T, false>, dim3((unsigned)a.blocks), 32 * kWarps, smem, st, a);
+    if (mode == 1) return launch_dependent(&k_norm_bwd<T, true>, dim3((unsigned)a.blocks), 32 * kWarps, smem, st, a);
+    const auto fn = &k_norm_bwd_rows<T>;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(fn, dim3((unsigned)a.blocks), kThreads, smem, st, a);
+}
+
 }  // namespace
 
 cudaError_t launch_norm(DType dt, int kind, NormArgs a, cudaStream_t st) {
@@ -715,50 +1017,52 @@ cudaError_t launch_norm(DType dt, int kind, NormArgs a, cudaStream_t st) {
     a.r.row_bytes = a.r.hd * es;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidValue;
-    const long long full = (long long)kBlocks * sms;
-    int slices = 1;
-    tile_of(a.r, a.r.rows, a.lanes, full, kMaxRows, &a.r.tile, &slices);
-    const long long tiles = ((long long)a.r.tokens + a.r.tile - 1) / a.r.tile;
-    const dim3 grid((unsigned)std::min(tiles, full), (unsigned)slices);
-    const size_t smem = ((size_t)2 * a.r.tile * a.r.rot + 2 * a.r.hd + (mode == 2 ? kThreads / 32 * a.r.hd : 0)) * sizeof(float);
+    dim3 grid;
+    size_t smem;
+    if (mode < 2) {
+        const long long full = 5LL * sms, pad = (a.r.rot + 3) / 4 * 4, group = 32 / a.lanes;
+        split_of(a.r, (a.r.rows + group - 1) / group, full * kWarps, &a.split, &a.its);
+        grid = dim3((unsigned)std::min(((long long)a.r.tokens * a.split + kWarps - 1) / kWarps, full));
+        smem = (size_t)((1 + kWarps) * pad + 2 * a.r.hd) * sizeof(float);
+    } else {
+        const long long full = (long long)kBlocks * sms;
+        int slices = 1;
+        tile_of(a.r, a.r.rows, 32, full, kMaxRows, &a.r.tile, &slices);
+        grid = dim3((unsigned)std::min(((long long)a.r.tokens + a.r.tile - 1) / a.r.tile, full), (unsigned)slices);
+        smem = ((size_t)2 * a.r.tile * a.r.rot + 2 * a.r.hd + kThreads / 32 * a.r.hd) * sizeof(float);
+    }
     if (dt == kF32) return launch_kind<float>(kind, a, mode, grid, smem, st);
     if (dt == kF16) return launch_kind<__half>(kind, a, mode, grid, smem, st);
     return launch_kind<__nv_bfloat16>(kind, a, mode, grid, smem, st);
 }
-
-namespace {
-template <typename T>
-cudaError_t launch_bwd_t(const NormArgs &a, int mode, size_t smem, cudaStream_t st) {
-    const auto fn = mode == 0 ? &k_norm_bwd<T, 0> : mode == 1 ? &k_norm_bwd<T, 1> : &k_norm_bwd<T, 2>;
-    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(fn, dim3((unsigned)a.blocks), kThreads, smem, st, a);
-}
-}  // namespace
 
 cudaError_t launch_norm_bwd(DType dt, NormArgs a, cudaStream_t st) {
     const int es = dt == kF32 ? 4 : 2;
     const int mode = mode_of(a.r, es, false, &a.lanes);
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidValue;
-    const long long full = std::min(2LL * sms, (long long)kNormBlocks - 2);
-    long long work[2] = {0, 0};
+    const long long full = std::min((mode < 2 ? 4LL : 2LL) * sms, (long long)kNormBlocks - 2), all = a.r.hq + a.r.hk;
+    long long blocks[2] = {0, 0};
     for (int k = 0; k < 2; ++k) {
         const int heads = k ? a.r.hk : a.r.hq;
         a.tile[k] = a.slices[k] = 1;
         if (heads == 0) continue;
-        tile_of(a.r, heads, a.lanes, full, kBwdRows, &a.tile[k], &a.slices[k]);
-        a.tiles[k] = (int)(((long long)a.r.tokens + a.tile[k] - 1) / a.tile[k]);
-        work[k] = (long long)a.tiles[k] * a.slices[k];
+        // blocks shared by how many rows there are
+        const long long share = std::max(1LL, k ? full - full * a.r.hq / all : full * a.r.hq / all);
+        if (mode < 2) {
+            const int group = 32 / a.lanes;
+            split_of(a.r, (heads + group - 1) / group, share * kWarps, &a.slices[k], &a.tile[k]);
+            blocks[k] = std::min(((long long)a.r.tokens * a.slices[k] + kWarps - 1) / kWarps, share);
+        } else {
+            tile_of(a.r, heads, 32, full, kBwdRows, &a.tile[k], &a.slices[k]);
+            a.tiles[k] = (int)(((long long)a.r.tokens + a.tile[k] - 1) / a.tile[k]);
+            blocks[k] = std::min((long long)a.tiles[k] * a.slices[k], share);
+        }
     }
-    // blocks shared by how many rows there are
-    const long long all = a.r.hq + a.r.hk;
-    const long long kq = std::max(1LL, std::min(work[0], full * a.r.hq / all));
-    const long long kk = a.r.hk ? std::max(1LL, std::min(work[1], full - full * a.r.hq / all)) : 0;
-    a.blocks_q = (int)kq;
-    a.blocks = (int)(kq + kk);
-    const int rows = mode == 2 ? kThreads / 32 * 3 : kThreads / a.lanes;
-    const size_t smem = ((size_t)2 * std::max(a.tile[0], a.tile[1]) * a.r.rot + a.r.hd + (size_t)rows * a.r.hd) * sizeof(float);
+    a.blocks_q = (int)blocks[0];
+    a.blocks = (int)(blocks[0] + blocks[1]);
+    const size_t smem = mode < 2 ? ((size_t)(1 + kWarps) * ((a.r.rot + 3) / 4 * 4) + (size_t)32 * kWarps / a.lanes * a.r.hd) * sizeof(float)
+                                 : ((size_t)2 * std::max(a.tile[0], a.tile[1]) * a.r.rot + a.r.hd + (size_t)kThreads / 32 * 3 * a.r.hd) * sizeof(float);
     const cudaError_t e = dt == kF32   ? launch_bwd_t<float>(a, mode, smem, st)
                           : dt == kF16 ? launch_bwd_t<__half>(a, mode, smem, st)
                                        : launch_bwd_t<__nv_bfloat16>(a, mode, smem, st);
@@ -770,7 +1074,7 @@ cudaError_t launch_read4(DType dt, const Read4Args &a, cudaStream_t st) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidValue;
     const long long items = 2LL * a.hk * (a.hd / 8) * a.tokens;
-    const dim3 grid((unsigned)std::min((items + kThreads - 1) / kThreads, 32LL * sms));
+    const dim3 grid((unsigned)std::min((items + kThreads - 1) / kThreads, 8LL * sms));
     if (dt == kF32) return launch_dependent(&k_read4<float>, grid, kThreads, 0, st, a);
     if (dt == kF16) return launch_dependent(&k_read4<__half>, grid, kThreads, 0, st, a);
     return launch_dependent(&k_read4<__nv_bfloat16>, grid, kThreads, 0, st, a);

@@ -369,6 +369,7 @@ struct NormArgs {
     int norm;                  // 0: rotary alone
     void *Ks, *Vs;             // scales of a cache in 4 bits
     int lanes;                 // of a row (set by the launcher, like the rest)
+    int split, its;            // slices of a token's rows, row groups of a slice
     int by_pairs;              // pairs off 16-byte pieces
     int sum_lanes, sum_turn;   // a warp a row: the lanes that would own pieces, those that turn (0: none could)
     // backward: r.Q, r.K are dQo, dKo (strides r.sq, r.sk), r.Qo, r.Ko are dQ, dK
@@ -377,7 +378,7 @@ struct NormArgs {
     float *dw[2];              // dwq, dwk, or null
     float *part;               // partial sums: [blocks][hd]
     int blocks_q, blocks;      // of the grid: of Q, of both
-    int tiles[2], tile[2], slices[2];
+    int tiles[2], tile[2], slices[2];   // rows on lane groups: slices as `split`, tile as `its`
 };
 // kind: 0 = Q, K -> Qo, Ko; 1 = into the cache; 2 = into the cache in 4 bits
 cudaError_t launch_norm(DType dt, int kind, NormArgs a, cudaStream_t st);
