@@ -279,11 +279,29 @@ __device__ __forceinline__ void token_turns(const RotaryArgs &p, const Lane &l, 
 __device__ __forceinline__ long long position_of(const RotaryArgs &p, unsigned t) {
     return (p.pos ? (long long)*GP(p.bnd, p.pos + t) : (long long)(t % p.n)) + p.pos0;
 }
-// Offset of token t in a tensor with these strides, in units of 16 bytes.
-__device__ __forceinline__ unsigned token_units(const RotaryArgs &p, unsigned t, const unsigned *s) {
-    if (p.n == p.tokens) return t * s[1];
-    const unsigned bb = t / p.n;
-    return bb * s[0] + (t - bb * p.n) * s[1];
+// x / d for x < 2^31: by = (2^32 - 1) / d gives it or one less.
+__device__ __forceinline__ unsigned divide(unsigned x, unsigned d, unsigned by) {
+    const unsigned q = __umulhi(x, by);
+    return x - q * d >= d ? q + 1u : q;
+}
+// Token t of sequence bb, its i-th; where it lies in a tensor, in units of 16 bytes.
+struct Token {
+    unsigned bb, i;
+    __device__ __forceinline__ unsigned units(const unsigned *s) const { return bb * s[0] + i * s[1]; }
+};
+// Unit u of the work: slice `slice` of the rows of a token.
+struct Unit {
+    unsigned t, slice;
+};
+__device__ __forceinline__ Unit unit_of(unsigned u, unsigned split, unsigned by_split) {
+    if (split == 1) return Unit{u, 0u};
+    const unsigned t = divide(u, split, by_split);
+    return Unit{t, u - t * split};
+}
+__device__ __forceinline__ Token token_of(const RotaryArgs &p, unsigned t, unsigned by_n) {
+    if (p.n == p.tokens) return Token{0u, t};
+    const unsigned bb = divide(t, p.n, by_n);
+    return Token{bb, t - bb * p.n};
 }
 
 template <typename T, bool kInter, int kKind>
@@ -300,6 +318,7 @@ __global__ void __launch_bounds__(32 * kWarps, 5) k_norm(const __grid_constant__
     const float by_hd = 1.f / (float)p.hd;
     // units of work: the `its` row groups of slice u % split of token u / split
     const unsigned split = a.split, its = a.its, units = p.tokens * split, step = gridDim.x * kWarps;
+    const unsigned by_split = 0xffffffffu / split, by_n = 0xffffffffu / p.n;
     unsigned u = blockIdx.x * kWarps + warp;
 
     // A lane's row e of a token moves on by a row group at a time: its address by a
@@ -307,11 +326,11 @@ __global__ void __launch_bounds__(32 * kWarps, 5) k_norm(const __grid_constant__
     // The loads run kAhead row groups ahead: row le at `from`.
     unsigned lu = u, li = 0, le = 0, lbound = 0, lstep = 0;
     const char *from = nullptr;
+    Token ltok{0, 0};
     auto aim_row = [&]() {
-        const unsigned t = lu / split;
         const bool is_q = le < hq, is_v = kKind > 0 && le >= hqk;
         const unsigned *s = is_q ? p.sq : is_v ? p.sv : p.sk;
-        const unsigned at = token_units(p, t, s) + (is_q ? le : is_v ? le - hqk : le - hq) * s[2];
+        const unsigned at = ltok.units(s) + (is_q ? le : is_v ? le - hqk : le - hq) * s[2];
         from = (const char *)(is_q ? p.Q : is_v ? p.V : p.K) + (unsigned long long)at * 16u;
         lstep = s[2] * group;
         lbound = le >= rows || !l.active ? 0 : is_q ? hq : is_v || kKind == 0 ? rows : hqk;     // 0: no row
@@ -319,7 +338,9 @@ __global__ void __launch_bounds__(32 * kWarps, 5) k_norm(const __grid_constant__
     auto aim = [&]() {                                 // the loads at unit lu
         lbound = 0;
         if (lu >= units) return;
-        le = (lu % split) * its * group + l.row;
+        const Unit x = unit_of(lu, split, by_split);
+        ltok = token_of(p, x.t, by_n);
+        le = x.slice * its * group + l.row;
         aim_row();
     };
     auto load = [&](uint4 &va, uint4 &vb) {
@@ -344,8 +365,9 @@ __global__ void __launch_bounds__(32 * kWarps, 5) k_norm(const __grid_constant__
     aim();
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) load(va[k], vb[k]);
-    long long at = u < units ? position_of(p, u / split) : 0;
-    int slot = kKind > 0 && u < units ? *GP(p.bnd, p.slots + u / split) : -1;
+    Unit now = unit_of(u, split, by_split);
+    long long at = u < units ? position_of(p, now.t) : 0;
+    int slot = kKind > 0 && u < units ? *GP(p.bnd, p.slots + now.t) : -1;
     for (int k = threadIdx.x; k < p.rot / 2; k += 32 * kWarps) turns[k] = *GP(p.bnd, p.turns + k);
     for (int c = threadIdx.x; c < 2 * p.hd; c += 32 * kWarps) {
         const T *w = reinterpret_cast<const T *>(c < p.hd ? a.wq : a.wk);
@@ -354,14 +376,15 @@ __global__ void __launch_bounds__(32 * kWarps, 5) k_norm(const __grid_constant__
     __syncthreads();
 
     for (; u < units; u += step) {
-        const unsigned t = u / split;
-        unsigned e = (u - t * split) * its * group + l.row;
+        const Token tok = token_of(p, now.t, by_n);
+        unsigned e = now.slice * its * group + l.row;
         uint64_t c[kH], s[kH];
         token_turns<T, kInter>(p, l, at, turns, cs, c, s);
         const int here = slot;
         if (u + step < units) {
-            at = position_of(p, (u + step) / split);
-            if (kKind > 0) slot = *GP(p.bnd, p.slots + (u + step) / split);
+            now = unit_of(u + step, split, by_split);
+            at = position_of(p, now.t);
+            if (kKind > 0) slot = *GP(p.bnd, p.slots + now.t);
         }
         const bool kept = kKind == 0 || (here >= 0 && here < p.n_slots);
         if (kKind > 0 && !kept && here != -1 && lane == 0) atomicOr(p.err, kErrInvalid);
@@ -378,7 +401,7 @@ __global__ void __launch_bounds__(32 * kWarps, 5) k_norm(const __grid_constant__
             bound = is_q ? hq : is_v || kKind == 0 ? rows : hqk;
             if (is_q || kKind == 0) {
                 const unsigned *so = is_q ? p.sqo : p.sko;
-                dst = (char *)(is_q ? p.Qo : p.Ko) + (unsigned long long)(token_units(p, t, so) + (is_q ? e : e - hq) * so[2]) * 16u;
+                dst = (char *)(is_q ? p.Qo : p.Ko) + (unsigned long long)(tok.units(so) + (is_q ? e : e - hq) * so[2]) * 16u;
                 dstep = (unsigned long long)(so[2] * group) * 16u;
             } else {
                 const unsigned blk = (unsigned)here >> p.page_log2, off = (unsigned)here & ((1u << p.page_log2) - 1u), head = e - (is_v ? hqk : hq);
@@ -591,49 +614,56 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm_rows(const __grid_co
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// Blocks 0 .. blocks_q - 1 take the rows of Q, the others those of K: each has the
-// weight gradient of one of them.
-constexpr int kBwdAhead = 2;
-
+// One row group is loaded ahead; a lane adds up both weights' gradients.
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(32 * kWarps, 4) k_norm_bwd(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 3) k_norm_bwd(const __grid_constant__ NormArgs a) {
     constexpr int kV = VecOf<T>::kN, kH = kV / 2;
+    constexpr unsigned kNever = 0xffffffffu;
     const RotaryArgs &p = a.r;
-    extern __shared__ __align__(16) float smem[];      // turns [rot / 2]; [rot] a warp; sums [32 kWarps / lanes][hd]
-    const int which = blockIdx.x >= a.blocks_q, heads = which ? p.hk : p.hq;
-    const int warp = threadIdx.x >> 5, L = a.lanes, group = 32 / L, pad = (p.rot + 3) / 4 * 4;
+    extern __shared__ __align__(16) float smem[];      // turns [rot / 2]; [rot] a warp; weights [2][hd]; sums [32 kWarps / lanes][hd]
+    const int warp = threadIdx.x >> 5, L = a.lanes, pad = (p.rot + 3) / 4 * 4;
+    const unsigned group = 32 / L, hq = p.hq, rows = p.rows;
     unsigned long long *turns = reinterpret_cast<unsigned long long *>(smem);
-    float *cs = smem + pad + warp * pad, *sums = smem + pad + kWarps * pad;
+    float *cs = smem + pad + warp * pad, *wtab = smem + pad + kWarps * pad, *sums = wtab + 2 * p.hd;
     const Lane l = lane_of<kInter>(L, p.hd / kV, p.rot / 2 / kV);
     const float by_hd = 1.f / (float)p.hd;
-    const unsigned split = a.slices[which], its = a.tile[which], units = p.tokens * split;
-    const unsigned step = (which ? a.blocks - a.blocks_q : a.blocks_q) * kWarps;
-    unsigned u = (which ? blockIdx.x - a.blocks_q : blockIdx.x) * kWarps + warp;
-    const unsigned *sg = which ? p.sk : p.sq, *sx = a.sx[which], *sd = which ? p.sko : p.sqo;
-    const char *base_g = (const char *)(which ? p.K : p.Q), *base_x = (const char *)a.X[which];
-    char *base_d = (char *)(which ? p.Ko : p.Qo);
+    const unsigned split = a.split, its = a.its, units = p.tokens * split, step = gridDim.x * kWarps;
+    const unsigned by_split = 0xffffffffu / split, by_n = 0xffffffffu / p.n;
+    unsigned u = blockIdx.x * kWarps + warp;
 
-    struct Raw {
-        uint4 xa, xb, ga, gb;
+    // the loads, a row group ahead: row le at from_x, from_g (as in k_norm)
+    unsigned lu = u, li = 0, le = 0, lbound = 0, step_x = 0, step_g = 0;
+    const char *from_x = nullptr, *from_g = nullptr;
+    Token ltok{0, 0};
+    auto aim_row = [&]() {
+        const bool is_q = le < hq;
+        const unsigned *sx = a.sx[is_q ? 0 : 1], *sg = is_q ? p.sq : p.sk, head = is_q ? le : le - hq;
+        from_x = (const char *)a.X[is_q ? 0 : 1] + (unsigned long long)(ltok.units(sx) + head * sx[2]) * 16u;
+        from_g = (const char *)(is_q ? p.Q : p.K) + (unsigned long long)(ltok.units(sg) + head * sg[2]) * 16u;
+        step_x = sx[2] * group;
+        step_g = sg[2] * group;
+        lbound = le >= rows || !l.active ? 0 : is_q ? hq : rows;               // 0: no row
     };
-    unsigned lu = u, li = 0, lrow = 0, og = 0, ox = 0;
     auto aim = [&]() {
+        lbound = 0;
         if (lu >= units) return;
-        const unsigned t = lu / split;
-        lrow = (lu - t * split) * its * group + l.row;
-        og = token_units(p, t, sg);
-        ox = token_units(p, t, sx);
+        const Unit x = unit_of(lu, split, by_split);
+        ltok = token_of(p, x.t, by_n);
+        le = x.slice * its * group + l.row;
+        aim_row();
     };
-    auto load = [&](Raw &r) {
-        r.xa = r.xb = r.ga = r.gb = make_uint4(0, 0, 0, 0);
-        if (lu >= units) return;
-        const unsigned e = lrow + li * group;
-        if (e < (unsigned)heads && l.active) {
-            const char *x = base_x + (unsigned long long)(ox + e * sx[2]) * 16u, *g = base_g + (unsigned long long)(og + e * sg[2]) * 16u;
-            r.xa = load16(GPN(p.bnd, x + l.pa * 16, 16));
-            r.xb = load16(GPN(p.bnd, x + l.pb * 16, 16));
-            r.ga = load16(GPN(p.bnd, g + l.pa * 16, 16));
-            r.gb = load16(GPN(p.bnd, g + l.pb * 16, 16));
+    uint4 rxa, rxb, rga, rgb;
+    auto load = [&]() {
+        rxa = rxb = rga = rgb = make_uint4(0, 0, 0, 0);
+        if (lbound) {
+            rxa = load16(GPN(p.bnd, from_x + l.pa * 16, 16));
+            rxb = load16(GPN(p.bnd, from_x + l.pb * 16, 16));
+            rga = load16(GPN(p.bnd, from_g + l.pa * 16, 16));
+            rgb = load16(GPN(p.bnd, from_g + l.pb * 16, 16));
+            le += group;
+            from_x += (unsigned long long)step_x * 16u;
+            from_g += (unsigned long long)step_g * 16u;
+            if (le >= lbound) aim_row();
         }
         if (++li == its) {
             li = 0;
@@ -644,52 +674,59 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_norm_bwd(const __grid_consta
 
     pdl_wait();
     pdl_trigger();
-    Raw raw[kBwdAhead];
     aim();
-#pragma unroll
-    for (int k = 0; k < kBwdAhead; ++k) load(raw[k]);
-    long long at = u < units ? position_of(p, u / split) : 0;
+    load();
+    Unit now = unit_of(u, split, by_split);
+    long long at = u < units ? position_of(p, now.t) : 0;
     for (int k = threadIdx.x; k < p.rot / 2; k += 32 * kWarps) turns[k] = *GP(p.bnd, p.turns + k);
-    uint64_t wa[kH], wb[kH], da[kH], db[kH];           // this lane's weights, and its share of dw
-    const T *w = reinterpret_cast<const T *>(which ? a.wk : a.wq);
-#pragma unroll
-    for (int k = 0; k < kH; ++k) {
-        da[k] = db[k] = 0;
-        wa[k] = wb[k] = f2(1.f, 1.f);
-        if (w && l.active) {
-            auto of = [&](int c) { return Elt<T>::to_f(*GP(p.bnd, w + c)) + a.offset; };
-            wa[k] = f2(of(l.pa * kV + 2 * k), of(l.pa * kV + 2 * k + 1));
-            wb[k] = f2(of(l.pb * kV + 2 * k), of(l.pb * kV + 2 * k + 1));
-        }
+    for (int c = threadIdx.x; c < 2 * p.hd; c += 32 * kWarps) {
+        const T *w = reinterpret_cast<const T *>(c < p.hd ? a.wq : a.wk);
+        wtab[c] = w ? Elt<T>::to_f(*GP(p.bnd, w + (c < p.hd ? c : c - p.hd))) + a.offset : 1.f;
     }
+    uint64_t dqa[kH], dqb[kH], dka[kH], dkb[kH];       // this lane's share of dwq, dwk
+#pragma unroll
+    for (int k = 0; k < kH; ++k) dqa[k] = dqb[k] = dka[k] = dkb[k] = 0;
     __syncthreads();
 
     for (; u < units; u += step) {
-        const unsigned t = u / split, row0 = (u - t * split) * its * group + l.row;
+        const Token tok = token_of(p, now.t, by_n);
+        unsigned e = now.slice * its * group + l.row;
         uint64_t c[kH], s[kH];
         token_turns<T, kInter>(p, l, at, turns, cs, c, s);
-        if (u + step < units) at = position_of(p, (u + step) / split);
-        const unsigned od = token_units(p, t, sd);
+        if (u + step < units) {
+            now = unit_of(u + step, split, by_split);
+            at = position_of(p, now.t);
+        }
+        unsigned bound = 0, dstep = 0;
+        char *dst = nullptr;
+        auto aim_out = [&]() {
+            bound = kNever;
+            if (e >= rows) return;
+            const bool is_q = e < hq;
+            const unsigned *so = is_q ? p.sqo : p.sko;
+            bound = is_q ? hq : rows;
+            dst = (char *)(is_q ? p.Qo : p.Ko) + (unsigned long long)(tok.units(so) + (is_q ? e : e - hq) * so[2]) * 16u;
+            dstep = so[2] * group;
+        };
+        aim_out();
         for (unsigned i = 0; i < its; ++i) {
-            const unsigned e = row0 + i * group;
+            const bool there = e < rows && l.active, is_q = e < hq;
             uint64_t fa[kH], fb[kH], ya[kH], yb[kH], va[kH], vb[kH];
-            unpack2<T>(raw[0].xa, fa);
-            unpack2<T>(raw[0].xb, fb);
-            unpack2<T>(raw[0].ga, ya);
-            unpack2<T>(raw[0].gb, yb);
-#pragma unroll
-            for (int m = 0; m + 1 < kBwdAhead; ++m) raw[m] = raw[m + 1];
-            load(raw[kBwdAhead - 1]);
+            unpack2<T>(rxa, fa);
+            unpack2<T>(rxb, fb);
+            unpack2<T>(rga, ya);
+            unpack2<T>(rgb, yb);
+            load();
             if (l.turns) {                             // R^T
                 if constexpr (kInter) {
-                    auto turn_back = [&](uint64_t (&f)[kH], int piece, int from) {
+                    auto turn_back = [&](uint64_t (&f)[kH], int piece, int first) {
                         if (piece * kV >= p.rot) return;
 #pragma unroll
                         for (int m = 0; m < kH; ++m) {
                             float x, y, c0, c1, s0, s1;
                             f2split(f[m], x, y);
-                            f2split(c[from + m / 2], c0, c1);
-                            f2split(s[from + m / 2], s0, s1);
+                            f2split(c[first + m / 2], c0, c1);
+                            f2split(s[first + m / 2], s0, s1);
                             const float co = m & 1 ? c1 : c0, si = m & 1 ? s1 : s0;
                             f[m] = f2(x * co + y * si, y * co - x * si);
                         }
@@ -706,11 +743,18 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_norm_bwd(const __grid_consta
                 }
             }
             uint64_t squares = 0, products = 0;
+            if (l.active) {
+                take2<kH>(wtab + (is_q ? 0 : p.hd) + l.pa * kV, va);
+                take2<kH>(wtab + (is_q ? 0 : p.hd) + l.pb * kV, vb);
+            } else {
+#pragma unroll
+                for (int m = 0; m < kH; ++m) va[m] = vb[m] = 0;
+            }
 #pragma unroll
             for (int m = 0; m < kH; ++m) {
                 squares = fma2(fa[m], fa[m], fma2(fb[m], fb[m], squares));
-                va[m] = mul2(wa[m], ya[m]);
-                vb[m] = mul2(wb[m], yb[m]);
+                va[m] = mul2(va[m], ya[m]);
+                vb[m] = mul2(vb[m], yb[m]);
                 products = fma2(va[m], fa[m], fma2(vb[m], fb[m], products));
             }
             float sum = sum2(squares), dot = sum2(products);
@@ -718,40 +762,55 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_norm_bwd(const __grid_consta
                 sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 dot += __shfl_xor_sync(0xffffffffu, dot, d);
             }
-            if (e >= (unsigned)heads || !l.active) continue;
-            const float rn = inverse_norm(sum, by_hd, a.eps), c2 = dot * by_hd * rn * rn;
-            const uint64_t rn2 = f2(rn, rn), less = f2(-c2, -c2);
+            if (there) {
+                const float rn = inverse_norm(sum, by_hd, a.eps), c2 = dot * by_hd * rn * rn;
+                const uint64_t rn2 = f2(rn, rn), less = f2(-c2, -c2);
 #pragma unroll
-            for (int m = 0; m < kH; ++m) {
-                da[m] = fma2(ya[m], mul2(fa[m], rn2), da[m]);
-                db[m] = fma2(yb[m], mul2(fb[m], rn2), db[m]);
-                fa[m] = mul2(rn2, fma2(less, fa[m], va[m]));
-                fb[m] = mul2(rn2, fma2(less, fb[m], vb[m]));
+                for (int m = 0; m < kH; ++m) {
+                    ya[m] = mul2(ya[m], mul2(fa[m], rn2));             // this row's term of dw
+                    yb[m] = mul2(yb[m], mul2(fb[m], rn2));
+                    fa[m] = mul2(rn2, fma2(less, fa[m], va[m]));
+                    fb[m] = mul2(rn2, fma2(less, fb[m], vb[m]));
+                }
+                *reinterpret_cast<uint4 *>(GPN(p.bnd, dst + l.pa * 16, 16)) = repack2<T>(fa);
+                *reinterpret_cast<uint4 *>(GPN(p.bnd, dst + l.pb * 16, 16)) = repack2<T>(fb);
+                if (is_q) {
+#pragma unroll
+                    for (int m = 0; m < kH; ++m) dqa[m] = add2(dqa[m], ya[m]), dqb[m] = add2(dqb[m], yb[m]);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < kH; ++m) dka[m] = add2(dka[m], ya[m]), dkb[m] = add2(dkb[m], yb[m]);
+                }
             }
-            char *d = base_d + (unsigned long long)(od + e * sd[2]) * 16u;
-            *reinterpret_cast<uint4 *>(GPN(p.bnd, d + l.pa * 16, 16)) = repack2<T>(fa);
-            *reinterpret_cast<uint4 *>(GPN(p.bnd, d + l.pb * 16, 16)) = repack2<T>(fb);
+            e += group;
+            dst += (unsigned long long)dstep * 16u;
+            if (e >= bound) aim_out();
         }
     }
-    if (!a.dw[which]) return;
     // the block's sums, in the order of its row groups
-    if (l.active) {
-        float *mine = sums + (warp * group + l.row) * p.hd;
 #pragma unroll
-        for (int k = 0; k < kH; ++k) {
-            *reinterpret_cast<unsigned long long *>(mine + l.pa * kV + 2 * k) = da[k];
-            *reinterpret_cast<unsigned long long *>(mine + l.pb * kV + 2 * k) = db[k];
+    for (int which = 0; which < 2; ++which) {
+        if (!a.dw[which]) continue;
+        __syncthreads();
+        if (l.active) {
+            float *mine = sums + (warp * group + l.row) * p.hd;
+#pragma unroll
+            for (int k = 0; k < kH; ++k) {
+                *reinterpret_cast<unsigned long long *>(mine + l.pa * kV + 2 * k) = which ? dka[k] : dqa[k];
+                *reinterpret_cast<unsigned long long *>(mine + l.pb * kV + 2 * k) = which ? dkb[k] : dqb[k];
+            }
         }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < p.hd; c += 32 * kWarps) {
-        float sum = 0.f;
-        for (int q = 0; q < kWarps * group; ++q) sum += sums[q * p.hd + c];
-        *GP(p.bnd, a.part + (long long)blockIdx.x * p.hd + c) = sum;
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.hd; c += 32 * kWarps) {
+            float sum = 0.f;
+            for (unsigned q = 0; q < kWarps * group; ++q) sum += sums[q * p.hd + c];
+            *GP(p.bnd, a.part + (2LL * blockIdx.x + which) * p.hd + c) = sum;
+        }
     }
 }
 
-// The rows that do not lie on lane groups: a warp a row.
+// The rows that do not lie on lane groups: a warp a row.  Blocks 0 .. blocks_q - 1
+// take the rows of Q, the others those of K: each has the weight gradient of one of them.
 struct BwdRow {
     uintptr_t g, x, d;         // of dy (low bits: the token of the tile), x, dx (0: none)
 };
@@ -862,14 +921,15 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const __grid_constant__ NormAr
     __shared__ float s[32][33];
     const RotaryArgs &p = a.r;
     const int which = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), seg = threadIdx.x >> 5;
-    const int lo = which ? a.blocks_q : 0, hi = which ? a.blocks : a.blocks_q;
+    // rows of sums: two a block, or one (blocks of Q, then of K)
+    const int lo = a.both ? which : which ? a.blocks_q : 0, hi = a.both || which ? a.blocks : a.blocks_q, by = a.both ? 2 : 1;
     pdl_wait();
     pdl_trigger();
     if (!a.dw[which]) return;
     float x = 0.f;
     if (c < p.hd) {
 #pragma unroll 8
-        for (int b = lo + seg; b < hi; b += 32) x += *GP(p.bnd, a.part + (long long)b * p.hd + c);
+        for (int b = lo + by * seg; b < hi; b += 32 * by) x += *GP(p.bnd, a.part + (long long)b * p.hd + c);
     }
     s[seg][threadIdx.x & 31] = x;
     __syncthreads();
@@ -1000,8 +1060,8 @@ void split_of(const RotaryArgs &r, long long all, long long warps, int *split, i
 
 template <typename T>
 cudaError_t launch_bwd_t(const NormArgs &a, int mode, size_t smem, cudaStream_t st) {
-    if (mode == 0) return launch_dependent(&k_norm_bwd<T, false>, dim3((unsigned)a.blocks), 32 * kWarps, smem, st, a);
-    if (mode == 1) return launch_dependent(&k_norm_bwd<T, true>, dim3((unsigned)a.blocks), 32 * kWarps, smem, st, a);
+    if (mode == 0) return launch_dependent(&k_norm_bwd<T, false>, dim3((unsigned)a.blocks_q), 32 * kWarps, smem, st, a);
+    if (mode == 1) return launch_dependent(&k_norm_bwd<T, true>, dim3((unsigned)a.blocks_q), 32 * kWarps, smem, st, a);
     const auto fn = &k_norm_bwd_rows<T>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), (int)smem);
     if (e != cudaSuccess) return e;
@@ -1039,30 +1099,34 @@ cudaError_t launch_norm(DType dt, int kind, NormArgs a, cudaStream_t st) {
 cudaError_t launch_norm_bwd(DType dt, NormArgs a, cudaStream_t st) {
     const int es = dt == kF32 ? 4 : 2;
     const int mode = mode_of(a.r, es, false, &a.lanes);
+    a.r.rows = a.r.hq + a.r.hk;
+    a.both = mode < 2;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidValue;
-    const long long full = std::min((mode < 2 ? 4LL : 2LL) * sms, (long long)kNormBlocks - 2), all = a.r.hq + a.r.hk;
-    long long blocks[2] = {0, 0};
-    for (int k = 0; k < 2; ++k) {
-        const int heads = k ? a.r.hk : a.r.hq;
-        a.tile[k] = a.slices[k] = 1;
-        if (heads == 0) continue;
-        // blocks shared by how many rows there are
-        const long long share = std::max(1LL, k ? full - full * a.r.hq / all : full * a.r.hq / all);
-        if (mode < 2) {
-            const int group = 32 / a.lanes;
-            split_of(a.r, (heads + group - 1) / group, share * kWarps, &a.slices[k], &a.tile[k]);
-            blocks[k] = std::min(((long long)a.r.tokens * a.slices[k] + kWarps - 1) / kWarps, share);
-        } else {
+    size_t smem;
+    if (mode < 2) {
+        const long long full = std::min(3LL * sms, (long long)kNormRows / 2), group = 32 / a.lanes;
+        split_of(a.r, (a.r.rows + group - 1) / group, full * kWarps, &a.split, &a.its);
+        a.blocks_q = (int)std::min(((long long)a.r.tokens * a.split + kWarps - 1) / kWarps, full);
+        a.blocks = 2 * a.blocks_q;                 // (rows of sums)
+        smem = ((size_t)(1 + kWarps) * ((a.r.rot + 3) / 4 * 4) + (size_t)(32 * kWarps / a.lanes + 2) * a.r.hd) * sizeof(float);
+    } else {
+        const long long full = std::min(2LL * sms, (long long)kNormRows - 2), all = a.r.rows;
+        long long blocks[2] = {0, 0};
+        for (int k = 0; k < 2; ++k) {
+            const int heads = k ? a.r.hk : a.r.hq;
+            a.tile[k] = a.slices[k] = 1;
+            if (heads == 0) continue;
+            // blocks shared by how many rows there are
+            const long long share = std::max(1LL, k ? full - full * a.r.hq / all : full * a.r.hq / all);
             tile_of(a.r, heads, 32, full, kBwdRows, &a.tile[k], &a.slices[k]);
             a.tiles[k] = (int)(((long long)a.r.tokens + a.tile[k] - 1) / a.tile[k]);
             blocks[k] = std::min((long long)a.tiles[k] * a.slices[k], share);
         }
+        a.blocks_q = (int)blocks[0];
+        a.blocks = (int)(blocks[0] + blocks[1]);
+        smem = ((size_t)2 * std::max(a.tile[0], a.tile[1]) * a.r.rot + a.r.hd + (size_t)kThreads / 32 * 3 * a.r.hd) * sizeof(float);
     }
-    a.blocks_q = (int)blocks[0];
-    a.blocks = (int)(blocks[0] + blocks[1]);
-    const size_t smem = mode < 2 ? ((size_t)(1 + kWarps) * ((a.r.rot + 3) / 4 * 4) + (size_t)32 * kWarps / a.lanes * a.r.hd) * sizeof(float)
-                                 : ((size_t)2 * std::max(a.tile[0], a.tile[1]) * a.r.rot + a.r.hd + (size_t)kThreads / 32 * 3 * a.r.hd) * sizeof(float);
     const cudaError_t e = dt == kF32   ? launch_bwd_t<float>(a, mode, smem, st)
                           : dt == kF16 ? launch_bwd_t<__half>(a, mode, smem, st)
                                        : launch_bwd_t<__nv_bfloat16>(a, mode, smem, st);

@@ -376,13 +376,14 @@ struct NormArgs {
     const void *X[2];          // Q, K
     unsigned sx[2][3];         // their strides
     float *dw[2];              // dwq, dwk, or null
-    float *part;               // partial sums: [blocks][hd]
-    int blocks_q, blocks;      // of the grid: of Q, of both
-    int tiles[2], tile[2], slices[2];   // rows on lane groups: slices as `split`, tile as `its`
+    float *part;               // partial sums, rows of [hd]
+    int both;                  // a block has sums of dwq and of dwk (rows on lane groups), else of one
+    int blocks_q, blocks;      // rows of sums: of Q (both: blocks), in all
+    int tiles[2], tile[2], slices[2];
 };
 // kind: 0 = Q, K -> Qo, Ko; 1 = into the cache; 2 = into the cache in 4 bits
 cudaError_t launch_norm(DType dt, int kind, NormArgs a, cudaStream_t st);
-constexpr int kNormBlocks = 608;     // most blocks of the backward, rows of its partial sums
+constexpr int kNormRows = 1216;      // most rows of the backward's partial sums
 cudaError_t launch_norm_bwd(DType dt, NormArgs a, cudaStream_t st);
 
 struct Read4Args {

@@ -232,7 +232,7 @@ swab_status check_norm(const swab_norm_desc *norm, const void *wq, const void *w
     return SWAB_OK;
 }
 [[maybe_unused]] Extent weight_extent(const swab_rotary_desc *d, const void *w) { return {w, (size_t)d->head_dim * elt(d->dtype)}; }
-size_t norm_workspace(const swab_rotary_desc *d) { return (size_t)kNormBlocks * d->head_dim * 4; }
+size_t norm_workspace(const swab_rotary_desc *d) { return (size_t)kNormRows * d->head_dim * 4; }
 
 // ---------------------------------------------------------------------------
 // decode
