@@ -7,7 +7,8 @@ Builds the workload's seeded inputs on the current CUDA device, calls the
 fused forward (``band_attention``), the fused forward then its backward
 (``band_attention_bwd``, only the backward repeated) or, the workload's
 sequences as prompts in the paged cache, steps of one token for each of them
-(``decode``: cache_slots, rotary_append, band_decode) ``--repeat`` times,
+(``decode``: cache_slots, rotary_append, band_decode; with ``--bits 4`` over a
+cache in 4 bits: rotary_append4, band_decode4) ``--repeat`` times,
 synchronises, checks the device status word and exits 0.  It prints nothing
 but one line with the call and the status, so a profiler's launch list holds
 only the library's kernels and torch's input copies.
@@ -29,11 +30,12 @@ def main() -> int:
     ap.add_argument("--workload", required=True, choices=sorted(names))
     ap.add_argument("--call", default="band_attention", choices=["band_attention", "band_attention_bwd", "decode"])
     ap.add_argument("--repeat", type=int, default=3)
+    ap.add_argument("--bits", type=int, choices=[4], help="decode: hold the cache in 4 bits")
     args = ap.parse_args()
     wl = names[args.workload]
     swab.load()
     if args.call == "decode":
-        return decode(wl, args.repeat)
+        return decode(wl, args.repeat, args.bits)
     d = swab.Desc.from_workload(wl)
     Q, K, V, dO = (x.cuda() for x in workload_inputs(wl))
     O = torch.empty_like(Q)
@@ -54,9 +56,9 @@ def main() -> int:
     return 0 if status == 0 else 1
 
 
-def decode(wl, repeat) -> int:
+def decode(wl, repeat, bits=None) -> int:
     """`repeat` steps behind the workload's sequences, replayed from a graph."""
-    loop = DecodeLoop.from_workload(wl)
+    loop = DecodeLoop.from_workload(wl, bits=bits)
     heads = [x.view(wl.b, wl.h, wl.n, wl.head_dim).transpose(1, 2).reshape(wl.b * wl.n, wl.h, wl.head_dim).cuda()
              for x in workload_inputs(wl, count=3)]
     qkv = torch.cat(heads, dim=1)

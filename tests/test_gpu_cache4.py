@@ -434,6 +434,13 @@ def test_loop_with_norms_and_in_16_bits(bits):
     assert loop.lens.tolist() == [51, 0]
 
 
+@pytest.mark.parametrize("name", ["tiny_fp32_n512_w32", "longformer_base_fp16_n4096_w256_d3", "train_bf16_b12_n4096_w256_g16"])
+def test_run_workload_decodes_in_4_bits(name):
+    res = subprocess.run([sys.executable, "-m", "sliding_window_attention_band_gb300.run_workload", "--workload", name, "--call",
+                          "decode", "--bits", "4", "--repeat", "3"], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout + res.stderr[-2000:]
+
+
 @pytest.mark.parametrize("dtype", [F16, F32])
 def test_compiled_calls_and_the_binding_agree(dtype, monkeypatch):
     B, h, hk, hd, page = 2, 4, 2, 64, 16

@@ -281,3 +281,14 @@ def test_structs_follow_the_header():
     a = nm._NormDesc.from_address(n._addr)
     assert a.offset == 1.0 and abs(a.eps - 1e-5) < 1e-12 and not any(a.q_stride) and not any(a.k_stride)
     assert ctypes.sizeof(nm._NormDesc) == 8 + 6 * 8
+
+
+def test_loop_refuses_what_its_calls_would(lib):
+    for kw, error in ((dict(bits=8), ValueError), (dict(bits=4, head_dim=80), ValueError), (dict(bits=4, head_dim=288), swab.SwabError),
+                      (dict(norm=swab.NormDesc(0.0)), swab.SwabError), (dict(wq=torch.ones(64)), ValueError),
+                      (dict(norm=swab.NormDesc(), wq=torch.ones(64)), ValueError),
+                      (dict(norm=swab.NormDesc(), wk=torch.ones(32, dtype=torch.bfloat16)), ValueError)):
+        with pytest.raises(error):
+            swab.DecodeLoop(**{**dict(batch=2, h=4, hk=2, head_dim=64, w=16, device="cpu"), **kw})
+    loop = swab.DecodeLoop(2, 4, 2, 64, 16, device="cpu", bits=4, norm=swab.NormDesc(), wq=torch.ones(64, dtype=torch.bfloat16))
+    assert loop.Kc.shape == (loop.cache.n_blocks, 2, 64, 32) and loop.Ks.shape[-1] == 2 and loop.Ks.dtype is torch.bfloat16
