@@ -398,8 +398,18 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
     return p;
 }
 
-// The same over a cache in 4 bits: tiles of 8 or 16 rows in blocks of four warps (16
-// or 12 of them an SM), lists cut in pieces of 128 keys and more.
+// The same over a cache in 4 bits.  Tiles of 8 rows where that holds them all, else 16:
+// the codes of a tile are turned into values once for its rows, and 57 requests x 4096
+// keys of 8 heads of 128 take 62 us with 8 rows, 88 with 16 (twice 62 as two tiles).
+// Blocks of four warps, 12 or 16 warps an SM by registers and shared memory (blocks of
+// two, of one: 128k keys 42.9, 45.9, 60.6 us).  Pieces as many as fit at once: 131072
+// keys of 8 heads in 38, 57, 76 pieces take 45, 42.5, 52 us, 57 being one each place.
+// Requests of one call differ in length, and who has a long list in one piece is still
+// busy when all others are done: with several of them no piece is above kLongPiece
+// keys, for at most four times the pieces (32 requests of 1 to 12000 tokens 144 us in
+// a piece each, 90 in two, 75 in three; 64 of 1 to 6000, 12 heads of 64, 70 in one, 67
+// in two; 48 under a window of 4096 91 in one, 93 in two, so a piece holds that).
+constexpr long long kLongPiece = 5120;
 DecodePlan plan_decode4(const swab_decode_desc *d) {
     DecodePlan p{};
     const long long group = d->h / d->hk, batch = d->cache.batch, keys = most_keys(d);
@@ -416,7 +426,8 @@ DecodePlan plan_decode4(const swab_decode_desc *d) {
     } else {
         blocks *= (group + 3) / 4;
     }
-    const long long want = std::max<long long>(1, hold / blocks);
+    long long want = std::max<long long>(1, hold / blocks);
+    if (p.rows && batch > 1) want = std::max(want, std::min((keys + kLongPiece - 1) / kLongPiece, 4 * want));
     const long long chunk = std::max<long long>(least, ((keys + want - 1) / want + 63) / 64 * 64);
     p.nsplit = (int)((keys + chunk - 1) / chunk);
     p.chunk = (int)std::min<long long>(chunk, 0x7fffffff);

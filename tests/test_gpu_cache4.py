@@ -192,8 +192,11 @@ class Decode4(Decode):
         o = torch.full_like(self.q, 7.0)
         l = torch.full(self.q.shape[:2], 7.0, dtype=F32, device="cuda") if lse else None
         ws = torch.empty(swab.band_decode4_workspace(self.desc) + 16, dtype=torch.uint8, device="cuda")[16:]
-        swab.band_decode4(self.desc, self.scale, self.q, *self.cells, i32(self.table), i32(self.lens), i32(self.q_start), o, l, ws,
-                          stream=stream)
+        ints = i32(self.table), i32(self.lens), i32(self.q_start)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+            self.held = ws, *ints                # in use behind this call: not for the next tensor made here
+        swab.band_decode4(self.desc, self.scale, self.q, *self.cells, *ints, o, l, ws, stream=stream)
         return o, l
 
 
@@ -240,6 +243,17 @@ def test_decode_of_many_requests(case, dtype, hd):
     o, lse = c.run()
     assert (o[int(c.q_start[-1]):] == 7.0).all() and not o.isnan().any()
     check_some(c, o, lse, sorted({0, 1, n // 3, n // 2, n - 2, n - 1}))
+
+
+@pytest.mark.parametrize("heads,m", [((4, 1, 64), 1), ((8, 1, 128), 2)])
+def test_decode_of_requests_of_very_different_lengths(heads, m):
+    """More lists than the GPU holds at once, a few of them long: several pieces a list, empty for the others."""
+    lens = [10300, 2, 5121, 5120] + [2 + 7 * r % 40 for r in range(396)]
+    new = [m if r % 3 else 1 for r in range(400)]
+    c = Decode4(BF16, lens, new, *heads, page=64, pad=2, seed=115)
+    o, lse = c.run()
+    assert (o[int(c.q_start[-1]):] == 7.0).all() and not o.isnan().any()
+    check_some(c, o, lse, [0, 1, 2, 3, 4, 200, 399])
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
