@@ -6,26 +6,40 @@
 // query heads that share a key head, of all the new tokens of a request, are the
 // rows of one tile, so every code is read from memory once for all of them.
 //
-// HBM-bound by bytes, but a byte carries four times the arithmetic of one in 16
-// bits: what counts is instructions a code.  So
+// A byte of codes carries four times the arithmetic of a byte in 16 bits, and what
+// bounds the kernel is instructions, not memory: 32 keys of 8 heads' rows cost a warp
+// about 700 (K 248 and V 268 of them, the rest scores, softmax and lookups), and the
+// copies alone would take 29 of 43 us.  So
 //  * the products are transposed: S^T = K Q^T and O^T = V^T P^T, the cache the A
 //    operand (16 keys or channels) and the few rows its 8 columns; half as many
 //    products as with the rows as A, and the values are made once for all rows;
-//  * a code becomes a value by two instructions for two of them: shifted so that it
+//  * a code becomes a value by three instructions for two of them: shifted so that it
 //    lies behind the exponent of 16 (x = 16 + c), masked and joined with it in one
 //    operation, then x s - 24 s = s (c - 8), exact because s has 5 significant bits;
 //  * codes stay as they lie: A's k order is any order that B's shares.  A lane takes
 //    32 (16) adjacent channels of a key, one group, in K; 16 (8) adjacent channels of
 //    four keys in V, whose words are joined by halves so that a register holds two
 //    keys of one channel.
-// A warp owns groups of 32 keys and runs on its own: lines looked up one stage
-// ahead, codes and scales brought in with cp.async into a ring of its own.  Which
-// key of a group sits in which row of the product (slot_of) and where a piece of a
-// line lies in the ring are chosen so that no read of the ring has bank conflicts.
+//  * a warp owns groups of 64 keys and runs on its own, with a ring of two stages (three
+//    for head_dim 64).  Undilated (kRun) a group is four halves of 16 adjacent keys,
+//    which never cross a block's end, as pages are multiples of 16: 16 lanes each start
+//    one bulk copy (codes or scales, of K or of V) on the stage's mbarrier.  Lines are
+//    looked up 32 halves at a time, a lane a half (one group ahead: 109 and 57 us for the
+//    two cases that this brought to 88 and 47).  With a dilation keys lie apart: cp.async,
+//    a key's line by its pieces.
+// Lines lie in the ring as in memory: the reads of K meet no bank twice (slot_of says
+// which key sits in which row of the product), V's of 8 bytes are spread by the same
+// order over its key pairs.
 // Absent keys are zero-filled, scale and all: their values are 0 whatever the cache
 // holds there.
 // The softmax is that of k_decode_rows: the running maximum raised only when a
-// score passes it by 2^8, weights rounded to 16 bits for the product, sums fp32.
+// score passes it by 2^8, weights rounded to 16 bits for the product (what the tensor
+// cores take; as in decode over 16 bits), sums fp32.
+//
+// Measured (8 heads of 128, 32 query heads, bf16): one request of 131072 tokens 42.7 us,
+// 3.5 TB/s of codes and scales; 57 requests x 4096 62 us, 4.4 TB/s; with 16 rows a tile
+// 88 us, 3.1 TB/s.  A single step of one short request 4.4 us, of which launch and join
+// are most.
 //
 // k_decode4_general: every type and head size (a multiple of 32), fp32 arithmetic.
 #include <type_traits>
@@ -401,8 +415,8 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
                 phase ^= 1u;
             }
 
-            // kX blocks of 16 keys at a time: all four for 8 rows (more products in flight),
-            // two for 16 (registers)
+            // kX blocks of 16 keys at a time: all four for 8 rows (more products in flight: 128k
+            // keys 42.5 us, two at a time 43.9), two for 16 (four do not fit the registers)
             constexpr int kX = N == 1 ? 4 : 2;
 #pragma unroll 1
             for (int x0 = 0; x0 < 4; x0 += kX) {
