@@ -30,8 +30,8 @@
 // Lines lie in the ring as in memory: the reads of K meet no bank twice (slot_of says
 // which key sits in which row of the product), V's of 8 bytes are spread by the same
 // order over its key pairs.
-// Absent keys are zero-filled, scale and all: their values are 0 whatever the cache
-// holds there.
+// A key that no row attends to, or that is not there, has a score of -inf and, in the
+// ring, a scale of 0 for its V: it adds 0 whatever the cache holds there.
 // The softmax is that of k_decode_rows: the running maximum raised only when a
 // score passes it by 2^8, weights rounded to 16 bits for the product (what the tensor
 // cores take; as in decode over 16 bits), sums fp32.

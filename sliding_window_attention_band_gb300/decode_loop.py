@@ -68,6 +68,8 @@ class DecodeLoop:
         i32 = dict(dtype=torch.int32, device=device)
         new = dict(dtype=dtype, device=device)
         self.wq, self.wk = (None if x is None else x.contiguous().to(device) for x in (wq, wk))
+        # (a slice of a larger tensor may start where the calls refuse it)
+        self.wq, self.wk = (x.clone() if x is not None and x.data_ptr() % 16 else x for x in (self.wq, self.wk))
         if bits == 4:
             codes, scales = cache4.cache4_shapes(self.cache, hk, head_dim)
             self.Kc, self.Vc = (torch.zeros(codes, dtype=torch.uint8, device=device) for _ in range(2))

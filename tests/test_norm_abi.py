@@ -283,6 +283,13 @@ def test_structs_follow_the_header():
     assert ctypes.sizeof(nm._NormDesc) == 8 + 6 * 8
 
 
+def test_loop_takes_weights_wherever_they_start(lib):
+    w = torch.arange(65, dtype=torch.bfloat16)
+    loop = swab.DecodeLoop(2, 4, 2, 64, 16, device="cpu", norm=swab.NormDesc(), wq=w[1:], wk=w[:64])
+    assert w[1:].data_ptr() % 16 and loop.wq.data_ptr() % 16 == loop.wk.data_ptr() % 16 == 0
+    assert torch.equal(loop.wq, w[1:]) and torch.equal(loop.wk, w[:64])
+
+
 def test_loop_refuses_what_its_calls_would(lib):
     for kw, error in ((dict(bits=8), ValueError), (dict(bits=4, head_dim=80), ValueError), (dict(bits=4, head_dim=288), swab.SwabError),
                       (dict(norm=swab.NormDesc(0.0)), swab.SwabError), (dict(wq=torch.ones(64)), ValueError),
