@@ -656,9 +656,10 @@ SWAB_API size_t band_decode4_workspace(const swab_decode_desc *desc);
  * handling of absent blocks, limits, workspace rules and launches, with K and V the
  * values of the codes Kc, Vc under the scales Ks, Vs.  head_dim a multiple of 32, at
  * most 256; no shared prefix (prefix_len must be 0), else SWAB_ERR_UNSUPPORTED.  The
- * values are exact in fp16 and bf16, so with head_dim 64 or 128 the products run on
- * the tensor cores as those of band_decode do (a weight, at most 2^8 relative to the
- * running reference, is rounded to dtype before it multiplies V); elsewhere in fp32. */
+ * values are exact in fp16 and bf16, so with head_dim 64, 128 or (without a dilation)
+ * 96 the products run on the tensor cores as those of band_decode do (a weight, at
+ * most 2^8 relative to the running reference, is rounded to dtype before it
+ * multiplies V); elsewhere in fp32. */
 SWAB_API swab_status band_decode4(const swab_decode_desc *desc, float scale, const void *Q,
                                   const void *Kc, const void *Ks, const void *Vc, const void *Vs,
                                   const int32_t *table, const int32_t *lens, const int32_t *q_start,

@@ -2,8 +2,8 @@
 // cache held in 4 bits: a code c of a channel stands for s (c - 8), s the scale of
 // its 32 adjacent channels.
 //
-// k_decode4_rows: fp16 / bf16 with head_dim 64 or 128, on the tensor cores.  The
-// query heads that share a key head, of all the new tokens of a request, are the
+// k_decode4_rows: fp16 / bf16 with head_dim 64 or 128, and 96 where keys are not apart
+// (no dilation), on the tensor cores.  The query heads that share a key head, of all the new tokens of a request, are the
 // rows of one tile, so every code is read from memory once for all of them.
 //
 // A byte of codes carries four times the arithmetic of a byte in 16 bits, and what
@@ -19,7 +19,8 @@
 //  * codes stay as they lie: A's k order is any order that B's shares.  A lane takes
 //    32 (16) adjacent channels of a key, one group, in K; 16 (8) adjacent channels of
 //    four keys in V, whose words are joined by halves so that a register holds two
-//    keys of one channel.
+//    keys of one channel.  Three groups (96) do not go round four lanes: there a word
+//    of each group (K) and four channels of each (V), with the scales of all three;
 //  * a warp owns groups of 64 keys and runs on its own, with a ring of two stages (three
 //    for head_dim 64).  Undilated (kRun) a group is four halves of 16 adjacent keys,
 //    which never cross a block's end, as pages are multiples of 16: 16 lanes each start
@@ -38,8 +39,9 @@
 //
 // Measured (8 heads of 128, 32 query heads, bf16): one request of 131072 tokens 42.7 us,
 // 3.5 TB/s of codes and scales; 57 requests x 4096 62 us, 4.4 TB/s; with 16 rows a tile
-// 88 us, 3.1 TB/s.  A single step of one short request 4.4 us, of which launch and join
-// are most.
+// 88 us, 3.1 TB/s.  16 requests of 3000 to 5000, 24 heads over 8 of 96: 28 us, where
+// the general kernel took 143.  A single step of one short request 4.4 us, of which
+// launch and join are most.
 //
 // k_decode4_general: every type and head size (a multiple of 32), fp32 arithmetic.
 #include <type_traits>
@@ -58,7 +60,7 @@ constexpr float kSlack = 8.f;      // log2 headroom of the running maximum
 template <int HD, int kN, int kWarps> struct Shape4 {
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kBlocks = (HD == 64 && kN == 1 ? 16 : 12) / kWarps;   // an SM holds, by registers and shared memory
-    static constexpr int kStages = HD == 128 ? 2 : 3;
+    static constexpr int kStages = HD == 64 ? 3 : 2;
     static constexpr int kLine = HD / 2;                            // bytes of codes of a key
     static constexpr int kScale = HD / 16;                          // bytes of its scales
     static constexpr int kCodes = kGroup * kLine, kScales = kGroup * kScale;
@@ -183,6 +185,11 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
     constexpr int kThreads = S::kThreads, kRows = 8 * kN;
     constexpr int kWords = HD / 32;                        // words of codes of a lane's share of a key (K)
     constexpr int kSteps = HD / 16, kTiles = HD / 16;      // products of 16 channels (S), of 16 channels (O)
+    constexpr int kQuads = HD / 32;                        // of four channels: a lane's share of a key (V)
+    // With three groups a lane's share cannot be one of them: word t4 of each group (K), quad g
+    // of each (V) instead of adjacent ones, and the scales of all groups.
+    constexpr bool kThree = HD == 96;
+    static_assert(!kThree || kRun, "lines of 48 bytes come by bulk copies only");
     constexpr int kChunks = S::kLine / 16, kPer = 32 / kChunks;   // 16-byte pieces of a line; lines of a copy instruction
     constexpr int kPad = HD + 8;                           // floats of a row in the final exchange
     static_assert(kRows * kPad * 4 <= S::kRing, "a warp's O fits its ring");
@@ -212,10 +219,11 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
     const uint32_t ring_s = smem_u32(ring);
     // what this lane reads: in K keys slot_of(g) and + 8 of each 16, in V keys t4 and 7 - t4 and + 8
     const int k_slot = slot_of(g), v_even = t4, v_odd = 4 + (t4 ^ 3);
-    const uint32_t k_at = k_slot * S::kLine + t4 * (HD / 8);
-    const uint32_t ve_at = S::kCodes + v_even * S::kLine + g * (HD / 16), vo_at = S::kCodes + v_odd * S::kLine + g * (HD / 16);
-    const uint32_t ks_at = k_slot * S::kScale + (HD == 128 ? t4 : t4 >> 1) * 2;
-    const int v_group = HD == 128 ? g >> 1 : g >> 2;
+    const uint32_t k_at = k_slot * S::kLine + t4 * (kThree ? 4 : HD / 8);
+    const uint32_t v_unit = kThree ? 2 : HD / 16;
+    const uint32_t ve_at = S::kCodes + v_even * S::kLine + g * v_unit, vo_at = S::kCodes + v_odd * S::kLine + g * v_unit;
+    const uint32_t ks_at = k_slot * S::kScale + (HD == 128 ? t4 : HD == 64 ? t4 >> 1 : 0) * 2;
+    const int v_group = HD == 128 ? g >> 1 : HD == 64 ? g >> 2 : 0;
     const uint32_t ves_at = S::kScales + v_even * S::kScale + v_group * 2;
     const uint32_t vos_at = S::kScales + v_odd * S::kScale + v_group * 2;
     // scores are scaled by |scale| inside the exponent; a negative one turns Q
@@ -364,10 +372,10 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
             const int rr = 8 * n + g;
             const bool live = rr < nrows;
             const int row = row0 + (live ? rr : 0), a = row / p.group, hh = kvh * p.group + row - a * p.group;
-            const T *src = reinterpret_cast<const T *>(p.Q) + (long long)(q.row0 + a) * p.q_stride + (long long)hh * HD + t4 * (HD / 4);
+            const T *src = reinterpret_cast<const T *>(p.Q) + (long long)(q.row0 + a) * p.q_stride + (long long)hh * HD + t4 * (kThree ? 8 : HD / 4);
 #pragma unroll
             for (int w = 0; w < kWords; ++w) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(GPN(p.bnd, src + 8 * w, 16));
+                const uint4 x = *reinterpret_cast<const uint4 *>(GPN(p.bnd, src + (kThree ? 32 : 8) * w, 16));
                 const uint32_t v[4] = {live ? (x.x & q_and) ^ q_xor : 0u, live ? (x.y & q_and) ^ q_xor : 0u,
                                        live ? (x.z & q_and) ^ q_xor : 0u, live ? (x.w & q_and) ^ q_xor : 0u};
 #pragma unroll
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
             }
         }
 
-        // O^T: channels kTiles g' .. of row 2 t4 + e: o[n][i][e] is channel 2 i, o[n][i][2 + e] 2 i + 1
+        // O^T of row 2 t4 + e: of the lane's channels o[n][i][e] is 2 i, o[n][i][2 + e] 2 i + 1
         float o[N][kTiles][4], m[N][2], l[N][2];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
@@ -416,8 +424,9 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
             }
 
             // kX blocks of 16 keys at a time: all four for 8 rows (more products in flight: 128k
-            // keys 42.5 us, two at a time 43.9), two for 16 (four do not fit the registers)
-            constexpr int kX = N == 1 ? 4 : 2;
+            // keys 42.5 us, two at a time 43.9), two where tiles may have 16 (registers: with four for
+            // those of 8 among them the window of 48 requests takes 90.7 us, so 89.9)
+            constexpr int kX = kN == 1 ? 4 : 2;
 #pragma unroll 1
             for (int x0 = 0; x0 < 4; x0 += kX) {
                 const int u0 = lo + kUnit * (warp + kWarps * n_it) + x0 * (kUnit / 4);
@@ -438,6 +447,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
                             if (!here) {
                                 uint8_t *zero = const_cast<uint8_t *>(sc) + S::kScales + (32 * i + lane) * S::kScale;
                                 if constexpr (HD == 128) *reinterpret_cast<uint2 *>(zero) = make_uint2(0u, 0u);
+                                else if constexpr (kThree) for (int k = 0; k < 3; ++k) reinterpret_cast<uint16_t *>(zero)[k] = 0;
                                 else *reinterpret_cast<uint32_t *>(zero) = 0u;
                             }
                         }
@@ -462,6 +472,11 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
 #pragma unroll
                         for (int e = 0; e < 4; ++e) c[n][x][e] = 0.f;
                 uint32_t w[kX][2][kWords], s[kX][2], b[kX][2];
+                auto k_scale = [&](int x, int h, int k) {  // of word k
+                    const uint32_t one = *reinterpret_cast<const uint16_t *>(sc + (16 * x + 8 * h) * S::kScale + ks_at + (kThree ? 2 * k : 0));
+                    s[x][h] = __byte_perm(one, one, 0x1010);
+                    b[x][h] = bias_of<T>(s[x][h]);
+                };
 #pragma unroll
                 for (int x = 0; x < kX; ++x)
 #pragma unroll
@@ -470,18 +485,20 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
                         if constexpr (HD == 128) {
                             const uint4 v = *reinterpret_cast<const uint4 *>(at);
                             w[x][h][0] = v.x, w[x][h][1] = v.y, w[x][h][kWords - 2] = v.z, w[x][h][kWords - 1] = v.w;
+                        } else if constexpr (kThree) {
+#pragma unroll
+                            for (int k = 0; k < kWords; ++k) w[x][h][k] = *reinterpret_cast<const uint32_t *>(at + 16 * k);
                         } else {
                             const uint2 v = *reinterpret_cast<const uint2 *>(at);
                             w[x][h][0] = v.x, w[x][h][1] = v.y;
                         }
-                        const uint32_t one = *reinterpret_cast<const uint16_t *>(sc + (16 * x + 8 * h) * S::kScale + ks_at);
-                        s[x][h] = __byte_perm(one, one, 0x1010);
-                        b[x][h] = bias_of<T>(s[x][h]);
+                        if (!kThree) k_scale(x, h, 0);
                     }
 #pragma unroll
                 for (int k = 0; k < kWords; ++k)
 #pragma unroll
                     for (int x = 0; x < kX; ++x) {
+                        if (kThree) k_scale(x, 0, k), k_scale(x, 1, k);
                         uint32_t va[4], vb[4];
                         values<T>(w[x][0][k], s[x][0], b[x][0], masks, va);
                         values<T>(w[x][1][k], s[x][1], b[x][1], masks, vb);
@@ -562,37 +579,46 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
 #pragma unroll
                 for (int x = 0; x < kX; ++x) {
                     // keys 16 x + 8 h + v_even, v_odd
-                    uint32_t we[2][HD / 64], wo[2][HD / 64], vs[2], vb[2];
+                    uint32_t we[2][kWords], wo[2][kWords], vs[2], vb[2];     // (kThree: a quad in each)
+                    auto v_scales = [&](int h, int k) {    // of both keys, quad k
+                        const uint8_t *of = sc + (16 * x + 8 * h) * S::kScale + (kThree ? 2 * k : 0);
+                        vs[h] = __byte_perm(*reinterpret_cast<const uint16_t *>(of + ves_at), *reinterpret_cast<const uint16_t *>(of + vos_at), 0x5410);
+                        vb[h] = bias_of<T>(vs[h]);
+                    };
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint8_t *at = st + (16 * x + 8 * h) * S::kLine;
                         if constexpr (HD == 128) {
                             const uint2 ve = *reinterpret_cast<const uint2 *>(at + ve_at), vo = *reinterpret_cast<const uint2 *>(at + vo_at);
-                            we[h][0] = ve.x, we[h][HD / 64 - 1] = ve.y;
-                            wo[h][0] = vo.x, wo[h][HD / 64 - 1] = vo.y;
+                            we[h][0] = ve.x, we[h][1] = ve.y;
+                            wo[h][0] = vo.x, wo[h][1] = vo.y;
+                        } else if constexpr (kThree) {
+#pragma unroll
+                            for (int k = 0; k < kQuads; ++k) {
+                                we[h][k] = *reinterpret_cast<const uint16_t *>(at + ve_at + 16 * k);
+                                wo[h][k] = *reinterpret_cast<const uint16_t *>(at + vo_at + 16 * k);
+                            }
                         } else {
                             we[h][0] = *reinterpret_cast<const uint32_t *>(at + ve_at);
                             wo[h][0] = *reinterpret_cast<const uint32_t *>(at + vo_at);
                         }
-                        const uint8_t *of = sc + (16 * x + 8 * h) * S::kScale;
-                        vs[h] = __byte_perm(*reinterpret_cast<const uint16_t *>(of + ves_at), *reinterpret_cast<const uint16_t *>(of + vos_at), 0x5410);
-                        vb[h] = bias_of<T>(vs[h]);
+                        if (!kThree) v_scales(h, 0);
                     }
 #pragma unroll
-                    for (int k = 0; k < HD / 64; ++k)
+                    for (int k = 0; k < kQuads; ++k) {
+                        // four channels (quad k of the lane's) of two keys
+                        const int word = kThree ? k : k / 2;
+                        const uint32_t pick = !kThree && k % 2 ? 0x7632 : 0x5410;
+                        if (kThree) v_scales(0, k), v_scales(1, k);
+                        uint32_t a0[4], a1[4];
+                        values<T>(__byte_perm(we[0][word], wo[0][word], pick), vs[0], vb[0], masks, a0);
+                        values<T>(__byte_perm(we[1][word], wo[1][word], pick), vs[1], vb[1], masks, a1);
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            // four channels (8 k + 4 half + 0..3 of the lane's) of two keys
-                            uint32_t a0[4], a1[4];
-                            values<T>(__byte_perm(we[0][k], wo[0][k], half ? 0x7632 : 0x5410), vs[0], vb[0], masks, a0);
-                            values<T>(__byte_perm(we[1][k], wo[1][k], half ? 0x7632 : 0x5410), vs[1], vb[1], masks, a1);
-                            const int i = 4 * k + 2 * half;
-#pragma unroll
-                            for (int n = 0; n < N; ++n) {
-                                mma16816<T>(o[n][i], a0[0], a0[1], a1[0], a1[1], pb[n][x][0], pb[n][x][1]);
-                                mma16816<T>(o[n][i + 1], a0[2], a0[3], a1[2], a1[3], pb[n][x][0], pb[n][x][1]);
-                            }
+                        for (int n = 0; n < N; ++n) {
+                            mma16816<T>(o[n][2 * k], a0[0], a0[1], a1[0], a1[1], pb[n][x][0], pb[n][x][1]);
+                            mma16816<T>(o[n][2 * k + 1], a0[2], a0[3], a1[2], a1[3], pb[n][x][0], pb[n][x][1]);
                         }
+                    }
                 }
             }
             __syncwarp();                        // every lane has read the stage
@@ -614,7 +640,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
                 if (g == 0) sml[warp][row] = make_float2(m[n][e], sum);
 #pragma unroll
                 for (int d = 0; d < kTiles; ++d)
-                    *reinterpret_cast<float2 *>(mine_o + row * kPad + g * (HD / 8) + 2 * d) = make_float2(o[n][d][e], o[n][d][2 + e]);
+                    *reinterpret_cast<float2 *>(mine_o + row * kPad + (kThree ? d / 2 * 32 + g * 4 + d % 2 * 2 : g * (HD / 8) + 2 * d)) = make_float2(o[n][d][e], o[n][d][2 + e]);
             }
         __syncthreads();
         if (threadIdx.x < 8 * N) {
@@ -822,7 +848,9 @@ __global__ void __launch_bounds__(kThreadsG, kR == 1 ? 8 : 4) k_decode4_general(
 template <typename T, int HD, int kN, int kWarps>
 cudaError_t launch_w(const DecodeArgs &a, cudaStream_t st) {
     using S = Shape4<HD, kN, kWarps>;
-    const auto fn = a.stride == 1 ? &k_decode4_rows<T, HD, kN, kWarps, true> : &k_decode4_rows<T, HD, kN, kWarps, false>;
+    auto fn = &k_decode4_rows<T, HD, kN, kWarps, true>;
+    if constexpr (HD != 96)
+        if (a.stride > 1) fn = &k_decode4_rows<T, HD, kN, kWarps, false>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), S::kSmem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)a.nsplit, (unsigned)(a.hk * a.row_tiles), (unsigned)a.batch);
@@ -849,8 +877,11 @@ cudaError_t launch_general_t(const DecodeArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_decode4_rows(DType dt, const DecodeArgs &a, cudaStream_t st) {
-    if (dt == kF16) return a.hd == 64 ? launch_hd<__half, 64>(a, st) : launch_hd<__half, 128>(a, st);
-    return a.hd == 64 ? launch_hd<__nv_bfloat16, 64>(a, st) : launch_hd<__nv_bfloat16, 128>(a, st);
+    auto launch = [&](auto of) {
+        using T = decltype(of);
+        return a.hd == 64 ? launch_hd<T, 64>(a, st) : a.hd == 96 ? launch_hd<T, 96>(a, st) : launch_hd<T, 128>(a, st);
+    };
+    return dt == kF16 ? launch(__half()) : launch(__nv_bfloat16());
 }
 cudaError_t launch_decode4_general(DType dt, const DecodeArgs &a, cudaStream_t st) {
     return dt == kF32 ? launch_general_t<float>(a, st) : dt == kF16 ? launch_general_t<__half>(a, st) : launch_general_t<__nv_bfloat16>(a, st);

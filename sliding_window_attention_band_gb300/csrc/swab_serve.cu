@@ -413,7 +413,7 @@ constexpr long long kLongPiece = 5120;
 DecodePlan plan_decode4(const swab_decode_desc *d) {
     DecodePlan p{};
     const long long group = d->h / d->hk, batch = d->cache.batch, keys = most_keys(d);
-    p.rows = d->dtype != SWAB_F32 && (d->head_dim == 64 || d->head_dim == 128);
+    p.rows = d->dtype != SWAB_F32 && (d->head_dim == 64 || d->head_dim == 128 || (d->head_dim == 96 && d->dilation == 0));
     long long blocks = batch * d->hk, hold = 8 * kSms, least = 64;
     if (p.rows) {
         const long long rows = d->dilation == 0 ? d->max_q * group : group;

@@ -245,6 +245,15 @@ def test_decode_of_many_requests(case, dtype, hd):
     check_some(c, o, lse, sorted({0, 1, n // 3, n // 2, n - 2, n - 1}))
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("case", [
+    dict(lens=[700, 33, 1, 260], new=[1, 1, 1, 1], h=4, hk=2), dict(lens=[500, 90, 64], new=[4, 0, 3], h=12, hk=3),
+    dict(lens=[1500], new=[2], h=40, hk=2, page=64), dict(lens=[400, 17], new=[2, 1], h=6, hk=2, w=50, n_sink=19),
+    dict(lens=[300, 120], new=[2, 2], h=8, hk=2, w=40, ring=True, n_sink=16), dict(lens=[300, 80], new=[3, 1], h=4, hk=2, w=30, dilation=2)])
+def test_decode_with_three_groups_a_head(case, dtype):
+    Decode4(dtype, hd=96, seed=116, pad=1, **case).check()
+
+
 @pytest.mark.parametrize("heads,m", [((4, 1, 64), 1), ((8, 1, 128), 2)])
 def test_decode_of_requests_of_very_different_lengths(heads, m):
     """More lists than the GPU holds at once, a few of them long: several pieces a list, empty for the others."""
