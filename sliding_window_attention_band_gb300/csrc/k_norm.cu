@@ -18,9 +18,9 @@
 // tile of tokens, rows listed and tables in shared memory, the gradient of 12 x 1365
 // tokens took 48 us: every tile waited for its list, its table and its first rows.)
 //
-// 4 bits.  A group of 32 channels is four pieces of 16-bit values, so four lanes:
-// the value of largest magnitude is a maximum over the integers (bits << 1 | sign
-// positive), two shuffles; the quotient x / s is decided exactly: the values have at
+// 4 bits.  A group of 32 channels is four pieces of 16-bit values, on four adjacent lanes
+// where the pairs of the rotation leave it so: the value of largest magnitude is a
+// maximum over the integers (bits << 1 | sign positive), two shuffles; the quotient x / s is decided exactly: the values have at
 // most 11 significant bits and s 5, so a quotient that is no tie is 2^-13 off one,
 // and fma(x, 1 / s, 768) rounds it to a multiple of 2^-14 before it is rounded to
 // a whole number.
@@ -179,20 +179,46 @@ __device__ __forceinline__ float sum2(uint64_t x) {
     return lo + hi;
 }
 
-// A lane's 16 bytes of a group of 16-bit values (already rounded): eight codes as a
-// word, and the group's scale.  Four adjacent lanes hold the group.  The rank is
-// taken on the 16 bits of two values at a time; a quotient is rounded to a multiple of
-// 2^-14 by the fma and to the nearest whole number, plus 8, by the addition (12582920 =
-// 1.5 * 2^23 + 8, even as 8 is, so that ties stay with the even quotient).
-template <typename T>
-__device__ __forceinline__ uint32_t quantise8(const uint4 &y, float &s) {
+// The largest rank of a lane's eight 16-bit values (already rounded), in 16 bits, two
+// values at a time.
+__device__ __forceinline__ uint32_t rank8(const uint4 &y) {
     const uint32_t w[4] = {y.x, y.y, y.z, y.w};
     uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) top = __vmaxu2(top, ((w[k] << 1) & 0xfffefffeu) | ((~w[k] >> 15) & 0x00010001u));
-    uint32_t rank = max(top & 0xffffu, top >> 16);
-    rank = max(rank, __shfl_xor_sync(0xffffffffu, rank, 1));
-    rank = max(rank, __shfl_xor_sync(0xffffffffu, rank, 2));
+    return max(top & 0xffffu, top >> 16);
+}
+// The ranks of the groups that a lane's two pieces belong to.  kAdjacent: four adjacent
+// lanes hold a group.  Else a row's groups, four at most, lie over its `lanes` lanes as
+// the pairs of the rotation want it: every lane puts what it has in its groups' places
+// of two words, whose maxima all take (8.9k tokens of 32 + 8 + 8 heads of 96 with their
+// reading back 61 us, a warp a row 221; of 128, a quarter turned, 67 and 254).
+template <bool kAdjacent>
+__device__ __forceinline__ void group_ranks(uint32_t &ra, uint32_t &rb, int pa, int pb, int lanes) {
+    if constexpr (kAdjacent) {
+#pragma unroll
+        for (int d = 1; d <= 2; d <<= 1) {
+            ra = max(ra, __shfl_xor_sync(0xffffffffu, ra, d));
+            rb = max(rb, __shfl_xor_sync(0xffffffffu, rb, d));
+        }
+    } else {
+        const int sa = pa / 4 * 16 & 16, sb = pb / 4 * 16 & 16;
+        const bool ha = pa >= 8, hb = pb >= 8;
+        uint32_t lo = __vmaxu2(ha ? 0u : ra << sa, hb ? 0u : rb << sb), hi = __vmaxu2(ha ? ra << sa : 0u, hb ? rb << sb : 0u);
+        for (int d = 1; d < lanes; d <<= 1) {
+            lo = __vmaxu2(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+            hi = __vmaxu2(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+        }
+        ra = (ha ? hi : lo) >> sa & 0xffffu;
+        rb = (hb ? hi : lo) >> sb & 0xffffu;
+    }
+}
+// The eight codes of a piece, and the scale of its group from the group's rank.  A
+// quotient is rounded to a multiple of 2^-14 by the fma and to the nearest whole
+// number, plus 8, by the addition (12582920 = 1.5 * 2^23 + 8, even as 8 is, so that ties
+// stay with the even quotient).
+template <typename T>
+__device__ __forceinline__ uint32_t quantise8(const uint4 &y, uint32_t rank, float &s) {
     s = scale_of<T>((__float_as_uint(lo16<T>(rank >> 1)) << 1) | (rank & 1u));
     const bool none = !(fabsf(s) > 0.f);                             // 0 or NaN
     const float inv = none ? 0.f : __frcp_rn(s);
@@ -233,7 +259,7 @@ __device__ __forceinline__ void turn2(uint64_t &a, uint64_t &b, uint64_t c, uint
 // ---------------------------------------------------------------------------
 // Rows on lane groups: kInter: adjacent pairs in 16-byte pieces, else halves.  kKind: 0
 // = Q, K -> Qo, Ko; 1 = into the cache; 2 = into the cache in 4 bits (16-bit types,
-// groups on four lanes).
+// groups on four adjacent lanes), 3 = the same with groups anywhere in the row.
 constexpr int kWarps = 4;
 constexpr int kAhead = 2;            // rows of a lane group loaded ahead
 
@@ -414,10 +440,10 @@ __global__ void __launch_bounds__(32 * kWarps, 5) k_norm(const __grid_constant__
             } else {
                 const unsigned blk = (unsigned)here >> p.page_log2, off = (unsigned)here & ((1u << p.page_log2) - 1u), head = e - (is_v ? hqk : hq);
                 const unsigned long long line = ((blk * (unsigned)p.hk + head) << p.page_log2) + off;     // below 2^32
-                const unsigned width = kKind == 2 ? p.hd / 2 : p.row_bytes;
+                const unsigned width = kKind >= 2 ? p.hd / 2 : p.row_bytes;
                 dst = (char *)(is_v ? p.Vc : p.Kc) + line * width;
                 dstep = (unsigned long long)(group << p.page_log2) * width;
-                if (kKind == 2) sc = (T *)(is_v ? a.Vs : a.Ks) + line * (p.hd / kGroup4);
+                if (kKind >= 2) sc = (T *)(is_v ? a.Vs : a.Ks) + line * (p.hd / kGroup4);
             }
         };
         aim_out();
@@ -473,17 +499,17 @@ __global__ void __launch_bounds__(32 * kWarps, 5) k_norm(const __grid_constant__
             }
             const uint4 ya = as_is ? xa : repack2<T>(fa), yb = as_is ? xb : repack2<T>(fb);
             bool whole = there && (is_q || kept);      // a row of the tensors' type to write
-            if constexpr (kKind == 2 && sizeof(T) == 2) {
+            if constexpr (kKind >= 2 && sizeof(T) == 2) {
                 if (__any_sync(0xffffffffu, there && !is_q)) {
                     float s0, s1;                      // (ya, yb: as the cache of this type would hold them)
-                    const uint32_t wa = quantise8<T>(ya, s0), wb = quantise8<T>(yb, s1);
+                    uint32_t ra = l.active ? rank8(ya) : 0u, rb = l.active ? rank8(yb) : 0u;
+                    group_ranks<kKind == 2>(ra, rb, l.pa, l.pb, L);
+                    const uint32_t wa = quantise8<T>(ya, ra, s0), wb = quantise8<T>(yb, rb, s1);
                     if (there && !is_q && kept) {
                         *reinterpret_cast<uint32_t *>(GPN(p.bnd, dst + l.pa * 4, 4)) = wa;
                         *reinterpret_cast<uint32_t *>(GPN(p.bnd, dst + l.pb * 4, 4)) = wb;
-                        if ((l.sub & 3) == 0) {
-                            *GP(p.bnd, sc + l.pa / 4) = Elt<T>::from_f(s0);
-                            *GP(p.bnd, sc + l.pb / 4) = Elt<T>::from_f(s1);
-                        }
+                        if ((l.pa & 3) == 0) *GP(p.bnd, sc + l.pa / 4) = Elt<T>::from_f(s0);
+                        if ((l.pb & 3) == 0) *GP(p.bnd, sc + l.pb / 4) = Elt<T>::from_f(s1);
                     }
                     sc += (unsigned long long)(group << p.page_log2) * (p.hd / kGroup4);
                 }
@@ -1009,9 +1035,9 @@ __global__ void __launch_bounds__(kThreads) k_read4(const __grid_constant__ Read
 }
 
 // Which kernel takes the rows: halves or adjacent pairs in 16-byte pieces on at
-// most 32 lanes (and, into 4 bits, 16-bit types whose groups lie on four lanes),
-// else a warp a row.  lanes: of a row, a power of two from 4.
-int mode_of(const RotaryArgs &r, int es, bool bits4, int *lanes, NormArgs *a = nullptr) {
+// most 32 lanes (and, into 4 bits, 16-bit types whose groups lie on four adjacent lanes or
+// are four at most), else a warp a row.  lanes: of a row, a power of two from 4.
+int mode_of(const RotaryArgs &r, int es, int *kind, int *lanes, NormArgs *a = nullptr) {
     const int vec = 16 / es, pieces = r.hd / vec, half = r.rot / 2;
     int L = 4;
     while (L < pieces / 2) L *= 2;
@@ -1024,7 +1050,11 @@ int mode_of(const RotaryArgs &r, int es, bool bits4, int *lanes, NormArgs *a = n
         a->sum_lanes = fits ? L : 0;
         a->sum_turn = nturn;
     }
-    if (bits4) fits = fits && es == 2 && nturn % 4 == 0 && (pieces - 2 * nturn) % 8 == 0;
+    if (*kind == 2) {
+        const bool adjacent = nturn % 4 == 0 && (pieces - 2 * nturn) % 8 == 0;
+        fits = fits && es == 2 && (adjacent || pieces <= 16);
+        if (fits && !adjacent) *kind = 3;
+    }
     if (!fits) *lanes = 32;
     return !fits ? 2 : r.interleaved ? 1 : 0;
 }
@@ -1035,12 +1065,15 @@ cudaError_t launch_t(const NormArgs &a, int mode, dim3 grid, size_t smem, cudaSt
         if (mode == 0) return launch_dependent(&k_norm<T, false, kKind>, grid, 32 * kWarps, smem, st, a);
         if (mode == 1) return launch_dependent(&k_norm<T, true, kKind>, grid, 32 * kWarps, smem, st, a);
     }
-    return launch_dependent(&k_norm_rows<T, kKind>, grid, kThreads, smem, st, a);
+    return launch_dependent(&k_norm_rows<T, kKind == 3 ? 2 : kKind>, grid, kThreads, smem, st, a);
 }
 template <typename T>
 cudaError_t launch_kind(int kind, const NormArgs &a, int mode, dim3 grid, size_t smem, cudaStream_t st) {
-    return kind == 0 ? launch_t<T, 0>(a, mode, grid, smem, st) : kind == 1 ? launch_t<T, 1>(a, mode, grid, smem, st)
-                                                                           : launch_t<T, 2>(a, mode, grid, smem, st);
+    if (kind == 0) return launch_t<T, 0>(a, mode, grid, smem, st);
+    if (kind == 1) return launch_t<T, 1>(a, mode, grid, smem, st);
+    if constexpr (sizeof(T) == 2)
+        if (kind == 3) return launch_t<T, 3>(a, mode, grid, smem, st);
+    return launch_t<T, 2>(a, mode, grid, smem, st);
 }
 
 constexpr long long kTable = 16384;      // bytes of the two tables at most
@@ -1080,7 +1113,7 @@ cudaError_t launch_bwd_t(const NormArgs &a, int mode, size_t smem, cudaStream_t 
 
 cudaError_t launch_norm(DType dt, int kind, NormArgs a, cudaStream_t st) {
     const int es = dt == kF32 ? 4 : 2;
-    const int mode = mode_of(a.r, es, kind == 2, &a.lanes, &a);
+    const int mode = mode_of(a.r, es, &kind, &a.lanes, &a);
     a.r.rows = a.r.hq + a.r.hk * (kind ? 2 : 1);
     a.r.row_bytes = a.r.hd * es;
     const int sms = device_sm_count();
@@ -1106,7 +1139,8 @@ cudaError_t launch_norm(DType dt, int kind, NormArgs a, cudaStream_t st) {
 
 cudaError_t launch_norm_bwd(DType dt, NormArgs a, cudaStream_t st) {
     const int es = dt == kF32 ? 4 : 2;
-    const int mode = mode_of(a.r, es, false, &a.lanes);
+    int kind = 0;
+    const int mode = mode_of(a.r, es, &kind, &a.lanes);
     a.r.rows = a.r.hq + a.r.hk;
     a.both = mode < 2;
     const int sms = device_sm_count();

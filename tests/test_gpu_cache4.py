@@ -44,7 +44,8 @@ def empty_cells(cache, hk, hd, dtype, fill=0xa5):
 APPEND = [  # h, hk, hd, rot, interleaved, page
     (4, 2, 64, 64, False, 16), (4, 2, 64, 32, True, 64), (4, 2, 64, 32, False, 64), (3, 1, 128, 128, False, 32), (3, 3, 128, 64, False, 16),
     (2, 2, 128, 128, True, 128), (6, 2, 96, 96, False, 32), (2, 1, 96, 48, True, 16), (2, 2, 32, 32, False, 16), (1, 1, 256, 256, False, 16),
-    (2, 1, 64, 0, False, 16), (2, 2, 160, 64, False, 16), (40, 8, 128, 128, False, 64)]
+    (2, 1, 64, 0, False, 16), (2, 2, 160, 64, False, 16), (40, 8, 128, 128, False, 64), (2, 2, 128, 32, False, 16), (6, 3, 96, 0, False, 16),
+    (3, 1, 96, 48, False, 32), (3, 2, 96, 96, True, 16), (2, 1, 64, 16, False, 16)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
