@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
                 bool all;
                 if constexpr (kRun) {
                     const uint32_t have = there4 >> x0 & ((1u << kX) - 1u);
-                    if (have == 0u) break;
+                    if (have == 0u) continue;              // (absent blocks: the next ones may be there)
                     all = (full4 >> x0 & ((1u << kX) - 1u)) == (1u << kX) - 1u;
                     if (!all) {
                         // scales of the values that no row attends to: 0, whatever is there

@@ -321,6 +321,34 @@ def test_decode_with_blocks_that_are_not_there(hd, dtype):
     swab.device_status(reset=True)
 
 
+@pytest.mark.parametrize("hd,dtype", [(64, F16), (96, BF16), (128, F16), (128, BF16)])
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("case", [dict(), dict(w=150), dict(w=130, n_sink=20), dict(w=90, n_sink=33, dilation=1)])
+def test_decode_with_present_keys_behind_absent_ones(case, page, hd, dtype):
+    """Tiles of 16 rows, and of 8 with a tail behind them.  Request r has holes where the bits of r are set in four
+    adjacent columns: every choice of the four halves of a group of 64 keys where page is 16 and lists start at 0, else
+    holes anywhere in a group, as windows and sinks start lists off multiples of 64."""
+    lens = [200 + 13 * r for r in range(16)]
+    for h, hk, m in ((16, 1, 1), (8, 2, 4), (12, 2, 3), (4, 2, 2)):
+        c = Decode4(dtype, lens, [m] * 16, h, hk, hd, page=page, pad=1, seed=122, **case)
+        for r in range(16):
+            first = (lens[r] - 120 if "w" in case else 64) // page
+            for k in range(4):
+                if r >> k & 1 and first + k < c.table.shape[1]:
+                    c.table[r, first + k] = -1
+        o, lse = c.run()
+        c.check(o, lse)
+        assert swab.device_status(reset=True) == 0
+        outside = np.where(np.arange(c.table.shape[1]) % 2 == 0, c.cells[0].shape[0] + 3, -2)
+        for r in range(16):                                          # ids outside the cache: the same keys, flagged
+            holes = (c.table[r] == -1) & (np.arange(c.table.shape[1]) < lens[r] // page)
+            c.table[r, holes] = outside[holes]
+        again = c.run()
+        assert swab.device_status(reset=True) == INVALID_BIT
+        same_bits(again[0], o)
+        same_bits(again[1], lse)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_values_that_are_not_finite_show(dtype, bad):
