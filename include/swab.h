@@ -526,9 +526,10 @@ SWAB_API size_t norm_rotary_bwd_workspace(const swab_rotary_desc *desc);
  *     dwq_c = sum over all rows of g_c x_c r,
  * the same for K.  Strides: q_stride, k_stride of desc are those of dQo, dKo,
  * qo_stride, ko_stride those of dQ, dK, and norm's those of Q, K.  dwq, dwk
- * [head_dim] fp32, 16-byte aligned; NULL leaves them out (they need wq, wk).  dQ
- * may be dQo or Q (same pointer and strides), dK likewise, no other overlap.  fp32,
- * the sums over rows in a fixed order (results repeat bitwise on one GPU).
+ * [head_dim] fp32, 16-byte aligned; NULL leaves them out (they need wq, wk; dwk is 0
+ * where hk is 0).  dQ may be dQo or Q (same pointer and strides), dK likewise, no
+ * other overlap.  fp32, the sums over rows in a fixed order (results repeat bitwise
+ * on one GPU).
  * workspace: norm_rotary_bwd_workspace(desc) bytes, 16-byte aligned, needed where
  * dwq or dwk is given; its contents on entry do not matter, calls that may overlap on
  * the GPU need one each. */

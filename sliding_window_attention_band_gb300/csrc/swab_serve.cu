@@ -669,7 +669,7 @@ SWAB_API swab_status norm_rotary_bwd(const swab_rotary_desc *desc, const swab_no
     a.X[0] = Q;
     a.X[1] = keys ? K : nullptr;
     a.dw[0] = dwq;
-    a.dw[1] = keys ? dwk : nullptr;
+    a.dw[1] = dwk;                       // (without keys a sum over no rows: 0)
     for (const float *w : a.dw)
         if (w && !aligned(w, 16)) return SWAB_ERR_MISALIGNED;
     if (a.dw[0] && a.dw[0] == a.dw[1]) return SWAB_ERR_INVALID_ARG;

@@ -96,7 +96,7 @@ def norm_rotary_bwd(desc: _s.RotaryDesc, norm: NormDesc, turns, dQo, Q, dQ, dKo=
                     dwk=None, workspace=None, pos=None, stream=None):
     """Gradient of norm_rotary: dQo and the call's Q -> dQ, dKo and K -> dK (dQ may
     be dQo or Q), and the weights' gradients dwq, dwk [hd] float32, summed over
-    all rows (None: left out; they need workspace)."""
+    all rows (without keys dwk is 0; None: left out; they need workspace)."""
     if stream is None and _s._done("norm_rotary_bwd", _calls().norm_rotary_bwd(desc._addr, norm._addr, turns, pos, dQo, dKo, Q, K, wq, wk,
                                                                                dQ, dK, dwq, dwk, workspace)):
         return

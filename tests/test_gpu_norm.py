@@ -289,6 +289,24 @@ def test_rows_that_are_not_finite(dtype):
     same_bits(y[0][rest], clean[0][rest])
 
 
+@pytest.mark.parametrize("hd,rot", [(64, 64), (80, 20)])                 # rows on lane groups, a warp a row
+@pytest.mark.parametrize("with_q", [False, True])
+def test_gradient_of_a_key_weight_without_keys(hd, rot, with_q):
+    """A sum over no rows is 0, not what the buffer held."""
+    turns, *_ = frequencies(rot, "none")
+    d, q, g, w = swab.RotaryDesc(1, 9, 3, 0, hd, rot, dtype=F16), *(randn(s, F16, 75) for s in ((1, 9, 3, hd), (1, 9, 3, hd), (hd,)))
+    ws = torch.empty(swab.norm_rotary_bwd_workspace(d), dtype=torch.uint8, device="cuda")
+    dwq, ref = (torch.full((hd,), 7.0, device="cuda") for _ in range(2))
+    swab.norm_rotary_bwd(d, swab.NormDesc(), turns, g, q, torch.empty_like(q), wq=w, dwq=ref, workspace=ws)
+    for wk in (w, None):
+        dwk = torch.full((hd,), 7.0, device="cuda")
+        swab.norm_rotary_bwd(d, swab.NormDesc(), turns, g, q, torch.empty_like(q), wq=w, wk=wk, dwq=dwq if with_q else None, dwk=dwk,
+                             workspace=ws)
+        assert (dwk == 0.0).all()
+    if with_q:
+        same_bits(dwq, ref)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("case", [(4, 2, 64, 64, False, 16), (3, 1, 128, 64, True, 64), (6, 6, 96, 96, False, 32), (2, 2, 80, 20, False, 16),
                                   (1, 1, 64, 0, False, 128)])
