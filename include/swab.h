@@ -529,7 +529,8 @@ SWAB_API size_t norm_rotary_bwd_workspace(const swab_rotary_desc *desc);
  * [head_dim] fp32, 16-byte aligned; NULL leaves them out (they need wq, wk; dwk is 0
  * where hk is 0).  dQ may be dQo or Q (same pointer and strides), dK likewise, no
  * other overlap.  fp32, the sums over rows in a fixed order (results repeat bitwise
- * on one GPU).
+ * on one GPU).  A row of Q or K whose squares pass fp32's range (there norm_rotary
+ * gives 0) has the gradient 0 and adds 0 to the weights'.
  * workspace: norm_rotary_bwd_workspace(desc) bytes, 16-byte aligned, needed where
  * dwq or dwk is given; its contents on entry do not matter, calls that may overlap on
  * the GPU need one each. */

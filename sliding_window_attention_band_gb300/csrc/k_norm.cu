@@ -240,6 +240,10 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 &y, uint32_t rank, flo
 // 1 / sqrt(mean of squares + eps), within 2 ulp
 __device__ __forceinline__ float inverse_norm(float sum, float by_hd, float eps) { return rsqrtf(__fmaf_rn(sum, by_hd, eps)); }
 
+// r^2 mean(g v x) of the gradient.  Where the squares pass fp32's range r is 0, and so
+// is all of the row: the products may have passed it too, and infinity times 0 is NaN.
+__device__ __forceinline__ float mean_part(float dot, float by_hd, float rn) { return rn == 0.f ? 0.f : dot * by_hd * rn * rn; }
+
 // A pair turned, rounded as k_rotary does (so that the cache holds the same bits
 // with and without norms, in either width): pieces, and pair by pair.
 __device__ __forceinline__ void turn(float &a, float &b, float c, float s, bool by_pairs = false) {
@@ -797,7 +801,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_norm_bwd(const __grid_consta
                 dot += __shfl_xor_sync(0xffffffffu, dot, d);
             }
             if (there) {
-                const float rn = inverse_norm(sum, by_hd, a.eps), c2 = dot * by_hd * rn * rn;
+                const float rn = inverse_norm(sum, by_hd, a.eps), c2 = mean_part(dot, by_hd, rn);
                 const uint64_t rn2 = f2(rn, rn), less = f2(-c2, -c2);
 #pragma unroll
                 for (int m = 0; m < kH; ++m) {
@@ -930,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_bwd_rows(const __grid_cons
                 sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 dot += __shfl_xor_sync(0xffffffffu, dot, d);
             }
-            const float rn = inverse_norm(sum, by_hd, a.eps), c2 = dot * by_hd * rn * rn;
+            const float rn = inverse_norm(sum, by_hd, a.eps), c2 = mean_part(dot, by_hd, rn);
             T *d = reinterpret_cast<T *>(r.d);
             for (int c = lane; c < p.hd; c += 32) {
                 dsum[c] = fmaf(sg[c], sx[c] * rn, dsum[c]);

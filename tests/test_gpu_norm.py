@@ -307,6 +307,35 @@ def test_gradient_of_a_key_weight_without_keys(hd, rot, with_q):
         same_bits(dwq, ref)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("hd,rot", [(64, 64), (80, 20)])                 # rows on lane groups, a warp a row
+def test_gradient_of_rows_past_the_range(hd, rot, dtype):
+    """A row whose squares pass fp32's range has the output 0 and the gradient 0, also where the products with it pass the
+    range, and adds nothing to the weights'; a NaN stays in its row."""
+    turns, *_ = frequencies(rot, "none")
+    q, g, w = randn((1, 8, 2, hd), dtype, 76), randn((1, 8, 2, hd), dtype, 77), randn((hd,), dtype, 78).abs() + 1.0
+    g[0, 3] = 1.0
+    d, nd = swab.RotaryDesc(1, 8, 2, 0, hd, rot, dtype=dtype), swab.NormDesc()
+    ws = torch.empty(swab.norm_rotary_bwd_workspace(d), dtype=torch.uint8, device="cuda")
+    out = []
+    for far in (0.0, 1e30, 1e38):
+        x = q.clone()
+        x[0, 3] = far
+        dq, dw = torch.full_like(q, 7.0), torch.full((hd,), 7.0, device="cuda")
+        swab.norm_rotary_bwd(d, nd, turns, g, x, dq, wq=w, dwq=dw, workspace=ws)
+        out.append((dq, dw))
+    for dq, dw in out[1:]:
+        assert (dq[0, 3] == 0.0).all()
+        dq[0, 3] = out[0][0][0, 3]
+        same_bits(dq, out[0][0])
+        same_bits(dw, out[0][1])
+    x[0, 3], x[0, 5, 1, 7] = 0.0, float("nan")
+    swab.norm_rotary_bwd(d, nd, turns, g, x, dq, wq=w, dwq=dw, workspace=ws)
+    assert dq[0, 5, 1].isnan().all() and dw.isnan().all()
+    dq[0, 5, 1] = out[0][0][0, 5, 1]
+    same_bits(dq, out[0][0])
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("case", [(4, 2, 64, 64, False, 16), (3, 1, 128, 64, True, 64), (6, 6, 96, 96, False, 32), (2, 2, 80, 20, False, 16),
                                   (1, 1, 64, 0, False, 128)])
