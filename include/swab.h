@@ -562,9 +562,13 @@ SWAB_API swab_status norm_rotary_append(const swab_rotary_desc *desc, const swab
  *         (fp16) or 2^-120 (bf16, fp32), and at most 1.25 * 2^11 or 1.25 * 2^123,
  *     c = min(max(rint(x / s), -8), 7) + 8   (ties to even; 8 where s is 0),
  * so that s (c - 8) has at most 8 significant bits: fp16 and bf16 hold it as
- * it is.  m's own code is 0, its value within 1/32 of m; the others are off by at
- * most |s| / 2, or 1.25 |s| next to -m.  A group with a NaN or infinity has a NaN scale,
- * codes 8: all its values are NaN.  4.5 bits a value in 16-bit types.
+ * it is.  With |m| from 2^-17 to 20480 (fp16) or 2^-113 to 1.25 * 2^126 (bf16, fp32)
+ * m's own code is 0, its value within 1/32 of m; the others are off by at most
+ * |s| / 2, or 1.25 |s| next to -m.  Beyond, values saturate: at 20480 (1.25 * 2^126) on
+ * m's side of 0, at 7/8 of that on the other.  Below, m is off by at most 2^-22
+ * (2^-118), and a group whose |m| is no more than that becomes zeros.  A group with a
+ * NaN or infinity has a NaN scale, codes 8: all its values are NaN.  4.5 bits a value in
+ * 16-bit types.
  * ------------------------------------------------------------------------- */
 
 /* rotary_append into a cache in 4 bits (codes Kc, Vc; scales Ks, Vs): Q -> Qo

@@ -74,6 +74,34 @@ def test_values_are_exact_in_their_type_and_near(dtype, torch_dtype):
     assert (np.abs(8 * np.abs(scales) - m) <= m / 32)[np.abs(scales) > 2.0 ** -18].all()
 
 
+@pytest.mark.parametrize("dtype,torch_dtype", [("f16", torch.float16), ("bf16", torch.bfloat16), ("f32", torch.float32)])
+def test_errors_by_the_size_of_the_largest_value(dtype, torch_dtype):
+    """What the header says of a group: near between two sizes, saturated above, within half a step of the smallest scale
+    below."""
+    low, high, least = (2.0 ** -17, 20480.0, 2.0 ** -22) if dtype == "f16" else (2.0 ** -113, 1.25 * 2.0 ** 126, 2.0 ** -118)
+    top = float(torch.finfo(torch_dtype).max)
+    rng = np.random.default_rng(9)
+    sizes = np.concatenate([np.exp2(rng.uniform(np.log2(low) - 8, np.log2(low) + 2, 300)), np.exp2(rng.uniform(np.log2(high) - 3, np.log2(top), 300)),
+                            [low, high, least, top]])
+    g = rng.uniform(-1, 1, (len(sizes), 32))
+    g[:, 3], g[::2, 5] = rng.choice([-1, 1], len(sizes)), -g[::2, 3]                   # one of the size, or both signs
+    x = torch.tensor(np.clip(g * sizes[:, None], -top, top)).to(torch_dtype).double().numpy()
+    codes, scales = quant.quantise(x, dtype)
+    v, s, m = quant.values(codes, scales), np.abs(scales), np.abs(x).max(1, keepdims=True)
+    first = np.where(x.max(1) == m[:, 0], x.argmax(1), x.argmin(1))[:, None]            # m: of two, the positive one
+    v_m = np.abs(np.take_along_axis(v, first, 1))
+    mine = np.sign(x) == np.sign(np.take_along_axis(x, first, 1))                      # on m's side of 0
+    assert np.isfinite(v).all()
+    mid, above, below = ((m >= low) & (m <= high))[:, 0], (m > high)[:, 0], (m < low)[:, 0]
+    assert min(mid.sum(), above.sum(), below.sum()) > 60
+    assert (np.abs(v_m - m) <= m / 32)[mid].all() and (np.take_along_axis(codes, first, 1) == 0)[mid].all()
+    assert (np.abs(v - x) <= s * np.where(codes == 15, 1.25, 0.5))[mid].all()
+    assert (np.abs(v) <= np.where(mine, high, 7 / 8 * high))[above].all() and (v_m == high)[above & (m[:, 0] > 33 / 32 * high)].all()
+    assert (np.abs(v_m - m) <= least)[below].all()
+    zeros = (m <= least)[:, 0]
+    assert zeros.any() and (v[zeros] == 0).all() and (s[~zeros] > 0).all()
+
+
 def test_planted_mistakes_show():
     x = torch.tensor(rows((50, 64), 7)).half().double().numpy()
     codes, scales = quant.quantise(x, "f16")
