@@ -37,9 +37,9 @@
 // score passes it by 2^8, weights rounded to 16 bits for the product (what the tensor
 // cores take; as in decode over 16 bits), sums fp32.
 //
-// Measured (8 heads of 128, 32 query heads, bf16): one request of 131072 tokens 42.7 us,
-// 3.5 TB/s of codes and scales; 57 requests x 4096 62 us, 4.4 TB/s; with 16 rows a tile
-// 88 us, 3.1 TB/s.  16 requests of 3000 to 5000, 24 heads over 8 of 96: 28 us, where
+// Measured (8 heads of 128, 32 query heads, bf16): one request of 131072 tokens 42.5 us,
+// 3.6 TB/s of codes and scales; 57 requests x 4096 61 us, 4.4 TB/s; with 16 rows a tile
+// 84 us, 3.2 TB/s.  16 requests of 3000 to 5000, 24 heads over 8 of 96: 28 us, where
 // the general kernel took 143.  A single step of one short request 4.4 us, of which
 // launch and join are most.
 //
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape4<HD, kN, kWarps>::kBlocks) 
 
             // kX blocks of 16 keys at a time: all four for 8 rows (more products in flight: 128k
             // keys 42.5 us, two at a time 43.9), two where tiles may have 16 (registers: with four for
-            // those of 8 among them the window of 48 requests takes 90.7 us, so 89.9)
+            // those of 8 among them the window of 48 requests takes 87.6 us, so 86.5)
             constexpr int kX = kN == 1 ? 4 : 2;
 #pragma unroll 1
             for (int x0 = 0; x0 < 4; x0 += kX) {

@@ -30,15 +30,17 @@
 // channels over all its rows, a block writes one row of sums, a second kernel adds
 // the blocks' in a fixed order.
 //
-// Every value is read once and written once.  The calls come near memory but are bound
-// by instruction issue and the latency behind it (issue slots 51 to 66 % busy with 12 to 20
-// warps an SM, which registers allow; more warps or more rows ahead were slower: 2
-// rows ahead 38 us for the prompt, 4 ahead 46, addresses that step by additions 34).
+// Every value is read once and written once.  Neither memory (27 to 47 % of its rate in
+// ncu) nor issue slots (51 to 66 %) are full: what bounds the calls is how much is in flight,
+// and that is what registers hold, 12 to 20 warps an SM with one or two row groups
+// each (more warps, or more rows ahead in registers, were slower: 2 rows ahead 38 us for
+// the prompt, 4 ahead 46, addresses that step by additions 34).
 // Measured: a prompt of 8192 tokens, 32 + 8 heads of 128, bf16: 34 us, 4.9 TB/s (the same
-// without the norms 28); prompts of 8.9k tokens, 12 + 12 + 12 heads of 64, fp16, into the
-// cache 20 us, 4.1 TB/s; of 32 + 8 + 8 heads of 128 into a cache in 4 bits 49 us by
-// itself, and 17 to read its rows back; the gradient of 12 x 1365 tokens, 24 heads of 64,
-// fp16, with both weights' 39 us, 3.9 TB/s (Q and K in blocks of their own 45 to 48).
+// without the norms 28), fp32 62 us, 5.4 TB/s; prompts of 8.9k tokens, 12 + 12 + 12 heads of
+// 64, fp16, into the cache 20 us, 4.1 TB/s; of 32 + 8 + 8 heads of 128, bf16, into a cache
+// in 4 bits 48 us, 4.0 TB/s (fp32, a warp a row, 278 us, 1.4 TB/s); the gradient of 12 x
+// 1365 tokens, 24 heads of 64, fp16, with both weights' 39 us, 3.9 TB/s (Q and K in blocks
+// of their own 45 to 48), of 8192 tokens, 32 + 8 heads of 128, bf16, 57 us, 4.4 TB/s.
 #include <algorithm>
 
 #include "swab_rows.cuh"
@@ -978,7 +980,9 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const __grid_constant__ NormAr
 }
 
 // ---------------------------------------------------------------------------
-// rows of a cache in 4 bits as values: a thread a word of codes (8 channels)
+// rows of a cache in 4 bits as values: a thread a word of codes (8 channels).  8.9k
+// tokens of 8 heads of 128, bf16, take 16 us, 2.9 TB/s, by instructions: 137 of a warp for
+// 32 words, as each divides for its row and has a slot, a scale and three addresses.
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_read4(const __grid_constant__ Read4Args p) {

@@ -400,15 +400,21 @@ DecodePlan plan_decode(const swab_decode_desc *d) {
 
 // The same over a cache in 4 bits.  Tiles of 8 rows where that holds them all, else 16:
 // the codes of a tile are turned into values once for its rows, and 57 requests x 4096
-// keys of 8 heads of 128 take 62 us with 8 rows, 88 with 16 (twice 62 as two tiles).
+// keys of 8 heads of 128 take 61 us with 8 rows, 84 with 16 (twice 61 as two tiles).
 // Blocks of four warps, 12 or 16 warps an SM by registers and shared memory (blocks of
 // two, of one: 128k keys 42.9, 45.9, 60.6 us).  Pieces as many as fit at once: 131072
 // keys of 8 heads in 38, 57, 76 pieces take 45, 42.5, 52 us, 57 being one each place.
 // Requests of one call differ in length, and who has a long list in one piece is still
 // busy when all others are done: with several of them no piece is above kLongPiece
 // keys, for at most four times the pieces (32 requests of 1 to 12000 tokens 144 us in
-// a piece each, 90 in two, 75 in three; 64 of 1 to 6000, 12 heads of 64, 70 in one, 67
-// in two; 48 under a window of 4096 91 in one, 93 in two, so a piece holds that).
+// a piece each, 90 in two, 75 in three; 64 of 1 to 6000, 12 heads of 64, 70 in one, 68
+// in two).  48 requests of 8 key heads of 128 under a window, in one piece and in as
+// many as this gives: 4096 86 (90 in two); 5200 77 and 83, of lengths 4 to 15600 103 and
+// 104; 6144 90 and 95, 121 and 118; 8192 117 and 122, 157 and 149; 16384 226 and 214, 299
+// and 247.  So equal lists just above it lose 7 %, what lies further up or differs
+// in length gains up to a fifth, where lengths spread widely half.  (The general kernel
+// cuts only to fill the GPU: by the same rule 64 requests of 1 to 6000 tokens, 12 heads
+// of 64, fp32, would take 153 us for 209, 32 of 1 to 12000 the same 182 to 184.)
 constexpr long long kLongPiece = 5120;
 DecodePlan plan_decode4(const swab_decode_desc *d) {
     DecodePlan p{};
